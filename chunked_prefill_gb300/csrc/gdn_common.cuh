@@ -25,6 +25,11 @@ __device__ __forceinline__ bool in_range(int64_t i, int64_t n, int* err) {
 __device__ __forceinline__ bool in_range(int64_t, int64_t, int*) { return true; }
 #endif
 
+// Activations of the prologue (the fused one and the recurrent step's).
+constexpr float PRO_EPS = 1e-6f;
+__device__ __forceinline__ float softplus_f(float x) { return x > 20.f ? x : log1pf(expf(x)); }
+__device__ __forceinline__ float sigmoid_f(float x) { return 1.f / (1.f + expf(-x)); }
+
 template <typename Op> struct OpTraits;
 template <> struct OpTraits<__nv_bfloat16> {
     static constexpr int PAD = 8;  // 16 bytes: ldmatrix rows land on distinct banks

@@ -18,17 +18,14 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "gdn_common.cuh"
 #include "gdn_internal.h"
 
 namespace gdn {
 namespace {
 
-constexpr float PRO_EPS = 1e-6f;
 constexpr int PRO_T = 256;         // threads per block
 constexpr int PRO_SPLITS = 1024;   // partial sums per head in the backward reduction
-
-__device__ __forceinline__ float softplus_f(float x) { return x > 20.f ? x : log1pf(expf(x)); }
-__device__ __forceinline__ float sigmoid_f(float x) { return 1.f / (1.f + expf(-x)); }
 
 // 4 consecutive elements of a 128-wide row per lane
 template <typename Op> struct Vec4;

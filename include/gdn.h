@@ -23,7 +23,7 @@
  *
  * Conventions, for every entry point:
  *   - Pointers are DEVICE pointers unless the field says host.  Every device pointer must
- *     be 16-byte aligned.  The caller owns all memory; the library never allocates, frees
+ *     be 16-byte aligned (an argument that may be less aligned says so).  The caller owns all memory; the library never allocates, frees
  *     or synchronises.  Work is enqueued on `stream` (a cudaStream_t; NULL = legacy stream)
  *     and runs asynchronously.
  *   - Arguments are validated before anything is launched; on a non-OK status nothing has
@@ -57,7 +57,9 @@ typedef enum {
     GDN_ERR_BOUNDS = 6         /* checked build: a store index fell outside its tensor (gdn_device_status) */
 } gdn_status;
 
-typedef enum { GDN_BF16 = 0, GDN_FP32 = 1 } gdn_dtype;
+/* GDN_E4M3 (8 bits: 1 sign, 4 exponent, 3 mantissa bits, no infinities) only where an entry
+ * point names it: a cache of gdn_paged_attn_decode, the output of gdn_rmsnorm_fwd. */
+typedef enum { GDN_BF16 = 0, GDN_FP32 = 1, GDN_E4M3 = 2 } gdn_dtype;
 
 /* Intra-GPU context parallelism over chunk ranges (FlashQLA pages, "AutoCP" section: when
  * batch * heads leaves SMs idle, each sequence's chunks are split into segments). */
@@ -218,6 +220,139 @@ gdn_status gdn_prologue_bwd(const gdn_problem* p, const void* q_raw, const void*
                             const float* dg, const float* dbeta, void* dq_raw, void* dk_raw,
                             float* da, float* db, float* dA_log, float* ddt_bias,
                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * Recurrent step: the gated delta rule one token after another, for decoding (one new token
+ * per sequence, or the few drafted ones that a verification pass runs) from the states that a
+ * prefill (gdn_chunk_fwd's ht) or an earlier step left.  Per sequence, v-head and token
+ *     u = beta (v - e^g h^T k),   h <- e^g h + k u^T,   o = scale h^T q
+ * which is the recurrence at the top of this file for h = S^T.  Arithmetic and states are fp32.
+ *
+ * The states live in pools [num_slots, Hv, K, V] fp32: sequence s reads slot slots[s] of
+ * state_in (NULL: zero states) and writes the same slot of state_out (NULL: not returned).
+ * state_out may be state_in (in place); the pools may not overlap otherwise.  Slots that no
+ * sequence names are not touched.  A sequence whose slot lies outside [0, num_slots) (-1 for the
+ * padding rows of a captured batch) reads and writes no state, and its o is 0.  No two
+ * sequences of a call may name the same slot (their states would race).  A sequence without
+ * tokens keeps its state (state_out gets a copy).
+ *
+ * With A_log and dt_bias given (both or neither), q and k are raw projections and g, beta the
+ * pre-activations a, b of gdn_prologue_fwd, whose formulas are applied on the way in.
+ *
+ * cu_seqlens is read on the device alone, so a captured graph serves every split of
+ * total_tokens; offsets outside [0, total_tokens] are clamped to it.  Tokens that no sequence
+ * covers get no output.  K = V = 128.
+ * ------------------------------------------------------------------------------------ */
+typedef struct gdn_step_problem {
+    int32_t num_seqs;
+    int32_t total_tokens;          /* rows of q, k, v, g, beta and o */
+    int32_t Hqk, Hv, K, V;
+    int32_t dtype;                 /* gdn_dtype of q, k, v and o (bf16 or fp32) */
+    float scale;                   /* finite and > 0 */
+    const int32_t* cu_seqlens;     /* device [num_seqs+1], or NULL: total_tokens / num_seqs each */
+    const int32_t* slots;          /* device [num_seqs], or NULL: sequence s has slot s */
+    int64_t num_slots;
+    /* elements from one token's row to the next, 0 for contiguous rows; a row's heads and
+     * features are contiguous.  Those of q, k, v are multiples of 16 bytes. */
+    int64_t q_stride, k_stride, v_stride, g_stride, beta_stride;
+} gdn_step_problem;
+
+gdn_status gdn_recurrent_step(const gdn_step_problem* p, const void* q, const void* k,
+                              const void* v, const float* g, const float* beta, /* g, beta: 4-byte aligned */
+                              const float* A_log, const float* dt_bias, const float* state_in,
+                              float* state_out, void* o, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * Attention of one new token per sequence over a paged key-value cache (the full-attention
+ * layers of a model that interleaves them with gated-delta-rule layers).  Per sequence n and
+ * query head h, with kv-head j = h / (Hq / Hkv) and the tokens t of [first, len),
+ * len = seq_lens[n], first = max(0, len - window) (0 without a window):
+ *     z_t = scale <q_h, k_t>,   o_h = sum_t softmax(z)_t v_t,   lse_h = log sum_t e^{z_t}
+ * Token t of sequence n lies in slot t % page_size of page page_table[n][t / page_size].
+ * lens count the new token: it attends to itself.
+ *
+ * k_new, v_new (both or neither): the new token's key and value, written by the call to
+ * position len - 1 of the caches (divided by k_scale, v_scale and rounded to the cache's type;
+ * in 8 bits clamped to +-448) and attended to as written.  No two sequences of such a call may
+ * share the page of that position.
+ * 8-bit caches hold k / k_scale[j] and v / v_scale[j]; NULL scales are 1.
+ *
+ * A sequence of length 0 gets o = 0 and lse = -inf.  Whatever lies in slots outside
+ * [first, len) is not used, NaN or not.  Page numbers outside [0, num_pages) are not read: the tokens of
+ * such a page count as masked (and a new token there is not written); a length past
+ * max_pages * page_size is cut to it.
+ *
+ * Caches of any page size and strides; features contiguous; D = 64, 128 or 256.  Partial
+ * results over ranges of the cache lie in the workspace and are joined in a fixed order.
+ * ------------------------------------------------------------------------------------ */
+typedef struct gdn_paged_problem {
+    int32_t num_seqs;
+    int32_t Hq, Hkv;               /* query heads, a multiple of the kv-heads */
+    int32_t D;                     /* 64, 128 or 256 */
+    int32_t dtype;                 /* gdn_dtype of q, k_new, v_new and o: bf16 or fp32 */
+    int32_t cache_dtype;           /* bf16 or e4m3 with bf16 queries, fp32 with fp32 queries */
+    float scale;                   /* finite and > 0 */
+    int32_t window;                /* tokens attended to, 0 for all */
+    int32_t page_size;             /* tokens per page */
+    int32_t max_pages;             /* columns of page_table */
+    int64_t num_pages;             /* pages in each cache */
+    int64_t q_stride, new_stride;  /* elements between the rows of q, of k_new and v_new (0: contiguous) */
+    int64_t table_stride;          /* elements between the rows of page_table (0: contiguous) */
+    /* elements between pages, a page's tokens and a token's heads; multiples of 16 bytes */
+    int64_t k_page_stride, k_token_stride, k_head_stride;
+    int64_t v_page_stride, v_token_stride, v_head_stride;
+} gdn_paged_problem;
+
+gdn_status gdn_paged_attn_workspace_size(const gdn_paged_problem* p, size_t* bytes);
+
+gdn_status gdn_paged_attn_decode(const gdn_paged_problem* p, const void* q, void* k_cache, void* v_cache,
+                                 const int32_t* page_table, const int32_t* seq_lens, /* 4-byte aligned */
+                                 const void* k_new, const void* v_new,
+                                 const float* k_scale, const float* v_scale, /* [Hkv], 4-byte aligned */
+                                 void* o, float* lse,  /* [num_seqs, Hq, D]; [num_seqs, Hq] or NULL */
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * Root-mean-square norm with the residual's addition, optionally with an 8-bit output.  Per
+ * row, with w = weight + weight_offset:
+ *     s = x + residual (x itself without a residual),   r = 1 / sqrt(mean(s^2) + eps),
+ *     y = r s w;   sum = s, rounded to dtype (y comes from the unrounded s)
+ * With out_dtype GDN_E4M3, y / scale is rounded to nearest even in 8 bits, with one fp32 scale
+ * per row (group = 0) or per `group` consecutive values of a row (y_scale [rows, dim / group]):
+ *     scale = max(max |y| / 448, 2^-126)
+ * A row with infinities or NaN gets NaN in that row alone.
+ * sum may be x or residual (in place), y may be x; NULL sum: not returned.
+ *
+ * gdn_rmsnorm_bwd: the gradients of <y, dy> + <sum, dsum> (dsum NULL: 0) with respect to s
+ * (x and residual alike) and to weight, for the s given:
+ *     dx = r (w dy - n mean(w dy n)) + dsum with n = r s;   dweight = sum over rows of dy n
+ * dweight is fp32, summed in a fixed order.  Rounding y to 8 bits passes the gradient through.
+ * dx may be dy or dsum (in place).
+ *
+ * Pointers and strides need only the alignment of their elements here; rows whose pointers and
+ * strides are all multiples of 16 bytes run faster.
+ * ------------------------------------------------------------------------------------ */
+typedef struct gdn_norm_problem {
+    int64_t rows;
+    int32_t dim;
+    int32_t dtype;                 /* gdn_dtype of x, residual, sum, dy, dsum, dx: bf16 or fp32 */
+    int32_t weight_dtype;          /* bf16 or fp32 */
+    int32_t out_dtype;             /* of y: dtype, or GDN_E4M3 */
+    int32_t group;                 /* values to a scale; 0: a row; else divides dim */
+    float eps;                     /* finite and >= 0 */
+    float weight_offset;           /* 0, or 1 for weights that are kept as w - 1 */
+    int64_t x_stride, residual_stride;  /* elements between rows (x_stride is s's in the backward), 0: dim */
+    int64_t dy_stride, dsum_stride;
+} gdn_norm_problem;
+
+gdn_status gdn_rmsnorm_fwd(const gdn_norm_problem* p, const void* x, const void* residual,
+                           const void* weight, void* y, float* y_scale, void* sum, void* stream);
+
+gdn_status gdn_rmsnorm_bwd_workspace_size(const gdn_norm_problem* p, size_t* bytes);
+
+gdn_status gdn_rmsnorm_bwd(const gdn_norm_problem* p, const void* s, const void* weight,
+                           const void* dy, const void* dsum, void* dx, float* dweight,
+                           void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------------------
  * Per-kernel timing (instrumentation for benchmarks; not needed for computation).
