@@ -125,6 +125,7 @@ size_t paged_bytes(const gdn_paged_problem& p, int splits) {
 
 gdn_status check_norm(gdn_norm_problem& p, bool backward) {
     if (p.rows < 0) return fail(GDN_ERR_INVALID_ARG, "rows must be >= 0");
+    if (p.rows > 0x7fffffff) return fail(GDN_ERR_UNSUPPORTED, "more than 2^31 - 1 rows");
     if (p.dim <= 0) return fail(GDN_ERR_INVALID_ARG, "dim must be positive (got %d)", p.dim);
     if (p.dtype != GDN_BF16 && p.dtype != GDN_FP32) return fail(GDN_ERR_INVALID_ARG, "dtype must be GDN_BF16 or GDN_FP32");
     if (p.weight_dtype != GDN_BF16 && p.weight_dtype != GDN_FP32) return fail(GDN_ERR_INVALID_ARG, "weight_dtype must be GDN_BF16 or GDN_FP32");

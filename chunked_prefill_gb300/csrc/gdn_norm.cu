@@ -2,6 +2,17 @@
 // backward pass (include/gdn.h, gdn_rmsnorm_fwd and gdn_rmsnorm_bwd).
 //   s = x + residual,  r = rsqrt(mean s^2 + eps),  y = r s w,  w = weight + offset
 //   dx = r (w dy - n mean(w dy n)) + dsum,  dweight = sum_rows dy n,  n = r s
+//
+// Bound: HBM (forward: x, residual in, sum, y out; backward: s, dy, dsum in, dx out).  A row is
+// read once into registers, NV vectors of VEC values a thread, and everything after its reductions
+// comes from there.  A row belongs to LPR lanes of a warp (8, 16 or 32: short rows, several to a
+// warp, no barrier) or, LPR = 0, to a whole CTA.  VEC is 16 bytes' worth of values where pointers,
+// strides and dim allow it and 1 elsewhere; rows past the registers' reach (max_threads x NV x
+// VEC values) take the looping kernels at the end.
+//
+// The backward keeps a CTA on a fixed sequence of rows (row = CTA, CTA + grid, ...) with its share
+// of dweight in registers; the CTAs' shares are then added in CTA order by a second launch, so
+// dweight has the same bits in every run.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -14,139 +25,564 @@
 namespace gdn {
 namespace {
 
-constexpr int NT = 256;               // threads per row
 constexpr float F8_MAX = 448.f;
 constexpr float F8_TINY = 1.17549435e-38f;  // 2^-126
+constexpr int ROWS_T = 256;                 // threads of a CTA of the lane-group kernels
+constexpr int LOOP_T = 512;                 // threads of the looping kernels
+// Threads of a CTA at most, so that a row's values fit the registers that many threads leave each.
+constexpr int max_threads(int vec, int nv, int lpr, bool backward) {
+    return lpr ? ROWS_T : vec == 1 ? (nv == 16 ? 512 : 256) : (backward || (nv == 4 && vec == 8)) ? 512 : 1024;
+}
 
-__device__ __forceinline__ float warp_sum(float v) {
+// The larger of two magnitudes, NaN above all: the order of their bits.
+__device__ __forceinline__ float mag_max(float a, float b) {
+    return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)));
+}
+
+template <bool MAX> __device__ __forceinline__ float join(float a, float b) { return MAX ? mag_max(a, b) : a + b; }
+
+template <bool MAX, int LANES>
+__device__ __forceinline__ float lane_red(float v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = LANES / 2; o > 0; o >>= 1) v = join<MAX>(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
 }
-// max that keeps a NaN
-__device__ __forceinline__ float nan_max(float a, float b) { return (a > b || a != a) ? a : b; }
-__device__ __forceinline__ float warp_max(float v) {
+// Over the threads of a row; a CTA's rows go through `red` (32 floats, not used again before every
+// thread has read it: callers alternate between two).
+template <bool MAX, int LPR>
+__device__ __forceinline__ float row_red(float v, float* red) {
+    if constexpr (LPR > 0) {
+        return lane_red<MAX, LPR>(v);
+    } else {
+        v = lane_red<MAX, 32>(v);
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+        __syncthreads();
+        const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+        return lane_red<MAX, 32>(lane < warps ? red[lane] : 0.f);
+    }
+}
+
+// VEC consecutive values as they lie in memory.
+template <typename T, int VEC> struct Vec {
+    T v[VEC];
+    __device__ __forceinline__ void load(const T* p) {
+        if constexpr (sizeof(T) * VEC == 16)
+            *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(p);
+        else if constexpr (sizeof(T) * VEC == 8)
+            *reinterpret_cast<uint2*>(v) = *reinterpret_cast<const uint2*>(p);
+        else if constexpr (sizeof(T) * VEC == 32) {
+            reinterpret_cast<uint4*>(v)[0] = reinterpret_cast<const uint4*>(p)[0];
+            reinterpret_cast<uint4*>(v)[1] = reinterpret_cast<const uint4*>(p)[1];
+        } else
+            v[0] = p[0];
+    }
+    __device__ __forceinline__ void store(T* p) const {
+        if constexpr (sizeof(T) * VEC == 16)
+            *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(v);
+        else
+            p[0] = v[0];
+    }
+    __device__ __forceinline__ float at(int i) const { return to_f(v[i]); }
+};
+
+template <int VEC>
+__device__ __forceinline__ void load_weight(const gdn_norm_problem& p, const void* w, int i, float (&out)[VEC]) {
+    if (p.weight_dtype == GDN_BF16) {
+        Vec<__nv_bfloat16, VEC> x;
+        x.load(static_cast<const __nv_bfloat16*>(w) + i);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = nan_max(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
+        for (int e = 0; e < VEC; ++e) out[e] = x.at(e) + p.weight_offset;
+    } else {
+        Vec<float, VEC> x;
+        x.load(static_cast<const float*>(w) + i);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) out[e] = x.at(e) + p.weight_offset;
+    }
 }
 
-template <bool MAX>
-__device__ float block_red(float v, float* red) {
-    v = MAX ? warp_max(v) : warp_sum(v);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float t = red[0];
-    for (int w = 1; w < NT / 32; ++w) t = MAX ? nan_max(t, red[w]) : t + red[w];
-    return t;
-}
-
-__device__ __forceinline__ float weight_at(const void* w, int dt, int i) {
-    return dt == GDN_BF16 ? to_f(static_cast<const __nv_bfloat16*>(w)[i]) : static_cast<const float*>(w)[i];
-}
-
-template <typename Op>
-__global__ void __launch_bounds__(NT) k_norm_fwd(const NormArgs A) {
-    const gdn_norm_problem& p = A.p;
-    __shared__ float red[NT / 32];
-    const Op* xr = static_cast<const Op*>(A.x);
-    const Op* rr = static_cast<const Op*>(A.residual);
-    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-        const Op* x = xr + row * p.x_stride;
-        const Op* res = rr ? rr + row * p.residual_stride : nullptr;
-        auto at = [&](int i) { return res ? to_f(x[i]) + to_f(res[i]) : to_f(x[i]); };
-        float ss = 0.f;
-        for (int i = threadIdx.x; i < p.dim; i += NT) {
-            const float v = at(i);
-            ss = fmaf(v, v, ss);
+// y * inv in 8 bits, round to nearest even (|y inv| <= 448 up to rounding; NaN stays NaN).
+template <int VEC>
+__device__ __forceinline__ void store8(uint8_t* p, const float (&y)[VEC], float inv) {
+    if constexpr (VEC == 1) {
+        *p = __nv_cvt_float_to_fp8(y[0] * inv, __NV_SATFINITE, __NV_E4M3);
+    } else {
+        uint32_t w[VEC / 4];
+#pragma unroll
+        for (int e = 0; e < VEC / 4; ++e) {
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * e] * inv, y[4 * e + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * e + 2] * inv, y[4 * e + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+            w[e] = lo | (hi << 16);
         }
-        const float r = rsqrtf(block_red<false>(ss, red) / float(p.dim) + p.eps);
-        auto y_at = [&](int i) { return at(i) * r * (weight_at(A.weight, p.weight_dtype, i) + p.weight_offset); };
-        if (p.out_dtype == GDN_E4M3) {
-            const int group = p.group ? p.group : p.dim;
-            for (int g = 0; g < p.dim / group; ++g) {
-                float m = 0.f;
-                for (int i = threadIdx.x; i < group; i += NT) m = nan_max(m, fabsf(y_at(g * group + i)));
-                m = block_red<true>(m, red);
-                const float sc = nan_max(m / F8_MAX, F8_TINY);
-                if (threadIdx.x == 0) A.y_scale[row * (p.dim / group) + g] = sc;
-                for (int i = threadIdx.x; i < group; i += NT)
-                    static_cast<__nv_fp8_e4m3*>(A.y)[row * p.dim + g * group + i] = __nv_fp8_e4m3(y_at(g * group + i) / sc);
+        if constexpr (VEC == 8)
+            *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+        else
+            *reinterpret_cast<uint32_t*>(p) = w[0];
+    }
+}
+
+__device__ __forceinline__ float scale_of(float mag) { return mag_max(mag / F8_MAX, F8_TINY); }
+
+// OUT8: 0 dtype out; 1 one scale per row; 2 groups of 2^n <= 32 lanes' vectors; 3 other groups
+// (magnitudes by shared-memory maxima, whose order does not matter).
+template <typename T, int VEC, int NV, int LPR, int OUT8>
+__global__ void __launch_bounds__(max_threads(VEC, NV, LPR, false)) k_norm_fwd(const NormArgs A) {
+    const gdn_norm_problem& p = A.p;
+    __shared__ float red[2][32];
+    extern __shared__ uint32_t mags[];  // OUT8 == 3: per group of the CTA's row(s)
+    const int tid = threadIdx.x, step = LPR ? LPR : blockDim.x, at0 = LPR ? tid % step : tid;
+    const int per = LPR ? int(blockDim.x) / step : 1, mine = LPR ? tid / step : 0;  // rows per CTA, and this thread's
+    const int nvec = p.dim / VEC;
+    const int64_t row = int64_t(blockIdx.x) * per + mine;
+    const bool live = row < p.rows;
+    const T* x = static_cast<const T*>(A.x) + row * p.x_stride;
+    const T* res = static_cast<const T*>(A.residual) + row * p.residual_stride;
+
+    Vec<T, VEC> xv[NV], rv[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int j = at0 + k * step;
+        if (live && j < nvec) {
+            xv[k].load(x + int64_t(j) * VEC);
+            if (A.residual) rv[k].load(res + int64_t(j) * VEC);
+        }
+    }
+    float s[NV][VEC], ss = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const bool in = live && at0 + k * step < nvec;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            s[k][e] = in ? (A.residual ? xv[k].at(e) + rv[k].at(e) : xv[k].at(e)) : 0.f;
+            ss = fmaf(s[k][e], s[k][e], ss);
+        }
+    }
+    if (A.sum) {
+        T* sum = static_cast<T*>(A.sum) + row * p.dim;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int j = at0 + k * step;
+            if (live && j < nvec) {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) xv[k].v[e] = from_f<T>(s[k][e]);
+                xv[k].store(sum + int64_t(j) * VEC);
+            }
+        }
+    }
+    const float r = rsqrtf(row_red<false, LPR>(ss, red[0]) / float(p.dim) + p.eps);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int j = at0 + k * step;
+        if (j < nvec) {
+            float w[VEC];
+            load_weight<VEC>(p, A.weight, j * VEC, w);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) s[k][e] = s[k][e] * r * w[e];
+        }
+    }
+    if constexpr (OUT8 == 0) {
+        T* y = static_cast<T*>(A.y) + row * p.dim;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int j = at0 + k * step;
+            if (live && j < nvec) {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) xv[k].v[e] = from_f<T>(s[k][e]);
+                xv[k].store(y + int64_t(j) * VEC);
+            }
+        }
+    } else {
+        uint8_t* y = static_cast<uint8_t*>(A.y) + row * p.dim;
+        float mag[NV];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            mag[k] = 0.f;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) mag[k] = mag_max(mag[k], fabsf(s[k][e]));
+        }
+        const int groups = p.group ? p.dim / p.group : 1;
+        float* scales = A.y_scale + row * groups;
+        if constexpr (OUT8 == 1) {
+#pragma unroll
+            for (int k = 1; k < NV; ++k) mag[0] = mag_max(mag[0], mag[k]);
+            const float sc = scale_of(row_red<true, LPR>(mag[0], red[1]));
+            if (live && at0 == 0) scales[0] = sc;
+            const float inv = 1.f / sc;
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+                if (live && at0 + k * step < nvec) store8<VEC>(y + int64_t(at0 + k * step) * VEC, s[k], inv);
+        } else if constexpr (OUT8 == 2) {
+            const int lanes = p.group / VEC;  // 2^n lanes hold a group, at a multiple of 2^n
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                for (int o = lanes / 2; o > 0; o >>= 1) mag[k] = mag_max(mag[k], __shfl_xor_sync(0xffffffffu, mag[k], o));
+                const int j = at0 + k * step;
+                if (live && j < nvec) {
+                    const float sc = scale_of(mag[k]);
+                    if ((j & (lanes - 1)) == 0) scales[j / lanes] = sc;
+                    store8<VEC>(y + int64_t(j) * VEC, s[k], 1.f / sc);
+                }
+            }
+        } else {
+            uint32_t* m = mags + mine * groups;
+            for (int g = at0; g < groups; g += step) m[g] = 0u;
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int j = at0 + k * step;
+                if (j < nvec) {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) atomicMax(m + (j * VEC + e) / p.group, __float_as_uint(fabsf(s[k][e])));
+                }
             }
             __syncthreads();
-        }
-        for (int i = threadIdx.x; i < p.dim; i += NT) {
-            const float v = at(i), y = y_at(i);
-            if (A.sum) static_cast<Op*>(A.sum)[row * p.dim + i] = from_f<Op>(v);
-            if (p.out_dtype != GDN_E4M3) static_cast<Op*>(A.y)[row * p.dim + i] = from_f<Op>(y);
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int j = at0 + k * step;
+                if (live && j < nvec) {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        const int i = j * VEC + e, g = i / p.group;
+                        const float sc = scale_of(__uint_as_float(m[g])), one[1] = {s[k][e]};
+                        if (i % p.group == 0) scales[g] = sc;
+                        store8<1>(y + i, one, 1.f / sc);
+                    }
+                }
+            }
         }
     }
 }
 
-template <typename Op>
-__global__ void __launch_bounds__(NT) k_norm_bwd(const NormArgs A) {
+template <typename T, int VEC, int NV, int LPR>
+__global__ void __launch_bounds__(max_threads(VEC, NV, LPR, true)) k_norm_bwd(const NormArgs A) {
     const gdn_norm_problem& p = A.p;
-    __shared__ float red[NT / 32];
-    float* part = A.part + int64_t(blockIdx.x) * p.dim;
-    for (int i = threadIdx.x; i < p.dim; i += NT) part[i] = 0.f;
-    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-        const Op* x = static_cast<const Op*>(A.x) + row * p.x_stride;
-        const Op* dy = static_cast<const Op*>(A.dy) + row * p.dy_stride;
-        const Op* ds = A.dsum ? static_cast<const Op*>(A.dsum) + row * p.dsum_stride : nullptr;
-        float ss = 0.f, c = 0.f;
-        for (int i = threadIdx.x; i < p.dim; i += NT) {
-            const float v = to_f(x[i]), w = weight_at(A.weight, p.weight_dtype, i) + p.weight_offset;
-            ss = fmaf(v, v, ss);
-            c = fmaf(w * to_f(dy[i]), v, c);
+    __shared__ float red[2][2][32];
+    const int tid = threadIdx.x, step = LPR ? LPR : blockDim.x, at0 = LPR ? tid % step : tid;
+    const int per = LPR ? int(blockDim.x) / step : 1, mine = LPR ? tid / step : 0;
+    const int nvec = p.dim / VEC;
+    constexpr bool KEEP = NV * VEC < 32;  // the weights stay in registers (else: read again, from L1)
+    float w[KEEP ? NV : 1][VEC], dw[NV][VEC];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) dw[k][e] = 0.f;
+        if (KEEP && at0 + k * step < nvec) load_weight<VEC>(p, A.weight, (at0 + k * step) * VEC, w[KEEP ? k : 0]);
+    }
+    const float inv_dim = 1.f / float(p.dim);
+    int turn = 0;
+    // every lane of a warp takes part in the shuffles of every turn
+    for (int64_t row0 = int64_t(blockIdx.x) * per; row0 < p.rows; row0 += int64_t(gridDim.x) * per, turn ^= 1) {
+        const int64_t row = row0 + mine;
+        const bool live = row < p.rows;
+        const T* x = static_cast<const T*>(A.x) + row * p.x_stride;
+        const T* dy = static_cast<const T*>(A.dy) + row * p.dy_stride;
+        const T* ds = static_cast<const T*>(A.dsum) + row * p.dsum_stride;
+        Vec<T, VEC> xv[NV], dv[NV], sv[NV];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int j = at0 + k * step;
+            if (live && j < nvec) {
+                xv[k].load(x + int64_t(j) * VEC);
+                dv[k].load(dy + int64_t(j) * VEC);
+                if (A.dsum) sv[k].load(ds + int64_t(j) * VEC);
+            }
         }
-        const float r = rsqrtf(block_red<false>(ss, red) / float(p.dim) + p.eps);
-        c = block_red<false>(c, red) * r / float(p.dim);
-        for (int i = threadIdx.x; i < p.dim; i += NT) {
-            const float n = to_f(x[i]) * r, d = to_f(dy[i]);
-            const float w = weight_at(A.weight, p.weight_dtype, i) + p.weight_offset;
-            const float add = ds ? to_f(ds[i]) : 0.f;
-            part[i] = fmaf(d, n, part[i]);
-            static_cast<Op*>(A.dx)[row * p.dim + i] = from_f<Op>(fmaf(r, w * d - n * c, add));
+        float ss = 0.f, c = 0.f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            if (!(live && at0 + k * step < nvec)) continue;
+            if (!KEEP) load_weight<VEC>(p, A.weight, (at0 + k * step) * VEC, w[0]);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                ss = fmaf(xv[k].at(e), xv[k].at(e), ss);
+                c = fmaf(w[KEEP ? k : 0][e] * dv[k].at(e), xv[k].at(e), c);
+            }
+        }
+        if constexpr (LPR > 0) {
+            ss = lane_red<false, LPR>(ss);
+            c = lane_red<false, LPR>(c);
+        } else {  // both sums behind one barrier
+            ss = lane_red<false, 32>(ss);
+            c = lane_red<false, 32>(c);
+            const int lane = tid & 31, warps = blockDim.x >> 5;
+            if (lane == 0) {
+                red[turn][0][tid >> 5] = ss;
+                red[turn][1][tid >> 5] = c;
+            }
+            __syncthreads();
+            ss = lane_red<false, 32>(lane < warps ? red[turn][0][lane] : 0.f);
+            c = lane_red<false, 32>(lane < warps ? red[turn][1][lane] : 0.f);
+        }
+        const float r = rsqrtf(ss * inv_dim + p.eps);
+        c *= r * inv_dim;
+        T* dx = static_cast<T*>(A.dx) + row * p.dim;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int j = at0 + k * step;
+            if (live && j < nvec) {
+                if (!KEEP) load_weight<VEC>(p, A.weight, j * VEC, w[0]);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const float n = xv[k].at(e) * r, d = dv[k].at(e);
+                    dw[k][e] = fmaf(d, n, dw[k][e]);
+                    xv[k].v[e] = from_f<T>(fmaf(r, w[KEEP ? k : 0][e] * d - n * c, A.dsum ? sv[k].at(e) : 0.f));
+                }
+                xv[k].store(dx + int64_t(j) * VEC);
+            }
+        }
+    }
+    float* part = A.part + int64_t(blockIdx.x) * p.dim;
+    if constexpr (LPR > 0) {  // the CTA's rows' shares, in row order
+        extern __shared__ float share[];  // [per][dim]
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int j = at0 + k * step;
+            if (j < nvec)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) share[mine * p.dim + j * VEC + e] = dw[k][e];
+        }
+        __syncthreads();
+        for (int i = tid; i < p.dim; i += blockDim.x) {
+            float t = 0.f;
+            for (int g = 0; g < per; ++g) t += share[g * p.dim + i];
+            part[i] = t;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int j = at0 + k * step;
+            if (j < nvec)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) part[j * VEC + e] = dw[k][e];
         }
     }
 }
 
-__global__ void __launch_bounds__(NT) k_norm_dw(const float* part, int parts, int dim, float* dw) {
-    const int i = blockIdx.x * NT + threadIdx.x;
-    if (i >= dim) return;
+// dweight from the CTAs' shares: 32 columns by 32 runs of consecutive shares, the runs then added in order.
+__global__ void __launch_bounds__(1024) k_norm_dw(const float* part, int parts, int dim, float* dw) {
+    __shared__ float run[32][33];
+    const int c = threadIdx.x & 31, y = threadIdx.x >> 5, i = blockIdx.x * 32 + c;
+    const int per = (parts + 31) / 32, b1 = min(parts, (y + 1) * per);
     float t = 0.f;
-    for (int b = 0; b < parts; ++b) t += part[int64_t(b) * dim + i];
-    dw[i] = t;
+    if (i < dim)
+        for (int b = y * per; b < b1; ++b) t += part[int64_t(b) * dim + i];
+    run[y][c] = t;
+    __syncthreads();
+    if (y == 0 && i < dim) {
+        for (int k = 1; k < 32; ++k) t += run[k][c];
+        dw[i] = t;
+    }
+}
+
+// ---- rows too long for the registers: value by value, a row read again (from L2) per phase
+__device__ __forceinline__ float weight_at(const NormArgs& A, int i) {
+    float w[1];
+    load_weight<1>(A.p, A.weight, i, w);
+    return w[0];
+}
+
+template <typename T>
+__global__ void __launch_bounds__(LOOP_T) k_norm_fwd_loop(const NormArgs A) {
+    const gdn_norm_problem& p = A.p;
+    __shared__ float red[2][32];
+    const int64_t row = blockIdx.x;
+    const T* x = static_cast<const T*>(A.x) + row * p.x_stride;
+    const T* res = A.residual ? static_cast<const T*>(A.residual) + row * p.residual_stride : nullptr;
+    auto at = [&](int i) { return res ? to_f(x[i]) + to_f(res[i]) : to_f(x[i]); };
+    float ss = 0.f;
+    for (int i = threadIdx.x; i < p.dim; i += LOOP_T) ss = fmaf(at(i), at(i), ss);
+    const float r = rsqrtf(row_red<false, 0>(ss, red[0]) / float(p.dim) + p.eps);
+    auto y_at = [&](int i) { return at(i) * r * weight_at(A, i); };
+    if (p.out_dtype == GDN_E4M3) {
+        const int group = p.group ? p.group : p.dim, groups = p.dim / group;
+        for (int g = 0; g < groups; ++g) {
+            float m = 0.f;
+            for (int i = threadIdx.x; i < group; i += LOOP_T) m = mag_max(m, fabsf(y_at(g * group + i)));
+            __syncthreads();  // the last group's maxima have been read
+            const float sc = scale_of(row_red<true, 0>(m, red[1]));
+            if (threadIdx.x == 0) A.y_scale[row * groups + g] = sc;
+            for (int i = threadIdx.x; i < group; i += LOOP_T) {
+                const float one[1] = {y_at(g * group + i)};
+                store8<1>(static_cast<uint8_t*>(A.y) + row * p.dim + g * group + i, one, 1.f / sc);
+            }
+        }
+        __syncthreads();  // sum may be x or residual, which other threads have read above
+    }
+    for (int i = threadIdx.x; i < p.dim; i += LOOP_T) {
+        const float v = at(i), y = y_at(i);
+        if (A.sum) static_cast<T*>(A.sum)[row * p.dim + i] = from_f<T>(v);
+        if (p.out_dtype != GDN_E4M3) static_cast<T*>(A.y)[row * p.dim + i] = from_f<T>(y);
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(LOOP_T) k_norm_bwd_loop(const NormArgs A) {
+    const gdn_norm_problem& p = A.p;
+    __shared__ float red[2][32];
+    float* part = A.part + int64_t(blockIdx.x) * p.dim;
+    for (int i = threadIdx.x; i < p.dim; i += LOOP_T) part[i] = 0.f;
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        const T* x = static_cast<const T*>(A.x) + row * p.x_stride;
+        const T* dy = static_cast<const T*>(A.dy) + row * p.dy_stride;
+        const T* ds = A.dsum ? static_cast<const T*>(A.dsum) + row * p.dsum_stride : nullptr;
+        float ss = 0.f, c = 0.f;
+        for (int i = threadIdx.x; i < p.dim; i += LOOP_T) {
+            const float v = to_f(x[i]);
+            ss = fmaf(v, v, ss);
+            c = fmaf(weight_at(A, i) * to_f(dy[i]), v, c);
+        }
+        const float r = rsqrtf(row_red<false, 0>(ss, red[0]) / float(p.dim) + p.eps);
+        c = row_red<false, 0>(c, red[1]) * r / float(p.dim);
+        for (int i = threadIdx.x; i < p.dim; i += LOOP_T) {
+            const float n = to_f(x[i]) * r, d = to_f(dy[i]), add = ds ? to_f(ds[i]) : 0.f;
+            part[i] = fmaf(d, n, part[i]);
+            static_cast<T*>(A.dx)[row * p.dim + i] = from_f<T>(fmaf(r, weight_at(A, i) * d - n * c, add));
+        }
+        __syncthreads();
+    }
+}
+
+// How a problem's rows are laid over threads.
+struct Layout {
+    int vec, nv, lpr, threads;  // lpr 0: a CTA per row; vec 0: the looping kernels
+    int per() const { return lpr ? threads / lpr : 1; }
+};
+bool wide(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+Layout layout_of(int dim, int full, bool vectors, bool backward) {
+    Layout L{vectors ? full : 1, 1, 0, ROWS_T};
+    const int n = dim / L.vec;
+    if (n <= 32) {
+        L.lpr = n <= 8 ? 8 : n <= 16 ? 16 : 32;
+        return L;
+    }
+    if (n <= 128) {
+        L.lpr = 32;
+        L.nv = n <= 64 ? 2 : 4;
+        return L;
+    }
+    // a CTA per row: two vectors a thread while 1024 threads hold the row so, else more
+    const int most = L.vec == 1 ? 16 : 4;
+    for (L.nv = 2; L.nv <= most; L.nv *= 2) {
+        L.threads = ((n + L.nv - 1) / L.nv + 31) / 32 * 32;
+        if (L.threads <= max_threads(L.vec, L.nv, 0, backward)) return L;
+    }
+    L.vec = 0;
+    L.threads = LOOP_T;
+    return L;
+}
+
+int full_vec(int dtype) { return dtype == GDN_BF16 ? 8 : 4; }
+
+template <int OUT8, typename T, int VEC, int NV, int LPR>
+cudaError_t fwd_launch(const NormArgs& A, const Layout& L, cudaStream_t st) {
+    const int64_t blocks = (A.p.rows + L.per() - 1) / L.per();
+    const size_t smem = OUT8 == 3 ? size_t(L.per()) * (A.p.dim / A.p.group) * 4 : 0;
+    if (smem > 40 * 1024) {
+        const cudaError_t e = smem_attr(k_norm_fwd<T, VEC, NV, LPR, OUT8>, int(smem));
+        if (e != cudaSuccess) return e;
+    }
+    k_norm_fwd<T, VEC, NV, LPR, OUT8><<<unsigned(blocks), L.threads, smem, st>>>(A);
+    return cudaGetLastError();
+}
+template <typename T, int VEC, int NV, int LPR>
+cudaError_t fwd_out(const NormArgs& A, const Layout& L, cudaStream_t st) {
+    if (A.p.out_dtype != GDN_E4M3) return fwd_launch<0, T, VEC, NV, LPR>(A, L, st);
+    if (A.p.group == 0 || A.p.group == A.p.dim) return fwd_launch<1, T, VEC, NV, LPR>(A, L, st);
+    const int lanes = A.p.group % VEC ? 0 : A.p.group / VEC;
+    const int whole = LPR ? LPR : 32;
+    if (lanes > 0 && lanes <= whole && (lanes & (lanes - 1)) == 0) return fwd_launch<2, T, VEC, NV, LPR>(A, L, st);
+    return fwd_launch<3, T, VEC, NV, LPR>(A, L, st);
+}
+
+template <typename T, int VEC, int NV, int LPR>
+cudaError_t bwd_out(const NormArgs& A, const Layout& L, int parts, cudaStream_t st) {
+    const size_t smem = LPR ? size_t(L.per()) * A.p.dim * 4 : 0;
+    k_norm_bwd<T, VEC, NV, LPR><<<parts, L.threads, smem, st>>>(A);
+    return cudaGetLastError();
+}
+
+// Calls f<VEC, NV, LPR> for the layout.
+#define NORM_LAYOUTS(F, T, FULL, ...)                                              \
+    do {                                                                            \
+        if (L.vec == FULL) {                                                        \
+            if (L.lpr == 8) return F<T, FULL, 1, 8>(__VA_ARGS__);                   \
+            if (L.lpr == 16) return F<T, FULL, 1, 16>(__VA_ARGS__);                 \
+            if (L.lpr == 32 && L.nv == 1) return F<T, FULL, 1, 32>(__VA_ARGS__);    \
+            if (L.lpr == 32 && L.nv == 2) return F<T, FULL, 2, 32>(__VA_ARGS__);    \
+            if (L.lpr == 32) return F<T, FULL, 4, 32>(__VA_ARGS__);                 \
+            if (L.nv == 2) return F<T, FULL, 2, 0>(__VA_ARGS__);                    \
+            return F<T, FULL, 4, 0>(__VA_ARGS__);                                   \
+        }                                                                           \
+        if (L.lpr == 8) return F<T, 1, 1, 8>(__VA_ARGS__);                          \
+        if (L.lpr == 16) return F<T, 1, 1, 16>(__VA_ARGS__);                        \
+        if (L.lpr == 32 && L.nv == 1) return F<T, 1, 1, 32>(__VA_ARGS__);           \
+        if (L.lpr == 32 && L.nv == 2) return F<T, 1, 2, 32>(__VA_ARGS__);           \
+        if (L.lpr == 32) return F<T, 1, 4, 32>(__VA_ARGS__);                        \
+        if (L.nv == 2) return F<T, 1, 2, 0>(__VA_ARGS__);                           \
+        if (L.nv == 4) return F<T, 1, 4, 0>(__VA_ARGS__);                           \
+        if (L.nv == 8) return F<T, 1, 8, 0>(__VA_ARGS__);                           \
+        return F<T, 1, 16, 0>(__VA_ARGS__);                                         \
+    } while (0)
+
+template <typename T>
+cudaError_t fwd_type(const NormArgs& A, cudaStream_t st) {
+    const gdn_norm_problem& p = A.p;
+    const int full = full_vec(p.dtype);
+    const bool vectors = p.dim % full == 0 && p.x_stride % full == 0 && p.residual_stride % full == 0 && wide(A.x) && wide(A.residual) &&
+                         wide(A.weight) && wide(A.y) && wide(A.sum);
+    const Layout L = layout_of(p.dim, full, vectors, false);
+    if (L.vec == 0) {
+        k_norm_fwd_loop<T><<<unsigned(p.rows), LOOP_T, 0, st>>>(A);
+        return cudaGetLastError();
+    }
+    NORM_LAYOUTS(fwd_out, T, (sizeof(T) == 2 ? 8 : 4), A, L, st);
+}
+
+int parts_of(const gdn_norm_problem& p, const Layout& L) {
+    const int64_t groups = (p.rows + L.per() - 1) / L.per();
+    int64_t most = int64_t(sm_count_cached()) * (1024 / L.threads > 0 ? 1024 / L.threads : 1);
+    if (groups < most) most = groups;
+    return int(most > 0 ? most : 1);
+}
+
+template <typename T>
+cudaError_t bwd_type(const NormArgs& A, const Layout& L, int parts, cudaStream_t st) {
+    if (L.vec == 0) {
+        k_norm_bwd_loop<T><<<parts, LOOP_T, 0, st>>>(A);
+        return cudaGetLastError();
+    }
+    NORM_LAYOUTS(bwd_out, T, (sizeof(T) == 2 ? 8 : 4), A, L, parts, st);
 }
 
 }  // namespace
 
+// CTAs of the backward at most, whatever the pointers' alignment turns out to be.
 int norm_bwd_parts(const gdn_norm_problem& p) {
-    const int64_t most = 8 * int64_t(sm_count_cached());
-    return int(p.rows < most ? (p.rows > 0 ? p.rows : 1) : most);
+    const int a = parts_of(p, layout_of(p.dim, full_vec(p.dtype), false, true));
+    if (p.dim % full_vec(p.dtype)) return a;
+    const int b = parts_of(p, layout_of(p.dim, full_vec(p.dtype), true, true));
+    return a > b ? a : b;
 }
 
 cudaError_t launch_norm_fwd(const NormArgs& A, cudaStream_t st) {
-    const int64_t most = 1 << 20;
-    const unsigned nb = unsigned(A.p.rows < most ? A.p.rows : most);
     timing_begin("rmsnorm_fwd", st);
-    if (A.p.dtype == GDN_BF16)
-        k_norm_fwd<__nv_bfloat16><<<nb, NT, 0, st>>>(A);
-    else
-        k_norm_fwd<float><<<nb, NT, 0, st>>>(A);
+    const cudaError_t e = A.p.dtype == GDN_BF16 ? fwd_type<__nv_bfloat16>(A, st) : fwd_type<float>(A, st);
     timing_end(st);
-    return cudaGetLastError();
+    return e;
 }
 
 cudaError_t launch_norm_bwd(const NormArgs& A, cudaStream_t st) {
-    const int parts = norm_bwd_parts(A.p);
+    const gdn_norm_problem& p = A.p;
+    const int full = full_vec(p.dtype);
+    const bool vectors = p.dim % full == 0 && p.x_stride % full == 0 && p.dy_stride % full == 0 && p.dsum_stride % full == 0 && wide(A.x) &&
+                         wide(A.dy) && wide(A.dsum) && wide(A.weight) && wide(A.dx);
+    const Layout L = layout_of(p.dim, full, vectors, true);
+    const int parts = parts_of(p, L);
     timing_begin("rmsnorm_bwd", st);
-    if (A.p.dtype == GDN_BF16)
-        k_norm_bwd<__nv_bfloat16><<<parts, NT, 0, st>>>(A);
-    else
-        k_norm_bwd<float><<<parts, NT, 0, st>>>(A);
-    k_norm_dw<<<(A.p.dim + NT - 1) / NT, NT, 0, st>>>(A.part, parts, A.p.dim, A.dweight);
+    const cudaError_t e = p.dtype == GDN_BF16 ? bwd_type<__nv_bfloat16>(A, L, parts, st) : bwd_type<float>(A, L, parts, st);
+    timing_end(st);
+    if (e != cudaSuccess) return e;
+    timing_begin("rmsnorm_dweight", st);
+    k_norm_dw<<<(p.dim + 31) / 32, 1024, 0, st>>>(A.part, parts, p.dim, A.dweight);
     timing_end(st);
     return cudaGetLastError();
 }
