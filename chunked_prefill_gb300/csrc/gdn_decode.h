@@ -20,6 +20,23 @@ struct StepArgs {
 };
 cudaError_t launch_step(const StepArgs& A, cudaStream_t st);
 
+// Division of 0 <= x < 2^31 by a constant 1 <= d < 2^31: x / d = (x * mul) >> (32 + shift), with
+// 2^shift the power of two that d lies above (2^shift < d <= 2^(shift+1)) and mul = ceil(2^(32+shift) / d)
+// < 2^32: the error x (mul d - 2^(32+shift)) / (d 2^(32+shift)) < x / 2^(32+shift) < 1 / d for x < 2^31.
+struct FastDiv {
+    uint32_t mul, shift;
+    void set(uint32_t d) {
+        shift = 0;
+        while ((2ull << shift) < d) ++shift;
+        mul = d == 1 ? 0u : uint32_t(((1ull << (32 + shift)) + d - 1) / d);
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ int of(int x) const {
+        return mul ? int(__umulhi(uint32_t(x), mul) >> shift) : x;
+    }
+#endif
+};
+
 struct PagedArgs {
     gdn_paged_problem p;  // strides filled in
     const void* q;
@@ -29,12 +46,20 @@ struct PagedArgs {
     const float *k_scale, *v_scale;
     void* o;
     float* lse;
-    float* part;     // partial outputs [rows][split][D], then their (max, sum) pairs
-    int splits;      // ranges of the cache per sequence at most
-    int split_len;   // tokens per range
+    int groups;       // of blocks of query heads (a block shares a kv-head)
+    int heads;        // blocks in a group
+    int64_t* before;  // [num_seqs + 1] tiles before each sequence, per block of heads
+    float* part;      // partial results: two places per CTA, of a block's rows by D ...
+    float2* part_ml;  // ... and their (max, sum) pairs
+    FastDiv page_div;
 };
-// Ranges that the cache is split into (a function of the problem and the device alone).
-void paged_plan(const gdn_paged_problem& p, int* splits, int* split_len);
+// The launch for a problem (a function of the problem and the device alone): CTAs (a multiple of the
+// groups of heads), rows to a block of query heads, and the bytes of the workspace (before, part_ml, part, in this order).
+struct PagedPlan {
+    int ctas, rows, groups, heads;
+    size_t off_ml, off_part, bytes;
+};
+PagedPlan paged_plan(const gdn_paged_problem& p);
 cudaError_t launch_paged(const PagedArgs& A, cudaStream_t st);
 
 struct NormArgs {

@@ -119,10 +119,6 @@ gdn_status check_paged(gdn_paged_problem& p) {
     return GDN_OK;
 }
 
-size_t paged_bytes(const gdn_paged_problem& p, int splits) {
-    return splits > 1 ? size_t(p.num_seqs) * p.Hq * splits * (p.D + 2) * sizeof(float) : 0;
-}
-
 gdn_status check_norm(gdn_norm_problem& p, bool backward) {
     if (p.rows < 0) return fail(GDN_ERR_INVALID_ARG, "rows must be >= 0");
     if (p.rows > 0x7fffffff) return fail(GDN_ERR_UNSUPPORTED, "more than 2^31 - 1 rows");
@@ -173,9 +169,7 @@ gdn_status gdn_paged_attn_workspace_size(const gdn_paged_problem* problem, size_
     if (!bytes) return fail(GDN_ERR_INVALID_ARG, "bytes is NULL");
     gdn_paged_problem p = *problem;
     TRY(check_paged(p));
-    int splits = 1, split_len = 1;
-    gdn::paged_plan(p, &splits, &split_len);
-    *bytes = paged_bytes(p, splits);
+    *bytes = p.num_seqs > 0 ? gdn::paged_plan(p).bytes : 0;
     return done(cudaSuccess);
 }
 
@@ -203,11 +197,11 @@ gdn_status gdn_paged_attn_decode(const gdn_paged_problem* problem, const void* q
     TRY(check_ptr("v_scale", v_scale, 4, true));
     TRY(check_ptr("lse", lse, 4, true));
     if ((k_new == nullptr) != (v_new == nullptr)) return fail(GDN_ERR_INVALID_ARG, "k_new and v_new go together");
-    gdn::paged_plan(p, &A.splits, &A.split_len);
-    const size_t need = paged_bytes(p, A.splits);
-    if (need && (!workspace || workspace_bytes < need))
-        return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? workspace_bytes : size_t(0));
-    if (need) TRY(check_ptr("workspace", workspace, 16));
+    const gdn::PagedPlan plan = gdn::paged_plan(p);
+    if (!workspace || workspace_bytes < plan.bytes)
+        return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", plan.bytes, workspace ? workspace_bytes : size_t(0));
+    TRY(check_ptr("workspace", workspace, 16));
+    A.page_div.set(uint32_t(p.page_size));
     A.q = q;
     A.k_cache = k_cache;
     A.v_cache = v_cache;
@@ -219,7 +213,12 @@ gdn_status gdn_paged_attn_decode(const gdn_paged_problem* problem, const void* q
     A.v_scale = v_scale;
     A.o = o;
     A.lse = lse;
-    A.part = static_cast<float*>(workspace);
+    char* ws = static_cast<char*>(workspace);
+    A.groups = plan.groups;
+    A.heads = plan.heads;
+    A.before = reinterpret_cast<int64_t*>(ws);
+    A.part_ml = reinterpret_cast<float2*>(ws + plan.off_ml);
+    A.part = reinterpret_cast<float*>(ws + plan.off_part);
     return done(gdn::launch_paged(A, static_cast<cudaStream_t>(stream)));
 }
 

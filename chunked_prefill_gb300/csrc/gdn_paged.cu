@@ -1,25 +1,27 @@
 // Attention of one new token per sequence over a paged key-value cache (include/gdn.h,
 // gdn_paged_attn_decode): o_h = sum_t softmax(scale <q_h, k_t>)_t v_t, lse_h = log sum_t e^{z_t}.
 //
-// A sequence's tokens are cut into ranges of split_len tokens; a CTA takes one range of one
-// kv-head (and a block of its query heads), keeping a running maximum m, sum l of e^{z - m} and
-// accumulator of e^{z - m} v: one pass over keys and values.  Ranges are joined by a second
-// kernel from (accumulator, m, l) triples in range order; a sequence of one range is written out
-// directly.  Bound: HBM, 2 D bytes-per-value per token and kv-head.
+// The blocks of up to 16 query heads that share a kv-head are dealt to `groups` groups (block b to group
+// b % groups).  A group's work is a list of tiles of tokens: sequence by sequence, its blocks of heads one
+// after another, tile by tile.  The grid fills the GPU once, with the same number of CTAs to each group,
+// each taking an equal, contiguous part of its group's list, so that uneven lengths neither leave a tail nor ask the host for the lengths; on each
+// (sequence, kv-head) in its part it keeps a running maximum m, sum l of e^{z - m} and accumulator of
+// e^{z - m} v: one pass over keys and values.  A pair that lies in one CTA's part is written out by
+// it; of others every CTA leaves (accumulator, m, l) -- at most two per CTA, its first pair's and its
+// last one's -- and a second kernel joins them in the list's order.  Bound: HBM, 2 D
+// bytes-per-value per token and kv-head.
 //
-// bf16 and 8-bit caches: k_paged_mma.  A warp takes tiles of 16 tokens.  Both products run on
-// m16n8k16 tensor-core fragments (up to 16 query heads are the 16 rows), whose operands a thread
-// can load straight from the cache in 16-byte pieces, because the order of a contraction index and
-// of output columns is free as long as both sides agree:
-//   S = Q K^T   thread (g = lane / 4, t = lane % 4) has token g of each 8 and the pieces t + 4 i of
-//               its row: 4 consecutive features stand for the fragment's k = 2t, 2t+1, 2t+8, 2t+9;
-//   O = P V     P is S's accumulator as it lies; the thread has tokens 2t, 2t+1, 2t+8, 2t+9 and the
-//               pieces g + 8 m of their rows: feature e of a piece is column g of n-tile e.
-// So no value is exchanged between threads: a thread copies its own pieces to its own slots in
-// shared memory (cp.async, STAGES tiles deep) and reads them back, without a barrier in the loop,
-// whatever the page size.  With 16 query rows a tcgen05 tile would be mostly padding, and its
-// operands would need the shared-memory layout that this avoids.
-// 8-bit values are converted to fp16 (exactly), with the query rows scaled by a power of two to
+// bf16 and 8-bit caches: k_paged_mma.  A warp takes tiles of 16 (or 32) tokens through shared memory of
+// its own, STAGES tiles deep (cp.async, whole rows by consecutive lanes), so that the loop has no barrier
+// of the CTA, whatever the page size.  Both products run on m16n8k16 tensor-core fragments, the block's
+// query heads being the 16 rows: S = Q K^T, and O = P V with P as S's accumulator lies.  Rows are kept
+// with their 16-byte pieces exchanged (piece ^ row % 8), which makes the copies and the fragments' reads
+// (ldmatrix; transposed for V) free of bank conflicts.  With 16 query rows a tcgen05 tile would be mostly
+// padding, and the time goes into loading: the first layout here, in which a thread copied the very pieces
+// its fragments need (a warp's lanes spread over 4 to 8 rows), ended at 68 % of the copy bandwidth with the
+// arithmetic taken out.
+// 8-bit values are converted to fp16 (exactly; ldmatrix hands out pairs of bytes, so a value row's bytes
+// are read as 16-byte pieces of 4 tokens and paired by byte permutes), with the query rows scaled by a power of two to
 // [-2, 2] for the fp16 range; the weights are rounded to bf16 (fp16 for 8-bit caches) for the second
 // product, 2^-9 (2^-12) of each on average, while their sum l adds them unrounded in fp32.
 //
@@ -41,9 +43,14 @@ namespace {
 constexpr float F8_MAX = 448.f;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
-// What a CTA has to do for sequence n.
+// Sequence n's tokens: those attended to are [first, len); its tiles of `tok` tokens start at base,
+// which is first down to a multiple of 16 (a tile's rows then share a page of 16 k tokens).
 struct Range {
-    int len, first, base, count;  // tokens, the first one attended to, it down to a tile's start, ranges
+    int len, first, base;
+    __device__ __forceinline__ int tiles(int tok) const {  // one at least: an empty row is written too
+        const int64_t n = (int64_t(len) - base + tok - 1) / tok;
+        return n > 1 ? int(n) : 1;
+    }
 };
 __device__ __forceinline__ Range range_of(const PagedArgs& A, int n) {
     const int64_t cap = int64_t(A.p.max_pages) * A.p.page_size;
@@ -52,10 +59,73 @@ __device__ __forceinline__ Range range_of(const PagedArgs& A, int n) {
     R.len = int(len < 0 ? 0 : len < cap ? len : cap);
     R.first = A.p.window > 0 && R.len > A.p.window ? R.len - A.p.window : 0;
     R.base = R.first & ~15;
-    R.count = int((int64_t(R.len) - R.base + A.split_len - 1) / A.split_len);
-    if (R.count < 1) R.count = 1;
     return R;
 }
+
+// A CTA's part [lo, hi) of the list of all tiles, and where it begins: tile `at` of block of heads
+// `head` (of the group's A.heads) of sequence n.
+struct Part {
+    int64_t lo, hi;
+    int n, head, at;
+};
+__device__ __forceinline__ int64_t share_of(int64_t total, int parts, int warps) {
+    const int64_t s = (total + parts - 1) / parts;  // a multiple of the warps, so that none is left out
+    return (s + warps - 1) / warps * warps;
+}
+// CTA 0 also leaves the number of tiles before each sequence (per block of heads) in A.before.
+template <int T>
+__device__ Part find_part(const PagedArgs& A, int tok, int warps) {
+    __shared__ int64_t wsum[T / 32];
+    __shared__ int found[3];
+    const int tid = threadIdx.x, lane = tid & 31, N = A.p.num_seqs;
+    const int per = (N + T - 1) / T, n0 = min(N, tid * per), n1 = min(N, n0 + per);
+    int64_t mine = 0;
+    for (int n = n0; n < n1; ++n) mine += range_of(A, n).tiles(tok);
+    int64_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+    }
+    if (lane == 31) wsum[tid >> 5] = upto;
+    __syncthreads();
+    int64_t total = 0;
+#pragma unroll
+    for (int w = 0; w < T / 32; ++w) {
+        if (w < tid >> 5) upto += wsum[w];
+        total += wsum[w];
+    }
+    int64_t run = upto - mine;
+    const int64_t share = share_of(total * A.heads, gridDim.x / A.groups, warps);
+    Part P;
+    P.lo = blockIdx.x / A.groups * share;
+    P.hi = min(P.lo + share, total * A.heads);
+    if (blockIdx.x == 0) {
+        int64_t r = run;
+        for (int n = n0; n < n1; ++n) {
+            A.before[n] = r;
+            r += range_of(A, n).tiles(tok);
+        }
+        if (tid == T - 1) A.before[N] = total;
+    }
+    if (P.lo < P.hi && run * A.heads <= P.lo && P.lo < upto * A.heads) {
+        int n = n0, t = range_of(A, n).tiles(tok);
+        while ((run + t) * A.heads <= P.lo) {
+            run += t;
+            t = range_of(A, ++n).tiles(tok);
+        }
+        const int64_t rest = P.lo - run * A.heads;
+        found[0] = n;
+        found[1] = int(rest / t);
+        found[2] = int(rest % t);
+    }
+    __syncthreads();
+    P.n = found[0], P.head = found[1], P.at = found[2];
+    return P;
+}
+// Where a CTA leaves rows [0, ROWS) of a pair that it has a part of: in its first place where the
+// pair began before its part, in its second where the pair goes on after it.
+__device__ __forceinline__ int64_t place_of(int cta, bool first, int rows) { return (int64_t(cta) * 2 + (first ? 0 : 1)) * rows; }
 
 // a value of the new token's row in the cache's type
 template <typename C> __device__ __forceinline__ C to_cache(float x, float scale);
@@ -67,151 +137,144 @@ template <> __device__ __forceinline__ __nv_fp8_e4m3 to_cache<__nv_fp8_e4m3>(flo
     const float y = x / scale;
     return __nv_fp8_e4m3(y != y ? y : fminf(fmaxf(y, -F8_MAX), F8_MAX));
 }
-__device__ __forceinline__ float from_cache(float x) { return x; }
 
-constexpr int PT = 128;  // threads
-constexpr int GB = 4;    // query heads per CTA
+// ------------------------------------------------------------------------------- fp32
+constexpr int PT = 128;   // threads
+constexpr int GB = 4;     // query heads per block of heads
+constexpr int PTOK = 32;  // tokens to a tile of the list
 
-template <typename C, int D> struct Lanes {
-    static constexpr int E = (16 / int(sizeof(C)) > D / 32) ? 16 / int(sizeof(C)) : D / 32;  // values per lane
-    static constexpr int LP = D / E;                                                         // lanes per token
+template <int D> struct Lanes {
+    static constexpr int E = D / 32 > 4 ? D / 32 : 4;  // values per lane
+    static constexpr int LP = D / E;                   // lanes per token
     static constexpr int GROUPS = PT / LP;
 };
-
-template <typename C, int E>
-__device__ __forceinline__ void load_row(const C* p, float (&x)[E]) {
-    constexpr int W = 16 / int(sizeof(C));
+template <int E>
+__device__ __forceinline__ void load_row(const float* p, float (&x)[E]) {
 #pragma unroll
-    for (int b = 0; b < E / W; ++b) {
-        C v[W];
-        *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(p + b * W);
-#pragma unroll
-        for (int e = 0; e < W; ++e) x[b * W + e] = from_cache(v[e]);
-    }
+    for (int b = 0; b < E / 4; ++b) *reinterpret_cast<float4*>(x + 4 * b) = *reinterpret_cast<const float4*>(p + 4 * b);
 }
 
-template <typename Act, typename C, int D>
-__global__ void __launch_bounds__(PT) k_paged(const PagedArgs A) {
-    using L = Lanes<C, D>;
+// Tokens over lane groups, each with its own running (m, l, accumulator) of GB heads.
+template <int D>
+__global__ void __launch_bounds__(PT, D == 256 ? 4 : 5) k_paged(const PagedArgs A) {
+    using L = Lanes<D>;
     constexpr int E = L::E, LP = L::LP, GROUPS = L::GROUPS;
     __shared__ __align__(16) float acc_s[GROUPS][GB][D];
     __shared__ float ml_s[GROUPS][GB][2];
-    __shared__ __align__(16) C new_s[2][D];
     const gdn_paged_problem& p = A.p;
     const int tid = threadIdx.x, lane = tid % LP, grp = tid / LP;
     const int G = p.Hq / p.Hkv, nb = (G + GB - 1) / GB;
-    const int split = blockIdx.x, hk = blockIdx.y / nb, hb = (blockIdx.y % nb) * GB, n = blockIdx.z;
-    const Range R = range_of(A, n);
-    if (split >= R.count) return;
-    const int start = R.base + split * A.split_len;
-    const int t0 = max(R.first, start), t1 = min(R.len, start + A.split_len);
-    const float ks = A.k_scale ? A.k_scale[hk] : 1.f, vs = A.v_scale ? A.v_scale[hk] : 1.f;
-    const int32_t* table = A.table + n * p.table_stride;
-    const C* kc = static_cast<const C*>(A.k_cache) + hk * p.k_head_stride;
-    const C* vc = static_cast<const C*>(A.v_cache) + hk * p.v_head_stride;
+    tc::pdl_launch_dependents();
+    Part P = find_part<PT>(A, PTOK, 1);
+    for (int64_t pos = P.lo; pos < P.hi;) {
+        const int n = P.n, block = P.head * A.groups + blockIdx.x % A.groups, hk = block / nb, hb = (block % nb) * GB;
+        const Range R = range_of(A, n);
+        const int tiles = R.tiles(PTOK), end = int(min(int64_t(tiles), P.at + (P.hi - pos)));
+        const bool whole = P.at == 0 && end == tiles, began = P.at > 0;
+        const int start = R.base + P.at * PTOK;
+        const int t0 = max(R.first, start), t1 = end == tiles ? R.len : R.base + end * PTOK;
+        pos += end - P.at;
+        P.at = 0;
+        if (++P.head == A.heads) P.head = 0, ++P.n;
 
-    int t_new = -1;  // the position whose row comes from k_new, v_new
-    if (A.k_new && R.len > 0 && R.len == t1) {
-        t_new = R.len - 1;
-        const int page = table[t_new / p.page_size], slot = t_new % p.page_size;
-        const bool in = page >= 0 && page < p.num_pages;
-        for (int i = tid; i < D; i += PT) {
-            const int64_t at = n * p.new_stride + hk * D + i;
-            new_s[0][i] = to_cache<C>(to_f(static_cast<const Act*>(A.k_new)[at]), ks);
-            new_s[1][i] = to_cache<C>(to_f(static_cast<const Act*>(A.v_new)[at]), vs);
-            if (in && hb == 0) {
-                const_cast<C*>(kc)[page * p.k_page_stride + slot * p.k_token_stride + i] = new_s[0][i];
-                const_cast<C*>(vc)[page * p.v_page_stride + slot * p.v_token_stride + i] = new_s[1][i];
+        const float ks = A.k_scale ? A.k_scale[hk] : 1.f, vs = A.v_scale ? A.v_scale[hk] : 1.f;
+        const int32_t* table = A.table + n * p.table_stride;
+        float* kc = static_cast<float*>(A.k_cache) + hk * p.k_head_stride;
+        float* vc = static_cast<float*>(A.v_cache) + hk * p.v_head_stride;
+        if (A.k_new && R.len > 0 && end == tiles) {  // every block of heads writes the same bits before it reads them
+            const int at = R.len - 1, page = table[A.page_div.of(at)], slot = at - A.page_div.of(at) * p.page_size;
+            if (page >= 0 && page < p.num_pages) {
+                const int64_t from = n * p.new_stride + int64_t(hk) * D;
+                for (int i = tid; i < D; i += PT) {
+                    kc[page * p.k_page_stride + slot * p.k_token_stride + i] = to_cache<float>(static_cast<const float*>(A.k_new)[from + i], ks);
+                    vc[page * p.v_page_stride + slot * p.v_token_stride + i] = to_cache<float>(static_cast<const float*>(A.v_new)[from + i], vs);
+                }
+            }
+            __syncthreads();
+        }
+
+        float q[GB][E], acc[GB][E], m[GB], l[GB];
+#pragma unroll
+        for (int h = 0; h < GB; ++h) {
+            m[h] = -INFINITY;
+            l[h] = 0.f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                acc[h][e] = 0.f;
+                q[h][e] = hb + h < G ? static_cast<const float*>(A.q)[n * p.q_stride + (hk * G + hb + h) * D + lane * E + e] : 0.f;
             }
         }
-        __syncthreads();
-    }
-
-    float q[GB][E], acc[GB][E], m[GB], l[GB];
-#pragma unroll
-    for (int h = 0; h < GB; ++h) {
-        m[h] = -INFINITY;
-        l[h] = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            acc[h][e] = 0.f;
-            q[h][e] = hb + h < G ? to_f(static_cast<const Act*>(A.q)[n * p.q_stride + (hk * G + hb + h) * D + lane * E + e]) : 0.f;
-        }
-    }
-    const float zs = p.scale * ks;
-    for (int t = t0 + grp; t - grp < t1; t += GROUPS) {
-        bool live = t < t1;
-        float kx[E] = {}, vx[E] = {};
-        if (live) {
-            if (t == t_new) {
-                load_row<C, E>(&new_s[0][lane * E], kx);
-                load_row<C, E>(&new_s[1][lane * E], vx);
-                const int page = table[t / p.page_size];
-                live = page >= 0 && page < p.num_pages;
-            } else {
-                const int page = table[t / p.page_size], slot = t % p.page_size;
+        const float zs = p.scale * ks * LOG2E;
+        for (int t = t0 + grp; t - grp < t1; t += GROUPS) {
+            bool live = t < t1;
+            float kx[E] = {}, vx[E] = {};
+            if (live) {
+                const int page = table[A.page_div.of(t)], slot = t - A.page_div.of(t) * p.page_size;
                 live = page >= 0 && page < p.num_pages;
                 if (live) {
-                    load_row<C, E>(kc + page * p.k_page_stride + slot * p.k_token_stride + lane * E, kx);
-                    load_row<C, E>(vc + page * p.v_page_stride + slot * p.v_token_stride + lane * E, vx);
+                    load_row<E>(kc + page * p.k_page_stride + slot * p.k_token_stride + lane * E, kx);
+                    load_row<E>(vc + page * p.v_page_stride + slot * p.v_token_stride + lane * E, vx);
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < GB; ++h) {
+                float z = 0.f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) z = fmaf(q[h][e], kx[e], z);
+#pragma unroll
+                for (int o = LP / 2; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+                if (live) {
+                    z *= zs;
+                    const float mn = fmaxf(m[h], z), c = m[h] == -INFINITY ? 0.f : exp2f(m[h] - mn);
+                    const float e0 = mn == -INFINITY ? 0.f : exp2f(z - mn);
+                    l[h] = fmaf(l[h], c, e0);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[h][e] = fmaf(acc[h][e], c, e0 * vx[e]);
+                    m[h] = mn;
                 }
             }
         }
 #pragma unroll
         for (int h = 0; h < GB; ++h) {
-            float z = 0.f;
 #pragma unroll
-            for (int e = 0; e < E; ++e) z = fmaf(q[h][e], kx[e], z);
-#pragma unroll
-            for (int o = LP / 2; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-            if (live) {
-                z *= zs;
-                const float mn = fmaxf(m[h], z), c = m[h] == -INFINITY ? 0.f : expf(m[h] - mn);
-                const float e0 = mn == -INFINITY ? 0.f : expf(z - mn);
-                l[h] = fmaf(l[h], c, e0);
-#pragma unroll
-                for (int e = 0; e < E; ++e) acc[h][e] = fmaf(acc[h][e], c, e0 * vx[e]);
-                m[h] = mn;
+            for (int e = 0; e < E; ++e) acc_s[grp][h][lane * E + e] = acc[h][e];
+            if (lane == 0) {
+                ml_s[grp][h][0] = m[h];
+                ml_s[grp][h][1] = l[h];
             }
         }
-    }
-#pragma unroll
-    for (int h = 0; h < GB; ++h) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc_s[grp][h][lane * E + e] = acc[h][e];
-        if (lane == 0) {
-            ml_s[grp][h][0] = m[h];
-            ml_s[grp][h][1] = l[h];
-        }
-    }
-    __syncthreads();
-    for (int i = tid; i < GB * D; i += PT) {
-        const int h = i / D, d = i % D;
-        if (hb + h >= G) break;
-        float M = -INFINITY, S = 0.f, a = 0.f;
-        for (int g = 0; g < GROUPS; ++g) M = fmaxf(M, ml_s[g][h][0]);
-        for (int g = 0; g < GROUPS; ++g) {
-            const float c = ml_s[g][h][0] == -INFINITY ? 0.f : expf(ml_s[g][h][0] - M);
-            S = fmaf(ml_s[g][h][1], c, S);
-            a = fmaf(acc_s[g][h][d], c, a);
-        }
-        const int64_t row = int64_t(n) * p.Hq + hk * G + hb + h;
-        if (R.count == 1) {
-            static_cast<Act*>(A.o)[row * D + d] = from_f<Act>(S > 0.f || S != S ? a / S * vs : 0.f);
-            if (A.lse && d == 0) A.lse[row] = M + logf(S);
-        } else {
-            A.part[(row * A.splits + split) * D + d] = a;
-            if (d == 0) {
-                float* ml = A.part + int64_t(p.num_seqs) * p.Hq * A.splits * D + (row * A.splits + split) * 2;
-                ml[0] = M * LOG2E;
-                ml[1] = S;
+        __syncthreads();
+        for (int i = tid; i < min(GB, G - hb) * D; i += PT) {
+            const int h = i / D, d = i % D;
+            float M = -INFINITY, S = 0.f, a = 0.f;
+            for (int g = 0; g < GROUPS; ++g) M = fmaxf(M, ml_s[g][h][0]);
+            for (int g = 0; g < GROUPS; ++g) {
+                const float c = ml_s[g][h][0] == -INFINITY ? 0.f : exp2f(ml_s[g][h][0] - M);
+                S = fmaf(ml_s[g][h][1], c, S);
+                a = fmaf(acc_s[g][h][d], c, a);
+            }
+            if (whole) {
+                const int64_t row = int64_t(n) * p.Hq + hk * G + hb + h;
+                const bool some = S > 0.f || S != S;
+                static_cast<float*>(A.o)[row * D + d] = some ? a / S * vs : 0.f;
+                if (A.lse && d == 0) A.lse[row] = some ? (M + log2f(S)) * LN2 : -INFINITY;
+            } else {
+                const int64_t at = place_of(blockIdx.x, began, GB) + h;
+                A.part[at * D + d] = a;
+                if (d == 0) A.part_ml[at] = make_float2(M, S);
             }
         }
+        __syncthreads();  // the shared arrays are read before the next pair writes them
     }
 }
 
 // ---------------------------------------------------------------- bf16 and 8-bit caches
-__device__ __forceinline__ float ex2(float x) { return exp2f(x); }
+// 2^x to 2^-22 of itself; -inf gives 0
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 template <typename C> struct Frag;
 template <> struct Frag<__nv_bfloat16> {
@@ -241,419 +304,596 @@ __device__ __forceinline__ uint32_t f8x2(uint32_t v) {
     return uint32_t(h.x) | (uint32_t(h.y) << 16);
 }
 
-// copy of B bytes to shared memory, zeros where !in (the address is not read then)
-template <int B>
+// copy of 16 bytes to shared memory, zeros where !in (the address is not read then)
 __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool in) {
-    if constexpr (B == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(dst), "l"(src), "r"(in ? 8 : 0) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory"); }
 
 template <typename C, int D> struct Tile {
     static constexpr int E = int(sizeof(C));
+    static constexpr int TT = D * E <= 128 ? 2 : 1;                // 16-token blocks of a tile
+    static constexpr int TOK = 16 * TT;                            // tokens of a tile
     static constexpr int W = D * E > 256 ? 2 : 4;                  // warps
     static constexpr int T = 32 * W;                               // threads
-    static constexpr int KC = D * E / 64;                          // pieces of a key row per thread
-    static constexpr int VB = D * E / 8 >= 16 ? 16 : D * E / 8;    // bytes of a piece of a value row
-    static constexpr int VC = D * E / (8 * VB);                    // pieces of a value row per thread
-    static constexpr int BYTES = 32 * KC + 4 * VC * VB;            // per thread and tile
-    static constexpr int STAGES = 98304 / (T * BYTES) < 8 ? 98304 / (T * BYTES) : 8;
+    static constexpr int CTAS = 2;                                 // per multiprocessor
+    static constexpr int ROW = D * E;                              // bytes of a row
+    static constexpr int CPR = ROW / 16;                           // 16-byte pieces of a row
+    static constexpr int RPI = 32 / CPR;                           // rows per copy instruction of a warp
+    static constexpr int VB = ROW / 8 >= 16 ? 16 : ROW / 8;        // 8-bit: bytes of a piece of a value row
+    static constexpr int VC = E == 1 ? ROW / (8 * VB) : 0;         // 8-bit: pieces of a value row per thread
+    static constexpr int BLOCK = 16 * ROW;                         // bytes of 16 rows
+    static constexpr int BYTES = 2 * TT * BLOCK;                   // of a warp's tile: K's blocks, V's blocks
+    static constexpr int FIT = 98304 / (W * BYTES), STAGES = FIT < 8 ? FIT : 8;
     static constexpr int PAD = D + 4;                              // floats between rows of the joined accumulators
-    static constexpr int SMEM = STAGES * T * BYTES;
+    static constexpr int SMEM = STAGES * W * BYTES;
     static_assert(STAGES >= 2 && W * 16 * PAD * 4 <= SMEM, "the warps' accumulators are joined in the stages' memory");
+    // what a row's pieces are exchanged by
+    static __host__ __device__ constexpr int swap(int row) { return CPR == 4 ? (row >> 1) & 3 : row & 7; }
 };
+__device__ __forceinline__ void ldmatrix4(uint32_t from, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(from)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4t(uint32_t from, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(from)
+                 : "memory");
+}
 
-template <typename C, int D, bool HALF>
-__global__ void __launch_bounds__(Tile<C, D>::T) k_paged_mma(const PagedArgs A) {
+template <typename C, int D, bool HALF, bool TILED>
+__global__ void __launch_bounds__(Tile<C, D>::T, Tile<C, D>::CTAS) k_paged_mma(const PagedArgs A) {
     using L = Tile<C, D>;
-    constexpr int KC = L::KC, VC = L::VC, VB = L::VB, STAGES = L::STAGES, W = L::W, R2 = HALF ? 1 : 2;
-    constexpr int CB = 16 / L::E;                 // values per 16-byte piece
+    constexpr int TT = L::TT, TOK = L::TOK, STAGES = L::STAGES, W = L::W, R2 = HALF ? 1 : 2;
+    constexpr int CPR = L::CPR, RPI = L::RPI, ROW = L::ROW, VB = L::VB, VC = L::VC;
+    constexpr int VE = VB / L::E;                 // 8-bit: values per piece of a value row
     constexpr int KS = D / 16;                    // k16 steps
     constexpr bool F8 = L::E == 1;
-    extern __shared__ __align__(16) unsigned char smem[];
+    constexpr bool QS = D == 256;                 // query fragments in shared memory: the registers hold the accumulators
+    extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ float ml_s[W][16][2];
+    __shared__ uint4 q_s[QS ? KS * R2 / 2 : 1][32];
     const gdn_paged_problem& p = A.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int G = p.Hq / p.Hkv, nb = (G + 15) / 16;
-    const int split = blockIdx.x, hk = blockIdx.y / nb, hb = (blockIdx.y % nb) * 16, n = blockIdx.z;
-    tc::pdl_launch_dependents();
-    const Range R = range_of(A, n);
-    if (split >= R.count) return;
-    const int start = R.base + split * A.split_len;
-    const int t0 = max(R.first, start), t1 = min(R.len, start + A.split_len);
-    const float ks = A.k_scale ? A.k_scale[hk] : 1.f, vs = A.v_scale ? A.v_scale[hk] : 1.f;
-    const int32_t* table = A.table + n * p.table_stride;
-    C* kc = static_cast<C*>(A.k_cache) + hk * p.k_head_stride;
-    C* vc = static_cast<C*>(A.v_cache) + hk * p.v_head_stride;
-    const unsigned psize = unsigned(p.page_size);
+    const uint32_t mem = tc::smem_addr(smem) + warp * STAGES * L::BYTES;  // this warp's stages
+    // copies: row copy_row + RPI j, piece copy_piece; a row's exchange is that of copy_row and that of RPI j
+    const int copy_row = lane / CPR, copy_piece = lane % CPR;
+    const uint32_t copy_to = mem + copy_row * ROW + ((copy_piece ^ L::swap(copy_row)) << 4);
+    // key fragments of 16 tokens: bf16, a step's two pieces of tokens 0-7, then of 8-15; 8-bit, a step's one
+    // piece of tokens 0-7 and 8-15, then the next step's
+    const int k_row = (lane & 7) + 8 * (F8 ? lane >> 3 & 1 : lane >> 4);
+    const uint32_t k_at = mem + k_row * ROW + (((F8 ? lane >> 4 : lane >> 3 & 1) ^ L::swap(k_row)) << 4);
+    // value fragments, bf16: piece c of tokens 0-7 and 8-15, then piece c + 1
+    const int v_row = (lane & 7) + 8 * (lane >> 3 & 1);
+    const uint32_t v_at = mem + TT * L::BLOCK + v_row * ROW + (((lane >> 4) ^ L::swap(v_row)) << 4);
+    // 8-bit: this thread's rows of 16 tokens 2t, 2t + 1, 2t + 8, 2t + 9 and its pieces g + 8 c of VB bytes
+    auto v8_at = [&](int r, int c) {
+        const int row = 2 * t + (r & 1) + 8 * (r >> 1), byte = (g + 8 * c) * VB;
+        return mem + TT * L::BLOCK + row * ROW + (((byte >> 4) ^ L::swap(row)) << 4) + (byte & 15);
+    };
+    auto slot_of = [&](int tok) { return tok - A.page_div.of(tok) * p.page_size; };
 
-    if (A.k_new && R.len > 0 && R.len == t1) {  // every block of heads writes the same bits before it reads them
-        const int at = R.len - 1, page = table[at / psize];
-        if (page >= 0 && page < p.num_pages) {
-            C* kd = kc + page * p.k_page_stride + (at % psize) * p.k_token_stride;
-            C* vd = vc + page * p.v_page_stride + (at % psize) * p.v_token_stride;
-            const int64_t from = n * p.new_stride + int64_t(hk) * D;
-            for (int i = tid; i < D; i += L::T) {
-                kd[i] = to_cache<C>(to_f(static_cast<const __nv_bfloat16*>(A.k_new)[from + i]), ks);
-                vd[i] = to_cache<C>(to_f(static_cast<const __nv_bfloat16*>(A.v_new)[from + i]), vs);
+    tc::pdl_launch_dependents();
+    Part P = find_part<L::T>(A, TOK, W);
+    for (int64_t pos = P.lo; pos < P.hi;) {
+        // ---- the next (sequence, block of heads) and this CTA's tiles of it
+        const int n = P.n, block = P.head * A.groups + blockIdx.x % A.groups, hk = block / nb, hb = (block % nb) * 16;
+        const Range R = range_of(A, n);
+        const int tiles_n = R.tiles(TOK), end = int(min(int64_t(tiles_n), P.at + (P.hi - pos)));
+        const bool whole = P.at == 0 && end == tiles_n, began = P.at > 0;
+        const int start = R.base + P.at * TOK;
+        const int t0 = max(R.first, start), t1 = end == tiles_n ? R.len : R.base + end * TOK;
+        const int all = end - P.at;
+        pos += all;
+        P.at = 0;
+        if (++P.head == A.heads) P.head = 0, ++P.n;
+        const float ks = A.k_scale ? A.k_scale[hk] : 1.f, vs = A.v_scale ? A.v_scale[hk] : 1.f;
+        const int32_t* table = A.table + n * p.table_stride;
+        C* kc = static_cast<C*>(A.k_cache) + hk * p.k_head_stride;
+        C* vc = static_cast<C*>(A.v_cache) + hk * p.v_head_stride;
+
+        if (A.k_new && R.len > 0 && end == tiles_n) {  // every block of heads writes the same bits before it reads them
+            const int at = R.len - 1, page = table[A.page_div.of(at)], slot = slot_of(at);
+            if (page >= 0 && page < p.num_pages) {
+                C* kd = kc + page * p.k_page_stride + slot * p.k_token_stride;
+                C* vd = vc + page * p.v_page_stride + slot * p.v_token_stride;
+                const int64_t from = n * p.new_stride + int64_t(hk) * D;
+                for (int i = tid; i < D; i += L::T) {
+                    kd[i] = to_cache<C>(to_f(static_cast<const __nv_bfloat16*>(A.k_new)[from + i]), ks);
+                    vd[i] = to_cache<C>(to_f(static_cast<const __nv_bfloat16*>(A.v_new)[from + i]), vs);
+                }
+            }
+            __syncthreads();
+        }
+
+        // ---- this warp's tiles: tokens from start + TOK (warp + W i)
+        const int tiles = all > warp ? (all - warp + W - 1) / W : 0;
+        auto token_of = [&](int i) { return start + TOK * (warp + W * i); };
+        // The page(s) of block b of tile i: with TILED (a page holds whole blocks) the block's page, in
+        // every lane; else lane l has that of token l % 16.  -1 where there is nothing to attend to.
+        auto page_at = [&](int i, int b) {
+            const int tok = token_of(i) + 16 * b + (TILED ? 0 : lane & 15);
+            if (i >= tiles || tok >= t1 || (!TILED && tok < t0)) return -1;
+            const int page = table[A.page_div.of(tok)];
+            return page >= 0 && page < p.num_pages ? page : -1;
+        };
+        // Requests the rows of block b of tile i (zeros where masked); returns which tokens count.
+        auto issue = [&](int i, int b, int stage, int pages) -> uint32_t {
+            const int tok = token_of(i) + 16 * b;
+            const uint32_t to = copy_to + stage * L::BYTES + b * L::BLOCK;
+            uint32_t valid;
+            if constexpr (TILED) {
+                valid = 0u;
+                if (pages >= 0) {
+                    valid = 0xffffu;
+                    if (t0 > tok) valid &= 0xffffu << (t0 - tok);
+                    if (t1 - tok < 16) valid &= 0xffffu >> (16 - (t1 - tok));
+                }
+                const int slot = slot_of(tok) + copy_row, page = pages < 0 ? 0 : pages;
+                const C* kt = kc + (page * p.k_page_stride + slot * p.k_token_stride) + copy_piece * (16 / L::E);
+                const C* vt = vc + (page * p.v_page_stride + slot * p.v_token_stride) + copy_piece * (16 / L::E);
+#pragma unroll
+                for (int j = 0; j < 16 / RPI; ++j) {
+                    const bool in = valid >> (copy_row + RPI * j) & 1;
+                    const uint32_t at = (to ^ (L::swap(RPI * j) << 4)) + RPI * j * ROW;
+                    cp_async(at, kt, in);
+                    cp_async(at + TT * L::BLOCK, vt, in);
+                    kt += RPI * p.k_token_stride;
+                    vt += RPI * p.v_token_stride;
+                }
+            } else {
+                valid = __ballot_sync(0xffffffffu, pages >= 0) & 0xffffu;
+#pragma unroll
+                for (int j = 0; j < 16 / RPI; ++j) {
+                    const int row = copy_row + RPI * j, page = __shfl_sync(0xffffffffu, pages, row), slot = slot_of(tok + row);
+                    const C *kt = kc, *vt = vc;
+                    if (page >= 0) {
+                        kt += page * p.k_page_stride + slot * p.k_token_stride + copy_piece * (16 / L::E);
+                        vt += page * p.v_page_stride + slot * p.v_token_stride + copy_piece * (16 / L::E);
+                    }
+                    const uint32_t at = (to ^ (L::swap(RPI * j) << 4)) + RPI * j * ROW;
+                    cp_async(at, kt, page >= 0);
+                    cp_async(at + TT * L::BLOCK, vt, page >= 0);
+                }
+            }
+            return valid << (16 * b);
+        };
+
+        uint32_t mask[STAGES];  // which tokens of the tiles in flight count, oldest first
+        int pages[TT];
+#pragma unroll
+        for (int i = 0; i < STAGES - 1; ++i) {
+            mask[i] = 0u;
+            if (i < tiles)
+#pragma unroll
+                for (int b = 0; b < TT; ++b) mask[i] |= issue(i, b, i, page_at(i, b));
+            cp_commit();
+        }
+#pragma unroll
+        for (int b = 0; b < TT; ++b) pages[b] = page_at(STAGES - 1, b);
+
+        // ---- query fragments: features 16 s + 2t, + 1 and 16 s + 8 + 2t, + 1 of step s; 8-bit, 16 s + 4t .. + 3
+        alignas(16) uint32_t qf[KS][2 * R2];
+        float zs[R2];
+#pragma unroll
+        for (int r = 0; r < R2; ++r) {
+            const int h = hb + g + 8 * r;
+            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(A.q) + n * p.q_stride + int64_t(hk * G + h) * D;
+            uint2 raw[KS];
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+                raw[s] = h >= G ? make_uint2(0u, 0u)
+                         : F8   ? *reinterpret_cast<const uint2*>(q + 16 * s + 4 * t)
+                                : make_uint2(*reinterpret_cast<const uint32_t*>(q + 16 * s + 2 * t), *reinterpret_cast<const uint32_t*>(q + 16 * s + 8 + 2 * t));
+            zs[r] = p.scale * ks * LOG2E;
+            if constexpr (F8) {
+                float top = 0.f;
+                float2 f[KS][2];
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    f[s][0] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw[s].x));
+                    f[s][1] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw[s].y));
+                    top = fmaxf(top, fmaxf(fmaxf(fabsf(f[s][0].x), fabsf(f[s][0].y)), fmaxf(fabsf(f[s][1].x), fabsf(f[s][1].y))));
+                }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const int e = top > 0.f && top < INFINITY ? ilogbf(top) : 0;
+                const float down = ldexpf(1.f, -e);
+                zs[r] = ldexpf(zs[r], e);
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    qf[s][r] = Frag<C>::pack(f[s][0].x * down, f[s][0].y * down);
+                    qf[s][R2 + r] = Frag<C>::pack(f[s][1].x * down, f[s][1].y * down);
+                }
+            } else {
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    qf[s][r] = raw[s].x;
+                    qf[s][R2 + r] = raw[s].y;
+                }
+            }
+        }
+
+        if constexpr (QS) {
+            if (warp == 0)
+#pragma unroll
+                for (int i = 0; i < KS * R2 / 2; ++i) q_s[i][lane] = reinterpret_cast<const uint4*>(&qf[0][0])[i];
+            __syncthreads();
+        }
+
+        float acc[D / 8][4], m[R2], l[R2];  // with HALF the upper two of a quad are the empty rows
+#pragma unroll
+        for (int r = 0; r < R2; ++r) {
+            m[r] = -INFINITY;
+            l[r] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
+        auto mma = [&](float (&c)[4], const uint32_t* a, uint32_t b0, uint32_t b1) {
+            if constexpr (HALF) {
+                const uint32_t af[4] = {a[0], 0u, a[1], 0u};
+                Frag<C>::mma(c, af, b0, b1);
+            } else {
+                const uint32_t af[4] = {a[0], a[1], a[2], a[3]};
+                Frag<C>::mma(c, af, b0, b1);
+            }
+        };
+
+        int stage = 0;
+        alignas(16) uint32_t q2[2][2 * R2];  // with QS: the fragments of two steps
+        for (int i = 0; i < tiles; ++i) {
+            cp_wait<STAGES - 2>();
+            __syncwarp();  // every lane's copies of tile i have landed, and tile i - 1 has been read
+            {
+                const int next = i + STAGES - 1;
+                mask[STAGES - 1] = 0u;
+                if (next < tiles)
+#pragma unroll
+                    for (int b = 0; b < TT; ++b) mask[STAGES - 1] |= issue(next, b, stage == 0 ? STAGES - 1 : stage - 1, pages[b]);
+                cp_commit();
+#pragma unroll
+                for (int b = 0; b < TT; ++b) pages[b] = page_at(next + 1, b);
+            }
+            const uint32_t kd = k_at + stage * L::BYTES;
+            float s[2 * TT][4] = {};  // of 8 tokens each
+            constexpr int SPL = F8 ? 2 : 1;  // steps per ldmatrix
+#pragma unroll
+            for (int c = 0; c < KS / SPL; ++c) {
+                alignas(16) uint32_t qc[2][2 * R2];  // of two steps
+                if constexpr (QS) {
+                    if (SPL == 2 || c % 2 == 0) {
+#pragma unroll
+                        for (int i = 0; i < R2; ++i) reinterpret_cast<uint4*>(&q2[0][0])[i] = q_s[(SPL == 2 ? c : c / 2) * R2 + i][lane];
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < SPL; ++i)
+#pragma unroll
+                    for (int e = 0; e < 2 * R2; ++e) qc[i][e] = QS ? q2[SPL == 2 ? i : c % 2][e] : qf[c * SPL + i][e];
+#pragma unroll
+                for (int b = 0; b < TT; ++b) {
+                    uint32_t k[4];
+                    ldmatrix4((kd ^ (c << 5)) + b * L::BLOCK, k);
+                    if constexpr (F8) {
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) mma(s[2 * b + (u & 1)], qc[u >> 1], f8x2(k[u]), f8x2(k[u] >> 16));
+                    } else {
+                        mma(s[2 * b], qc[0], k[0], k[1]);
+                        mma(s[2 * b + 1], qc[0], k[2], k[3]);
+                    }
+                }
+            }
+            // scores in units of log 2: s[r][e] is token 8 r + 2 t + e % 2
+            const uint32_t mk = mask[0];
+            float top[R2];
+#pragma unroll
+            for (int r = 0; r < R2; ++r) top[r] = -INFINITY;
+#pragma unroll
+            for (int r = 0; r < 2 * TT; ++r)
+#pragma unroll
+                for (int e = 0; e < 2 * R2; ++e) s[r][e] *= zs[e >> 1];
+            if (mk != (TT == 2 ? 0xffffffffu : 0xffffu)) {
+#pragma unroll
+                for (int r = 0; r < 2 * TT; ++r)
+#pragma unroll
+                    for (int e = 0; e < 2 * R2; ++e)
+                        if (!(mk >> (8 * r + 2 * t + (e & 1)) & 1)) s[r][e] = -INFINITY;
+            }
+#pragma unroll
+            for (int r = 0; r < 2 * TT; ++r)
+#pragma unroll
+                for (int e = 0; e < 2 * R2; ++e) top[e >> 1] = fmaxf(top[e >> 1], s[r][e]);
+            bool grows = false;
+#pragma unroll
+            for (int r = 0; r < R2; ++r) {
+                top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+                top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+                grows |= top[r] > m[r];
+            }
+            if (__any_sync(0xffffffffu, grows)) {
+#pragma unroll
+                for (int r = 0; r < R2; ++r) {
+                    const float mn = fmaxf(m[r], top[r]), c = mn == -INFINITY ? 1.f : ex2(m[r] - mn);
+                    m[r] = mn;
+                    l[r] *= c;
+#pragma unroll
+                    for (int j = 0; j < D / 8; ++j) {
+                        acc[j][2 * r] *= c;
+                        acc[j][2 * r + 1] *= c;
+                    }
+                }
+            }
+            uint32_t pf[TT][2 * R2];
+#pragma unroll
+            for (int r = 0; r < R2; ++r) {
+                const float sub = m[r] == -INFINITY ? 0.f : m[r];
+#pragma unroll
+                for (int b = 0; b < TT; ++b) {
+                    float w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[e] = ex2(s[2 * b + (e >> 1)][2 * r + (e & 1)] - sub);
+                    l[r] += (w[0] + w[1]) + (w[2] + w[3]);
+                    pf[b][r] = Frag<C>::pack(w[0], w[1]);
+                    pf[b][R2 + r] = Frag<C>::pack(w[2], w[3]);
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < TT; ++b) {
+                const uint32_t off = stage * L::BYTES + b * L::BLOCK;
+                if constexpr (F8) {
+#pragma unroll
+                    for (int c = 0; c < VC; ++c) {
+                        uint32_t v[4][VB / 4];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            if constexpr (VB == 16) {
+                                const uint4 x = tc::lds128(v8_at(r, c) + off);
+                                v[r][0] = x.x, v[r][1] = x.y, v[r][2] = x.z, v[r][3] = x.w;
+                            } else {
+                                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];\n" : "=r"(v[r][0]), "=r"(v[r][1]) : "r"(v8_at(r, c) + off) : "memory");
+                            }
+                        }
+#pragma unroll
+                        for (int x = 0; x < VB / 4; ++x)
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {  // features 4x + 2y, 4x + 2y + 1
+                                const uint32_t lo = __byte_perm(v[0][x], v[1][x], y ? 0x7362 : 0x5140);
+                                const uint32_t hi = __byte_perm(v[2][x], v[3][x], y ? 0x7362 : 0x5140);
+                                mma(acc[c * VE + 4 * x + 2 * y], pf[b], f8x2(lo), f8x2(hi));
+                                mma(acc[c * VE + 4 * x + 2 * y + 1], pf[b], f8x2(lo >> 16), f8x2(hi >> 16));
+                            }
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < D / 8; c += 2) {
+                        uint32_t v[4];
+                        ldmatrix4t((v_at ^ (c << 4)) + off, v);
+                        mma(acc[c], pf[b], v[0], v[1]);
+                        mma(acc[c + 1], pf[b], v[2], v[3]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int j = 0; j + 1 < STAGES; ++j) mask[j] = mask[j + 1];
+            stage = stage + 1 == STAGES ? 0 : stage + 1;
+        }
+
+        // ---- join the warps: sums over a row's 4 lanes, then over the warps in order
+        cp_wait<0>();
+        __syncthreads();
+        float* accs = reinterpret_cast<float*>(smem) + warp * 16 * L::PAD;
+#pragma unroll
+        for (int r = 0; r < R2; ++r) {
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+            if (t == 0) {
+                ml_s[warp][g + 8 * r][0] = m[r];
+                ml_s[warp][g + 8 * r][1] = l[r];
+            }
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j) {
+                const int d = F8 ? (2 * t + 8 * (j / VE)) * VE + j % VE : 8 * j + 2 * t;
+                accs[(g + 8 * r) * L::PAD + d] = acc[j][2 * r];
+                accs[(g + 8 * r) * L::PAD + d + (F8 ? VE : 1)] = acc[j][2 * r + 1];
             }
         }
         __syncthreads();
-    }
-
-    // ---- this warp's tiles: tokens start + 16 (warp + W i)
-    const int all = t1 > start ? (t1 - start + 15) / 16 : 0;
-    const int tiles = all > warp ? (all - warp + W - 1) / W : 0;
-    auto token_of = [&](int i) { return start + 16 * (warp + W * i); };
-    // lane l < 16: page of token l of tile i, or -1 where there is nothing to attend to
-    auto page_at = [&](int i) {
-        const int tok = token_of(i) + (lane & 15);
-        if (i >= tiles || tok < t0 || tok >= t1) return -1;
-        const int page = table[unsigned(tok) / psize];
-        return page >= 0 && page < p.num_pages ? page : -1;
-    };
-    const uint32_t kslot = tc::smem_addr(smem) + tid * 16, vslot = tc::smem_addr(smem) + L::T * 32 * KC + tid * VB;
-    auto issue = [&](int i, int stage, int pages) -> uint32_t {
-        const uint32_t valid = __ballot_sync(0xffffffffu, pages >= 0) & 0xffffu;
-        const int tok = token_of(i);
-        const uint32_t kd = kslot + stage * (L::T * L::BYTES), vd = vslot + stage * (L::T * L::BYTES);
+        const float* all_acc = reinterpret_cast<const float*>(smem);
+        const int rows = min(16, G - hb);
+        for (int i = tid; i < rows * (D / 4); i += L::T) {
+            const int h = i / (D / 4), d = i % (D / 4) * 4;
+            float M = -INFINITY, S = 0.f;
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int row = g + 8 * r, page = __shfl_sync(0xffffffffu, pages, row);
-            const C* src = kc;
-            if (page >= 0) src += page * p.k_page_stride + int64_t(unsigned(tok + row) % psize) * p.k_token_stride + t * CB;
+            for (int w = 0; w < W; ++w) M = fmaxf(M, ml_s[w][h][0]);
 #pragma unroll
-            for (int c = 0; c < KC; ++c) cp_async<16>(kd + (r * KC + c) * (L::T * 16), src + c * 4 * CB, page >= 0);
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = 2 * t + (r & 1) + 8 * (r >> 1), page = __shfl_sync(0xffffffffu, pages, row);
-            const C* src = vc;
-            if (page >= 0) src += page * p.v_page_stride + int64_t(unsigned(tok + row) % psize) * p.v_token_stride + g * (VB / L::E);
-#pragma unroll
-            for (int c = 0; c < VC; ++c) cp_async<VB>(vd + (r * VC + c) * (L::T * VB), src + c * 8 * (VB / L::E), page >= 0);
-        }
-        return valid;
-    };
-
-    uint32_t mask[STAGES];  // which tokens of the tiles in flight count, oldest first
-#pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i) {
-        mask[i] = i < tiles ? issue(i, i, page_at(i)) : 0u;
-        cp_commit();
-    }
-    int pages = page_at(STAGES - 1);
-
-    // ---- query fragments, in the key pieces' order of features
-    uint32_t qf[KS][2 * R2];
-    float zs[R2];
-#pragma unroll
-    for (int r = 0; r < R2; ++r) {
-        const int h = hb + g + 8 * r;
-        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(A.q) + n * p.q_stride + int64_t(hk * G + h) * D;
-        uint2 raw[KS];
-#pragma unroll
-        for (int s = 0; s < KS; ++s)
-            raw[s] = h < G ? *reinterpret_cast<const uint2*>(q + (t + 4 * (s / (CB / 4))) * CB + 4 * (s % (CB / 4))) : make_uint2(0u, 0u);
-        zs[r] = p.scale * ks * LOG2E;
-        if constexpr (F8) {
-            float top = 0.f;
-            float2 f[KS][2];
-#pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                f[s][0] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw[s].x));
-                f[s][1] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw[s].y));
-                top = fmaxf(top, fmaxf(fmaxf(fabsf(f[s][0].x), fabsf(f[s][0].y)), fmaxf(fabsf(f[s][1].x), fabsf(f[s][1].y))));
+            for (int w = 0; w < W; ++w) {
+                const float c = ml_s[w][h][0] == -INFINITY ? 0.f : ex2(ml_s[w][h][0] - M);
+                const float4 x = *reinterpret_cast<const float4*>(all_acc + (w * 16 + h) * L::PAD + d);
+                S = fmaf(ml_s[w][h][1], c, S);
+                a.x = fmaf(x.x, c, a.x);
+                a.y = fmaf(x.y, c, a.y);
+                a.z = fmaf(x.z, c, a.z);
+                a.w = fmaf(x.w, c, a.w);
             }
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const int e = top > 0.f && top < INFINITY ? ilogbf(top) : 0;
-            const float down = ldexpf(1.f, -e);
-            zs[r] = ldexpf(zs[r], e);
-#pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                qf[s][r] = Frag<C>::pack(f[s][0].x * down, f[s][0].y * down);
-                qf[s][R2 + r] = Frag<C>::pack(f[s][1].x * down, f[s][1].y * down);
-            }
-        } else {
-#pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                qf[s][r] = raw[s].x;
-                qf[s][R2 + r] = raw[s].y;
+            if (whole) {
+                const int64_t row = int64_t(n) * p.Hq + hk * G + hb + h;
+                const bool some = S > 0.f || S != S;
+                const float f = some ? vs / S : 0.f;
+                const uint2 o = make_uint2(tc::pack_bf16(a.x * f, a.y * f), tc::pack_bf16(a.z * f, a.w * f));
+                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(A.o) + row * D + d) = o;
+                if (A.lse && d == 0) A.lse[row] = some ? (M + log2f(S)) * LN2 : -INFINITY;
+            } else {
+                const int64_t at = place_of(blockIdx.x, began, 16) + h;
+                *reinterpret_cast<float4*>(A.part + at * D + d) = a;
+                if (d == 0) A.part_ml[at] = make_float2(M, S);
             }
         }
-    }
-
-    float acc[D / 8][2 * R2], m[R2], l[R2];
-#pragma unroll
-    for (int r = 0; r < R2; ++r) {
-        m[r] = -INFINITY;
-        l[r] = 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-        for (int e = 0; e < 2 * R2; ++e) acc[i][e] = 0.f;
-    // the fragments of 16 rows, the lower 8 alone being real with HALF
-    auto mma = [&](float (&c)[2 * R2], const uint32_t* a, uint32_t b0, uint32_t b1) {
-        if constexpr (HALF) {
-            float full[4] = {c[0], c[1], 0.f, 0.f};
-            const uint32_t af[4] = {a[0], 0u, a[1], 0u};
-            Frag<C>::mma(full, af, b0, b1);
-            c[0] = full[0];
-            c[1] = full[1];
-        } else {
-            const uint32_t af[4] = {a[0], a[1], a[2], a[3]};
-            Frag<C>::mma(c, af, b0, b1);
-        }
-    };
-
-    int stage = 0;
-    for (int i = 0; i < tiles; ++i) {
-        {
-            const int next = i + STAGES - 1;
-            mask[STAGES - 1] = next < tiles ? issue(next, stage == 0 ? STAGES - 1 : stage - 1, pages) : 0u;
-            cp_commit();
-            pages = page_at(next + 1);
-        }
-        cp_wait<STAGES - 1>();
-        const uint32_t kd = kslot + stage * (L::T * L::BYTES), vd = vslot + stage * (L::T * L::BYTES);
-        float s[2][2 * R2] = {};
-#pragma unroll
-        for (int c = 0; c < KC; ++c) {
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const uint4 k = tc::lds128(kd + (r * KC + c) * (L::T * 16));
-                const uint32_t kw[4] = {k.x, k.y, k.z, k.w};
-                if constexpr (F8) {
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) mma(s[r], qf[4 * c + u], f8x2(kw[u]), f8x2(kw[u] >> 16));
-                } else {
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) mma(s[r], qf[2 * c + u], kw[2 * u], kw[2 * u + 1]);
-                }
-            }
-        }
-        // scores in units of log 2; token 2t + e of 8 r'
-        const uint32_t mk = mask[0];
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-            for (int e = 0; e < 2 * R2; ++e) {
-                s[r][e] *= zs[e >> 1];
-                if (mk != 0xffffu && !(mk >> (8 * r + 2 * t + (e & 1)) & 1)) s[r][e] = -INFINITY;
-            }
-        bool grows = false;
-        float top[R2];
-#pragma unroll
-        for (int r = 0; r < R2; ++r) {
-            float x = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-            top[r] = fmaxf(m[r], x);
-            grows |= top[r] > m[r];
-        }
-        if (__any_sync(0xffffffffu, grows)) {
-#pragma unroll
-            for (int r = 0; r < R2; ++r) {
-                const float c = top[r] == -INFINITY ? 1.f : ex2(m[r] - top[r]);
-                m[r] = top[r];
-                l[r] *= c;
-#pragma unroll
-                for (int j = 0; j < D / 8; ++j) {
-                    acc[j][2 * r] *= c;
-                    acc[j][2 * r + 1] *= c;
-                }
-            }
-        }
-        uint32_t pf[2 * R2];
-#pragma unroll
-        for (int r = 0; r < R2; ++r) {
-            const float sub = m[r] == -INFINITY ? 0.f : m[r];
-            float w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = ex2(s[e >> 1][2 * r + (e & 1)] - sub);
-            l[r] += (w[0] + w[1]) + (w[2] + w[3]);
-            pf[r] = Frag<C>::pack(w[0], w[1]);
-            pf[R2 + r] = Frag<C>::pack(w[2], w[3]);
-        }
-#pragma unroll
-        for (int c = 0; c < VC; ++c) {
-            uint32_t v[4][VB / 4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const uint32_t from = vd + (r * VC + c) * (L::T * VB);
-                if constexpr (VB == 16) {
-                    const uint4 x = tc::lds128(from);
-                    v[r][0] = x.x, v[r][1] = x.y, v[r][2] = x.z, v[r][3] = x.w;
-                } else {
-                    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];\n" : "=r"(v[r][0]), "=r"(v[r][1]) : "r"(from) : "memory");
-                }
-            }
-#pragma unroll
-            for (int x = 0; x < VB / 4; ++x) {
-                if constexpr (F8) {
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {  // features 4x + 2y, 4x + 2y + 1
-                        const uint32_t a = __byte_perm(v[0][x], v[1][x], y ? 0x7362 : 0x5140);
-                        const uint32_t b = __byte_perm(v[2][x], v[3][x], y ? 0x7362 : 0x5140);
-                        mma(acc[c * VB + 4 * x + 2 * y], pf, f8x2(a), f8x2(b));
-                        mma(acc[c * VB + 4 * x + 2 * y + 1], pf, f8x2(a >> 16), f8x2(b >> 16));
-                    }
-                } else {
-                    mma(acc[c * 8 + 2 * x], pf, __byte_perm(v[0][x], v[1][x], 0x5410), __byte_perm(v[2][x], v[3][x], 0x5410));
-                    mma(acc[c * 8 + 2 * x + 1], pf, __byte_perm(v[0][x], v[1][x], 0x7632), __byte_perm(v[2][x], v[3][x], 0x7632));
-                }
-            }
-        }
-#pragma unroll
-        for (int j = 0; j + 1 < STAGES; ++j) mask[j] = mask[j + 1];
-        stage = stage + 1 == STAGES ? 0 : stage + 1;
-    }
-
-    // ---- join the warps: sums over a row's 4 lanes, then over the warps in order
-    cp_wait<0>();
-    __syncthreads();
-    float* accs = reinterpret_cast<float*>(smem) + warp * 16 * L::PAD;
-#pragma unroll
-    for (int r = 0; r < R2; ++r) {
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-        if (t == 0) {
-            ml_s[warp][g + 8 * r][0] = m[r];
-            ml_s[warp][g + 8 * r][1] = l[r];
-        }
-        constexpr int VE = VB / L::E;  // features of a value piece
-#pragma unroll
-        for (int j = 0; j < D / 8; ++j) {
-            const int d = (2 * t + 8 * (j / VE)) * VE + j % VE;
-            accs[(g + 8 * r) * L::PAD + d] = acc[j][2 * r];
-            accs[(g + 8 * r) * L::PAD + d + VE] = acc[j][2 * r + 1];
-        }
-    }
-    __syncthreads();
-    const float* all_acc = reinterpret_cast<const float*>(smem);
-    const int rows = min(16, G - hb);
-    for (int i = tid; i < rows * (D / 4); i += L::T) {
-        const int h = i / (D / 4), d = i % (D / 4) * 4;
-        float M = -INFINITY, S = 0.f;
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < W; ++w) M = fmaxf(M, ml_s[w][h][0]);
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-            const float c = ml_s[w][h][0] == -INFINITY ? 0.f : ex2(ml_s[w][h][0] - M);
-            const float4 x = *reinterpret_cast<const float4*>(all_acc + (w * 16 + h) * L::PAD + d);
-            S = fmaf(ml_s[w][h][1], c, S);
-            a.x = fmaf(x.x, c, a.x);
-            a.y = fmaf(x.y, c, a.y);
-            a.z = fmaf(x.z, c, a.z);
-            a.w = fmaf(x.w, c, a.w);
-        }
-        const int64_t row = int64_t(n) * p.Hq + hk * G + hb + h;
-        if (R.count == 1) {
-            const float f = S > 0.f || S != S ? vs / S : 0.f;
-            const uint2 o = make_uint2(tc::pack_bf16(a.x * f, a.y * f), tc::pack_bf16(a.z * f, a.w * f));
-            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(A.o) + row * D + d) = o;
-            if (A.lse && d == 0) A.lse[row] = S > 0.f || S != S ? (M + log2f(S)) * LN2 : -INFINITY;
-        } else {
-            *reinterpret_cast<float4*>(A.part + (row * A.splits + split) * D + d) = a;
-            if (d == 0) {
-                float* ml = A.part + int64_t(p.num_seqs) * p.Hq * A.splits * D + (row * A.splits + split) * 2;
-                *reinterpret_cast<float2*>(ml) = make_float2(M, S);
-            }
-        }
+        __syncthreads();  // the stages and ml_s are read before the next pair writes them
     }
 }
 
-// Joins the ranges of one (sequence, query head) in order.
-template <typename Act>
-__global__ void k_paged_join(const PagedArgs A) {
+// Joins the parts of the rows that several CTAs have parts of, in the list's order.  A block of 8
+// warps takes RPB rows: a warp each (8), or all 8 warps one row's parts (1: few rows, many parts).
+constexpr int JW = 8;
+template <typename Act, int D, int RPB>
+__global__ void __launch_bounds__(32 * JW) k_paged_join(const PagedArgs A, int tok, int rows, int ctas, int warps) {
+    constexpr int E = D / 32;
+    __shared__ float acc_s[RPB == 1 ? JW : 1][D], ml_s[RPB == 1 ? JW : 1][2];
     tc::pdl_wait();
     const gdn_paged_problem& p = A.p;
-    const int64_t row = blockIdx.x;
-    const int n = int(row / p.Hq), h = int(row % p.Hq), d = threadIdx.x, D = p.D;
-    const Range R = range_of(A, n);
-    if (R.count == 1) return;
-    const float* ml = A.part + int64_t(p.num_seqs) * p.Hq * A.splits * D + row * A.splits * 2;
-    float M = -INFINITY, S = 0.f, a = 0.f;
-    for (int i = 0; i < R.count; ++i) M = fmaxf(M, ml[2 * i]);
-#pragma unroll 4
-    for (int i = 0; i < R.count; ++i) {
-        const float c = ml[2 * i] == -INFINITY ? 0.f : ex2(ml[2 * i] - M);
-        S = fmaf(ml[2 * i + 1], c, S);
-        a = fmaf(A.part[(row * A.splits + i) * D + d], c, a);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t row = RPB == 1 ? blockIdx.x : int64_t(blockIdx.x) * JW + warp;
+    if (row >= int64_t(p.num_seqs) * p.Hq) return;  // with RPB == 1 never
+    const int n = int(row / p.Hq), h = int(row % p.Hq), G = p.Hq / p.Hkv, nb = (G + rows - 1) / rows;
+    const int block = (h / G) * nb + (h % G) / rows, in = (h % G) % rows;
+    const int head = block / A.groups, group = block % A.groups;
+    const int64_t before = A.before[n], tiles = A.before[n + 1] - before;
+    const int64_t share = share_of(A.before[p.num_seqs] * A.heads, ctas / A.groups, warps);
+    const int64_t at0 = before * A.heads + head * tiles, at1 = at0 + tiles;
+    const int c0 = int(at0 / share), c1 = int((at1 - 1) / share);
+    if (c0 == c1) return;  // that CTA wrote it out
+    // parts c0 .. c1; this warp's: c0 + first, first + step, ...
+    const int parts = c1 - c0 + 1, first = RPB == 1 ? warp : 0, step = RPB == 1 ? JW : 1;
+    auto place = [&](int i) { return place_of((c0 + i) * A.groups + group, i > 0 || at0 < c0 * share, rows) + in; };
+    float M = -INFINITY;
+    for (int i = first + step * lane; i < parts; i += step * 32) M = fmaxf(M, A.part_ml[place(i)].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float S = 0.f, acc[E] = {};
+#pragma unroll 8
+    for (int i = first; i < parts; i += step) {
+        const int64_t at = place(i);
+        const float2 ml = A.part_ml[at];
+        const float c = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+        S = fmaf(ml.y, c, S);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(A.part[at * D + 32 * e + lane], c, acc[e]);
     }
-    const float vs = A.v_scale ? A.v_scale[h / (p.Hq / p.Hkv)] : 1.f;
-    static_cast<Act*>(A.o)[row * D + d] = from_f<Act>(S > 0.f || S != S ? a / S * vs : 0.f);
-    if (A.lse && d == 0) A.lse[row] = S > 0.f || S != S ? (M + log2f(S)) * LN2 : -INFINITY;
+    if constexpr (RPB == 1) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc_s[warp][32 * e + lane] = acc[e];
+        if (lane == 0) {
+            ml_s[warp][0] = M;
+            ml_s[warp][1] = S;
+        }
+        __syncthreads();
+        if (warp > 0) return;
+        S = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll
+        for (int w = 0; w < JW; ++w) M = fmaxf(M, ml_s[w][0]);
+#pragma unroll
+        for (int w = 0; w < JW; ++w) {
+            const float c = ml_s[w][0] == -INFINITY ? 0.f : ex2(ml_s[w][0] - M);
+            S = fmaf(ml_s[w][1], c, S);
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(acc_s[w][32 * e + lane], c, acc[e]);
+        }
+    }
+    const bool some = S > 0.f || S != S;
+    const float f = some ? (A.v_scale ? A.v_scale[h / G] : 1.f) / S : 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) static_cast<Act*>(A.o)[row * D + 32 * e + lane] = from_f<Act>(acc[e] * f);
+    if (A.lse && lane == 0) A.lse[row] = some ? (M + log2f(S)) * LN2 : -INFINITY;
 }
 
-template <typename Act>
-cudaError_t launch_join(const PagedArgs& A, cudaStream_t st) {
-    if (A.splits == 1) return cudaGetLastError();
+// What the launches need to know of a kernel.
+struct Shape {
+    int tok, rows, warps, ctas;  // tokens of a tile, rows of a block of heads, warps that share tiles, CTAs per multiprocessor
+};
+template <typename C, int D> constexpr Shape mma_shape() { return {Tile<C, D>::TOK, 16, Tile<C, D>::W, Tile<C, D>::CTAS}; }
+template <int D> constexpr Shape fp32_shape() { return {PTOK, GB, 1, D == 256 ? 4 : 5}; }
+Shape shape_of(const gdn_paged_problem& p) {
+    if (p.dtype == GDN_FP32) return p.D == 64 ? fp32_shape<64>() : p.D == 128 ? fp32_shape<128>() : fp32_shape<256>();
+    if (p.cache_dtype == GDN_BF16)
+        return p.D == 64 ? mma_shape<__nv_bfloat16, 64>() : p.D == 128 ? mma_shape<__nv_bfloat16, 128>() : mma_shape<__nv_bfloat16, 256>();
+    return p.D == 64 ? mma_shape<__nv_fp8_e4m3, 64>() : p.D == 128 ? mma_shape<__nv_fp8_e4m3, 128>() : mma_shape<__nv_fp8_e4m3, 256>();
+}
+
+template <typename Act, int D>
+cudaError_t launch_join(const PagedArgs& A, const PagedPlan& plan, const Shape& s, cudaStream_t st) {
+    const int64_t rows = int64_t(A.p.num_seqs) * A.p.Hq;
     timing_begin("paged_attn_join", st);
-    const cudaError_t e = launch_pdl(k_paged_join<Act>, dim3(unsigned(int64_t(A.p.num_seqs) * A.p.Hq)), dim3(unsigned(A.p.D)), 0, st, A);
+    const cudaError_t e =
+        rows <= 1024 ? launch_pdl(k_paged_join<Act, D, 1>, dim3(unsigned(rows)), dim3(32 * JW), 0, st, A, s.tok, s.rows, plan.ctas, s.warps)
+                     : launch_pdl(k_paged_join<Act, D, JW>, dim3(unsigned((rows + JW - 1) / JW)), dim3(32 * JW), 0, st, A, s.tok, s.rows, plan.ctas, s.warps);
     timing_end(st);
     return e;
 }
 
 template <int D>
-cudaError_t launch_fp32(const PagedArgs& A, cudaStream_t st) {
-    const int G = A.p.Hq / A.p.Hkv;
+cudaError_t launch_fp32(const PagedArgs& A, const PagedPlan& plan, cudaStream_t st) {
     timing_begin("paged_attn", st);
-    k_paged<float, float, D><<<dim3(A.splits, A.p.Hkv * ((G + GB - 1) / GB), A.p.num_seqs), PT, 0, st>>>(A);
+    k_paged<D><<<plan.ctas, PT, 0, st>>>(A);
     timing_end(st);
-    return launch_join<float>(A, st);
+    return launch_join<float, D>(A, plan, fp32_shape<D>(), st);
 }
 
-template <typename C, int D, bool HALF>
-cudaError_t launch_mma(const PagedArgs& A, cudaStream_t st) {
+template <typename C, int D, bool HALF, bool TILED>
+cudaError_t launch_mma(const PagedArgs& A, const PagedPlan& plan, cudaStream_t st) {
     using L = Tile<C, D>;
-    const int G = A.p.Hq / A.p.Hkv;
-    const cudaError_t e = smem_attr(k_paged_mma<C, D, HALF>, L::SMEM);
+    const cudaError_t e = smem_attr(k_paged_mma<C, D, HALF, TILED>, L::SMEM);
     if (e != cudaSuccess) return e;
     timing_begin("paged_attn", st);
-    k_paged_mma<C, D, HALF><<<dim3(A.splits, A.p.Hkv * ((G + 15) / 16), A.p.num_seqs), L::T, L::SMEM, st>>>(A);
+    k_paged_mma<C, D, HALF, TILED><<<plan.ctas, L::T, L::SMEM, st>>>(A);
     timing_end(st);
-    return launch_join<__nv_bfloat16>(A, st);
+    return launch_join<__nv_bfloat16, D>(A, plan, mma_shape<C, D>(), st);
+}
+
+template <typename C, int D>
+cudaError_t launch_dim(const PagedArgs& A, const PagedPlan& plan, cudaStream_t st) {
+    const bool half = A.p.Hq / A.p.Hkv <= 8, tiled = A.p.page_size % 16 == 0;
+    if (half) return tiled ? launch_mma<C, D, true, true>(A, plan, st) : launch_mma<C, D, true, false>(A, plan, st);
+    return tiled ? launch_mma<C, D, false, true>(A, plan, st) : launch_mma<C, D, false, false>(A, plan, st);
 }
 
 template <typename C>
-cudaError_t launch_type(const PagedArgs& A, cudaStream_t st) {
-    const bool half = A.p.Hq / A.p.Hkv <= 8;
-    if (A.p.D == 64) return half ? launch_mma<C, 64, true>(A, st) : launch_mma<C, 64, false>(A, st);
-    if (A.p.D == 128) return half ? launch_mma<C, 128, true>(A, st) : launch_mma<C, 128, false>(A, st);
-    return half ? launch_mma<C, 256, true>(A, st) : launch_mma<C, 256, false>(A, st);
+cudaError_t launch_type(const PagedArgs& A, const PagedPlan& plan, cudaStream_t st) {
+    return A.p.D == 64 ? launch_dim<C, 64>(A, plan, st) : A.p.D == 128 ? launch_dim<C, 128>(A, plan, st) : launch_dim<C, 256>(A, plan, st);
 }
 
 }  // namespace
 
-void paged_plan(const gdn_paged_problem& p, int* splits, int* split_len) {
-    const int64_t cap = int64_t(p.max_pages) * p.page_size;
-    int64_t most = p.window > 0 && p.window + 16 < cap ? p.window + 16 : cap;  // a range's start goes down to a tile's
-    if (most < 1) most = 1;
+PagedPlan paged_plan(const gdn_paged_problem& p) {
+    const Shape s = shape_of(p);
     const int G = p.Hq / p.Hkv;
-    const int64_t groups = int64_t(p.num_seqs > 0 ? p.num_seqs : 1) * p.Hkv * ((G + 15) / 16);
-    const int64_t slots = 2 * int64_t(sm_count_cached());  // two CTAs run on a multiprocessor at a time
-    // One wave of equal ranges where that gives short ones; else ranges short enough that uneven
-    // sequences leave no long tail, with the number of partial results bounded.
-    int64_t len = (groups * most + slots - 1) / slots;
-    if (len > 2048) len = len / 32 > 512 ? len / 32 : 512;
-    if (len < 256) len = 256;
-    if (len > most) len = most;
-    len = (len + 63) / 64 * 64;
-    *split_len = int(len);
-    *splits = int((most + len - 1) / len);
+    PagedPlan r;
+    r.rows = s.rows;
+    const int blocks = p.Hkv * ((G + s.rows - 1) / s.rows);
+    // Groups of heads: with as many as there are blocks of heads, CTAs next to one another read the same
+    // tokens for different heads at about the same time (a token's heads lie side by side in a page);
+    // fewer where the CTAs could not be dealt out evenly otherwise.
+    const int full = s.ctas * sm_count_cached();
+    r.groups = 1;
+    for (int g = 1; g <= blocks && g <= full; ++g)
+        if (blocks % g == 0 && (full / g * g >= full / r.groups * r.groups || full / g * g * 50 >= full * 49)) r.groups = g;
+    r.heads = blocks / r.groups;
+    // no more CTAs than the problem can have shares of one tile per warp
+    const int64_t cap = int64_t(p.max_pages) * p.page_size, most = p.window > 0 && p.window + 16 < cap ? p.window + 16 : cap;
+    const int64_t tiles = (most / s.tok + 1) * r.heads * p.num_seqs, want = (tiles + s.warps - 1) / s.warps;
+    const int parts = full / r.groups;
+    r.ctas = r.groups * int(want < parts ? (want > 0 ? want : 1) : parts);
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    r.off_ml = up(size_t(p.num_seqs + 1) * sizeof(int64_t));
+    r.off_part = r.off_ml + up(size_t(r.ctas) * 2 * s.rows * sizeof(float2));
+    r.bytes = r.off_part + size_t(r.ctas) * 2 * s.rows * p.D * sizeof(float);
+    return r;
 }
 
 cudaError_t launch_paged(const PagedArgs& A, cudaStream_t st) {
+    const PagedPlan plan = paged_plan(A.p);
     if (A.p.dtype == GDN_FP32)
-        return A.p.D == 64 ? launch_fp32<64>(A, st) : A.p.D == 128 ? launch_fp32<128>(A, st) : launch_fp32<256>(A, st);
-    return A.p.cache_dtype == GDN_BF16 ? launch_type<__nv_bfloat16>(A, st) : launch_type<__nv_fp8_e4m3>(A, st);
+        return A.p.D == 64 ? launch_fp32<64>(A, plan, st) : A.p.D == 128 ? launch_fp32<128>(A, plan, st) : launch_fp32<256>(A, plan, st);
+    return A.p.cache_dtype == GDN_BF16 ? launch_type<__nv_bfloat16>(A, plan, st) : launch_type<__nv_fp8_e4m3>(A, plan, st);
 }
 
 }  // namespace gdn
