@@ -30,6 +30,11 @@ constexpr float PRO_EPS = 1e-6f;
 __device__ __forceinline__ float softplus_f(float x) { return x > 20.f ? x : log1pf(expf(x)); }
 __device__ __forceinline__ float sigmoid_f(float x) { return 1.f / (1.f + expf(-x)); }
 
+// The larger of two magnitudes (signs clear), NaN above all: the order of their bits.
+__device__ __forceinline__ float mag_max(float a, float b) {
+    return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)));
+}
+
 template <typename Op> struct OpTraits;
 template <> struct OpTraits<__nv_bfloat16> {
     static constexpr int PAD = 8;  // 16 bytes: ldmatrix rows land on distinct banks

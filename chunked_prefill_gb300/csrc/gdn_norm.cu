@@ -34,11 +34,6 @@ constexpr int max_threads(int vec, int nv, int lpr, bool backward) {
     return lpr ? ROWS_T : vec == 1 ? (nv == 16 ? 512 : 256) : (backward || (nv == 4 && vec == 8)) ? 512 : 1024;
 }
 
-// The larger of two magnitudes, NaN above all: the order of their bits.
-__device__ __forceinline__ float mag_max(float a, float b) {
-    return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)));
-}
-
 template <bool MAX> __device__ __forceinline__ float join(float a, float b) { return MAX ? mag_max(a, b) : a + b; }
 
 template <bool MAX, int LANES>

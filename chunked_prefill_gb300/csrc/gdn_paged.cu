@@ -20,9 +20,9 @@
 // padding, and the time goes into loading: the first layout here, in which a thread copied the very pieces
 // its fragments need (a warp's lanes spread over 4 to 8 rows), ended at 68 % of the copy bandwidth with the
 // arithmetic taken out.
-// 8-bit values are converted to fp16 (exactly; ldmatrix hands out pairs of bytes, so a value row's bytes
-// are read as 16-byte pieces of 4 tokens and paired by byte permutes), with the query rows scaled by a power of two to
-// [-2, 2] for the fp16 range; the weights are rounded to bf16 (fp16 for 8-bit caches) for the second
+// 8-bit caches: S is a product of 8-bit operands, each query value the sum of two; values are converted to
+// fp16 (exactly; ldmatrix hands out pairs of bytes, so a value row's bytes are read as 16-byte pieces of 4
+// tokens and paired by byte permutes).  The weights are rounded to bf16 (fp16 for 8-bit caches) for the second
 // product, 2^-9 (2^-12) of each on average, while their sum l adds them unrounded in fp32.
 //
 // fp32: k_paged, on the CUDA cores.
@@ -298,10 +298,27 @@ template <> struct Frag<__nv_fp8_e4m3> {
         return *reinterpret_cast<const uint32_t*>(&h);
     }
 };
-// two 8-bit values (the low 16 bits) as fp16
-__device__ __forceinline__ uint32_t f8x2(uint32_t v) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v & 0xffffu), __NV_E4M3);
-    return uint32_t(h.x) | (uint32_t(h.y) << 16);
+// four 8-bit values as two pairs of fp16
+__device__ __forceinline__ void f8x4(uint32_t v, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}\n"
+        : "=r"(lo), "=r"(hi)
+        : "r"(v));
+}
+// the product of 8-bit operands over 32 features
+__device__ __forceinline__ void mma_f8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// x, y, z, w (magnitudes below 448) as four 8-bit values, and what is left of them in their place
+__device__ __forceinline__ uint32_t split_f8(float& x, float& y, float& z, float& w) {
+    const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t b = __nv_cvt_float2_to_fp8x2(make_float2(z, w), __NV_SATFINITE, __NV_E4M3);
+    uint32_t lo, hi;
+    f8x4(a | b << 16, lo, hi);
+    const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&lo)), q = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    x -= p.x, y -= p.y, z -= q.x, w -= q.y;
+    return a | b << 16;
 }
 
 // copy of 16 bytes to shared memory, zeros where !in (the address is not read then)
@@ -352,11 +369,15 @@ __global__ void __launch_bounds__(Tile<C, D>::T, Tile<C, D>::CTAS) k_paged_mma(c
     constexpr int CPR = L::CPR, RPI = L::RPI, ROW = L::ROW, VB = L::VB, VC = L::VC;
     constexpr int VE = VB / L::E;                 // 8-bit: values per piece of a value row
     constexpr int KS = D / 16;                    // k16 steps
+    constexpr int QF = KS;                        // entries of the query fragments (2 per step of 32 with 8 bits)
     constexpr bool F8 = L::E == 1;
+    // fp16 weights are 2^14 e^{z - m}: those down to 2^-38 of the largest count then (2^-24 without; a long
+    // sequence's many small weights add up beside one large one)
+    constexpr float LIFT = F8 ? 14.f : 0.f;
     constexpr bool QS = D == 256;                 // query fragments in shared memory: the registers hold the accumulators
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ float ml_s[W][16][2];
-    __shared__ uint4 q_s[QS ? KS * R2 / 2 : 1][32];
+    __shared__ uint4 q_s[QS ? QF * R2 / 2 : 1][32];
     const gdn_paged_problem& p = A.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int G = p.Hq / p.Hkv, nb = (G + 15) / 16;
@@ -364,10 +385,9 @@ __global__ void __launch_bounds__(Tile<C, D>::T, Tile<C, D>::CTAS) k_paged_mma(c
     // copies: row copy_row + RPI j, piece copy_piece; a row's exchange is that of copy_row and that of RPI j
     const int copy_row = lane / CPR, copy_piece = lane % CPR;
     const uint32_t copy_to = mem + copy_row * ROW + ((copy_piece ^ L::swap(copy_row)) << 4);
-    // key fragments of 16 tokens: bf16, a step's two pieces of tokens 0-7, then of 8-15; 8-bit, a step's one
-    // piece of tokens 0-7 and 8-15, then the next step's
-    const int k_row = (lane & 7) + 8 * (F8 ? lane >> 3 & 1 : lane >> 4);
-    const uint32_t k_at = mem + k_row * ROW + (((F8 ? lane >> 4 : lane >> 3 & 1) ^ L::swap(k_row)) << 4);
+    // key fragments of 16 tokens: two consecutive pieces of tokens 0-7, then of 8-15
+    const int k_row = (lane & 7) + 8 * (lane >> 4);
+    const uint32_t k_at = mem + k_row * ROW + (((lane >> 3 & 1) ^ L::swap(k_row)) << 4);
     // value fragments, bf16: piece c of tokens 0-7 and 8-15, then piece c + 1
     const int v_row = (lane & 7) + 8 * (lane >> 3 & 1);
     const uint32_t v_at = mem + TT * L::BLOCK + v_row * ROW + (((lane >> 4) ^ L::swap(v_row)) << 4);
@@ -477,52 +497,57 @@ __global__ void __launch_bounds__(Tile<C, D>::T, Tile<C, D>::CTAS) k_paged_mma(c
 #pragma unroll
         for (int b = 0; b < TT; ++b) pages[b] = page_at(STAGES - 1, b);
 
-        // ---- query fragments: features 16 s + 2t, + 1 and 16 s + 8 + 2t, + 1 of step s; 8-bit, 16 s + 4t .. + 3
-        alignas(16) uint32_t qf[KS][2 * R2];
+        // ---- query fragments, of 16-feature step s: features 2t, + 1 and 8 + 2t, + 1.  8-bit caches, of
+        // 32-feature step s: features 4t .. 4t + 3 and 16 + 4t .., each value the sum of two 8-bit ones of
+        // the row scaled to [128, 256): exact for bf16's 8 significant bits down to 2^-9 of the row's
+        // largest value (4 bits each, the second with a sign of its own), off by 2^-18 of it below.
+        alignas(16) uint32_t qf[QF][2 * R2];
         float zs[R2];
 #pragma unroll
         for (int r = 0; r < R2; ++r) {
             const int h = hb + g + 8 * r;
             const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(A.q) + n * p.q_stride + int64_t(hk * G + h) * D;
-            uint2 raw[KS];
-#pragma unroll
-            for (int s = 0; s < KS; ++s)
-                raw[s] = h >= G ? make_uint2(0u, 0u)
-                         : F8   ? *reinterpret_cast<const uint2*>(q + 16 * s + 4 * t)
-                                : make_uint2(*reinterpret_cast<const uint32_t*>(q + 16 * s + 2 * t), *reinterpret_cast<const uint32_t*>(q + 16 * s + 8 + 2 * t));
             zs[r] = p.scale * ks * LOG2E;
             if constexpr (F8) {
+                uint2 raw[KS];  // features 16 s + 4t .. + 3
                 float top = 0.f;
-                float2 f[KS][2];
 #pragma unroll
                 for (int s = 0; s < KS; ++s) {
-                    f[s][0] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw[s].x));
-                    f[s][1] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw[s].y));
-                    top = fmaxf(top, fmaxf(fmaxf(fabsf(f[s][0].x), fabsf(f[s][0].y)), fmaxf(fabsf(f[s][1].x), fabsf(f[s][1].y))));
+                    raw[s] = h < G ? *reinterpret_cast<const uint2*>(q + 16 * s + 4 * t) : make_uint2(0u, 0u);
+                    const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw[s].x));
+                    const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw[s].y));
+                    top = mag_max(top, mag_max(mag_max(fabsf(x.x), fabsf(x.y)), mag_max(fabsf(y.x), fabsf(y.y))));
                 }
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const int e = top > 0.f && top < INFINITY ? ilogbf(top) : 0;
-                const float down = ldexpf(1.f, -e);
-                zs[r] = ldexpf(zs[r], e);
+                top = mag_max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = mag_max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const bool fine = top > 0.f && top < INFINITY;
+                const int e = fine ? ilogbf(top) - 7 : 0;
+                const float down = fine ? ldexpf(1.f, -e) : 1.f;
+                // an infinite or NaN query makes every score NaN (as inf - inf does in the definition)
+                const float bad = top < INFINITY ? 0.f : NAN;
+                zs[r] = ldexpf(zs[r], e) + bad;
 #pragma unroll
                 for (int s = 0; s < KS; ++s) {
-                    qf[s][r] = Frag<C>::pack(f[s][0].x * down, f[s][0].y * down);
-                    qf[s][R2 + r] = Frag<C>::pack(f[s][1].x * down, f[s][1].y * down);
+                    float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw[s].x));
+                    float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw[s].y));
+                    x.x *= down, x.y *= down, y.x *= down, y.y *= down;
+                    // step s / 2, features 0-15 or 16-31 of it; HALF: rows 0-7 the first, 8-15 the second values
+                    const uint32_t first = split_f8(x.x, x.y, y.x, y.y), second = split_f8(x.x, x.y, y.x, y.y);
+                    qf[HALF ? s / 2 * 2 + s % 2 : s / 2 * 2][HALF ? 0 : (s % 2) * 2 + r] = first;
+                    qf[HALF ? s / 2 * 2 + s % 2 : s / 2 * 2 + 1][HALF ? 1 : (s % 2) * 2 + r] = second;
                 }
             } else {
 #pragma unroll
                 for (int s = 0; s < KS; ++s) {
-                    qf[s][r] = raw[s].x;
-                    qf[s][R2 + r] = raw[s].y;
+                    qf[s][r] = h < G ? *reinterpret_cast<const uint32_t*>(q + 16 * s + 2 * t) : 0u;
+                    qf[s][R2 + r] = h < G ? *reinterpret_cast<const uint32_t*>(q + 16 * s + 8 + 2 * t) : 0u;
                 }
             }
         }
-
         if constexpr (QS) {
             if (warp == 0)
 #pragma unroll
-                for (int i = 0; i < KS * R2 / 2; ++i) q_s[i][lane] = reinterpret_cast<const uint4*>(&qf[0][0])[i];
+                for (int i = 0; i < QF * R2 / 2; ++i) q_s[i][lane] = reinterpret_cast<const uint4*>(&qf[0][0])[i];
             __syncthreads();
         }
 
@@ -547,7 +572,6 @@ __global__ void __launch_bounds__(Tile<C, D>::T, Tile<C, D>::CTAS) k_paged_mma(c
         };
 
         int stage = 0;
-        alignas(16) uint32_t q2[2][2 * R2];  // with QS: the fragments of two steps
         for (int i = 0; i < tiles; ++i) {
             cp_wait<STAGES - 2>();
             __syncwarp();  // every lane's copies of tile i have landed, and tile i - 1 has been read
@@ -563,31 +587,47 @@ __global__ void __launch_bounds__(Tile<C, D>::T, Tile<C, D>::CTAS) k_paged_mma(c
             }
             const uint32_t kd = k_at + stage * L::BYTES;
             float s[2 * TT][4] = {};  // of 8 tokens each
-            constexpr int SPL = F8 ? 2 : 1;  // steps per ldmatrix
 #pragma unroll
-            for (int c = 0; c < KS / SPL; ++c) {
-                alignas(16) uint32_t qc[2][2 * R2];  // of two steps
+            for (int c = 0; c < KS / 2; ++c) {  // 32 features
+                alignas(16) uint32_t qc[2][2 * R2];
                 if constexpr (QS) {
-                    if (SPL == 2 || c % 2 == 0) {
 #pragma unroll
-                        for (int i = 0; i < R2; ++i) reinterpret_cast<uint4*>(&q2[0][0])[i] = q_s[(SPL == 2 ? c : c / 2) * R2 + i][lane];
-                    }
+                    for (int i = 0; i < R2; ++i) reinterpret_cast<uint4*>(&qc[0][0])[i] = q_s[c * R2 + i][lane];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int e = 0; e < 2 * R2; ++e) qc[i][e] = qf[2 * c + i][e];
                 }
-#pragma unroll
-                for (int i = 0; i < SPL; ++i)
-#pragma unroll
-                    for (int e = 0; e < 2 * R2; ++e) qc[i][e] = QS ? q2[SPL == 2 ? i : c % 2][e] : qf[c * SPL + i][e];
 #pragma unroll
                 for (int b = 0; b < TT; ++b) {
                     uint32_t k[4];
-                    ldmatrix4((kd ^ (c << 5)) + b * L::BLOCK, k);
-                    if constexpr (F8) {
+                    if constexpr (F8) {  // both pieces of tokens 0-7, then of 8-15
+                        ldmatrix4((kd ^ (c << 5)) + b * L::BLOCK, k);
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) mma(s[2 * b + (u & 1)], qc[u >> 1], f8x2(k[u]), f8x2(k[u] >> 16));
+                        for (int u = 0; u < 2; ++u) {
+                            if constexpr (HALF) {
+                                mma_f8(s[2 * b + u], qc[0][0], qc[0][1], qc[1][0], qc[1][1], k[2 * u], k[2 * u + 1]);
+                            } else {
+                                mma_f8(s[2 * b + u], qc[0][0], qc[0][1], qc[0][2], qc[0][3], k[2 * u], k[2 * u + 1]);
+                                mma_f8(s[2 * b + u], qc[1][0], qc[1][1], qc[1][2], qc[1][3], k[2 * u], k[2 * u + 1]);
+                            }
+                        }
                     } else {
-                        mma(s[2 * b], qc[0], k[0], k[1]);
-                        mma(s[2 * b + 1], qc[0], k[2], k[3]);
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            ldmatrix4((kd ^ ((2 * c + u) << 5)) + b * L::BLOCK, k);
+                            mma(s[2 * b], qc[u], k[0], k[1]);
+                            mma(s[2 * b + 1], qc[u], k[2], k[3]);
+                        }
                     }
+                }
+            }
+            if constexpr (F8 && HALF) {  // the two values' products
+#pragma unroll
+                for (int r = 0; r < 2 * TT; ++r) {
+                    s[r][0] += s[r][2];
+                    s[r][1] += s[r][3];
                 }
             }
             // scores in units of log 2: s[r][e] is token 8 r + 2 t + e % 2
@@ -633,7 +673,7 @@ __global__ void __launch_bounds__(Tile<C, D>::T, Tile<C, D>::CTAS) k_paged_mma(c
             uint32_t pf[TT][2 * R2];
 #pragma unroll
             for (int r = 0; r < R2; ++r) {
-                const float sub = m[r] == -INFINITY ? 0.f : m[r];
+                const float sub = m[r] == -INFINITY ? 0.f : m[r] - LIFT;
 #pragma unroll
                 for (int b = 0; b < TT; ++b) {
                     float w[4];
@@ -666,8 +706,11 @@ __global__ void __launch_bounds__(Tile<C, D>::T, Tile<C, D>::CTAS) k_paged_mma(c
                             for (int y = 0; y < 2; ++y) {  // features 4x + 2y, 4x + 2y + 1
                                 const uint32_t lo = __byte_perm(v[0][x], v[1][x], y ? 0x7362 : 0x5140);
                                 const uint32_t hi = __byte_perm(v[2][x], v[3][x], y ? 0x7362 : 0x5140);
-                                mma(acc[c * VE + 4 * x + 2 * y], pf[b], f8x2(lo), f8x2(hi));
-                                mma(acc[c * VE + 4 * x + 2 * y + 1], pf[b], f8x2(lo >> 16), f8x2(hi >> 16));
+                                uint32_t b0[2], b1[2];
+                                f8x4(lo, b0[0], b0[1]);
+                                f8x4(hi, b1[0], b1[1]);
+                                mma(acc[c * VE + 4 * x + 2 * y], pf[b], b0[0], b1[0]);
+                                mma(acc[c * VE + 4 * x + 2 * y + 1], pf[b], b0[1], b1[1]);
                             }
                     }
                 } else {
@@ -694,7 +737,7 @@ __global__ void __launch_bounds__(Tile<C, D>::T, Tile<C, D>::CTAS) k_paged_mma(c
             l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
             l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
             if (t == 0) {
-                ml_s[warp][g + 8 * r][0] = m[r];
+                ml_s[warp][g + 8 * r][0] = m[r] - LIFT;
                 ml_s[warp][g + 8 * r][1] = l[r];
             }
 #pragma unroll
