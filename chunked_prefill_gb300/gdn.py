@@ -519,32 +519,26 @@ def chunk_gated_delta_rule(q, k, v, g, beta, scale=None, initial_state=None,
 
 
 # ---------------------------------------------------------------------------- decoding
-def _need(ok, msg):
-    if not ok:
-        raise ValueError(msg)
+# The checks and the marshalling of these calls are native (csrc/binding.cpp): a decoding step is
+# made of many calls that take a few microseconds on the GPU.
+_native = None
 
 
-def _need_cuda(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and (not t.is_cuda or t.device != device):
-            raise ValueError(f"{name} must be a CUDA tensor on {device}")
-
-
-def _token_stride(name, t, inner):
-    """Elements from one token to the next of a [B, T, ...] tensor whose last dimensions are
-    contiguous (`inner` values) and whose tokens lie at one stride."""
-    shape, st = t.shape, t.stride()
-    want = 1
-    for d in range(t.dim() - 1, 1, -1):
-        _need(shape[d] == 1 or st[d] == want, f"the heads and features of {name} must be contiguous")
-        want *= shape[d]
-    B, T = shape[0], shape[1]
-    if B * T <= 1:
-        return inner
-    if T == 1:
-        return st[0]
-    _need(B == 1 or st[0] == T * st[1], f"the tokens of {name} must lie at one stride")
-    return st[1]
+def _binding():
+    """Load _binding.so (built in-tree next to libgdn.so) and hand it the library's functions."""
+    global _native
+    if _native is None:
+        L = lib()
+        path = os.path.join(_HERE, "_binding.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with "
+                               "`python -m chunked_prefill_gb300.build` (no fallback exists)")
+        from chunked_prefill_gb300 import _binding as B
+        B.bind(*(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
+            "gdn_recurrent_step", "gdn_paged_attn_workspace_size", "gdn_paged_attn_decode",
+            "gdn_rmsnorm_fwd", "gdn_rmsnorm_bwd_workspace_size", "gdn_rmsnorm_bwd")), _check)
+        _native = B
+    return _native
 
 
 def gdn_recurrent_step(q, k, v, g, beta, scale, state_in=None, state_out=None, slots=None,
@@ -553,61 +547,8 @@ def gdn_recurrent_step(q, k, v, g, beta, scale, state_in=None, state_out=None, s
     g, beta [B,T,Hv] fp32, each with contiguous rows at any token stride; state_in, state_out
     [num_slots,Hv,K,V] fp32 pools; slots int32 [num_seqs]; cu_seqlens int32 [num_seqs+1] with
     B = 1, else B sequences of T tokens.  Returns o [B,T,Hv,V]."""
-    _need(q.dim() == 4 and k.shape == q.shape and v.dim() == 4 and v.shape[:2] == q.shape[:2]
-          and v.shape[2] > 0 and q.shape[2] > 0, "q and k must be [B,T,Hqk,K] and v [B,T,Hv,V]")
-    _need(k.dtype == q.dtype and v.dtype == q.dtype, "q, k and v must match in dtype")
-    B, T, Hqk, K = q.shape
-    Hv, V = v.shape[2:]
-    _need(g.shape == (B, T, Hv) and beta.shape == g.shape, "g and beta must be [B,T,Hv]")
-    _need(g.dtype == torch.float32 and beta.dtype == torch.float32, "g and beta must be float32")
-    _need_cuda(q.device, q=q, k=k, v=v, g=g, beta=beta, state_in=state_in, state_out=state_out,
-               slots=slots, cu_seqlens=cu_seqlens, A_log=A_log, dt_bias=dt_bias, o=o)
-    n = B
-    if cu_seqlens is not None:
-        _need(B == 1, "cu_seqlens needs B == 1")
-        _need(cu_seqlens.dtype == torch.int32 and cu_seqlens.dim() == 1 and cu_seqlens.numel() >= 1
-              and cu_seqlens.is_contiguous(), "cu_seqlens must be a contiguous int32 [num_seqs+1]")
-        n = cu_seqlens.numel() - 1
-    if slots is not None:
-        _need(slots.dtype == torch.int32 and slots.shape == (n,) and slots.is_contiguous(),
-              "slots must be a contiguous int32 [num_seqs]")
-    num_slots = n
-    for name, pool in (("state_in", state_in), ("state_out", state_out)):
-        if pool is None:
-            continue
-        _need(pool.dtype == torch.float32 and pool.dim() == 4 and pool.shape[1:] == (Hv, K, V)
-              and pool.is_contiguous(), f"{name} must be a contiguous float32 [num_slots,Hv,K,V]")
-        num_slots = pool.shape[0]
-    if state_in is not None and state_out is not None:
-        _need(state_in.shape == state_out.shape, "state_in and state_out must have the same slots")
-    _need(slots is not None or num_slots >= n, f"{num_slots} slots for {n} sequences")
-    for name, t in (("A_log", A_log), ("dt_bias", dt_bias)):
-        _need(t is None or (t.dtype == torch.float32 and t.shape == (Hv,) and t.is_contiguous()),
-              f"{name} must be a contiguous float32 [Hv]")
-    if o is None:
-        o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
-    else:
-        _need(o.shape == v.shape and o.dtype == v.dtype and o.is_contiguous(),
-              "o must be contiguous and match v")
-    p = GdnStepProblem(n, B * T, Hqk, Hv, K, V, _dtype_code(q.dtype), scale,
-                       None if cu_seqlens is None else cu_seqlens.data_ptr(),
-                       None if slots is None else slots.data_ptr(), num_slots,
-                       _token_stride("q", q, Hqk * K), _token_stride("k", k, Hqk * K),
-                       _token_stride("v", v, Hv * V), _token_stride("g", g, Hv),
-                       _token_stride("beta", beta, Hv))
-    _check(lib().gdn_recurrent_step(ctypes.byref(p), q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                    g.data_ptr(), beta.data_ptr(), _addr(A_log), _addr(dt_bias),
-                                    _addr(state_in), _addr(state_out), o.data_ptr(),
-                                    _stream_of(q, stream)))
-    return o
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _stream_of(t, stream):
-    return (torch.cuda.current_stream(t.device) if stream is None else stream).cuda_stream
+    return (_native or _binding()).step(q, k, v, g, beta, scale, state_in, state_out, slots,
+                                        cu_seqlens, A_log, dt_bias, o, stream)
 
 
 def gated_delta_rule_step(q, k, v, g, beta, scale=None, state=None, state_out=None, slots=None,
@@ -622,26 +563,26 @@ def gated_delta_rule_step(q, k, v, g, beta, scale=None, state=None, state_out=No
     which slot each sequence has (None: its own index; -1: a padding row, whose o is 0).
     cu_seqlens int32 [N+1] (device, B = 1) packs sequences of different token counts.  For
     inference: nothing is differentiated here."""
-    if torch.is_grad_enabled():
-        for name, t in (("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta), ("state", state)):
-            if t is not None and t.requires_grad:
-                raise RuntimeError(f"gated_delta_rule_step is not differentiable, but {name} requires a "
-                                   "gradient: train with chunk_gated_delta_rule")
+    if stream is not None:  # what is allocated here belongs to that stream, too
+        with torch.cuda.stream(stream):
+            return gated_delta_rule_step(q, k, v, g, beta, scale, state, state_out, slots, cu_seqlens,
+                                         A_log, dt_bias, o)
+    native = _native or _binding()
+    if native.wants_grad(q, k, v, g, beta, state):
+        raise RuntimeError("gated_delta_rule_step is not differentiable, but an argument requires a "
+                           "gradient: train with chunk_gated_delta_rule")
     if scale is None:
         scale = q.shape[-1] ** -0.5
     if state_out is None:
         state_out = state
         if state is None:
+            if slots is not None:
+                raise ValueError("slots need a state pool (state or state_out)")
             n = q.shape[0] if cu_seqlens is None else cu_seqlens.numel() - 1
-            _need(slots is None, "slots need a state pool (state or state_out)")
             state_out = torch.empty(n, v.shape[2], q.shape[-1], v.shape[-1], dtype=torch.float32,
                                     device=q.device)
-    o = gdn_recurrent_step(q, k, v, g, beta, scale, state, state_out, slots, cu_seqlens, A_log,
-                           dt_bias, o, stream)
-    return o, state_out
-
-
-_CACHE_CODE = {torch.bfloat16: GDN_BF16, torch.float32: GDN_FP32, torch.float8_e4m3fn: GDN_E4M3}
+    return native.step(q, k, v, g, beta, scale, state, state_out, slots, cu_seqlens, A_log, dt_bias,
+                       o, None), state_out
 
 
 def gdn_paged_attn_decode(q, k_cache, v_cache, page_table, seq_lens, scale, k_new=None, v_new=None,
@@ -649,60 +590,8 @@ def gdn_paged_attn_decode(q, k_cache, v_cache, page_table, seq_lens, scale, k_ne
                           stream=None):
     """Paged decode attention through the C ABI (see include/gdn.h).  Returns o; lse is written
     when given."""
-    _need(q.dim() == 3 and k_cache.dim() == 4 and v_cache.shape == k_cache.shape,
-          "q must be [N,Hq,D], k_cache and v_cache [num_pages,page_size,Hkv,D]")
-    N, Hq, D = q.shape
-    pages, page_size, Hkv = k_cache.shape[:3]
-    _need(k_cache.shape[3] == D, "q and the caches must match in D")
-    _need(v_cache.dtype == k_cache.dtype and k_cache.dtype in _CACHE_CODE,
-          "k_cache and v_cache must both be bfloat16, float32 or float8_e4m3fn")
-    _need_cuda(q.device, q=q, k_cache=k_cache, v_cache=v_cache, page_table=page_table,
-               seq_lens=seq_lens, k_new=k_new, v_new=v_new, k_scale=k_scale, v_scale=v_scale, o=o,
-               lse=lse, workspace=workspace)
-    _need(page_table.dtype == torch.int32 and page_table.dim() == 2 and page_table.shape[0] == N
-          and (page_table.shape[1] <= 1 or page_table.stride(1) == 1),
-          "page_table must be int32 [N,max_pages] with contiguous rows")
-    _need(seq_lens.dtype == torch.int32 and seq_lens.shape == (N,) and seq_lens.is_contiguous(),
-          "seq_lens must be a contiguous int32 [N]")
-    _need((k_new is None) == (v_new is None), "k_new and v_new go together")
-    for name, t in (("q", q), ("k_new", k_new), ("v_new", v_new)):
-        if t is not None:
-            heads = Hq if t is q else Hkv
-            _need(t.shape == (N, heads, D) and t.dtype == q.dtype,
-                  f"{name} must be [N,{heads},D] of q's dtype")
-            _need(t.stride(2) == 1 and (heads == 1 or t.stride(1) == D),
-                  f"the heads and features of {name} must be contiguous")
-    new_stride = 0
-    if k_new is not None and N > 1:
-        new_stride = k_new.stride(0)
-        _need(v_new.stride(0) == new_stride, "k_new and v_new must have the same row stride")
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        _need(t is None or (t.dtype == torch.float32 and t.shape == (Hkv,) and t.is_contiguous()),
-              f"{name} must be a contiguous float32 [Hkv]")
-    ks, vs = k_cache.stride(), v_cache.stride()
-    _need(ks[3] == 1 and vs[3] == 1, "the features of the caches must be contiguous")
-    if o is None:
-        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    else:
-        _need(o.shape == q.shape and o.dtype == q.dtype and o.is_contiguous(),
-              "o must be contiguous and match q")
-    _need(lse is None or (lse.shape == (N, Hq) and lse.dtype == torch.float32 and lse.is_contiguous()),
-          "lse must be a contiguous float32 [N,Hq]")
-    p = GdnPagedProblem(N, Hq, Hkv, D, _dtype_code(q.dtype), _CACHE_CODE[k_cache.dtype], scale, window,
-                        page_size, page_table.shape[1], pages, q.stride(0) if N > 1 else 0, new_stride,
-                        page_table.stride(0) if N > 1 else 0, *ks[:3], *vs[:3])
-    L, ref = lib(), ctypes.byref(p)
-    need = ctypes.c_size_t(0)
-    _check(L.gdn_paged_attn_workspace_size(ref, ctypes.byref(need)))
-    if need.value:
-        workspace = _workspace(need.value, q.device, workspace)
-    _check(L.gdn_paged_attn_decode(ref, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                                   page_table.data_ptr(), seq_lens.data_ptr(), _addr(k_new), _addr(v_new),
-                                   _addr(k_scale), _addr(v_scale), o.data_ptr(), _addr(lse),
-                                   workspace.data_ptr() if need.value else None,
-                                   workspace.numel() * workspace.element_size() if need.value else 0,
-                                   _stream_of(q, stream)))
-    return o
+    return (_native or _binding()).paged(q, k_cache, v_cache, page_table, seq_lens, scale, k_new,
+                                         v_new, k_scale, v_scale, window, o, lse, workspace, stream)
 
 
 def paged_attention_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None, k_new=None,
@@ -715,76 +604,36 @@ def paged_attention_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None
     e4m3 (with fp32 scales [Hkv]) under bf16 queries, fp32 under fp32 ones; page_table int32
     [N,max_pages]; seq_lens int32 [N], the new token counted.  k_new, v_new [N,Hkv,D]: the new
     token's key and value, which the call then writes to position seq_lens - 1 of the caches
-    before it attends to them.  window > 0 attends to the last `window` tokens."""
-    if torch.is_grad_enabled() and (q.requires_grad or (k_new is not None and k_new.requires_grad)
-                                    or (v_new is not None and v_new.requires_grad)):
-        raise RuntimeError("paged_attention_decode is not differentiable")
+    before it attends to them.  window > 0 attends to the last `window` tokens.  For inference:
+    nothing is differentiated here."""
+    if stream is not None:  # what is allocated here belongs to that stream, too
+        with torch.cuda.stream(stream):
+            return paged_attention_decode(q, k_cache, v_cache, page_table, seq_lens, scale, k_new, v_new,
+                                          k_scale, v_scale, window, return_lse, o, workspace)
+    native = _native or _binding()
+    if native.wants_grad(q, k_new, v_new):
+        raise RuntimeError("paged_attention_decode is not differentiable, but an argument requires "
+                           "a gradient")
     if scale is None:
         scale = q.shape[-1] ** -0.5
     lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if return_lse else None
-    o = gdn_paged_attn_decode(q, k_cache, v_cache, page_table, seq_lens, scale, k_new, v_new, k_scale,
-                              v_scale, window, o, lse, workspace, stream)
+    o = native.paged(q, k_cache, v_cache, page_table, seq_lens, scale, k_new, v_new, k_scale,
+                     v_scale, window, o, lse, workspace, None)
     return (o, lse) if return_lse else o
-
-
-def _norm_rows(name, t, like=None):
-    """The elements between the rows of a [..., dim] tensor (0: contiguous)."""
-    if like is not None:
-        _need(t.shape == like.shape and t.dtype == like.dtype, f"{name} must match the rows in shape and dtype")
-    if t.is_contiguous():
-        return 0
-    _need(t.dim() == 2 and t.stride(1) == 1, f"{name} must be contiguous, or two-dimensional with contiguous rows")
-    return t.stride(0) if t.shape[0] > 1 else 0
-
-
-def _norm_problem(x, weight, eps, weight_offset):
-    _need(x.dim() >= 1 and x.shape[-1] > 0, "rows must be [..., dim]")
-    dim = x.shape[-1]
-    _need(weight.shape == (dim,) and weight.is_contiguous(), "weight must be a contiguous [dim]")
-    code = _dtype_code(x.dtype)
-    return GdnNormProblem(x.numel() // dim, dim, code, _dtype_code(weight.dtype), code, 0, eps, weight_offset)
 
 
 def gdn_rmsnorm_fwd(x, weight, residual=None, eps=1e-6, weight_offset=0.0, quant=False, group=0,
                     want_sum=True, stream=None):
     """Norm with the residual's addition through the C ABI (see include/gdn.h).  Returns
     (y, y_scale, sum): y_scale is None without quant, sum None without a residual (or want_sum)."""
-    _need_cuda(x.device, x=x, weight=weight, residual=residual)
-    p = _norm_problem(x, weight, eps, weight_offset)
-    p.x_stride = _norm_rows("x", x)
-    total = scale = None
-    if residual is not None:
-        p.residual_stride = _norm_rows("residual", residual, x)
-        if want_sum:
-            total = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    if quant:
-        _need(group >= 0 and (group == 0 or p.dim % group == 0), "group must be 0 or divide dim")
-        p.out_dtype, p.group = GDN_E4M3, group
-        scale = torch.empty(*x.shape[:-1], p.dim // group if group else 1, dtype=torch.float32, device=x.device)
-    y = torch.empty(x.shape, dtype=torch.float8_e4m3fn if quant else x.dtype, device=x.device)
-    _check(lib().gdn_rmsnorm_fwd(ctypes.byref(p), x.data_ptr(), _addr(residual), weight.data_ptr(),
-                                 y.data_ptr(), _addr(scale), _addr(total), _stream_of(x, stream)))
-    return y, scale, total
+    return (_native or _binding()).norm_fwd(x, weight, residual, eps, weight_offset, quant, group,
+                                            want_sum, stream)
 
 
 def gdn_rmsnorm_bwd(s, weight, dy, dsum=None, eps=1e-6, weight_offset=0.0, workspace=None, stream=None):
     """Gradients of the norm at its summed input s: (dx, dweight fp32).  dsum is the gradient
     with respect to the sum (None: zero)."""
-    _need_cuda(s.device, s=s, weight=weight, dy=dy, dsum=dsum, workspace=workspace)
-    p = _norm_problem(s, weight, eps, weight_offset)
-    p.x_stride, p.dy_stride = _norm_rows("s", s), _norm_rows("dy", dy, s)
-    if dsum is not None:
-        p.dsum_stride = _norm_rows("dsum", dsum, s)
-    dx = torch.empty(s.shape, dtype=s.dtype, device=s.device)
-    dw = torch.empty(p.dim, dtype=torch.float32, device=s.device)
-    L, ref = lib(), ctypes.byref(p)
-    need = ctypes.c_size_t(0)
-    _check(L.gdn_rmsnorm_bwd_workspace_size(ref, ctypes.byref(need)))
-    ws = _workspace(need.value, s.device, workspace)
-    _check(L.gdn_rmsnorm_bwd(ref, s.data_ptr(), weight.data_ptr(), dy.data_ptr(), _addr(dsum),
-                             dx.data_ptr(), dw.data_ptr(), ws.data_ptr(),
-                             ws.numel() * ws.element_size(), _stream_of(s, stream)))
-    return dx, dw
+    return (_native or _binding()).norm_bwd(s, weight, dy, dsum, eps, weight_offset, workspace, stream)
 
 
 class _RMSNorm(torch.autograd.Function):
@@ -813,10 +662,10 @@ def rms_norm(x, weight, residual=None, eps=1e-6, weight_offset=0.0):
     + eps) * (weight + weight_offset) over the last dimension.  Returns (y, s), s None without a
     residual.  x, residual [..., dim] bf16 or fp32; weight [dim] bf16 or fp32.  Differentiable with
     respect to x, residual and weight (the backward pass takes s as it was rounded)."""
-    if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad
-                                    or (residual is not None and residual.requires_grad)):
+    native = _native or _binding()
+    if native.wants_grad(x, weight, residual):
         return _RMSNorm.apply(x, weight, residual, eps, weight_offset)
-    y, _, total = gdn_rmsnorm_fwd(x, weight, residual, eps, weight_offset)
+    y, _, total = native.norm_fwd(x, weight, residual, eps, weight_offset, False, 0, True, None)
     return y, total
 
 
@@ -824,4 +673,5 @@ def rms_norm_quant(x, weight, residual=None, eps=1e-6, weight_offset=0.0, group=
     """rms_norm with y in 8 bits (float8_e4m3fn): returns (y, scale, s) with the normed row
     approximately y * scale; scale fp32 [..., 1], or [..., dim / group] with one scale to `group`
     consecutive values."""
-    return gdn_rmsnorm_fwd(x, weight, residual, eps, weight_offset, quant=True, group=group)
+    return (_native or _binding()).norm_fwd(x, weight, residual, eps, weight_offset, True, group,
+                                            True, None)
