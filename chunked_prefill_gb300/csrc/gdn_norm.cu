@@ -18,9 +18,14 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <map>
+#include <mutex>
+#include <tuple>
+
 #include "gdn_common.cuh"
 #include "gdn_decode.h"
 #include "gdn_internal.h"
+#include "tc05.cuh"
 
 namespace gdn {
 namespace {
@@ -31,7 +36,7 @@ constexpr int ROWS_T = 256;                 // threads of a CTA of the lane-grou
 constexpr int LOOP_T = 512;                 // threads of the looping kernels
 // Threads of a CTA at most, so that a row's values fit the registers that many threads leave each.
 constexpr int max_threads(int vec, int nv, int lpr, bool backward) {
-    return lpr ? ROWS_T : vec == 1 ? (nv == 16 ? 512 : 256) : (backward || (nv == 4 && vec == 8)) ? 512 : 1024;
+    return lpr ? ROWS_T : vec == 1 ? (nv == 16 ? 512 : 256) : (backward || nv >= 2) ? 512 : 1024;
 }
 
 template <bool MAX> __device__ __forceinline__ float join(float a, float b) { return MAX ? mag_max(a, b) : a + b; }
@@ -115,12 +120,12 @@ __device__ __forceinline__ void store8(uint8_t* p, const float (&y)[VEC], float 
     }
 }
 
-__device__ __forceinline__ float scale_of(float mag) { return mag_max(mag / F8_MAX, F8_TINY); }
+__device__ __forceinline__ float scale_of(float mag) { return mag_max(mag * (1.f / F8_MAX), F8_TINY); }
 
 // OUT8: 0 dtype out; 1 one scale per row; 2 groups of 2^n <= 32 lanes' vectors; 3 other groups
 // (magnitudes by shared-memory maxima, whose order does not matter).
 template <typename T, int VEC, int NV, int LPR, int OUT8>
-__global__ void __launch_bounds__(max_threads(VEC, NV, LPR, false)) k_norm_fwd(const NormArgs A) {
+__global__ void __launch_bounds__(max_threads(VEC, NV, LPR, false), LPR == 0 && VEC > 1 && NV == 2 ? 4 : 1) k_norm_fwd(const NormArgs A) {
     const gdn_norm_problem& p = A.p;
     __shared__ float red[2][32];
     extern __shared__ uint32_t mags[];  // OUT8 == 3: per group of the CTA's row(s)
@@ -201,20 +206,22 @@ __global__ void __launch_bounds__(max_threads(VEC, NV, LPR, false)) k_norm_fwd(c
             for (int k = 1; k < NV; ++k) mag[0] = mag_max(mag[0], mag[k]);
             const float sc = scale_of(row_red<true, LPR>(mag[0], red[1]));
             if (live && at0 == 0) scales[0] = sc;
-            const float inv = 1.f / sc;
+            const float inv = __frcp_rn(sc);
 #pragma unroll
             for (int k = 0; k < NV; ++k)
                 if (live && at0 + k * step < nvec) store8<VEC>(y + int64_t(at0 + k * step) * VEC, s[k], inv);
         } else if constexpr (OUT8 == 2) {
-            const int lanes = p.group / VEC;  // 2^n lanes hold a group, at a multiple of 2^n
+            const int lanes = p.group / VEC, shift = __ffs(lanes) - 1;  // 2^shift lanes hold a group, at a multiple of 2^shift
+            for (int o = lanes / 2; o > 0; o >>= 1)
+#pragma unroll
+                for (int k = 0; k < NV; ++k) mag[k] = mag_max(mag[k], __shfl_xor_sync(0xffffffffu, mag[k], o));
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                for (int o = lanes / 2; o > 0; o >>= 1) mag[k] = mag_max(mag[k], __shfl_xor_sync(0xffffffffu, mag[k], o));
                 const int j = at0 + k * step;
                 if (live && j < nvec) {
                     const float sc = scale_of(mag[k]);
-                    if ((j & (lanes - 1)) == 0) scales[j / lanes] = sc;
-                    store8<VEC>(y + int64_t(j) * VEC, s[k], 1.f / sc);
+                    if ((j & (lanes - 1)) == 0) scales[j >> shift] = sc;
+                    store8<VEC>(y + int64_t(j) * VEC, s[k], __frcp_rn(sc));
                 }
             }
         } else {
@@ -239,7 +246,7 @@ __global__ void __launch_bounds__(max_threads(VEC, NV, LPR, false)) k_norm_fwd(c
                         const int i = j * VEC + e, g = i / p.group;
                         const float sc = scale_of(__uint_as_float(m[g])), one[1] = {s[k][e]};
                         if (i % p.group == 0) scales[g] = sc;
-                        store8<1>(y + i, one, 1.f / sc);
+                        store8<1>(y + i, one, __frcp_rn(sc));
                     }
                 }
             }
@@ -254,6 +261,7 @@ __global__ void __launch_bounds__(max_threads(VEC, NV, LPR, true)) k_norm_bwd(co
     const int tid = threadIdx.x, step = LPR ? LPR : blockDim.x, at0 = LPR ? tid % step : tid;
     const int per = LPR ? int(blockDim.x) / step : 1, mine = LPR ? tid / step : 0;
     const int nvec = p.dim / VEC;
+    tc::pdl_launch_dependents();
     constexpr bool KEEP = NV * VEC < 32;  // the weights stay in registers (else: read again, from L1)
     float w[KEEP ? NV : 1][VEC], dw[NV][VEC];
 #pragma unroll
@@ -264,23 +272,35 @@ __global__ void __launch_bounds__(max_threads(VEC, NV, LPR, true)) k_norm_bwd(co
     }
     const float inv_dim = 1.f / float(p.dim);
     int turn = 0;
-    // every lane of a warp takes part in the shuffles of every turn
-    for (int64_t row0 = int64_t(blockIdx.x) * per; row0 < p.rows; row0 += int64_t(gridDim.x) * per, turn ^= 1) {
-        const int64_t row = row0 + mine;
-        const bool live = row < p.rows;
+    // the next row of this thread's lanes is requested before the present one is reduced, where it fits
+    constexpr bool AHEAD = NV * VEC < 16 || (VEC == 8 && NV == 2);
+    Vec<T, VEC> xn[NV], dn[NV], sn[NV];
+    const int64_t hop = int64_t(gridDim.x) * per;
+    auto fetch = [&](int64_t row) {
+        if (row >= p.rows) return;
         const T* x = static_cast<const T*>(A.x) + row * p.x_stride;
         const T* dy = static_cast<const T*>(A.dy) + row * p.dy_stride;
         const T* ds = static_cast<const T*>(A.dsum) + row * p.dsum_stride;
-        Vec<T, VEC> xv[NV], dv[NV], sv[NV];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int j = at0 + k * step;
-            if (live && j < nvec) {
-                xv[k].load(x + int64_t(j) * VEC);
-                dv[k].load(dy + int64_t(j) * VEC);
-                if (A.dsum) sv[k].load(ds + int64_t(j) * VEC);
+            if (j < nvec) {
+                xn[k].load(x + int64_t(j) * VEC);
+                dn[k].load(dy + int64_t(j) * VEC);
+                if (A.dsum) sn[k].load(ds + int64_t(j) * VEC);
             }
         }
+    };
+    if (AHEAD) fetch(int64_t(blockIdx.x) * per + mine);
+    // every lane of a warp takes part in the shuffles of every turn
+    for (int64_t row0 = int64_t(blockIdx.x) * per; row0 < p.rows; row0 += hop, turn ^= 1) {
+        const int64_t row = row0 + mine;
+        const bool live = row < p.rows;
+        if (!AHEAD) fetch(row);
+        Vec<T, VEC> xv[NV], dv[NV], sv[NV];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) xv[k] = xn[k], dv[k] = dn[k], sv[k] = sn[k];
+        if (AHEAD) fetch(row + hop);
         float ss = 0.f, c = 0.f;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
@@ -352,20 +372,25 @@ __global__ void __launch_bounds__(max_threads(VEC, NV, LPR, true)) k_norm_bwd(co
     }
 }
 
-// dweight from the CTAs' shares: 32 columns by 32 runs of consecutive shares, the runs then added in order.
-__global__ void __launch_bounds__(1024) k_norm_dw(const float* part, int parts, int dim, float* dw) {
-    __shared__ float run[32][33];
-    const int c = threadIdx.x & 31, y = threadIdx.x >> 5, i = blockIdx.x * 32 + c;
-    const int per = (parts + 31) / 32, b1 = min(parts, (y + 1) * per);
+// dweight from the CTAs' shares: 16 columns by 64 runs of consecutive shares, the runs then added in a
+// tree of fixed shape.
+constexpr int DW_C = 16, DW_R = 64;
+__global__ void __launch_bounds__(DW_C * DW_R) k_norm_dw(const float* part, int parts, int dim, float* dw) {
+    __shared__ float run[DW_R][DW_C];
+    const int c = threadIdx.x % DW_C, y = threadIdx.x / DW_C, i = blockIdx.x * DW_C + c;
+    const int per = (parts + DW_R - 1) / DW_R, b1 = min(parts, (y + 1) * per);
     float t = 0.f;
+    tc::pdl_wait();
     if (i < dim)
+#pragma unroll 8
         for (int b = y * per; b < b1; ++b) t += part[int64_t(b) * dim + i];
     run[y][c] = t;
-    __syncthreads();
-    if (y == 0 && i < dim) {
-        for (int k = 1; k < 32; ++k) t += run[k][c];
-        dw[i] = t;
+#pragma unroll
+    for (int o = DW_R / 2; o > 0; o >>= 1) {
+        __syncthreads();
+        if (y < o) run[y][c] += run[y + o][c];
     }
+    if (y == 0 && i < dim) dw[i] = run[0][c];
 }
 
 // ---- rows too long for the registers: value by value, a row read again (from L2) per phase
@@ -397,7 +422,7 @@ __global__ void __launch_bounds__(LOOP_T) k_norm_fwd_loop(const NormArgs A) {
             if (threadIdx.x == 0) A.y_scale[row * groups + g] = sc;
             for (int i = threadIdx.x; i < group; i += LOOP_T) {
                 const float one[1] = {y_at(g * group + i)};
-                store8<1>(static_cast<uint8_t*>(A.y) + row * p.dim + g * group + i, one, 1.f / sc);
+                store8<1>(static_cast<uint8_t*>(A.y) + row * p.dim + g * group + i, one, __frcp_rn(sc));
             }
         }
         __syncthreads();  // sum may be x or residual, which other threads have read above
@@ -411,6 +436,7 @@ __global__ void __launch_bounds__(LOOP_T) k_norm_fwd_loop(const NormArgs A) {
 
 template <typename T>
 __global__ void __launch_bounds__(LOOP_T) k_norm_bwd_loop(const NormArgs A) {
+    tc::pdl_launch_dependents();
     const gdn_norm_problem& p = A.p;
     __shared__ float red[2][32];
     float* part = A.part + int64_t(blockIdx.x) * p.dim;
@@ -442,7 +468,7 @@ struct Layout {
     int per() const { return lpr ? threads / lpr : 1; }
 };
 bool wide(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-Layout layout_of(int dim, int full, bool vectors, bool backward) {
+Layout layout_of(int64_t rows, int dim, int full, bool vectors, bool backward) {
     Layout L{vectors ? full : 1, 1, 0, ROWS_T};
     const int n = dim / L.vec;
     if (n <= 32) {
@@ -454,9 +480,12 @@ Layout layout_of(int dim, int full, bool vectors, bool backward) {
         L.nv = n <= 64 ? 2 : 4;
         return L;
     }
-    // a CTA per row: two vectors a thread while 1024 threads hold the row so, else more
+    // a CTA per row: two vectors a thread while its threads hold the row so, else more.  Rows that leave
+    // multiprocessors free take one, for the shorter way through the kernel (16 rows of 2048: 2.5 us
+    // instead of 2.9; 8191 rows of 5120: 62 us instead of 53).
+    const bool few = rows <= sm_count_cached();
     const int most = L.vec == 1 ? 16 : 4;
-    for (L.nv = 2; L.nv <= most; L.nv *= 2) {
+    for (L.nv = L.vec == 1 ? 2 : few ? 1 : 2; L.nv <= most; L.nv *= 2) {
         L.threads = ((n + L.nv - 1) / L.nv + 31) / 32 * 32;
         if (L.threads <= max_threads(L.vec, L.nv, 0, backward)) return L;
     }
@@ -466,6 +495,18 @@ Layout layout_of(int dim, int full, bool vectors, bool backward) {
 }
 
 int full_vec(int dtype) { return dtype == GDN_BF16 ? 8 : 4; }
+
+// CTAs of a kernel that a multiprocessor holds (looked up once per kernel, device and launch shape).
+int resident(const void* kern, int threads, size_t smem) {
+    static std::mutex mu;
+    static std::map<std::tuple<const void*, int, int, size_t>, int> known;
+    int dev = 0, n = 1;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+    std::lock_guard<std::mutex> lock(mu);
+    auto& r = known[{kern, dev, threads, smem}];
+    if (r == 0) r = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, smem) == cudaSuccess && n > 0 ? n : 1;
+    return r;
+}
 
 template <int OUT8, typename T, int VEC, int NV, int LPR>
 cudaError_t fwd_launch(const NormArgs& A, const Layout& L, cudaStream_t st) {
@@ -489,8 +530,10 @@ cudaError_t fwd_out(const NormArgs& A, const Layout& L, cudaStream_t st) {
 }
 
 template <typename T, int VEC, int NV, int LPR>
-cudaError_t bwd_out(const NormArgs& A, const Layout& L, int parts, cudaStream_t st) {
+cudaError_t bwd_out(const NormArgs& A, const Layout& L, int& parts, cudaStream_t st) {
     const size_t smem = LPR ? size_t(L.per()) * A.p.dim * 4 : 0;
+    const int fit = resident(reinterpret_cast<const void*>(k_norm_bwd<T, VEC, NV, LPR>), L.threads, smem) * sm_count_cached();
+    if (parts > fit) parts = fit;  // one wave: the rows are dealt out to the CTAs in turn
     k_norm_bwd<T, VEC, NV, LPR><<<parts, L.threads, smem, st>>>(A);
     return cudaGetLastError();
 }
@@ -504,6 +547,7 @@ cudaError_t bwd_out(const NormArgs& A, const Layout& L, int parts, cudaStream_t 
             if (L.lpr == 32 && L.nv == 1) return F<T, FULL, 1, 32>(__VA_ARGS__);    \
             if (L.lpr == 32 && L.nv == 2) return F<T, FULL, 2, 32>(__VA_ARGS__);    \
             if (L.lpr == 32) return F<T, FULL, 4, 32>(__VA_ARGS__);                 \
+            if (L.nv == 1) return F<T, FULL, 1, 0>(__VA_ARGS__);                    \
             if (L.nv == 2) return F<T, FULL, 2, 0>(__VA_ARGS__);                    \
             return F<T, FULL, 4, 0>(__VA_ARGS__);                                   \
         }                                                                           \
@@ -524,7 +568,7 @@ cudaError_t fwd_type(const NormArgs& A, cudaStream_t st) {
     const int full = full_vec(p.dtype);
     const bool vectors = p.dim % full == 0 && p.x_stride % full == 0 && p.residual_stride % full == 0 && wide(A.x) && wide(A.residual) &&
                          wide(A.weight) && wide(A.y) && wide(A.sum);
-    const Layout L = layout_of(p.dim, full, vectors, false);
+    const Layout L = layout_of(p.rows, p.dim, full, vectors, false);
     if (L.vec == 0) {
         k_norm_fwd_loop<T><<<unsigned(p.rows), LOOP_T, 0, st>>>(A);
         return cudaGetLastError();
@@ -534,13 +578,13 @@ cudaError_t fwd_type(const NormArgs& A, cudaStream_t st) {
 
 int parts_of(const gdn_norm_problem& p, const Layout& L) {
     const int64_t groups = (p.rows + L.per() - 1) / L.per();
-    int64_t most = int64_t(sm_count_cached()) * (1024 / L.threads > 0 ? 1024 / L.threads : 1);
+    int64_t most = int64_t(sm_count_cached()) * (2048 / L.threads);
     if (groups < most) most = groups;
     return int(most > 0 ? most : 1);
 }
 
 template <typename T>
-cudaError_t bwd_type(const NormArgs& A, const Layout& L, int parts, cudaStream_t st) {
+cudaError_t bwd_type(const NormArgs& A, const Layout& L, int& parts, cudaStream_t st) {
     if (L.vec == 0) {
         k_norm_bwd_loop<T><<<parts, LOOP_T, 0, st>>>(A);
         return cudaGetLastError();
@@ -552,9 +596,9 @@ cudaError_t bwd_type(const NormArgs& A, const Layout& L, int parts, cudaStream_t
 
 // CTAs of the backward at most, whatever the pointers' alignment turns out to be.
 int norm_bwd_parts(const gdn_norm_problem& p) {
-    const int a = parts_of(p, layout_of(p.dim, full_vec(p.dtype), false, true));
+    const int a = parts_of(p, layout_of(p.rows, p.dim, full_vec(p.dtype), false, true));
     if (p.dim % full_vec(p.dtype)) return a;
-    const int b = parts_of(p, layout_of(p.dim, full_vec(p.dtype), true, true));
+    const int b = parts_of(p, layout_of(p.rows, p.dim, full_vec(p.dtype), true, true));
     return a > b ? a : b;
 }
 
@@ -570,16 +614,16 @@ cudaError_t launch_norm_bwd(const NormArgs& A, cudaStream_t st) {
     const int full = full_vec(p.dtype);
     const bool vectors = p.dim % full == 0 && p.x_stride % full == 0 && p.dy_stride % full == 0 && p.dsum_stride % full == 0 && wide(A.x) &&
                          wide(A.dy) && wide(A.dsum) && wide(A.weight) && wide(A.dx);
-    const Layout L = layout_of(p.dim, full, vectors, true);
-    const int parts = parts_of(p, L);
+    const Layout L = layout_of(p.rows, p.dim, full, vectors, true);
+    int parts = parts_of(p, L);
     timing_begin("rmsnorm_bwd", st);
     const cudaError_t e = p.dtype == GDN_BF16 ? bwd_type<__nv_bfloat16>(A, L, parts, st) : bwd_type<float>(A, L, parts, st);
     timing_end(st);
     if (e != cudaSuccess) return e;
     timing_begin("rmsnorm_dweight", st);
-    k_norm_dw<<<(p.dim + 31) / 32, 1024, 0, st>>>(A.part, parts, p.dim, A.dweight);
+    const cudaError_t e2 = launch_pdl(k_norm_dw, dim3((p.dim + DW_C - 1) / DW_C), dim3(DW_C * DW_R), 0, st, static_cast<const float*>(A.part), parts, int(p.dim), A.dweight);
     timing_end(st);
-    return cudaGetLastError();
+    return e2;
 }
 
 }  // namespace gdn
