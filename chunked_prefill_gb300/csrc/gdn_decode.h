@@ -17,6 +17,7 @@ struct StepArgs {
     const float *g, *beta, *A_log, *dt_bias, *state_in;
     float* state_out;
     void* o;
+    int ahead;  // items from one whose state is in use to the one asked into L2 (set by the launch)
 };
 cudaError_t launch_step(const StepArgs& A, cudaStream_t st);
 

@@ -145,7 +145,7 @@ gdn_status gdn_recurrent_step(const gdn_step_problem* problem, const void* q, co
                               const float* dt_bias, const float* state_in, float* state_out,
                               void* o, void* stream) {
     if (!problem) return fail(GDN_ERR_INVALID_ARG, "problem is NULL");
-    gdn::StepArgs A{*problem, q, k, v, g, beta, A_log, dt_bias, state_in, state_out, o};
+    gdn::StepArgs A{*problem, q, k, v, g, beta, A_log, dt_bias, state_in, state_out, o, 0};
     gdn_step_problem& p = A.p;
     TRY(check_step(p));
     const bool none = p.total_tokens == 0;

@@ -475,9 +475,9 @@ Layout layout_of(int64_t rows, int dim, int full, bool vectors, bool backward) {
         L.lpr = n <= 8 ? 8 : n <= 16 ? 16 : 32;
         return L;
     }
-    if (n <= 128) {
+    if (n <= 64) {
         L.lpr = 32;
-        L.nv = n <= 64 ? 2 : 4;
+        L.nv = 2;
         return L;
     }
     // a CTA per row: two vectors a thread while its threads hold the row so, else more.  Rows that leave
@@ -545,8 +545,7 @@ cudaError_t bwd_out(const NormArgs& A, const Layout& L, int& parts, cudaStream_t
             if (L.lpr == 8) return F<T, FULL, 1, 8>(__VA_ARGS__);                   \
             if (L.lpr == 16) return F<T, FULL, 1, 16>(__VA_ARGS__);                 \
             if (L.lpr == 32 && L.nv == 1) return F<T, FULL, 1, 32>(__VA_ARGS__);    \
-            if (L.lpr == 32 && L.nv == 2) return F<T, FULL, 2, 32>(__VA_ARGS__);    \
-            if (L.lpr == 32) return F<T, FULL, 4, 32>(__VA_ARGS__);                 \
+            if (L.lpr == 32) return F<T, FULL, 2, 32>(__VA_ARGS__);                 \
             if (L.nv == 1) return F<T, FULL, 1, 0>(__VA_ARGS__);                    \
             if (L.nv == 2) return F<T, FULL, 2, 0>(__VA_ARGS__);                    \
             return F<T, FULL, 4, 0>(__VA_ARGS__);                                   \
@@ -554,8 +553,7 @@ cudaError_t bwd_out(const NormArgs& A, const Layout& L, int& parts, cudaStream_t
         if (L.lpr == 8) return F<T, 1, 1, 8>(__VA_ARGS__);                          \
         if (L.lpr == 16) return F<T, 1, 1, 16>(__VA_ARGS__);                        \
         if (L.lpr == 32 && L.nv == 1) return F<T, 1, 1, 32>(__VA_ARGS__);           \
-        if (L.lpr == 32 && L.nv == 2) return F<T, 1, 2, 32>(__VA_ARGS__);           \
-        if (L.lpr == 32) return F<T, 1, 4, 32>(__VA_ARGS__);                        \
+        if (L.lpr == 32) return F<T, 1, 2, 32>(__VA_ARGS__);                        \
         if (L.nv == 2) return F<T, 1, 2, 0>(__VA_ARGS__);                           \
         if (L.nv == 4) return F<T, 1, 4, 0>(__VA_ARGS__);                           \
         if (L.nv == 8) return F<T, 1, 8, 0>(__VA_ARGS__);                           \

@@ -68,9 +68,13 @@ struct Part {
     int64_t lo, hi;
     int n, head, at;
 };
+// a / b for a >= 0, b > 0; 64-bit division costs half a microsecond that small problems feel
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? int64_t(uint32_t(a) / uint32_t(b)) : a / b;
+}
 __device__ __forceinline__ int64_t share_of(int64_t total, int parts, int warps) {
-    const int64_t s = (total + parts - 1) / parts;  // a multiple of the warps, so that none is left out
-    return (s + warps - 1) / warps * warps;
+    // a multiple of the warps (a power of two), so that none is left out
+    return (quotient(total + parts - 1, parts) + warps - 1) & ~int64_t(warps - 1);
 }
 // CTA 0 also leaves the number of tiles before each sequence (per block of heads) in A.before.
 template <int T>
@@ -114,10 +118,10 @@ __device__ Part find_part(const PagedArgs& A, int tok, int warps) {
             run += t;
             t = range_of(A, ++n).tiles(tok);
         }
-        const int64_t rest = P.lo - run * A.heads;
+        const int64_t rest = P.lo - run * A.heads, head = quotient(rest, t);
         found[0] = n;
-        found[1] = int(rest / t);
-        found[2] = int(rest % t);
+        found[1] = int(head);
+        found[2] = int(rest - head * t);
     }
     __syncthreads();
     P.n = found[0], P.head = found[1], P.at = found[2];
@@ -417,6 +421,23 @@ __global__ void __launch_bounds__(Tile<C, D>::T, Tile<C, D>::CTAS) k_paged_mma(c
         C* kc = static_cast<C*>(A.k_cache) + hk * p.k_head_stride;
         C* vc = static_cast<C*>(A.v_cache) + hk * p.v_head_stride;
 
+        // ---- this warp's tiles: tokens from start + TOK (warp + W i)
+        const int tiles = all > warp ? (all - warp + W - 1) / W : 0;
+        auto token_of = [&](int i) { return start + TOK * (warp + W * i); };
+        // The page(s) of block b of tile i: with TILED (a page holds whole blocks) the block's page, in
+        // every lane; else lane l has that of token l % 16.  -1 where there is nothing to attend to.
+        auto page_at = [&](int i, int b) {
+            const int tok = token_of(i) + 16 * b + (TILED ? 0 : lane & 15);
+            if (i >= tiles || tok >= t1 || (!TILED && tok < t0)) return -1;
+            const int page = table[A.page_div.of(tok)];
+            return page >= 0 && page < p.num_pages ? page : -1;
+        };
+        int first[STAGES - 1][TT];  // of the tiles requested ahead
+#pragma unroll
+        for (int i = 0; i < STAGES - 1; ++i)
+#pragma unroll
+            for (int b = 0; b < TT; ++b) first[i][b] = page_at(i, b);
+
         if (A.k_new && R.len > 0 && end == tiles_n) {  // every block of heads writes the same bits before it reads them
             const int at = R.len - 1, page = table[A.page_div.of(at)], slot = slot_of(at);
             if (page >= 0 && page < p.num_pages) {
@@ -431,17 +452,6 @@ __global__ void __launch_bounds__(Tile<C, D>::T, Tile<C, D>::CTAS) k_paged_mma(c
             __syncthreads();
         }
 
-        // ---- this warp's tiles: tokens from start + TOK (warp + W i)
-        const int tiles = all > warp ? (all - warp + W - 1) / W : 0;
-        auto token_of = [&](int i) { return start + TOK * (warp + W * i); };
-        // The page(s) of block b of tile i: with TILED (a page holds whole blocks) the block's page, in
-        // every lane; else lane l has that of token l % 16.  -1 where there is nothing to attend to.
-        auto page_at = [&](int i, int b) {
-            const int tok = token_of(i) + 16 * b + (TILED ? 0 : lane & 15);
-            if (i >= tiles || tok >= t1 || (!TILED && tok < t0)) return -1;
-            const int page = table[A.page_div.of(tok)];
-            return page >= 0 && page < p.num_pages ? page : -1;
-        };
         // Requests the rows of block b of tile i (zeros where masked); returns which tokens count.
         auto issue = [&](int i, int b, int stage, int pages) -> uint32_t {
             const int tok = token_of(i) + 16 * b;
@@ -491,7 +501,7 @@ __global__ void __launch_bounds__(Tile<C, D>::T, Tile<C, D>::CTAS) k_paged_mma(c
             mask[i] = 0u;
             if (i < tiles)
 #pragma unroll
-                for (int b = 0; b < TT; ++b) mask[i] |= issue(i, b, i, page_at(i, b));
+                for (int b = 0; b < TT; ++b) mask[i] |= issue(i, b, i, first[i][b]);
             cp_commit();
         }
 #pragma unroll
@@ -795,13 +805,13 @@ __global__ void __launch_bounds__(32 * JW) k_paged_join(const PagedArgs A, int t
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t row = RPB == 1 ? blockIdx.x : int64_t(blockIdx.x) * JW + warp;
     if (row >= int64_t(p.num_seqs) * p.Hq) return;  // with RPB == 1 never
-    const int n = int(row / p.Hq), h = int(row % p.Hq), G = p.Hq / p.Hkv, nb = (G + rows - 1) / rows;
+    const int n = int(quotient(row, p.Hq)), h = int(row - int64_t(n) * p.Hq), G = p.Hq / p.Hkv, nb = (G + rows - 1) / rows;
     const int block = (h / G) * nb + (h % G) / rows, in = (h % G) % rows;
     const int head = block / A.groups, group = block % A.groups;
     const int64_t before = A.before[n], tiles = A.before[n + 1] - before;
     const int64_t share = share_of(A.before[p.num_seqs] * A.heads, ctas / A.groups, warps);
     const int64_t at0 = before * A.heads + head * tiles, at1 = at0 + tiles;
-    const int c0 = int(at0 / share), c1 = int((at1 - 1) / share);
+    const int c0 = int(quotient(at0, share)), c1 = int(quotient(at1 - 1, share));
     if (c0 == c1) return;  // that CTA wrote it out
     // parts c0 .. c1; this warp's: c0 + first, first + step, ...
     const int parts = c1 - c0 + 1, first = RPB == 1 ? warp : 0, step = RPB == 1 ? JW : 1;
