@@ -47,6 +47,7 @@ struct PagedArgs {
     const float *k_scale, *v_scale;
     void* o;
     float* lse;
+    bool unsplit;     // a CTA per (sequence, block of heads), nothing to join
     int groups;       // of blocks of query heads (a block shares a kv-head)
     int heads;        // blocks in a group
     int64_t* before;  // [num_seqs + 1] tiles before each sequence, per block of heads
@@ -58,6 +59,7 @@ struct PagedArgs {
 // groups of heads), rows to a block of query heads, and the bytes of the workspace (before, part_ml, part, in this order).
 struct PagedPlan {
     int ctas, rows, groups, heads;
+    bool unsplit;
     size_t off_ml, off_part, bytes;
 };
 PagedPlan paged_plan(const gdn_paged_problem& p);

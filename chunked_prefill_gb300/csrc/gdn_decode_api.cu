@@ -198,9 +198,9 @@ gdn_status gdn_paged_attn_decode(const gdn_paged_problem* problem, const void* q
     TRY(check_ptr("lse", lse, 4, true));
     if ((k_new == nullptr) != (v_new == nullptr)) return fail(GDN_ERR_INVALID_ARG, "k_new and v_new go together");
     const gdn::PagedPlan plan = gdn::paged_plan(p);
-    if (!workspace || workspace_bytes < plan.bytes)
+    if (plan.bytes && (!workspace || workspace_bytes < plan.bytes))
         return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", plan.bytes, workspace ? workspace_bytes : size_t(0));
-    TRY(check_ptr("workspace", workspace, 16));
+    if (plan.bytes) TRY(check_ptr("workspace", workspace, 16));
     A.page_div.set(uint32_t(p.page_size));
     A.q = q;
     A.k_cache = k_cache;
@@ -214,6 +214,7 @@ gdn_status gdn_paged_attn_decode(const gdn_paged_problem* problem, const void* q
     A.o = o;
     A.lse = lse;
     char* ws = static_cast<char*>(workspace);
+    A.unsplit = plan.unsplit;
     A.groups = plan.groups;
     A.heads = plan.heads;
     A.before = reinterpret_cast<int64_t*>(ws);

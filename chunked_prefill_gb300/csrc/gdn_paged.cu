@@ -79,6 +79,10 @@ __device__ __forceinline__ int64_t share_of(int64_t total, int parts, int warps)
 // CTA 0 also leaves the number of tiles before each sequence (per block of heads) in A.before.
 template <int T>
 __device__ Part find_part(const PagedArgs& A, int tok, int warps) {
+    if (A.unsplit) {  // a CTA per (sequence, block of heads)
+        const int blocks = A.groups * A.heads, n = blockIdx.x / blocks;
+        return {0, range_of(A, n).tiles(tok), n, int(blockIdx.x % blocks) / A.groups, 0};
+    }
     __shared__ int64_t wsum[T / 32];
     __shared__ int found[3];
     const int tid = threadIdx.x, lane = tid & 31, N = A.p.num_seqs;
@@ -816,19 +820,41 @@ __global__ void __launch_bounds__(32 * JW) k_paged_join(const PagedArgs A, int t
     // parts c0 .. c1; this warp's: c0 + first, first + step, ...
     const int parts = c1 - c0 + 1, first = RPB == 1 ? warp : 0, step = RPB == 1 ? JW : 1;
     auto place = [&](int i) { return place_of((c0 + i) * A.groups + group, i > 0 || at0 < c0 * share, rows) + in; };
-    float M = -INFINITY;
-    for (int i = first + step * lane; i < parts; i += step * 32) M = fmaxf(M, A.part_ml[place(i)].x);
+    float M = -INFINITY, S = 0.f, acc[E] = {};
+    // batches of parts, everything of a batch requested at once
+    constexpr int NB = D == 256 ? 4 : 8;
+    for (int i0 = first; i0 < parts; i0 += step * NB) {
+        float2 ml[NB];
+        float x[NB][E];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float S = 0.f, acc[E] = {};
-#pragma unroll 8
-    for (int i = first; i < parts; i += step) {
-        const int64_t at = place(i);
-        const float2 ml = A.part_ml[at];
-        const float c = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-        S = fmaf(ml.y, c, S);
+        for (int b = 0; b < NB; ++b) {
+            const int i = i0 + step * b;
+            ml[b] = make_float2(-INFINITY, 0.f);
+            if (i < parts) {
+                const int64_t at = place(i);
+                ml[b] = A.part_ml[at];
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(A.part[at * D + 32 * e + lane], c, acc[e]);
+                for (int e = 0; e < E; ++e) x[b][e] = A.part[at * D + 32 * e + lane];
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; ++e) x[b][e] = 0.f;
+            }
+        }
+        float top = M;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) top = fmaxf(top, ml[b].x);
+        const float c = M == -INFINITY ? 0.f : ex2(M - top);
+        M = top;
+        S *= c;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] *= c;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const float w = ml[b].x == -INFINITY ? 0.f : ex2(ml[b].x - M);
+            S = fmaf(ml[b].y, w, S);
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(x[b][e], w, acc[e]);
+        }
     }
     if constexpr (RPB == 1) {
 #pragma unroll
@@ -859,6 +885,8 @@ __global__ void __launch_bounds__(32 * JW) k_paged_join(const PagedArgs A, int t
     if (A.lse && lane == 0) A.lse[row] = some ? (M + log2f(S)) * LN2 : -INFINITY;
 }
 
+constexpr int UNSPLIT = 8;
+
 // What the launches need to know of a kernel.
 struct Shape {
     int tok, rows, warps, ctas;  // tokens of a tile, rows of a block of heads, warps that share tiles, CTAs per multiprocessor
@@ -874,6 +902,7 @@ Shape shape_of(const gdn_paged_problem& p) {
 
 template <typename Act, int D>
 cudaError_t launch_join(const PagedArgs& A, const PagedPlan& plan, const Shape& s, cudaStream_t st) {
+    if (plan.unsplit) return cudaGetLastError();
     const int64_t rows = int64_t(A.p.num_seqs) * A.p.Hq;
     timing_begin("paged_attn_join", st);
     const cudaError_t e =
@@ -935,10 +964,15 @@ PagedPlan paged_plan(const gdn_paged_problem& p) {
     const int64_t tiles = (most / s.tok + 1) * r.heads * p.num_seqs, want = (tiles + s.warps - 1) / s.warps;
     const int parts = full / r.groups;
     r.ctas = r.groups * int(want < parts ? (want > 0 ? want : 1) : parts);
+    // Short caches are not split: finding a CTA's part of the list and joining take as long as
+    // UNSPLIT tiles per warp.
+    r.unsplit = most <= int64_t(UNSPLIT) * s.warps * s.tok && int64_t(p.num_seqs) * blocks < (1 << 30);
+    if (r.unsplit) r.ctas = p.num_seqs * blocks;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     r.off_ml = up(size_t(p.num_seqs + 1) * sizeof(int64_t));
     r.off_part = r.off_ml + up(size_t(r.ctas) * 2 * s.rows * sizeof(float2));
     r.bytes = r.off_part + size_t(r.ctas) * 2 * s.rows * p.D * sizeof(float);
+    if (r.unsplit) r.off_ml = r.off_part = r.bytes = 0;
     return r;
 }
 
