@@ -148,29 +148,45 @@ template <> __device__ __forceinline__ __nv_fp8_e4m3 to_cache<__nv_fp8_e4m3>(flo
 
 // ------------------------------------------------------------------------------- fp32
 constexpr int PT = 128;   // threads
+constexpr int PW = PT / 32;
 constexpr int GB = 4;     // query heads per block of heads
+constexpr int PU = 4;     // tokens a warp takes at a time
 constexpr int PTOK = 32;  // tokens to a tile of the list
 
-template <int D> struct Lanes {
-    static constexpr int E = D / 32 > 4 ? D / 32 : 4;  // values per lane
-    static constexpr int LP = D / E;                   // lanes per token
-    static constexpr int GROUPS = PT / LP;
-};
 template <int E>
 __device__ __forceinline__ void load_row(const float* p, float (&x)[E]) {
+    if constexpr (E == 2) {
+        *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(p);
+    } else {
 #pragma unroll
-    for (int b = 0; b < E / 4; ++b) *reinterpret_cast<float4*>(x + 4 * b) = *reinterpret_cast<const float4*>(p + 4 * b);
+        for (int b = 0; b < E / 4; ++b) *reinterpret_cast<float4*>(x + 4 * b) = *reinterpret_cast<const float4*>(p + 4 * b);
+    }
+}
+// 16 values a lane, summed over the warp: lane l gets value l / 2 (bit 4 of the lane is bit 3 of the value).
+__device__ __forceinline__ float sum16(float (&v)[16]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int n = 8; n > 0; n >>= 1) {
+        const bool up = lane & (2 * n);
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const float keep = up ? v[i + n] : v[i], give = up ? v[i] : v[i + n];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, 2 * n);
+        }
+    }
+    return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
 }
 
-// Tokens over lane groups, each with its own running (m, l, accumulator) of GB heads.
+// A warp takes 4 tokens at a time, a lane D / 32 features of their rows and of 4 query heads.  The 16
+// scores are summed across the warp so that each ends up in two lanes (16 exchanges instead of 80), which
+// alone work out its weight; the next 4 tokens' rows are requested meanwhile.
 template <int D>
-__global__ void __launch_bounds__(PT, D == 256 ? 4 : 5) k_paged(const PagedArgs A) {
-    using L = Lanes<D>;
-    constexpr int E = L::E, LP = L::LP, GROUPS = L::GROUPS;
-    __shared__ __align__(16) float acc_s[GROUPS][GB][D];
-    __shared__ float ml_s[GROUPS][GB][2];
+__global__ void __launch_bounds__(PT, D == 256 ? 2 : 4) k_paged(const PagedArgs A) {
+    constexpr int E = D / 32;
+    __shared__ __align__(16) float acc_s[PW][GB][D];
+    __shared__ float ml_s[PW][GB][2];
     const gdn_paged_problem& p = A.p;
-    const int tid = threadIdx.x, lane = tid % LP, grp = tid / LP;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = p.Hq / p.Hkv, nb = (G + GB - 1) / GB;
     tc::pdl_launch_dependents();
     Part P = find_part<PT>(A, PTOK, 1);
@@ -201,62 +217,107 @@ __global__ void __launch_bounds__(PT, D == 256 ? 4 : 5) k_paged(const PagedArgs 
             __syncthreads();
         }
 
-        float q[GB][E], acc[GB][E], m[GB], l[GB];
+        // page of token t + lane % 4, or -1 where there is nothing to attend to
+        auto page_at = [&](int t) {
+            t += lane & (PU - 1);
+            if (t < t0 || t >= t1) return -1;
+            const int page = table[A.page_div.of(t)];
+            return page >= 0 && page < p.num_pages ? page : -1;
+        };
+        float kn[PU][E], vn[PU][E];
+        auto fetch = [&](int t, int pages) {
 #pragma unroll
-        for (int h = 0; h < GB; ++h) {
-            m[h] = -INFINITY;
-            l[h] = 0.f;
+            for (int u = 0; u < PU; ++u) {
+                const int page = __shfl_sync(0xffffffffu, pages, u), slot = t + u - A.page_div.of(t + u) * p.page_size;
+                if (page >= 0) {
+                    load_row<E>(kc + page * p.k_page_stride + slot * p.k_token_stride + lane * E, kn[u]);
+                    load_row<E>(vc + page * p.v_page_stride + slot * p.v_token_stride + lane * E, vn[u]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < E; ++e) kn[u][e] = vn[u][e] = 0.f;
+                }
+            }
+        };
+        constexpr int HOP = PW * PU;
+        const int first = start + warp * PU;
+        int pages = page_at(first);
+        fetch(first, pages);
+        int next = page_at(first + HOP);
+
+        float q[GB][E], acc[GB][E];
+#pragma unroll
+        for (int h = 0; h < GB; ++h)
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 acc[h][e] = 0.f;
                 q[h][e] = hb + h < G ? static_cast<const float*>(A.q)[n * p.q_stride + (hk * G + hb + h) * D + lane * E + e] : 0.f;
             }
-        }
         const float zs = p.scale * ks * LOG2E;
-        for (int t = t0 + grp; t - grp < t1; t += GROUPS) {
-            bool live = t < t1;
-            float kx[E] = {}, vx[E] = {};
-            if (live) {
-                const int page = table[A.page_div.of(t)], slot = t - A.page_div.of(t) * p.page_size;
-                live = page >= 0 && page < p.num_pages;
-                if (live) {
-                    load_row<E>(kc + page * p.k_page_stride + slot * p.k_token_stride + lane * E, kx);
-                    load_row<E>(vc + page * p.v_page_stride + slot * p.v_token_stride + lane * E, vx);
+        float m = -INFINITY, l = 0.f;  // of this lane's head, bits 1 and 2 of the lane; its token: bits 3 and 4
+        for (int t = first; t < t1; t += HOP) {
+            const bool live = __shfl_sync(0xffffffffu, pages, lane >> 3) >= 0;
+            float k[PU][E], v[PU][E];
+#pragma unroll
+            for (int u = 0; u < PU; ++u)
+#pragma unroll
+                for (int e = 0; e < E; ++e) k[u][e] = kn[u][e], v[u][e] = vn[u][e];
+            pages = next;
+            fetch(t + HOP, pages);
+            next = page_at(t + 2 * HOP);
+            float z16[16];
+#pragma unroll
+            for (int u = 0; u < PU; ++u)
+#pragma unroll
+                for (int h = 0; h < GB; ++h) {
+                    float z = 0.f;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) z = fmaf(q[h][e], k[u][e], z);
+                    z16[u * GB + h] = z;
+                }
+            float z = sum16(z16) * zs;
+            if (!live) z = -INFINITY;
+            float top = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 16));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            if (__any_sync(0xffffffffu, top > m)) {
+                const float mn = fmaxf(m, top), c = mn == -INFINITY ? 1.f : exp2f(m - mn);
+                m = mn;
+                l *= c;
+#pragma unroll
+                for (int h = 0; h < GB; ++h) {
+                    const float ch = __shfl_sync(0xffffffffu, c, 2 * h);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[h][e] *= ch;
                 }
             }
+            const float w = exp2f(z - (m == -INFINITY ? 0.f : m));
+            l += w;
 #pragma unroll
-            for (int h = 0; h < GB; ++h) {
-                float z = 0.f;
+            for (int u = 0; u < PU; ++u)
 #pragma unroll
-                for (int e = 0; e < E; ++e) z = fmaf(q[h][e], kx[e], z);
+                for (int h = 0; h < GB; ++h) {
+                    const float wu = __shfl_sync(0xffffffffu, w, 8 * u + 2 * h);
 #pragma unroll
-                for (int o = LP / 2; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-                if (live) {
-                    z *= zs;
-                    const float mn = fmaxf(m[h], z), c = m[h] == -INFINITY ? 0.f : exp2f(m[h] - mn);
-                    const float e0 = mn == -INFINITY ? 0.f : exp2f(z - mn);
-                    l[h] = fmaf(l[h], c, e0);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) acc[h][e] = fmaf(acc[h][e], c, e0 * vx[e]);
-                    m[h] = mn;
+                    for (int e = 0; e < E; ++e) acc[h][e] = fmaf(wu, v[u][e], acc[h][e]);
                 }
-            }
         }
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
 #pragma unroll
-        for (int h = 0; h < GB; ++h) {
+        for (int h = 0; h < GB; ++h)
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc_s[grp][h][lane * E + e] = acc[h][e];
-            if (lane == 0) {
-                ml_s[grp][h][0] = m[h];
-                ml_s[grp][h][1] = l[h];
-            }
+            for (int e = 0; e < E; ++e) acc_s[warp][h][lane * E + e] = acc[h][e];
+        if (lane < 8 && (lane & 1) == 0) {
+            ml_s[warp][lane >> 1][0] = m;
+            ml_s[warp][lane >> 1][1] = l;
         }
         __syncthreads();
         for (int i = tid; i < min(GB, G - hb) * D; i += PT) {
             const int h = i / D, d = i % D;
             float M = -INFINITY, S = 0.f, a = 0.f;
-            for (int g = 0; g < GROUPS; ++g) M = fmaxf(M, ml_s[g][h][0]);
-            for (int g = 0; g < GROUPS; ++g) {
+#pragma unroll
+            for (int g = 0; g < PW; ++g) M = fmaxf(M, ml_s[g][h][0]);
+#pragma unroll
+            for (int g = 0; g < PW; ++g) {
                 const float c = ml_s[g][h][0] == -INFINITY ? 0.f : exp2f(ml_s[g][h][0] - M);
                 S = fmaf(ml_s[g][h][1], c, S);
                 a = fmaf(acc_s[g][h][d], c, a);
@@ -342,7 +403,7 @@ template <typename C, int D> struct Tile {
     static constexpr int TOK = 16 * TT;                            // tokens of a tile
     static constexpr int W = D * E > 256 ? 2 : 4;                  // warps
     static constexpr int T = 32 * W;                               // threads
-    static constexpr int CTAS = 2;                                 // per multiprocessor
+    static constexpr int CTAS = D == 64 && E == 2 ? 3 : 2;         // per multiprocessor
     static constexpr int ROW = D * E;                              // bytes of a row
     static constexpr int CPR = ROW / 16;                           // 16-byte pieces of a row
     static constexpr int RPI = 32 / CPR;                           // rows per copy instruction of a warp
@@ -350,7 +411,7 @@ template <typename C, int D> struct Tile {
     static constexpr int VC = E == 1 ? ROW / (8 * VB) : 0;         // 8-bit: pieces of a value row per thread
     static constexpr int BLOCK = 16 * ROW;                         // bytes of 16 rows
     static constexpr int BYTES = 2 * TT * BLOCK;                   // of a warp's tile: K's blocks, V's blocks
-    static constexpr int FIT = 98304 / (W * BYTES), STAGES = FIT < 8 ? FIT : 8;
+    static constexpr int FIT = (CTAS == 3 ? 65536 : 98304) / (W * BYTES), STAGES = FIT < 8 ? FIT : 8;
     static constexpr int PAD = D + 4;                              // floats between rows of the joined accumulators
     static constexpr int SMEM = STAGES * W * BYTES;
     static_assert(STAGES >= 2 && W * 16 * PAD * 4 <= SMEM, "the warps' accumulators are joined in the stages' memory");
@@ -382,7 +443,9 @@ __global__ void __launch_bounds__(Tile<C, D>::T, Tile<C, D>::CTAS) k_paged_mma(c
     // fp16 weights are 2^14 e^{z - m}: those down to 2^-38 of the largest count then (2^-24 without; a long
     // sequence's many small weights add up beside one large one)
     constexpr float LIFT = F8 ? 14.f : 0.f;
-    constexpr bool QS = D == 256;                 // query fragments in shared memory: the registers hold the accumulators
+    // query fragments in shared memory: of 256 features, the registers hold the accumulators; 8-bit ones are
+    // much work to make, shared out to the warps
+    constexpr bool QS = D == 256 || F8;
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ float ml_s[W][16][2];
     __shared__ uint4 q_s[QS ? QF * R2 / 2 : 1][32];
@@ -542,6 +605,7 @@ __global__ void __launch_bounds__(Tile<C, D>::T, Tile<C, D>::CTAS) k_paged_mma(c
                 zs[r] = ldexpf(zs[r], e) + bad;
 #pragma unroll
                 for (int s = 0; s < KS; ++s) {
+                    if (s / 2 % W != warp) continue;
                     float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw[s].x));
                     float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw[s].y));
                     x.x *= down, x.y *= down, y.x *= down, y.y *= down;
@@ -559,9 +623,9 @@ __global__ void __launch_bounds__(Tile<C, D>::T, Tile<C, D>::CTAS) k_paged_mma(c
             }
         }
         if constexpr (QS) {
-            if (warp == 0)
 #pragma unroll
-                for (int i = 0; i < QF * R2 / 2; ++i) q_s[i][lane] = reinterpret_cast<const uint4*>(&qf[0][0])[i];
+            for (int i = 0; i < QF * R2 / 2; ++i)
+                if (F8 ? i / R2 % W == warp : warp == 0) q_s[i][lane] = reinterpret_cast<const uint4*>(&qf[0][0])[i];
             __syncthreads();
         }
 
@@ -890,7 +954,7 @@ struct Shape {
     int tok, rows, warps, ctas;  // tokens of a tile, rows of a block of heads, warps that share tiles, CTAs per multiprocessor
 };
 template <typename C, int D> constexpr Shape mma_shape() { return {Tile<C, D>::TOK, 16, Tile<C, D>::W, Tile<C, D>::CTAS}; }
-template <int D> constexpr Shape fp32_shape() { return {PTOK, GB, 1, D == 256 ? 4 : 5}; }
+template <int D> constexpr Shape fp32_shape() { return {PTOK, GB, 1, D == 256 ? 2 : 4}; }
 Shape shape_of(const gdn_paged_problem& p) {
     if (p.dtype == GDN_FP32) return p.D == 64 ? fp32_shape<64>() : p.D == 128 ? fp32_shape<128>() : fp32_shape<256>();
     if (p.cache_dtype == GDN_BF16)
@@ -962,12 +1026,12 @@ PagedPlan paged_plan(const gdn_paged_problem& p) {
     const int64_t tiles = (most / s.tok + 1) * r.heads * p.num_seqs, want = (tiles + s.warps - 1) / s.warps;
     const int parts = full / r.groups;
     r.ctas = r.groups * int(want < parts ? (want > 0 ? want : 1) : parts);
-    // Short caches are not split: finding a CTA's part of the list and joining take longer than the up to 16
-    // tiles per warp that a CTA then has in a row, 32 where there are enough CTAs to even them out (32
-    // sequences of up to 1000 tokens, 8 kv-heads: 18 us instead of 26; 256 of up to 2000: 155 instead of 161;
-    // 40 of 1000 each, 320 CTAs for 304 places: 36 instead of 34; 128 of up to 4000: 157 instead of 153).
-    const int64_t pairs = int64_t(p.num_seqs) * blocks;
-    r.unsplit = most <= int64_t(pairs >= full ? 32 : 16) * s.warps * s.tok && pairs < (1 << 30);
+    // Short caches are not split: finding a CTA's part of the list and joining take 4 to 5 us, the time of
+    // some 16384 / D tokens per warp.  With one CTA to a (sequence, kv-head) a warp has at most `longest`
+    // tokens, in an even split longest * pairs / full.  Enough CTAs even themselves out, so that the
+    // list is worth its while from 512 tokens per warp on.
+    const int64_t pairs = int64_t(p.num_seqs) * blocks, longest = (most + s.warps - 1) / s.warps;
+    r.unsplit = pairs < (1 << 30) && (pairs >= full ? longest <= 512 : longest * (full - pairs) / full * p.D <= 16384);
     if (r.unsplit) r.ctas = int(pairs);
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     r.off_ml = up(size_t(p.num_seqs + 1) * sizeof(int64_t));
