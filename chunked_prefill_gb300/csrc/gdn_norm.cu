@@ -7,7 +7,9 @@
 // read once into registers, NV vectors of VEC values a thread, and everything after its reductions
 // comes from there.  A row belongs to LPR lanes of a warp (8, 16 or 32: short rows, several to a
 // warp, no barrier) or, LPR = 0, to a whole CTA.  VEC is 16 bytes' worth of values where pointers,
-// strides and dim allow it and 1 elsewhere; rows past the registers' reach (max_threads x NV x
+// strides and dim allow it.  Contiguous rows of any other dim are taken in the 16-byte pieces of memory that
+// they lie in (SHIFT: piece j of a row starts a0 = row dim mod VEC values before the row's value j VEC),
+// value by value only in a row's first and last piece; other rows value by value (VEC = 1); rows past the registers' reach (max_threads x NV x
 // VEC values) take the looping kernels at the end.
 //
 // The backward keeps a CTA on a fixed sequence of rows (row = CTA, CTA + grid, ...) with its share
@@ -85,6 +87,38 @@ template <typename T, int VEC> struct Vec {
     __device__ __forceinline__ float at(int i) const { return to_f(v[i]); }
 };
 
+// The values of a row's piece that starts at value `off` of the row.  `left`: values of the tensor from the
+// row's start on.  A piece that reaches into a neighbouring row is read whole (the row before it is there, the
+// one after it where `left` says so); whatever is written there meanwhile does not matter, for the values
+// outside [0, dim) are masked by mask_piece (apart, so that a load need not be waited for where it is asked for).
+template <bool SHIFT, typename T, int VEC>
+__device__ __forceinline__ void load_piece(Vec<T, VEC>& v, const T* row, int off, int dim, int64_t left) {
+    if (!SHIFT || off + VEC <= left) {
+        v.load(row + off);
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v.v[e] = unsigned(off + e) < unsigned(dim) ? row[off + e] : from_f<T>(0.f);
+    }
+}
+template <bool SHIFT, typename T, int VEC>
+__device__ __forceinline__ void mask_piece(Vec<T, VEC>& v, int off, int dim) {
+    if (SHIFT && (off < 0 || off + VEC > dim)) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            if (unsigned(off + e) >= unsigned(dim)) v.v[e] = from_f<T>(0.f);
+    }
+}
+template <bool SHIFT, typename T, int VEC>
+__device__ __forceinline__ void store_piece(const Vec<T, VEC>& v, T* row, int off, int dim) {
+    if (!SHIFT || (off >= 0 && off + VEC <= dim)) {
+        v.store(row + off);
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            if (unsigned(off + e) < unsigned(dim)) row[off + e] = v.v[e];
+    }
+}
+
 template <int VEC>
 __device__ __forceinline__ void load_weight(const gdn_norm_problem& p, const void* w, int i, float (&out)[VEC]) {
     if (p.weight_dtype == GDN_BF16) {
@@ -97,6 +131,21 @@ __device__ __forceinline__ void load_weight(const gdn_norm_problem& p, const voi
         x.load(static_cast<const float*>(w) + i);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) out[e] = x.at(e) + p.weight_offset;
+    }
+}
+
+// The weights (with their offset) of a piece, zeros outside the row.
+template <bool SHIFT, int VEC>
+__device__ __forceinline__ void weight_piece(const gdn_norm_problem& p, const void* w, int off, float (&out)[VEC]) {
+    if constexpr (!SHIFT) {
+        load_weight<VEC>(p, w, off, out);
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            float one[1] = {0.f};
+            if (unsigned(off + e) < unsigned(p.dim)) load_weight<1>(p, w, off + e, one);
+            out[e] = one[0];
+        }
     }
 }
 
@@ -124,32 +173,37 @@ __device__ __forceinline__ float scale_of(float mag) { return mag_max(mag * (1.f
 
 // OUT8: 0 dtype out; 1 one scale per row; 2 groups of 2^n <= 32 lanes' vectors; 3 other groups
 // (magnitudes by shared-memory maxima, whose order does not matter).
-template <typename T, int VEC, int NV, int LPR, int OUT8>
-__global__ void __launch_bounds__(max_threads(VEC, NV, LPR, false), LPR == 0 && VEC > 1 && NV == 2 ? 4 : 1) k_norm_fwd(const NormArgs A) {
+template <typename T, int VEC, int NV, int LPR, bool SHIFT, int OUT8>
+__global__ void __launch_bounds__(max_threads(VEC, NV, LPR, false), LPR == 0 && VEC > 1 && NV == 2 && !SHIFT ? 4 : 1) k_norm_fwd(const NormArgs A) {
     const gdn_norm_problem& p = A.p;
     __shared__ float red[2][32];
     extern __shared__ uint32_t mags[];  // OUT8 == 3: per group of the CTA's row(s)
     const int tid = threadIdx.x, step = LPR ? LPR : blockDim.x, at0 = LPR ? tid % step : tid;
     const int per = LPR ? int(blockDim.x) / step : 1, mine = LPR ? tid / step : 0;  // rows per CTA, and this thread's
-    const int nvec = p.dim / VEC;
     const int64_t row = int64_t(blockIdx.x) * per + mine;
+    const int a0 = SHIFT ? int(row * p.dim & (VEC - 1)) : 0, nvec = SHIFT ? (a0 + p.dim + VEC - 1) / VEC : p.dim / VEC;
     const bool live = row < p.rows;
     const T* x = static_cast<const T*>(A.x) + row * p.x_stride;
     const T* res = static_cast<const T*>(A.residual) + row * p.residual_stride;
+    const int64_t left = (p.rows - row) * p.dim;
 
     Vec<T, VEC> xv[NV], rv[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int j = at0 + k * step;
         if (live && j < nvec) {
-            xv[k].load(x + int64_t(j) * VEC);
-            if (A.residual) rv[k].load(res + int64_t(j) * VEC);
+            load_piece<SHIFT>(xv[k], x, j * VEC - a0, p.dim, left);
+            if (A.residual) load_piece<SHIFT>(rv[k], res, j * VEC - a0, p.dim, left);
         }
     }
     float s[NV][VEC], ss = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const bool in = live && at0 + k * step < nvec;
+        if (in) {
+            mask_piece<SHIFT>(xv[k], (at0 + k * step) * VEC - a0, p.dim);
+            if (A.residual) mask_piece<SHIFT>(rv[k], (at0 + k * step) * VEC - a0, p.dim);
+        }
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             s[k][e] = in ? (A.residual ? xv[k].at(e) + rv[k].at(e) : xv[k].at(e)) : 0.f;
@@ -164,7 +218,7 @@ __global__ void __launch_bounds__(max_threads(VEC, NV, LPR, false), LPR == 0 && 
             if (live && j < nvec) {
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) xv[k].v[e] = from_f<T>(s[k][e]);
-                xv[k].store(sum + int64_t(j) * VEC);
+                store_piece<SHIFT>(xv[k], sum, j * VEC - a0, p.dim);
             }
         }
     }
@@ -174,7 +228,7 @@ __global__ void __launch_bounds__(max_threads(VEC, NV, LPR, false), LPR == 0 && 
         const int j = at0 + k * step;
         if (j < nvec) {
             float w[VEC];
-            load_weight<VEC>(p, A.weight, j * VEC, w);
+            weight_piece<SHIFT, VEC>(p, A.weight, j * VEC - a0, w);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) s[k][e] = s[k][e] * r * w[e];
         }
@@ -187,7 +241,7 @@ __global__ void __launch_bounds__(max_threads(VEC, NV, LPR, false), LPR == 0 && 
             if (live && j < nvec) {
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) xv[k].v[e] = from_f<T>(s[k][e]);
-                xv[k].store(y + int64_t(j) * VEC);
+                store_piece<SHIFT>(xv[k], y, j * VEC - a0, p.dim);
             }
         }
     } else {
@@ -209,7 +263,18 @@ __global__ void __launch_bounds__(max_threads(VEC, NV, LPR, false), LPR == 0 && 
             const float inv = __frcp_rn(sc);
 #pragma unroll
             for (int k = 0; k < NV; ++k)
-                if (live && at0 + k * step < nvec) store8<VEC>(y + int64_t(at0 + k * step) * VEC, s[k], inv);
+                if (live && at0 + k * step < nvec) {
+                    const int off = (at0 + k * step) * VEC - a0;
+                    if (!SHIFT || (off >= 0 && off + VEC <= p.dim)) {
+                        store8<VEC>(y + off, s[k], inv);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) {
+                            const float one[1] = {s[k][e]};
+                            if (unsigned(off + e) < unsigned(p.dim)) store8<1>(y + off + e, one, inv);
+                        }
+                    }
+                }
         } else if constexpr (OUT8 == 2) {
             const int lanes = p.group / VEC, shift = __ffs(lanes) - 1;  // 2^shift lanes hold a group, at a multiple of 2^shift
             for (int o = lanes / 2; o > 0; o >>= 1)
@@ -254,13 +319,16 @@ __global__ void __launch_bounds__(max_threads(VEC, NV, LPR, false), LPR == 0 && 
     }
 }
 
-template <typename T, int VEC, int NV, int LPR>
+// With SHIFT the CTAs' rows are 8 k apart, so that a0 is the same for all of a thread's rows and its columns
+// stay its own.
+template <typename T, int VEC, int NV, int LPR, bool SHIFT>
 __global__ void __launch_bounds__(max_threads(VEC, NV, LPR, true)) k_norm_bwd(const NormArgs A) {
     const gdn_norm_problem& p = A.p;
     __shared__ float red[2][2][32];
     const int tid = threadIdx.x, step = LPR ? LPR : blockDim.x, at0 = LPR ? tid % step : tid;
     const int per = LPR ? int(blockDim.x) / step : 1, mine = LPR ? tid / step : 0;
-    const int nvec = p.dim / VEC;
+    const int64_t first = int64_t(blockIdx.x) * per + mine;
+    const int a0 = SHIFT ? int(first * p.dim & (VEC - 1)) : 0, nvec = SHIFT ? (a0 + p.dim + VEC - 1) / VEC : p.dim / VEC;
     tc::pdl_launch_dependents();
     constexpr bool KEEP = NV * VEC < 32;  // the weights stay in registers (else: read again, from L1)
     float w[KEEP ? NV : 1][VEC], dw[NV][VEC];
@@ -268,7 +336,7 @@ __global__ void __launch_bounds__(max_threads(VEC, NV, LPR, true)) k_norm_bwd(co
     for (int k = 0; k < NV; ++k) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) dw[k][e] = 0.f;
-        if (KEEP && at0 + k * step < nvec) load_weight<VEC>(p, A.weight, (at0 + k * step) * VEC, w[KEEP ? k : 0]);
+        if (KEEP && at0 + k * step < nvec) weight_piece<SHIFT, VEC>(p, A.weight, (at0 + k * step) * VEC - a0, w[KEEP ? k : 0]);
     }
     const float inv_dim = 1.f / float(p.dim);
     int turn = 0;
@@ -281,17 +349,18 @@ __global__ void __launch_bounds__(max_threads(VEC, NV, LPR, true)) k_norm_bwd(co
         const T* x = static_cast<const T*>(A.x) + row * p.x_stride;
         const T* dy = static_cast<const T*>(A.dy) + row * p.dy_stride;
         const T* ds = static_cast<const T*>(A.dsum) + row * p.dsum_stride;
+        const int64_t left = (p.rows - row) * p.dim;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int j = at0 + k * step;
             if (j < nvec) {
-                xn[k].load(x + int64_t(j) * VEC);
-                dn[k].load(dy + int64_t(j) * VEC);
-                if (A.dsum) sn[k].load(ds + int64_t(j) * VEC);
+                load_piece<SHIFT>(xn[k], x, j * VEC - a0, p.dim, left);
+                load_piece<SHIFT>(dn[k], dy, j * VEC - a0, p.dim, left);
+                if (A.dsum) load_piece<SHIFT>(sn[k], ds, j * VEC - a0, p.dim, left);
             }
         }
     };
-    if (AHEAD) fetch(int64_t(blockIdx.x) * per + mine);
+    if (AHEAD) fetch(first);
     // every lane of a warp takes part in the shuffles of every turn
     for (int64_t row0 = int64_t(blockIdx.x) * per; row0 < p.rows; row0 += hop, turn ^= 1) {
         const int64_t row = row0 + mine;
@@ -305,7 +374,9 @@ __global__ void __launch_bounds__(max_threads(VEC, NV, LPR, true)) k_norm_bwd(co
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             if (!(live && at0 + k * step < nvec)) continue;
-            if (!KEEP) load_weight<VEC>(p, A.weight, (at0 + k * step) * VEC, w[0]);
+            mask_piece<SHIFT>(xv[k], (at0 + k * step) * VEC - a0, p.dim);
+            mask_piece<SHIFT>(dv[k], (at0 + k * step) * VEC - a0, p.dim);
+            if (!KEEP) weight_piece<SHIFT, VEC>(p, A.weight, (at0 + k * step) * VEC - a0, w[0]);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 ss = fmaf(xv[k].at(e), xv[k].at(e), ss);
@@ -334,14 +405,14 @@ __global__ void __launch_bounds__(max_threads(VEC, NV, LPR, true)) k_norm_bwd(co
         for (int k = 0; k < NV; ++k) {
             const int j = at0 + k * step;
             if (live && j < nvec) {
-                if (!KEEP) load_weight<VEC>(p, A.weight, j * VEC, w[0]);
+                if (!KEEP) weight_piece<SHIFT, VEC>(p, A.weight, j * VEC - a0, w[0]);
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
                     const float n = xv[k].at(e) * r, d = dv[k].at(e);
                     dw[k][e] = fmaf(d, n, dw[k][e]);
                     xv[k].v[e] = from_f<T>(fmaf(r, w[KEEP ? k : 0][e] * d - n * c, A.dsum ? sv[k].at(e) : 0.f));
                 }
-                xv[k].store(dx + int64_t(j) * VEC);
+                store_piece<SHIFT>(xv[k], dx, j * VEC - a0, p.dim);
             }
         }
     }
@@ -353,7 +424,8 @@ __global__ void __launch_bounds__(max_threads(VEC, NV, LPR, true)) k_norm_bwd(co
             const int j = at0 + k * step;
             if (j < nvec)
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) share[mine * p.dim + j * VEC + e] = dw[k][e];
+                for (int e = 0; e < VEC; ++e)
+                    if (!SHIFT || unsigned(j * VEC - a0 + e) < unsigned(p.dim)) share[mine * p.dim + j * VEC - a0 + e] = dw[k][e];
         }
         __syncthreads();
         for (int i = tid; i < p.dim; i += blockDim.x) {
@@ -367,7 +439,8 @@ __global__ void __launch_bounds__(max_threads(VEC, NV, LPR, true)) k_norm_bwd(co
             const int j = at0 + k * step;
             if (j < nvec)
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) part[j * VEC + e] = dw[k][e];
+                for (int e = 0; e < VEC; ++e)
+                    if (!SHIFT || unsigned(j * VEC - a0 + e) < unsigned(p.dim)) part[j * VEC - a0 + e] = dw[k][e];
         }
     }
 }
@@ -465,31 +538,33 @@ __global__ void __launch_bounds__(LOOP_T) k_norm_bwd_loop(const NormArgs A) {
 // How a problem's rows are laid over threads.
 struct Layout {
     int vec, nv, lpr, threads;  // lpr 0: a CTA per row; vec 0: the looping kernels
+    bool shift;
     int per() const { return lpr ? threads / lpr : 1; }
 };
-bool wide(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-Layout layout_of(int64_t rows, int dim, int full, bool vectors, bool backward) {
-    Layout L{vectors ? full : 1, 1, 0, ROWS_T};
-    const int n = dim / L.vec;
+Layout layout_of(int64_t rows, int dim, int vec, bool shift, bool backward) {
+    Layout L{vec, 1, 0, ROWS_T, shift};
+    const bool wide = vec > 1;
+    const int n = shift ? (dim + 2 * vec - 2) / vec : dim / vec;  // pieces of a row at most
     if (n <= 32) {
         L.lpr = n <= 8 ? 8 : n <= 16 ? 16 : 32;
         return L;
     }
-    if (n <= 64) {
+    // a warp per row: two pieces of 16 bytes a lane, up to 16 values otherwise
+    if (n <= (wide ? 64 : 512)) {
         L.lpr = 32;
-        L.nv = 2;
+        for (L.nv = 2; n > 32 * L.nv; L.nv *= 2) {}
         return L;
     }
-    // a CTA per row: two vectors a thread while its threads hold the row so, else more.  Rows that leave
+    // a CTA per row: two pieces a thread while its threads hold the row so, else more.  Rows that leave
     // multiprocessors free take one, for the shorter way through the kernel (16 rows of 2048: 2.5 us
     // instead of 2.9; 8191 rows of 5120: 62 us instead of 53).
     const bool few = rows <= sm_count_cached();
-    const int most = L.vec == 1 ? 16 : 4;
-    for (L.nv = L.vec == 1 ? 2 : few ? 1 : 2; L.nv <= most; L.nv *= 2) {
+    for (L.nv = !wide ? 8 : few ? 1 : 2; L.nv <= (wide ? 4 : 16); L.nv *= 2) {
         L.threads = ((n + L.nv - 1) / L.nv + 31) / 32 * 32;
         if (L.threads <= max_threads(L.vec, L.nv, 0, backward)) return L;
     }
     L.vec = 0;
+    L.shift = false;
     L.threads = LOOP_T;
     return L;
 }
@@ -508,65 +583,82 @@ int resident(const void* kern, int threads, size_t smem) {
     return r;
 }
 
-template <int OUT8, typename T, int VEC, int NV, int LPR>
+template <int OUT8, typename T, int VEC, int NV, int LPR, bool SHIFT>
 cudaError_t fwd_launch(const NormArgs& A, const Layout& L, cudaStream_t st) {
     const int64_t blocks = (A.p.rows + L.per() - 1) / L.per();
     const size_t smem = OUT8 == 3 ? size_t(L.per()) * (A.p.dim / A.p.group) * 4 : 0;
     if (smem > 40 * 1024) {
-        const cudaError_t e = smem_attr(k_norm_fwd<T, VEC, NV, LPR, OUT8>, int(smem));
+        const cudaError_t e = smem_attr(k_norm_fwd<T, VEC, NV, LPR, SHIFT, OUT8>, int(smem));
         if (e != cudaSuccess) return e;
     }
-    k_norm_fwd<T, VEC, NV, LPR, OUT8><<<unsigned(blocks), L.threads, smem, st>>>(A);
+    k_norm_fwd<T, VEC, NV, LPR, SHIFT, OUT8><<<unsigned(blocks), L.threads, smem, st>>>(A);
     return cudaGetLastError();
 }
-template <typename T, int VEC, int NV, int LPR>
+template <typename T, int VEC, int NV, int LPR, bool SHIFT>
 cudaError_t fwd_out(const NormArgs& A, const Layout& L, cudaStream_t st) {
-    if (A.p.out_dtype != GDN_E4M3) return fwd_launch<0, T, VEC, NV, LPR>(A, L, st);
-    if (A.p.group == 0 || A.p.group == A.p.dim) return fwd_launch<1, T, VEC, NV, LPR>(A, L, st);
-    const int lanes = A.p.group % VEC ? 0 : A.p.group / VEC;
-    const int whole = LPR ? LPR : 32;
-    if (lanes > 0 && lanes <= whole && (lanes & (lanes - 1)) == 0) return fwd_launch<2, T, VEC, NV, LPR>(A, L, st);
-    return fwd_launch<3, T, VEC, NV, LPR>(A, L, st);
+    if (A.p.out_dtype != GDN_E4M3) return fwd_launch<0, T, VEC, NV, LPR, SHIFT>(A, L, st);
+    if (A.p.group == 0 || A.p.group == A.p.dim) return fwd_launch<1, T, VEC, NV, LPR, SHIFT>(A, L, st);
+    if constexpr (SHIFT) {
+        return cudaErrorNotSupported;  // groups of rows that lie off 16-byte pieces go value by value
+    } else {
+        const int lanes = A.p.group % VEC ? 0 : A.p.group / VEC;
+        const int whole = LPR ? LPR : 32;
+        if (lanes > 0 && lanes <= whole && (lanes & (lanes - 1)) == 0) return fwd_launch<2, T, VEC, NV, LPR, SHIFT>(A, L, st);
+        return fwd_launch<3, T, VEC, NV, LPR, SHIFT>(A, L, st);
+    }
 }
 
-template <typename T, int VEC, int NV, int LPR>
+template <typename T, int VEC, int NV, int LPR, bool SHIFT>
 cudaError_t bwd_out(const NormArgs& A, const Layout& L, int& parts, cudaStream_t st) {
     const size_t smem = LPR ? size_t(L.per()) * A.p.dim * 4 : 0;
-    const int fit = resident(reinterpret_cast<const void*>(k_norm_bwd<T, VEC, NV, LPR>), L.threads, smem) * sm_count_cached();
+    const int fit = resident(reinterpret_cast<const void*>(k_norm_bwd<T, VEC, NV, LPR, SHIFT>), L.threads, smem) * sm_count_cached();
     if (parts > fit) parts = fit;  // one wave: the rows are dealt out to the CTAs in turn
-    k_norm_bwd<T, VEC, NV, LPR><<<parts, L.threads, smem, st>>>(A);
+    // four rows to a CTA at least where the multiprocessors have one each: a CTA's share of dweight costs as much
+    // as a row or two (2003 rows of 1024: 10.1 us instead of 11.7)
+    const int64_t quarter = A.p.rows / 4, sms = sm_count_cached();
+    if (parts > quarter && parts > sms) parts = int(quarter > sms ? quarter : sms);
+    if (SHIFT) parts = parts > 8 ? parts / 8 * 8 : 8;
+    k_norm_bwd<T, VEC, NV, LPR, SHIFT><<<parts, L.threads, smem, st>>>(A);
     return cudaGetLastError();
 }
 
-// Calls f<VEC, NV, LPR> for the layout.
+// Calls f<VEC, NV, LPR, SHIFT> for the layout.
+#define NORM_WIDE(F, T, FULL, SHIFT, ...)                                          \
+    do {                                                                            \
+        if (L.lpr == 8) return F<T, FULL, 1, 8, SHIFT>(__VA_ARGS__);                \
+        if (L.lpr == 16) return F<T, FULL, 1, 16, SHIFT>(__VA_ARGS__);              \
+        if (L.lpr == 32 && L.nv == 1) return F<T, FULL, 1, 32, SHIFT>(__VA_ARGS__); \
+        if (L.lpr == 32) return F<T, FULL, 2, 32, SHIFT>(__VA_ARGS__);              \
+        if (L.nv == 1) return F<T, FULL, 1, 0, SHIFT>(__VA_ARGS__);                 \
+        if (L.nv == 2) return F<T, FULL, 2, 0, SHIFT>(__VA_ARGS__);                 \
+        return F<T, FULL, 4, 0, SHIFT>(__VA_ARGS__);                                \
+    } while (0)
 #define NORM_LAYOUTS(F, T, FULL, ...)                                              \
     do {                                                                            \
-        if (L.vec == FULL) {                                                        \
-            if (L.lpr == 8) return F<T, FULL, 1, 8>(__VA_ARGS__);                   \
-            if (L.lpr == 16) return F<T, FULL, 1, 16>(__VA_ARGS__);                 \
-            if (L.lpr == 32 && L.nv == 1) return F<T, FULL, 1, 32>(__VA_ARGS__);    \
-            if (L.lpr == 32) return F<T, FULL, 2, 32>(__VA_ARGS__);                 \
-            if (L.nv == 1) return F<T, FULL, 1, 0>(__VA_ARGS__);                    \
-            if (L.nv == 2) return F<T, FULL, 2, 0>(__VA_ARGS__);                    \
-            return F<T, FULL, 4, 0>(__VA_ARGS__);                                   \
-        }                                                                           \
-        if (L.lpr == 8) return F<T, 1, 1, 8>(__VA_ARGS__);                          \
-        if (L.lpr == 16) return F<T, 1, 1, 16>(__VA_ARGS__);                        \
-        if (L.lpr == 32 && L.nv == 1) return F<T, 1, 1, 32>(__VA_ARGS__);           \
-        if (L.lpr == 32) return F<T, 1, 2, 32>(__VA_ARGS__);                        \
-        if (L.nv == 2) return F<T, 1, 2, 0>(__VA_ARGS__);                           \
-        if (L.nv == 4) return F<T, 1, 4, 0>(__VA_ARGS__);                           \
-        if (L.nv == 8) return F<T, 1, 8, 0>(__VA_ARGS__);                           \
-        return F<T, 1, 16, 0>(__VA_ARGS__);                                         \
+        if (L.shift) NORM_WIDE(F, T, FULL, true, __VA_ARGS__);                      \
+        if (L.vec > 1) NORM_WIDE(F, T, FULL, false, __VA_ARGS__);                   \
+        if (L.lpr == 8) return F<T, 1, 1, 8, false>(__VA_ARGS__);                   \
+        if (L.lpr == 16) return F<T, 1, 1, 16, false>(__VA_ARGS__);                 \
+        if (L.lpr == 32 && L.nv <= 2) return F<T, 1, 2, 32, false>(__VA_ARGS__);    \
+        if (L.lpr == 32 && L.nv <= 8) return F<T, 1, 8, 32, false>(__VA_ARGS__);    \
+        if (L.lpr == 32) return F<T, 1, 16, 32, false>(__VA_ARGS__);                \
+        if (L.nv == 8) return F<T, 1, 8, 0, false>(__VA_ARGS__);                    \
+        return F<T, 1, 16, 0, false>(__VA_ARGS__);                                  \
     } while (0)
+
+bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 template <typename T>
 cudaError_t fwd_type(const NormArgs& A, cudaStream_t st) {
     const gdn_norm_problem& p = A.p;
     const int full = full_vec(p.dtype);
-    const bool vectors = p.dim % full == 0 && p.x_stride % full == 0 && p.residual_stride % full == 0 && wide(A.x) && wide(A.residual) &&
-                         wide(A.weight) && wide(A.y) && wide(A.sum);
-    const Layout L = layout_of(p.rows, p.dim, full, vectors, false);
+    const bool rows16 = on16(A.x) && on16(A.residual) && on16(A.sum) && on16(A.y);
+    const bool vectors = rows16 && on16(A.weight) && p.dim % full == 0 && p.x_stride % full == 0 && p.residual_stride % full == 0;
+    const bool groups = p.out_dtype == GDN_E4M3 && p.group != 0 && p.group != p.dim;
+    // short rows are quicker value by value, a warp to a row (38544 rows of 235: 15.1 us instead of 17.8; 30000
+    // of 1001: 72 instead of 40)
+    const bool shift = p.dim > 512 && !vectors && rows16 && !groups && p.x_stride == p.dim && (!A.residual || p.residual_stride == p.dim);
+    const Layout L = layout_of(p.rows, p.dim, vectors || shift ? full : 1, shift, false);
     if (L.vec == 0) {
         k_norm_fwd_loop<T><<<unsigned(p.rows), LOOP_T, 0, st>>>(A);
         return cudaGetLastError();
@@ -594,10 +686,14 @@ cudaError_t bwd_type(const NormArgs& A, const Layout& L, int& parts, cudaStream_
 
 // CTAs of the backward at most, whatever the pointers' alignment turns out to be.
 int norm_bwd_parts(const gdn_norm_problem& p) {
-    const int a = parts_of(p, layout_of(p.rows, p.dim, full_vec(p.dtype), false, true));
-    if (p.dim % full_vec(p.dtype)) return a;
-    const int b = parts_of(p, layout_of(p.rows, p.dim, full_vec(p.dtype), true, true));
-    return a > b ? a : b;
+    const int full = full_vec(p.dtype);
+    int most = 8;
+    for (int i = 0; i < 3; ++i) {
+        if (i == 1 && p.dim % full) continue;
+        const int n = parts_of(p, layout_of(p.rows, p.dim, i ? full : 1, i == 2, true));
+        if (n > most) most = n;
+    }
+    return most;
 }
 
 cudaError_t launch_norm_fwd(const NormArgs& A, cudaStream_t st) {
@@ -610,9 +706,10 @@ cudaError_t launch_norm_fwd(const NormArgs& A, cudaStream_t st) {
 cudaError_t launch_norm_bwd(const NormArgs& A, cudaStream_t st) {
     const gdn_norm_problem& p = A.p;
     const int full = full_vec(p.dtype);
-    const bool vectors = p.dim % full == 0 && p.x_stride % full == 0 && p.dy_stride % full == 0 && p.dsum_stride % full == 0 && wide(A.x) &&
-                         wide(A.dy) && wide(A.dsum) && wide(A.weight) && wide(A.dx);
-    const Layout L = layout_of(p.rows, p.dim, full, vectors, true);
+    const bool rows16 = on16(A.x) && on16(A.dy) && on16(A.dsum) && on16(A.dx);
+    const bool vectors = rows16 && on16(A.weight) && p.dim % full == 0 && p.x_stride % full == 0 && p.dy_stride % full == 0 && p.dsum_stride % full == 0;
+    const bool shift = !vectors && rows16 && p.x_stride == p.dim && p.dy_stride == p.dim && (!A.dsum || p.dsum_stride == p.dim);
+    const Layout L = layout_of(p.rows, p.dim, vectors || shift ? full : 1, shift, true);
     int parts = parts_of(p, L);
     timing_begin("rmsnorm_bwd", st);
     const cudaError_t e = p.dtype == GDN_BF16 ? bwd_type<__nv_bfloat16>(A, L, parts, st) : bwd_type<float>(A, L, parts, st);

@@ -14,7 +14,7 @@ from oracle import decode
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
-SHAPES = [(1, 1), (3, 7), (5, 64), (2, 1000), (17, 1024), (4, 2048), (3, 4100), (2, 5120), (1, 8192), (2, 16384), (1, 20000)]
+SHAPES = [(1, 1), (3, 7), (40, 77), (33, 235), (9, 1001), (3, 5001), (2, 8190), (5, 64), (2, 1000), (17, 1024), (4, 2048), (3, 4100), (2, 5120), (1, 8192), (2, 16384), (1, 20000)]
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -66,7 +66,7 @@ def test_forward(rows, dim, dtype, residual, offset):
 
 
 @pytest.mark.parametrize("rows,dim,group", [(1, 1, 0), (3, 7, 0), (2, 1000, 8), (17, 1024, 128), (4, 2048, 0), (3, 4100, 4), (2, 5120, 128), (3, 8192, 64),
-                                            (2, 16384, 0), (1, 20000, 0), (1, 20000, 32), (2, 384, 384), (2, 768, 256), (2, 640, 5)])
+                                            (2, 16384, 0), (1, 20000, 0), (1, 20000, 32), (2, 384, 384), (2, 768, 256), (2, 640, 5), (33, 235, 0), (9, 1001, 0), (9, 1002, 6), (3, 5001, 0)])
 @pytest.mark.parametrize("dtype,residual", [(BF, True), (BF, False), (F32, True)])
 def test_8_bit_output(rows, dim, group, dtype, residual):
     from chunked_prefill_gb300 import gdn
