@@ -120,6 +120,7 @@ at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, const at::Tensor& l
 }
 // device scratch of n bytes: the caller's where it is large enough
 at::Tensor scratch(size_t n, const at::Tensor* given, const at::Tensor& like) {
+    if (n == 0) return like;  // not used
     if (given && size_t(given->numel()) * given->element_size() >= n) return *given;
     return empty({int64_t(n < 16 ? 16 : n)}, at::kByte, like);
 }
@@ -224,7 +225,14 @@ PyObject* paged(Args& a) {
     const double scale = a.number();
     const at::Tensor *kn = a.maybe("k_new"), *vn = a.maybe("v_new"), *ks = a.maybe("k_scale"), *vs = a.maybe("v_scale");
     const int64_t window = a.integer();
-    const at::Tensor *given = a.maybe("o"), *lse = a.maybe("lse"), *ws = a.maybe("workspace");
+    const at::Tensor* given = a.maybe("o");
+    const bool make_lse = a.at < a.n && a.a[a.at] == Py_True;  // lse: a tensor, None, or True for a new one
+    const at::Tensor* lse = nullptr;
+    if (make_lse)
+        ++a.at;
+    else
+        lse = a.maybe("lse");
+    const at::Tensor* ws = a.maybe("workspace");
     need(q.dim() == 3 && kc.dim() == 4 && vc.sizes() == kc.sizes(), "q must be [N,Hq,D], k_cache and v_cache [num_pages,page_size,Hkv,D]");
     const int64_t N = q.size(0), Hq = q.size(1), D = q.size(2), Hkv = kc.size(2);
     need(kc.size(3) == D, "q and the caches must match in D");
@@ -289,9 +297,19 @@ PyObject* paged(Args& a) {
     size_t bytes = 0;
     check(f_paged_size(&p, &bytes));
     const at::Tensor work = scratch(bytes, ws, q), o = given ? *given : empty(q.sizes(), q.scalar_type(), q);
+    at::Tensor new_lse;
+    if (make_lse) {
+        new_lse = empty({N, Hq}, at::kFloat, q);
+        lse = &new_lse;
+    }
     check(f_paged(&p, q.data_ptr(), kc.data_ptr(), vc.data_ptr(), ptr<int32_t>(table), ptr<int32_t>(lens), ptr<void>(kn), ptr<void>(vn), ptr(ks), ptr(vs),
-                  o.data_ptr(), ptr(lse), work.data_ptr(), size_t(work.numel()) * work.element_size(), on.stream));
-    return THPVariable_Wrap(o);
+                  o.data_ptr(), ptr(lse), bytes ? work.data_ptr() : nullptr, bytes ? size_t(work.numel()) * work.element_size() : 0, on.stream));
+    if (!make_lse) return THPVariable_Wrap(o);
+    PyObject* r = PyTuple_New(2);
+    if (!r) throw Bad{nullptr, ""};
+    PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(o));
+    PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(new_lse));
+    return r;
 }
 
 // The elements between the rows of a [..., dim] tensor (0: contiguous).

@@ -606,20 +606,14 @@ def paged_attention_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None
     token's key and value, which the call then writes to position seq_lens - 1 of the caches
     before it attends to them.  window > 0 attends to the last `window` tokens.  For inference:
     nothing is differentiated here."""
-    if stream is not None:  # what is allocated here belongs to that stream, too
-        with torch.cuda.stream(stream):
-            return paged_attention_decode(q, k_cache, v_cache, page_table, seq_lens, scale, k_new, v_new,
-                                          k_scale, v_scale, window, return_lse, o, workspace)
     native = _native or _binding()
     if native.wants_grad(q, k_new, v_new):
         raise RuntimeError("paged_attention_decode is not differentiable, but an argument requires "
                            "a gradient")
     if scale is None:
         scale = q.shape[-1] ** -0.5
-    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if return_lse else None
-    o = native.paged(q, k_cache, v_cache, page_table, seq_lens, scale, k_new, v_new, k_scale,
-                     v_scale, window, o, lse, workspace, None)
-    return (o, lse) if return_lse else o
+    return native.paged(q, k_cache, v_cache, page_table, seq_lens, scale, k_new, v_new, k_scale,
+                        v_scale, window, o, True if return_lse else None, workspace, stream)
 
 
 def gdn_rmsnorm_fwd(x, weight, residual=None, eps=1e-6, weight_offset=0.0, quant=False, group=0,

@@ -193,3 +193,28 @@ def test_refusals():
         gdn.rms_norm(x, w, weight_offset=float("inf"))
     with pytest.raises(TypeError):
         gdn.rms_norm(x.half(), w)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows,dim", [(5, 1024), (7, 1001), (3, 235), (2, 20000)])
+def test_in_place(dtype, rows, dim):
+    """sum over the residual and y over x; dx over dy: the bits of the calls with outputs of their own."""
+    import ctypes
+    from chunked_prefill_gb300 import gdn
+    d = make(rows, dim, dtype, True, 6)
+    x = cuda(d)
+    want = gdn.rms_norm(x["x"], x["weight"], residual=x["residual"])
+    code = gdn._dtype_code(dtype)
+    p = gdn.GdnNormProblem(rows, dim, code, code, code, 0, 1e-6, 0.0)
+    xi, ri, dyi = x["x"].clone(), x["residual"].clone(), x["dy"].clone()
+    L = gdn.lib()
+    gdn._check(L.gdn_rmsnorm_fwd(ctypes.byref(p), xi.data_ptr(), ri.data_ptr(), x["weight"].data_ptr(), xi.data_ptr(), None, ri.data_ptr(),
+                                 torch.cuda.current_stream().cuda_stream))
+    assert torch.equal(xi, want[0]) and torch.equal(ri, want[1])
+    gwant = gdn.gdn_rmsnorm_bwd(x["x"], x["weight"], x["dy"])
+    n = ctypes.c_size_t(0)
+    gdn._check(L.gdn_rmsnorm_bwd_workspace_size(ctypes.byref(p), ctypes.byref(n)))
+    ws, dw = torch.empty(n.value, dtype=torch.uint8, device="cuda"), torch.empty(dim, device="cuda")
+    gdn._check(L.gdn_rmsnorm_bwd(ctypes.byref(p), x["x"].data_ptr(), x["weight"].data_ptr(), dyi.data_ptr(), None, dyi.data_ptr(), dw.data_ptr(),
+                                 ws.data_ptr(), n.value, torch.cuda.current_stream().cuda_stream))
+    assert torch.equal(dyi, gwant[0]) and torch.equal(dw, gwant[1])

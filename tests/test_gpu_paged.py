@@ -246,3 +246,49 @@ def test_refusals():
         f(x["q"][..., :96].contiguous(), x["k"][..., :96].contiguous(), x["v"][..., :96].contiguous(), *args[3:])
     with pytest.raises(RuntimeError, match="differentiable"):
         f(x["q"].clone().requires_grad_(True), *args[1:])
+
+
+@pytest.mark.parametrize("cache", [BF, FP8, F32])
+def test_one_large_weight_beside_many_small_ones(cache):
+    """A first token that takes most of the weight, and thousands of others at e^-12 of it, whose
+    values agree: their sum still counts."""
+    L = 6000
+    x = make([L], 2, 1, 128, 16, cache, seed=13)
+    scale = 128 ** -0.5
+    x["q"].fill_(1.0)
+    pages = [int(p) for p in x["table"][0, :L // 16]]
+    x["k"][pages] = torch.zeros(1, device="cuda").to(x["k"].dtype) if cache != FP8 else 0
+    x["k"].view(torch.uint8)[pages[0], 0] = torch.full((1, 128), 12 * 128 ** 0.5 / 128, device="cuda").to(cache).view(torch.uint8)
+    x["v"].view(torch.uint8)[pages] = torch.full((375, 16, 1, 128), 2.0, device="cuda").to(cache).view(torch.uint8)
+    x["v"].view(torch.uint8)[pages[0], 0] = torch.full((1, 128), -1.0, device="cuda").to(cache).view(torch.uint8)
+    if x["ks"] is not None:
+        x["ks"].fill_(1.0)
+        x["vs"].fill_(1.0)
+    check(x, *call(x), scale=scale)
+
+
+@pytest.mark.parametrize("cache", [BF, FP8, F32])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_not_finite_rows_stay_where_they_are(cache, bad):
+    """An infinite or NaN query row, and a NaN value row that is attended to, give NaN in their own
+    heads alone."""
+    x = make([200, 50, 2000], 8, 2, 128, 16, cache, seed=17)
+    x["q"][1, 2, 5] = bad
+    page = int(x["table"][0, 3])
+    x["v"].view(torch.uint8)[page, 7, 1] = 0x7F if cache == FP8 else 0xFF
+    o, lse = call(x)
+    nan = torch.isnan(o).any(-1)
+    want = torch.zeros(3, 8, dtype=torch.bool, device="cuda")
+    want[1, 2] = True
+    want[0, 4:] = True
+    assert torch.equal(nan, want)
+
+
+def test_many_sequences_and_many_heads():
+    """More (sequence, kv-head) pairs than multiprocessors hold CTAs, split and unsplit."""
+    gen = torch.Generator().manual_seed(1)
+    for most in (3, 3000):
+        lens = torch.randint(0, most + 1, (90,), generator=gen).tolist()
+        lens[0] = most
+        x = make(lens, 8, 8, 64, 32, BF, seed=most)
+        check(x, *call(x))
