@@ -47,7 +47,7 @@ struct PagedArgs {
     const float *k_scale, *v_scale;
     void* o;
     float* lse;
-    bool unsplit;     // a CTA per (sequence, block of heads), nothing to join
+    int cluster;      // CTAs per (sequence, block of heads), joined in the kernel; 0: parts of a list
     int groups;       // of blocks of query heads (a block shares a kv-head)
     int heads;        // blocks in a group
     int64_t* before;  // [num_seqs + 1] tiles before each sequence, per block of heads
@@ -59,7 +59,7 @@ struct PagedArgs {
 // groups of heads), rows to a block of query heads, and the bytes of the workspace (before, part_ml, part, in this order).
 struct PagedPlan {
     int ctas, rows, groups, heads;
-    bool unsplit;
+    int cluster;
     size_t off_ml, off_part, bytes;
 };
 PagedPlan paged_plan(const gdn_paged_problem& p);

@@ -214,7 +214,7 @@ gdn_status gdn_paged_attn_decode(const gdn_paged_problem* problem, const void* q
     A.o = o;
     A.lse = lse;
     char* ws = static_cast<char*>(workspace);
-    A.unsplit = plan.unsplit;
+    A.cluster = plan.cluster;
     A.groups = plan.groups;
     A.heads = plan.heads;
     A.before = reinterpret_cast<int64_t*>(ws);

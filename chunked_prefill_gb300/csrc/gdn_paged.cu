@@ -66,7 +66,7 @@ __device__ __forceinline__ Range range_of(const PagedArgs& A, int n) {
 // `head` (of the group's A.heads) of sequence n.
 struct Part {
     int64_t lo, hi;
-    int n, head, at;
+    int n, group, head, at;
 };
 // a / b for a >= 0, b > 0; 64-bit division costs half a microsecond that small problems feel
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
@@ -79,9 +79,11 @@ __device__ __forceinline__ int64_t share_of(int64_t total, int parts, int warps)
 // CTA 0 also leaves the number of tiles before each sequence (per block of heads) in A.before.
 template <int T>
 __device__ Part find_part(const PagedArgs& A, int tok, int warps) {
-    if (A.unsplit) {  // a CTA per (sequence, block of heads)
-        const int blocks = A.groups * A.heads, n = blockIdx.x / blocks;
-        return {0, range_of(A, n).tiles(tok), n, int(blockIdx.x % blocks) / A.groups, 0};
+    if (A.cluster) {  // a cluster of CTAs per (sequence, block of heads), equal parts of its tiles
+        const int pair = blockIdx.x / A.cluster, r = blockIdx.x % A.cluster, blocks = A.groups * A.heads, n = pair / blocks, b = pair % blocks;
+        const int tiles = range_of(A, n).tiles(tok), share = ((tiles + A.cluster - 1) / A.cluster + warps - 1) / warps * warps;
+        const int at = min(r * share, tiles);
+        return {0, min(share, tiles - at), n, b % A.groups, b / A.groups, at};
     }
     __shared__ int64_t wsum[T / 32];
     __shared__ int found[3];
@@ -128,12 +130,67 @@ __device__ Part find_part(const PagedArgs& A, int tok, int warps) {
         found[2] = int(rest - head * t);
     }
     __syncthreads();
-    P.n = found[0], P.head = found[1], P.at = found[2];
+    P.n = found[0], P.group = blockIdx.x % A.groups, P.head = found[1], P.at = found[2];
     return P;
 }
 // Where a CTA leaves rows [0, ROWS) of a pair that it has a part of: in its first place where the
 // pair began before its part, in its second where the pair goes on after it.
 __device__ __forceinline__ int64_t place_of(int cta, bool first, int rows) { return (int64_t(cta) * 2 + (first ? 0 : 1)) * rows; }
+
+// ---- clusters: the join through distributed shared memory
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, int rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+// Joins the cluster's CTAs' results -- rows of D at `res`, (max, sum) pairs at `ml`, at the same places of
+// every CTA's shared memory -- in rank order, each CTA a slice of the values, and writes them out.
+template <typename Act, int D, int T>
+__device__ void join_cluster(const PagedArgs& A, uint32_t res, uint32_t ml, int n, int hk, int hb, int rows) {
+    const gdn_paged_problem& p = A.p;
+    const int r = blockIdx.x % A.cluster, total = rows * (D / 4), each = (total + A.cluster - 1) / A.cluster;
+    const float vs = A.v_scale ? A.v_scale[hk] : 1.f;
+    cluster_sync();
+    for (int i = r * each + threadIdx.x; i < min(total, (r + 1) * each); i += T) {
+        const int h = i / (D / 4), d = i % (D / 4) * 4;
+        float2 m[8];
+        float4 x[8];
+        float M = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            if (c >= A.cluster) continue;
+            asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];\n" : "=f"(m[c].x), "=f"(m[c].y) : "r"(in_cta(ml + h * 8, c)) : "memory");
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n"
+                         : "=f"(x[c].x), "=f"(x[c].y), "=f"(x[c].z), "=f"(x[c].w)
+                         : "r"(in_cta(res + (h * D + d) * 4, c))
+                         : "memory");
+            M = fmaxf(M, m[c].x);
+        }
+        float S = 0.f;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            if (c >= A.cluster || m[c].y == 0.f) continue;  // an empty part has no rows
+            const float w = m[c].x == -INFINITY ? 0.f : exp2f(m[c].x - M);
+            S = fmaf(m[c].y, w, S);
+            a.x = fmaf(x[c].x, w, a.x);
+            a.y = fmaf(x[c].y, w, a.y);
+            a.z = fmaf(x[c].z, w, a.z);
+            a.w = fmaf(x[c].w, w, a.w);
+        }
+        const int64_t row = int64_t(n) * p.Hq + hk * (p.Hq / p.Hkv) + hb + h;
+        const bool some = S > 0.f || S != S;
+        const float f = some ? vs / S : 0.f;
+        Act* o = static_cast<Act*>(A.o) + row * D + d;
+        st2(o, a.x * f, a.y * f);
+        st2(o + 2, a.z * f, a.w * f);
+        if (A.lse && d == 0) A.lse[row] = some ? (M + log2f(S)) * LN2 : -INFINITY;
+    }
+    cluster_sync();  // the others have read this CTA's results
+}
 
 // a value of the new token's row in the cache's type
 template <typename C> __device__ __forceinline__ C to_cache(float x, float scale);
@@ -183,15 +240,18 @@ __device__ __forceinline__ float sum16(float (&v)[16]) {
 template <int D>
 __global__ void __launch_bounds__(PT, D == 256 ? 2 : 4) k_paged(const PagedArgs A) {
     constexpr int E = D / 32;
-    __shared__ __align__(16) float acc_s[PW][GB][D];
+    __shared__ __align__(16) float acc_s[PW][GB][D], res_s[GB][D];
     __shared__ float ml_s[PW][GB][2];
+    __shared__ float2 res_ml[GB];
     const gdn_paged_problem& p = A.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = p.Hq / p.Hkv, nb = (G + GB - 1) / GB;
     tc::pdl_launch_dependents();
     Part P = find_part<PT>(A, PTOK, 1);
+    const Part P0 = P;
+    if (A.cluster > 1 && tid < GB) res_ml[tid] = make_float2(-INFINITY, 0.f);
     for (int64_t pos = P.lo; pos < P.hi;) {
-        const int n = P.n, block = P.head * A.groups + blockIdx.x % A.groups, hk = block / nb, hb = (block % nb) * GB;
+        const int n = P.n, block = P.head * A.groups + P.group, hk = block / nb, hb = (block % nb) * GB;
         const Range R = range_of(A, n);
         const int tiles = R.tiles(PTOK), end = int(min(int64_t(tiles), P.at + (P.hi - pos)));
         const bool whole = P.at == 0 && end == tiles, began = P.at > 0;
@@ -322,7 +382,10 @@ __global__ void __launch_bounds__(PT, D == 256 ? 2 : 4) k_paged(const PagedArgs 
                 S = fmaf(ml_s[g][h][1], c, S);
                 a = fmaf(acc_s[g][h][d], c, a);
             }
-            if (whole) {
+            if (A.cluster > 1) {
+                res_s[h][d] = a;
+                if (d == 0) res_ml[h] = make_float2(M, S);
+            } else if (whole) {
                 const int64_t row = int64_t(n) * p.Hq + hk * G + hb + h;
                 const bool some = S > 0.f || S != S;
                 static_cast<float*>(A.o)[row * D + d] = some ? a / S * vs : 0.f;
@@ -334,6 +397,10 @@ __global__ void __launch_bounds__(PT, D == 256 ? 2 : 4) k_paged(const PagedArgs 
             }
         }
         __syncthreads();  // the shared arrays are read before the next pair writes them
+    }
+    if (A.cluster > 1) {
+        const int block = P0.head * A.groups + P0.group, hb = (block % nb) * GB;
+        join_cluster<float, D, PT>(A, tc::smem_addr(res_s), tc::smem_addr(res_ml), P0.n, block / nb, hb, min(GB, G - hb));
     }
 }
 
@@ -414,7 +481,7 @@ template <typename C, int D> struct Tile {
     static constexpr int FIT = (CTAS == 3 ? 65536 : 98304) / (W * BYTES), STAGES = FIT < 8 ? FIT : 8;
     static constexpr int PAD = D + 4;                              // floats between rows of the joined accumulators
     static constexpr int SMEM = STAGES * W * BYTES;
-    static_assert(STAGES >= 2 && W * 16 * PAD * 4 <= SMEM, "the warps' accumulators are joined in the stages' memory");
+    static_assert(STAGES >= 2 && W * 16 * PAD * 4 + 16 * D * 4 <= SMEM, "the warps' accumulators are joined in the stages' memory");
     // what a row's pieces are exchanged by
     static __host__ __device__ constexpr int swap(int row) { return CPR == 4 ? (row >> 1) & 3 : row & 7; }
 };
@@ -471,9 +538,13 @@ __global__ void __launch_bounds__(Tile<C, D>::T, Tile<C, D>::CTAS) k_paged_mma(c
 
     tc::pdl_launch_dependents();
     Part P = find_part<L::T>(A, TOK, W);
+    const Part P0 = P;
+    float* res = reinterpret_cast<float*>(smem) + W * 16 * L::PAD;  // clusters: this CTA's result
+    __shared__ float2 res_ml[16];
+    if (A.cluster > 1 && tid < 16) res_ml[tid] = make_float2(-INFINITY, 0.f);
     for (int64_t pos = P.lo; pos < P.hi;) {
         // ---- the next (sequence, block of heads) and this CTA's tiles of it
-        const int n = P.n, block = P.head * A.groups + blockIdx.x % A.groups, hk = block / nb, hb = (block % nb) * 16;
+        const int n = P.n, block = P.head * A.groups + P.group, hk = block / nb, hb = (block % nb) * 16;
         const Range R = range_of(A, n);
         const int tiles_n = R.tiles(TOK), end = int(min(int64_t(tiles_n), P.at + (P.hi - pos)));
         const bool whole = P.at == 0 && end == tiles_n, began = P.at > 0;
@@ -844,7 +915,10 @@ __global__ void __launch_bounds__(Tile<C, D>::T, Tile<C, D>::CTAS) k_paged_mma(c
                 a.z = fmaf(x.z, c, a.z);
                 a.w = fmaf(x.w, c, a.w);
             }
-            if (whole) {
+            if (A.cluster > 1) {
+                *reinterpret_cast<float4*>(res + h * D + d) = a;
+                if (d == 0) res_ml[h] = make_float2(M, S);
+            } else if (whole) {
                 const int64_t row = int64_t(n) * p.Hq + hk * G + hb + h;
                 const bool some = S > 0.f || S != S;
                 const float f = some ? vs / S : 0.f;
@@ -858,6 +932,10 @@ __global__ void __launch_bounds__(Tile<C, D>::T, Tile<C, D>::CTAS) k_paged_mma(c
             }
         }
         __syncthreads();  // the stages and ml_s are read before the next pair writes them
+    }
+    if (A.cluster > 1) {
+        const int block = P0.head * A.groups + P0.group, hb = (block % nb) * 16;
+        join_cluster<__nv_bfloat16, D, L::T>(A, tc::smem_addr(res), tc::smem_addr(res_ml), P0.n, block / nb, hb, min(16, G - hb));
     }
 }
 
@@ -949,6 +1027,8 @@ __global__ void __launch_bounds__(32 * JW) k_paged_join(const PagedArgs A, int t
     if (A.lse && lane == 0) A.lse[row] = some ? (M + log2f(S)) * LN2 : -INFINITY;
 }
 
+constexpr int CLUSTER_WORK = 4096;  // values of a key row's feature times tokens per warp that are not worth splitting
+
 // What the launches need to know of a kernel.
 struct Shape {
     int tok, rows, warps, ctas;  // tokens of a tile, rows of a block of heads, warps that share tiles, CTAs per multiprocessor
@@ -962,9 +1042,25 @@ Shape shape_of(const gdn_paged_problem& p) {
     return p.D == 64 ? mma_shape<__nv_fp8_e4m3, 64>() : p.D == 128 ? mma_shape<__nv_fp8_e4m3, 128>() : mma_shape<__nv_fp8_e4m3, 256>();
 }
 
+template <typename... K>
+cudaError_t launch_clusters(void (*kern)(K...), const PagedArgs& A, int ctas, int threads, size_t smem, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = A.cluster > 1 ? A.cluster : 1;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = A.cluster > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, A);
+}
+
 template <typename Act, int D>
 cudaError_t launch_join(const PagedArgs& A, const PagedPlan& plan, const Shape& s, cudaStream_t st) {
-    if (plan.unsplit) return cudaGetLastError();
+    if (plan.cluster) return cudaGetLastError();
     const int64_t rows = int64_t(A.p.num_seqs) * A.p.Hq;
     timing_begin("paged_attn_join", st);
     const cudaError_t e =
@@ -977,19 +1073,21 @@ cudaError_t launch_join(const PagedArgs& A, const PagedPlan& plan, const Shape& 
 template <int D>
 cudaError_t launch_fp32(const PagedArgs& A, const PagedPlan& plan, cudaStream_t st) {
     timing_begin("paged_attn", st);
-    k_paged<D><<<plan.ctas, PT, 0, st>>>(A);
+    const cudaError_t e = launch_clusters(k_paged<D>, A, plan.ctas, PT, 0, st);
     timing_end(st);
+    if (e != cudaSuccess) return e;
     return launch_join<float, D>(A, plan, fp32_shape<D>(), st);
 }
 
 template <typename C, int D, bool HALF, bool TILED>
 cudaError_t launch_mma(const PagedArgs& A, const PagedPlan& plan, cudaStream_t st) {
     using L = Tile<C, D>;
-    const cudaError_t e = smem_attr(k_paged_mma<C, D, HALF, TILED>, L::SMEM);
+    cudaError_t e = smem_attr(k_paged_mma<C, D, HALF, TILED>, L::SMEM);
     if (e != cudaSuccess) return e;
     timing_begin("paged_attn", st);
-    k_paged_mma<C, D, HALF, TILED><<<plan.ctas, L::T, L::SMEM, st>>>(A);
+    e = launch_clusters(k_paged_mma<C, D, HALF, TILED>, A, plan.ctas, L::T, L::SMEM, st);
     timing_end(st);
+    if (e != cudaSuccess) return e;
     return launch_join<__nv_bfloat16, D>(A, plan, mma_shape<C, D>(), st);
 }
 
@@ -1026,18 +1124,22 @@ PagedPlan paged_plan(const gdn_paged_problem& p) {
     const int64_t tiles = (most / s.tok + 1) * r.heads * p.num_seqs, want = (tiles + s.warps - 1) / s.warps;
     const int parts = full / r.groups;
     r.ctas = r.groups * int(want < parts ? (want > 0 ? want : 1) : parts);
-    // Short caches are not split: finding a CTA's part of the list and joining take 4 to 5 us, the time of
-    // some 16384 / D tokens per warp.  With one CTA to a (sequence, kv-head) a warp has at most `longest`
-    // tokens, in an even split longest * pairs / full.  Enough CTAs even themselves out, so that the
-    // list is worth its while from 512 tokens per warp on.
+    // Short caches take no list: a cluster of 1 to 8 CTAs has each (sequence, kv-head) and joins it through
+    // distributed shared memory.  Finding a CTA's part of the list and the second kernel take 4 to 5 us, the
+    // time of some 16384 / D tokens per warp; a cluster's warps have at most longest / c tokens, in an even
+    // split longest * pairs / full.  Enough CTAs even themselves out, so that the list is worth its while from
+    // 512 tokens per warp on.
     const int64_t pairs = int64_t(p.num_seqs) * blocks, longest = (most + s.warps - 1) / s.warps;
-    r.unsplit = pairs < (1 << 30) && (pairs >= full ? longest <= 512 : longest * (full - pairs) / full * p.D <= 16384);
-    if (r.unsplit) r.ctas = int(pairs);
+    int c = 1;
+    while (c < 8 && pairs * c * 2 <= full && longest * p.D > int64_t(c) * CLUSTER_WORK) c *= 2;
+    const bool brief = pairs >= full ? longest <= 512 : (longest / c - longest * pairs / full) * p.D <= 16384;
+    r.cluster = brief && pairs * c < (1 << 30) ? c : 0;
+    if (r.cluster) r.ctas = int(pairs * c);
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     r.off_ml = up(size_t(p.num_seqs + 1) * sizeof(int64_t));
     r.off_part = r.off_ml + up(size_t(r.ctas) * 2 * s.rows * sizeof(float2));
     r.bytes = r.off_part + size_t(r.ctas) * 2 * s.rows * p.D * sizeof(float);
-    if (r.unsplit) r.off_ml = r.off_part = r.bytes = 0;
+    if (r.cluster) r.off_ml = r.off_part = r.bytes = 0;
     return r;
 }
 
