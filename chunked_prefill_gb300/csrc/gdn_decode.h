@@ -60,9 +60,19 @@ struct PagedArgs {
 struct PagedPlan {
     int ctas, rows, groups, heads;
     int cluster;
+    bool solo;  // CTAs of one warp
     size_t off_ml, off_part, bytes;
 };
 PagedPlan paged_plan(const gdn_paged_problem& p);
+// What a launch needs to know of a kernel: tokens of a tile, rows of a block of heads, warps that share
+// tiles, CTAs per multiprocessor.
+struct PagedShape {
+    int tok, rows, warps, ctas;
+};
+PagedShape paged_shape_bf16(int D);
+PagedShape paged_shape_f8(int D);
+cudaError_t launch_paged_bf16(const PagedArgs& A, const PagedPlan& plan, cudaStream_t st);
+cudaError_t launch_paged_f8(const PagedArgs& A, const PagedPlan& plan, cudaStream_t st);
 cudaError_t launch_paged(const PagedArgs& A, cudaStream_t st);
 
 struct NormArgs {
@@ -76,6 +86,11 @@ struct NormArgs {
     float *dweight, *part;
 };
 int norm_bwd_parts(const gdn_norm_problem& p);
+// By the type of the rows; parts: the CTAs' shares of dweight that were written.
+cudaError_t norm_fwd_bf16(const NormArgs& A, cudaStream_t st);
+cudaError_t norm_fwd_fp32(const NormArgs& A, cudaStream_t st);
+cudaError_t norm_bwd_bf16(const NormArgs& A, int& parts, cudaStream_t st);
+cudaError_t norm_bwd_fp32(const NormArgs& A, int& parts, cudaStream_t st);
 cudaError_t launch_norm_fwd(const NormArgs& A, cudaStream_t st);
 cudaError_t launch_norm_bwd(const NormArgs& A, cudaStream_t st);
 
