@@ -84,6 +84,7 @@ struct NormArgs {
     const void *dy, *dsum;  // backward
     void* dx;
     float *dweight, *part;
+    float inv_dim;  // 1 / dim
 };
 int norm_bwd_parts(const gdn_norm_problem& p);
 // By the type of the rows; parts: the CTAs' shares of dweight that were written.

@@ -133,6 +133,8 @@ gdn_status check_norm(gdn_norm_problem& p, bool backward) {
     TRY(check_stride("residual_stride", p.residual_stride, p.dim, 1));
     TRY(check_stride("dy_stride", p.dy_stride, p.dim, 1));
     TRY(check_stride("dsum_stride", p.dsum_stride, p.dim, 1));
+    for (int64_t s : {p.x_stride, p.residual_stride, p.dy_stride, p.dsum_stride})
+        if (s > 0x7fffffff) return fail(GDN_ERR_UNSUPPORTED, "row strides of more than 2^31 - 1 values");
     return GDN_OK;
 }
 
@@ -239,6 +241,7 @@ gdn_status gdn_rmsnorm_fwd(const gdn_norm_problem* problem, const void* x, const
     TRY(check_ptr("y_scale", y_scale, 4, none || p.out_dtype != GDN_E4M3));
     TRY(check_ptr("sum", sum, e, true));
     if (none) return done(cudaSuccess);
+    A.inv_dim = 1.f / float(p.dim);
     A.x = x;
     A.residual = residual;
     A.weight = weight;
@@ -277,6 +280,7 @@ gdn_status gdn_rmsnorm_bwd(const gdn_norm_problem* problem, const void* s, const
     if (!workspace || workspace_bytes < need)
         return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? workspace_bytes : size_t(0));
     TRY(check_ptr("workspace", workspace, 16));
+    A.inv_dim = 1.f / float(p.dim);
     A.x = s;
     A.weight = weight;
     A.dy = dy;

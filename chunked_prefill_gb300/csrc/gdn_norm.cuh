@@ -26,7 +26,19 @@ constexpr int max_threads(int vec, int nv, int lpr, bool backward) {
     return lpr ? ROWS_T : vec == 1 ? (nv == 16 ? 512 : 256) : (backward || nv >= 2) ? 512 : 1024;
 }
 
-template <bool MAX> __device__ __forceinline__ float join(float a, float b) { return MAX ? mag_max(a, b) : a + b; }
+// the larger of two values, NaN if one is
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
+// 1 / x to 2^-23 of itself
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+template <bool MAX> __device__ __forceinline__ float join(float a, float b) { return MAX ? max_nan(a, b) : a + b; }
 
 template <bool MAX, int LANES>
 __device__ __forceinline__ float lane_red(float v) {
@@ -48,6 +60,8 @@ __device__ __forceinline__ float row_red(float v, float* red) {
         return lane_red<MAX, 32>(lane < warps ? red[lane] : 0.f);
     }
 }
+
+__device__ __forceinline__ int64_t wide_mul(uint32_t a, int64_t b) { return int64_t(uint64_t(a) * uint32_t(b)); }
 
 // VEC consecutive values as they lie in memory.
 template <typename T, int VEC> struct Vec {
@@ -154,7 +168,7 @@ __device__ __forceinline__ void store8(uint8_t* p, const float (&y)[VEC], float 
     }
 }
 
-__device__ __forceinline__ float scale_of(float mag) { return mag_max(mag * (1.f / F8_MAX), F8_TINY); }
+__device__ __forceinline__ float scale_of(float mag) { return max_nan(mag * (1.f / F8_MAX), F8_TINY); }
 
 // OUT8: 0 dtype out; 1 one scale per row; 2 groups of 2^n <= 32 lanes' vectors; 3 other groups
 // (magnitudes by shared-memory maxima, whose order does not matter).
@@ -165,12 +179,12 @@ __global__ void __launch_bounds__(max_threads(VEC, NV, LPR, false), LPR == 0 && 
     extern __shared__ uint32_t mags[];  // OUT8 == 3: per group of the CTA's row(s)
     const int tid = threadIdx.x, step = LPR ? LPR : blockDim.x, at0 = LPR ? tid % step : tid;
     const int per = LPR ? int(blockDim.x) / step : 1, mine = LPR ? tid / step : 0;  // rows per CTA, and this thread's
-    const int64_t row = int64_t(blockIdx.x) * per + mine;
-    const int a0 = SHIFT ? int(row * p.dim & (VEC - 1)) : 0, nvec = SHIFT ? (a0 + p.dim + VEC - 1) / VEC : p.dim / VEC;
-    const bool live = row < p.rows;
-    const T* x = static_cast<const T*>(A.x) + row * p.x_stride;
-    const T* res = static_cast<const T*>(A.residual) + row * p.residual_stride;
-    const int64_t left = (p.rows - row) * p.dim;
+    const uint32_t row = blockIdx.x * per + mine;  // rows, strides and dim are below 2^31, products of two 64 bits
+    const int a0 = SHIFT ? int(row * uint32_t(p.dim) & (VEC - 1)) : 0, nvec = SHIFT ? (a0 + p.dim + VEC - 1) / VEC : p.dim / VEC;
+    const bool live = row < uint32_t(p.rows);
+    const T* x = static_cast<const T*>(A.x) + wide_mul(row, p.x_stride);
+    const T* res = static_cast<const T*>(A.residual) + wide_mul(row, p.residual_stride);
+    const int64_t left = wide_mul(uint32_t(p.rows) - row, p.dim);
 
     Vec<T, VEC> xv[NV], rv[NV];
 #pragma unroll
@@ -196,7 +210,7 @@ __global__ void __launch_bounds__(max_threads(VEC, NV, LPR, false), LPR == 0 && 
         }
     }
     if (A.sum) {
-        T* sum = static_cast<T*>(A.sum) + row * p.dim;
+        T* sum = static_cast<T*>(A.sum) + wide_mul(row, p.dim);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int j = at0 + k * step;
@@ -207,7 +221,7 @@ __global__ void __launch_bounds__(max_threads(VEC, NV, LPR, false), LPR == 0 && 
             }
         }
     }
-    const float r = rsqrtf(row_red<false, LPR>(ss, red[0]) / float(p.dim) + p.eps);
+    const float r = rsqrtf(row_red<false, LPR>(ss, red[0]) * A.inv_dim + p.eps);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int j = at0 + k * step;
@@ -219,7 +233,7 @@ __global__ void __launch_bounds__(max_threads(VEC, NV, LPR, false), LPR == 0 && 
         }
     }
     if constexpr (OUT8 == 0) {
-        T* y = static_cast<T*>(A.y) + row * p.dim;
+        T* y = static_cast<T*>(A.y) + wide_mul(row, p.dim);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int j = at0 + k * step;
@@ -230,22 +244,22 @@ __global__ void __launch_bounds__(max_threads(VEC, NV, LPR, false), LPR == 0 && 
             }
         }
     } else {
-        uint8_t* y = static_cast<uint8_t*>(A.y) + row * p.dim;
+        uint8_t* y = static_cast<uint8_t*>(A.y) + wide_mul(row, p.dim);
         float mag[NV];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             mag[k] = 0.f;
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) mag[k] = mag_max(mag[k], fabsf(s[k][e]));
+            for (int e = 0; e < VEC; ++e) mag[k] = max_nan(mag[k], fabsf(s[k][e]));
         }
         const int groups = p.group ? p.dim / p.group : 1;
-        float* scales = A.y_scale + row * groups;
+        float* scales = A.y_scale + wide_mul(row, groups);
         if constexpr (OUT8 == 1) {
 #pragma unroll
-            for (int k = 1; k < NV; ++k) mag[0] = mag_max(mag[0], mag[k]);
+            for (int k = 1; k < NV; ++k) mag[0] = max_nan(mag[0], mag[k]);
             const float sc = scale_of(row_red<true, LPR>(mag[0], red[1]));
             if (live && at0 == 0) scales[0] = sc;
-            const float inv = __frcp_rn(sc);
+            const float inv = rcp(sc);
 #pragma unroll
             for (int k = 0; k < NV; ++k)
                 if (live && at0 + k * step < nvec) {
@@ -264,14 +278,14 @@ __global__ void __launch_bounds__(max_threads(VEC, NV, LPR, false), LPR == 0 && 
             const int lanes = p.group / VEC, shift = __ffs(lanes) - 1;  // 2^shift lanes hold a group, at a multiple of 2^shift
             for (int o = lanes / 2; o > 0; o >>= 1)
 #pragma unroll
-                for (int k = 0; k < NV; ++k) mag[k] = mag_max(mag[k], __shfl_xor_sync(0xffffffffu, mag[k], o));
+                for (int k = 0; k < NV; ++k) mag[k] = max_nan(mag[k], __shfl_xor_sync(0xffffffffu, mag[k], o));
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 const int j = at0 + k * step;
                 if (live && j < nvec) {
                     const float sc = scale_of(mag[k]);
                     if ((j & (lanes - 1)) == 0) scales[j >> shift] = sc;
-                    store8<VEC>(y + int64_t(j) * VEC, s[k], __frcp_rn(sc));
+                    store8<VEC>(y + int64_t(j) * VEC, s[k], rcp(sc));
                 }
             }
         } else {
@@ -296,7 +310,7 @@ __global__ void __launch_bounds__(max_threads(VEC, NV, LPR, false), LPR == 0 && 
                         const int i = j * VEC + e, g = i / p.group;
                         const float sc = scale_of(__uint_as_float(m[g])), one[1] = {s[k][e]};
                         if (i % p.group == 0) scales[g] = sc;
-                        store8<1>(y + i, one, __frcp_rn(sc));
+                        store8<1>(y + i, one, rcp(sc));
                     }
                 }
             }
@@ -312,8 +326,8 @@ __global__ void __launch_bounds__(max_threads(VEC, NV, LPR, true)) k_norm_bwd(co
     __shared__ float red[2][2][32];
     const int tid = threadIdx.x, step = LPR ? LPR : blockDim.x, at0 = LPR ? tid % step : tid;
     const int per = LPR ? int(blockDim.x) / step : 1, mine = LPR ? tid / step : 0;
-    const int64_t first = int64_t(blockIdx.x) * per + mine;
-    const int a0 = SHIFT ? int(first * p.dim & (VEC - 1)) : 0, nvec = SHIFT ? (a0 + p.dim + VEC - 1) / VEC : p.dim / VEC;
+    const uint32_t first = blockIdx.x * per + mine;
+    const int a0 = SHIFT ? int(first * uint32_t(p.dim) & (VEC - 1)) : 0, nvec = SHIFT ? (a0 + p.dim + VEC - 1) / VEC : p.dim / VEC;
     tc::pdl_launch_dependents();
     constexpr bool KEEP = NV * VEC < 32;  // the weights stay in registers (else: read again, from L1)
     float w[KEEP ? NV : 1][VEC], dw[NV][VEC];
@@ -323,18 +337,18 @@ __global__ void __launch_bounds__(max_threads(VEC, NV, LPR, true)) k_norm_bwd(co
         for (int e = 0; e < VEC; ++e) dw[k][e] = 0.f;
         if (KEEP && at0 + k * step < nvec) weight_piece<SHIFT, VEC>(p, A.weight, (at0 + k * step) * VEC - a0, w[KEEP ? k : 0]);
     }
-    const float inv_dim = 1.f / float(p.dim);
+    const float inv_dim = A.inv_dim;
     int turn = 0;
     // the next row of this thread's lanes is requested before the present one is reduced, where it fits
     constexpr bool AHEAD = NV * VEC < 16 || (VEC == 8 && NV == 2);
     Vec<T, VEC> xn[NV], dn[NV], sn[NV];
-    const int64_t hop = int64_t(gridDim.x) * per;
-    auto fetch = [&](int64_t row) {
-        if (row >= p.rows) return;
-        const T* x = static_cast<const T*>(A.x) + row * p.x_stride;
-        const T* dy = static_cast<const T*>(A.dy) + row * p.dy_stride;
-        const T* ds = static_cast<const T*>(A.dsum) + row * p.dsum_stride;
-        const int64_t left = (p.rows - row) * p.dim;
+    const uint32_t hop = gridDim.x * per, rows = uint32_t(p.rows);
+    auto fetch = [&](uint32_t row) {
+        if (row >= rows) return;
+        const T* x = static_cast<const T*>(A.x) + wide_mul(row, p.x_stride);
+        const T* dy = static_cast<const T*>(A.dy) + wide_mul(row, p.dy_stride);
+        const T* ds = static_cast<const T*>(A.dsum) + wide_mul(row, p.dsum_stride);
+        const int64_t left = wide_mul(rows - row, p.dim);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int j = at0 + k * step;
@@ -347,9 +361,9 @@ __global__ void __launch_bounds__(max_threads(VEC, NV, LPR, true)) k_norm_bwd(co
     };
     if (AHEAD) fetch(first);
     // every lane of a warp takes part in the shuffles of every turn
-    for (int64_t row0 = int64_t(blockIdx.x) * per; row0 < p.rows; row0 += hop, turn ^= 1) {
-        const int64_t row = row0 + mine;
-        const bool live = row < p.rows;
+    for (uint32_t row0 = blockIdx.x * per; row0 < rows; row0 += hop, turn ^= 1) {
+        const uint32_t row = row0 + mine;
+        const bool live = row < rows;
         if (!AHEAD) fetch(row);
         Vec<T, VEC> xv[NV], dv[NV], sv[NV];
 #pragma unroll
@@ -385,7 +399,7 @@ __global__ void __launch_bounds__(max_threads(VEC, NV, LPR, true)) k_norm_bwd(co
         }
         const float r = rsqrtf(ss * inv_dim + p.eps);
         c *= r * inv_dim;
-        T* dx = static_cast<T*>(A.dx) + row * p.dim;
+        T* dx = static_cast<T*>(A.dx) + wide_mul(row, p.dim);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int j = at0 + k * step;
@@ -447,19 +461,19 @@ __global__ void __launch_bounds__(LOOP_T) k_norm_fwd_loop(const NormArgs A) {
     auto at = [&](int i) { return res ? to_f(x[i]) + to_f(res[i]) : to_f(x[i]); };
     float ss = 0.f;
     for (int i = threadIdx.x; i < p.dim; i += LOOP_T) ss = fmaf(at(i), at(i), ss);
-    const float r = rsqrtf(row_red<false, 0>(ss, red[0]) / float(p.dim) + p.eps);
+    const float r = rsqrtf(row_red<false, 0>(ss, red[0]) * A.inv_dim + p.eps);
     auto y_at = [&](int i) { return at(i) * r * weight_at(A, i); };
     if (p.out_dtype == GDN_E4M3) {
         const int group = p.group ? p.group : p.dim, groups = p.dim / group;
         for (int g = 0; g < groups; ++g) {
             float m = 0.f;
-            for (int i = threadIdx.x; i < group; i += LOOP_T) m = mag_max(m, fabsf(y_at(g * group + i)));
+            for (int i = threadIdx.x; i < group; i += LOOP_T) m = max_nan(m, fabsf(y_at(g * group + i)));
             __syncthreads();  // the last group's maxima have been read
             const float sc = scale_of(row_red<true, 0>(m, red[1]));
             if (threadIdx.x == 0) A.y_scale[row * groups + g] = sc;
             for (int i = threadIdx.x; i < group; i += LOOP_T) {
                 const float one[1] = {y_at(g * group + i)};
-                store8<1>(static_cast<uint8_t*>(A.y) + row * p.dim + g * group + i, one, __frcp_rn(sc));
+                store8<1>(static_cast<uint8_t*>(A.y) + row * p.dim + g * group + i, one, rcp(sc));
             }
         }
         __syncthreads();  // sum may be x or residual, which other threads have read above
@@ -488,8 +502,8 @@ __global__ void __launch_bounds__(LOOP_T) k_norm_bwd_loop(const NormArgs A) {
             ss = fmaf(v, v, ss);
             c = fmaf(weight_at(A, i) * to_f(dy[i]), v, c);
         }
-        const float r = rsqrtf(row_red<false, 0>(ss, red[0]) / float(p.dim) + p.eps);
-        c = row_red<false, 0>(c, red[1]) * r / float(p.dim);
+        const float r = rsqrtf(row_red<false, 0>(ss, red[0]) * A.inv_dim + p.eps);
+        c = row_red<false, 0>(c, red[1]) * r * A.inv_dim;
         for (int i = threadIdx.x; i < p.dim; i += LOOP_T) {
             const float n = to_f(x[i]) * r, d = to_f(dy[i]), add = ds ? to_f(ds[i]) : 0.f;
             part[i] = fmaf(d, n, part[i]);
