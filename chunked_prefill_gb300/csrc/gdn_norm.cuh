@@ -318,9 +318,19 @@ __global__ void __launch_bounds__(max_threads(VEC, NV, LPR, false), LPR == 0 && 
     }
 }
 
+// The backward asks for the next row before it reduces the present one: into registers, or, RINGED, into a ring of
+// RING rows in shared memory, each thread copying and reading its own pieces (no barrier), which takes a third
+// fewer registers.  That pays for rows of a CTA with SHIFT (30000 rows of 1001: 48 us instead of 57) and where
+// two CTAs fit a multiprocessor instead of one (16384 of 5120: 103 us instead of 126), not elsewhere (65536 of
+// 1000: 100 us instead of 88).
+constexpr int RING = 3;
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, int bytes) {  // the rest of the 16 is 0
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+}
+
 // With SHIFT the CTAs' rows are 8 k apart, so that a0 is the same for all of a thread's rows and its columns
 // stay its own.
-template <typename T, int VEC, int NV, int LPR, bool SHIFT>
+template <typename T, int VEC, int NV, int LPR, bool SHIFT, bool RINGED>
 __global__ void __launch_bounds__(max_threads(VEC, NV, LPR, true)) k_norm_bwd(const NormArgs A) {
     const gdn_norm_problem& p = A.p;
     __shared__ float red[2][2][32];
@@ -339,12 +349,13 @@ __global__ void __launch_bounds__(max_threads(VEC, NV, LPR, true)) k_norm_bwd(co
     }
     const float inv_dim = A.inv_dim;
     int turn = 0;
-    // the next row of this thread's lanes is requested before the present one is reduced, where it fits
-    constexpr bool AHEAD = NV * VEC < 16 || (VEC == 8 && NV == 2);
-    Vec<T, VEC> xn[NV], dn[NV], sn[NV];
+    constexpr bool AHEAD = !RINGED && (NV * VEC < 16 || (VEC == 8 && NV == 2));
+    extern __shared__ __align__(16) unsigned char dyn[];
+    const uint32_t ring = RINGED ? tc::smem_addr(dyn) + tid * 16 : 0, slot = blockDim.x * 16;
+    Vec<T, VEC> xn[RINGED ? 1 : NV], dn[RINGED ? 1 : NV], sn[RINGED ? 1 : NV];
     const uint32_t hop = gridDim.x * per, rows = uint32_t(p.rows);
     auto fetch = [&](uint32_t row) {
-        if (row >= rows) return;
+        if (RINGED || row >= rows) return;
         const T* x = static_cast<const T*>(A.x) + wide_mul(row, p.x_stride);
         const T* dy = static_cast<const T*>(A.dy) + wide_mul(row, p.dy_stride);
         const T* ds = static_cast<const T*>(A.dsum) + wide_mul(row, p.dsum_stride);
@@ -353,22 +364,64 @@ __global__ void __launch_bounds__(max_threads(VEC, NV, LPR, true)) k_norm_bwd(co
         for (int k = 0; k < NV; ++k) {
             const int j = at0 + k * step;
             if (j < nvec) {
-                load_piece<SHIFT>(xn[k], x, j * VEC - a0, p.dim, left);
-                load_piece<SHIFT>(dn[k], dy, j * VEC - a0, p.dim, left);
-                if (A.dsum) load_piece<SHIFT>(sn[k], ds, j * VEC - a0, p.dim, left);
+                load_piece<SHIFT>(xn[RINGED ? 0 : k], x, j * VEC - a0, p.dim, left);
+                load_piece<SHIFT>(dn[RINGED ? 0 : k], dy, j * VEC - a0, p.dim, left);
+                if (A.dsum) load_piece<SHIFT>(sn[RINGED ? 0 : k], ds, j * VEC - a0, p.dim, left);
             }
         }
     };
+    // the pieces of a row into the ring's place `at`
+    auto copy = [&](uint32_t row, int at) {
+        if (row < rows) {
+            const T* x = static_cast<const T*>(A.x) + wide_mul(row, p.x_stride);
+            const T* dy = static_cast<const T*>(A.dy) + wide_mul(row, p.dy_stride);
+            const T* ds = static_cast<const T*>(A.dsum) + wide_mul(row, p.dsum_stride);
+            const int64_t left = wide_mul(rows - row, p.dim);
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int j = at0 + k * step, off = j * VEC - a0;
+                const int64_t there = (left - off) * int64_t(sizeof(T));
+                const int bytes = !SHIFT || there >= 16 ? 16 : int(there);
+                const uint32_t to = ring + (at * 3 * NV + k) * slot;
+                if (j < nvec) {
+                    copy16(to, x + off, bytes);
+                    copy16(to + NV * slot, dy + off, bytes);
+                    if (A.dsum) copy16(to + 2 * NV * slot, ds + off, bytes);
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;\n" ::: "memory");
+    };
+    int place = 0;
+    if (RINGED) {
+#pragma unroll
+        for (int i = 0; i < RING - 1; ++i) copy(first + i * hop, i);
+    }
     if (AHEAD) fetch(first);
     // every lane of a warp takes part in the shuffles of every turn
     for (uint32_t row0 = blockIdx.x * per; row0 < rows; row0 += hop, turn ^= 1) {
         const uint32_t row = row0 + mine;
         const bool live = row < rows;
-        if (!AHEAD) fetch(row);
         Vec<T, VEC> xv[NV], dv[NV], sv[NV];
+        if constexpr (RINGED) {
+            asm volatile("cp.async.wait_group %0;\n" ::"n"(RING - 2) : "memory");
+            copy(row + (RING - 1) * hop, place == 0 ? RING - 1 : place - 1);
 #pragma unroll
-        for (int k = 0; k < NV; ++k) xv[k] = xn[k], dv[k] = dn[k], sv[k] = sn[k];
-        if (AHEAD) fetch(row + hop);
+            for (int k = 0; k < NV; ++k) {
+                const uint32_t from = ring + (place * 3 * NV + k) * slot;
+                if (live && at0 + k * step < nvec) {
+                    *reinterpret_cast<uint4*>(xv[k].v) = tc::lds128(from);
+                    *reinterpret_cast<uint4*>(dv[k].v) = tc::lds128(from + NV * slot);
+                    if (A.dsum) *reinterpret_cast<uint4*>(sv[k].v) = tc::lds128(from + 2 * NV * slot);
+                }
+            }
+            place = place + 1 == RING ? 0 : place + 1;
+        } else {
+            if (!AHEAD) fetch(row);
+#pragma unroll
+            for (int k = 0; k < NV; ++k) xv[k] = xn[k], dv[k] = dn[k], sv[k] = sn[k];
+            if (AHEAD) fetch(row + hop);
+        }
         float ss = 0.f, c = 0.f;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
@@ -417,7 +470,7 @@ __global__ void __launch_bounds__(max_threads(VEC, NV, LPR, true)) k_norm_bwd(co
     }
     float* part = A.part + int64_t(blockIdx.x) * p.dim;
     if constexpr (LPR > 0) {  // the CTA's rows' shares, in row order
-        extern __shared__ float share[];  // [per][dim]
+        float* share = reinterpret_cast<float*>(dyn);  // [per][dim]
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int j = at0 + k * step;
@@ -565,8 +618,8 @@ template <int OUT8, typename T, int VEC, int NV, int LPR, bool SHIFT>
 cudaError_t fwd_launch(const NormArgs& A, const Layout& L, cudaStream_t st) {
     const int64_t blocks = (A.p.rows + L.per() - 1) / L.per();
     const size_t smem = OUT8 == 3 ? size_t(L.per()) * (A.p.dim / A.p.group) * 4 : 0;
-    if (smem > 40 * 1024) {
-        const cudaError_t e = smem_attr(k_norm_fwd<T, VEC, NV, LPR, SHIFT, OUT8>, int(smem));
+    if (smem > 40 * 1024) {  // (set once, so to the most that the kernel is launched with: a group to a value)
+        const cudaError_t e = smem_attr(k_norm_fwd<T, VEC, NV, LPR, SHIFT, OUT8>, max_threads(VEC, NV, LPR, false) * NV * VEC * 4);
         if (e != cudaSuccess) return e;
     }
     k_norm_fwd<T, VEC, NV, LPR, SHIFT, OUT8><<<unsigned(blocks), L.threads, smem, st>>>(A);
@@ -586,18 +639,35 @@ cudaError_t fwd_out(const NormArgs& A, const Layout& L, cudaStream_t st) {
     }
 }
 
-template <typename T, int VEC, int NV, int LPR, bool SHIFT>
-cudaError_t bwd_out(const NormArgs& A, const Layout& L, int& parts, cudaStream_t st) {
-    const size_t smem = LPR ? size_t(L.per()) * A.p.dim * 4 : 0;
-    const int fit = resident(reinterpret_cast<const void*>(k_norm_bwd<T, VEC, NV, LPR, SHIFT>), L.threads, smem) * sm_count_cached();
+template <typename T, int VEC, int NV, int LPR, bool SHIFT, bool RINGED>
+cudaError_t bwd_launch(const NormArgs& A, const Layout& L, int& parts, cudaStream_t st) {
+    const size_t smem = LPR ? size_t(L.per()) * A.p.dim * 4 : RINGED ? size_t(RING) * 3 * NV * L.threads * 16 : 0;
+    if (smem > 40 * 1024) {  // (set once, so to the most that the kernel is launched with)
+        const cudaError_t e = smem_attr(k_norm_bwd<T, VEC, NV, LPR, SHIFT, RINGED>, RING * 3 * NV * max_threads(VEC, NV, LPR, true) * 16);
+        if (e != cudaSuccess) return e;
+    }
+    const int fit = resident(reinterpret_cast<const void*>(k_norm_bwd<T, VEC, NV, LPR, SHIFT, RINGED>), L.threads, smem) * sm_count_cached();
     if (parts > fit) parts = fit;  // one wave: the rows are dealt out to the CTAs in turn
     // four rows to a CTA at least where the multiprocessors have one each: a CTA's share of dweight costs as much
     // as a row or two (2003 rows of 1024: 10.1 us instead of 11.7)
     const int64_t quarter = A.p.rows / 4, sms = sm_count_cached();
     if (parts > quarter && parts > sms) parts = int(quarter > sms ? quarter : sms);
     if (SHIFT) parts = parts > 8 ? parts / 8 * 8 : 8;
-    k_norm_bwd<T, VEC, NV, LPR, SHIFT><<<parts, L.threads, smem, st>>>(A);
+    k_norm_bwd<T, VEC, NV, LPR, SHIFT, RINGED><<<parts, L.threads, smem, st>>>(A);
     return cudaGetLastError();
+}
+
+template <typename T, int VEC, int NV, int LPR, bool SHIFT>
+cudaError_t bwd_out(const NormArgs& A, const Layout& L, int& parts, cudaStream_t st) {
+    constexpr bool CAN = LPR == 0 && VEC > 1 && NV <= 2;
+    if constexpr (CAN && SHIFT) {
+        return bwd_launch<T, VEC, NV, LPR, SHIFT, true>(A, L, parts, st);
+    } else if constexpr (CAN && NV == 2 && sizeof(T) == 2) {
+        if (L.threads > 256 && L.threads <= 384) return bwd_launch<T, VEC, NV, LPR, SHIFT, true>(A, L, parts, st);
+        return bwd_launch<T, VEC, NV, LPR, SHIFT, false>(A, L, parts, st);
+    } else {
+        return bwd_launch<T, VEC, NV, LPR, SHIFT, false>(A, L, parts, st);
+    }
 }
 
 // Calls f<VEC, NV, LPR, SHIFT> for the layout.

@@ -218,3 +218,23 @@ def test_in_place(dtype, rows, dim):
     gdn._check(L.gdn_rmsnorm_bwd(ctypes.byref(p), x["x"].data_ptr(), x["weight"].data_ptr(), dyi.data_ptr(), None, dyi.data_ptr(), dw.data_ptr(),
                                  ws.data_ptr(), n.value, torch.cuda.current_stream().cuda_stream))
     assert torch.equal(dyi, gwant[0]) and torch.equal(dw, gwant[1])
+
+
+def test_shapes_alternate():
+    """Calls of one kernel with more and less shared memory, in turn."""
+    from chunked_prefill_gb300 import gdn
+    for _ in range(2):
+        for rows, dim, group in ((2, 16384, 1), (2, 12000, 3), (2, 14000, 1)):
+            d = make(rows, dim, BF, True, dim)
+            x = cuda(d)
+            y, scale, _ = gdn.rms_norm_quant(x["x"], x["weight"], residual=x["residual"], group=group)
+            ry = decode.norm(np64(d["x"]), np64(d["weight"]), np64(d["residual"]))[0]
+            sc = decode.norm_scales(ry, group)
+            assert (np.abs(np64(scale) - sc) <= 4 * eps_of(dim) * sc).all()
+        for rows, dim in ((700, 8192), (700, 5000), (700, 7999)):
+            d = make(rows, dim, BF, False, dim)
+            x = cuda(d)
+            dx, dw = gdn.gdn_rmsnorm_bwd(x["x"], x["weight"], x["dy"], dsum=x["dsum"])
+            rx, rw, sx, sw = decode.norm_bwd(np64(d["x"]), np64(d["weight"]), np64(d["dy"]), np64(d["dsum"]))
+            close(dx, rx, sx, BF, eps_of(dim))
+            assert (np.abs(np64(dw) - rw) <= ((64 + rows) * 2.0 ** -24 + 4 * eps_of(dim)) * sw + 1e-38).all()
