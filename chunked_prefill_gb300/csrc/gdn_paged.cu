@@ -1,15 +1,18 @@
 // Attention of one new token per sequence over a paged key-value cache (include/gdn.h,
 // gdn_paged_attn_decode): o_h = sum_t softmax(scale <q_h, k_t>)_t v_t, lse_h = log sum_t e^{z_t}.
 //
-// The blocks of up to 16 query heads that share a kv-head are dealt to `groups` groups (block b to group
-// b % groups).  A group's work is a list of tiles of tokens: sequence by sequence, its blocks of heads one
-// after another, tile by tile.  The grid fills the GPU once, with the same number of CTAs to each group,
-// each taking an equal, contiguous part of its group's list, so that uneven lengths neither leave a tail nor ask the host for the lengths; on each
-// (sequence, kv-head) in its part it keeps a running maximum m, sum l of e^{z - m} and accumulator of
-// e^{z - m} v: one pass over keys and values.  A pair that lies in one CTA's part is written out by
-// it; of others every CTA leaves (accumulator, m, l) -- at most two per CTA, its first pair's and its
-// last one's -- and a second kernel joins them in the list's order.  Bound: HBM, 2 D
-// bytes-per-value per token and kv-head.
+// Long caches.  The blocks of up to 16 query heads that share a kv-head are dealt to `groups` groups
+// (block b to group b % groups).  A group's work is a list of tiles of tokens: sequence by sequence,
+// its blocks of heads one after another, tile by tile.  The grid fills the GPU once, with the same
+// number of CTAs to each group, each taking an equal, contiguous part of its group's list, so that
+// uneven lengths neither leave a tail nor ask the host for the lengths.  On each (sequence, block of
+// heads) in its part a CTA keeps a running maximum m, sum l of e^{z - m} and accumulator of e^{z - m} v:
+// one pass over keys and values.  A pair that lies in one CTA's part is written out by it; of others
+// every CTA leaves (accumulator, m, l) -- at most two per CTA, its first pair's and its last one's --
+// and a second kernel joins them in the list's order.
+// Short caches.  A cluster of 1 to 8 CTAs, or a CTA of one warp where there are very many, has each
+// (sequence, block of heads); a cluster joins its parts through distributed shared memory.
+// Bound: HBM, 2 D bytes-per-value per token and kv-head.
 //
 // bf16 and 8-bit caches: k_paged_mma.  A warp takes tiles of 16 (or 32) tokens through shared memory of
 // its own, STAGES tiles deep (cp.async, whole rows by consecutive lanes), so that the loop has no barrier
@@ -26,6 +29,11 @@
 // product, 2^-9 (2^-12) of each on average, while their sum l adds them unrounded in fp32.
 //
 // fp32: k_paged, on the CUDA cores.
+//
+// Measured (of the copy bandwidth measured on the same GPUs): 64 sequences of up to 8192 tokens, 32 / 8 heads,
+// 128 features, bf16, 162 us (6.7 TB/s, 1.00); 128 of up to 16384, 64 / 8, 8 bits, 316 us (6.7 TB/s, 1.00); one
+// of 131071, 32 / 4, bf16, 47.5 us (5.7 TB/s, 0.84: finding the parts and the join take 6 us); 4 of up to 700,
+// 16 / 2, 256 features, the new token written, 9.2 us (latency).
 #include "gdn_paged.cuh"
 
 namespace gdn {

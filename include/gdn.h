@@ -282,8 +282,11 @@ gdn_status gdn_recurrent_step(const gdn_step_problem* p, const void* q, const vo
  * such a page count as masked (and a new token there is not written); a length past
  * max_pages * page_size is cut to it.
  *
- * Caches of any page size and strides; features contiguous; D = 64, 128 or 256.  Partial
- * results over ranges of the cache lie in the workspace and are joined in a fixed order.
+ * Caches of any page size and strides; features contiguous; D = 64, 128 or 256.  Lengths, pages
+ * and tables are read on the device alone, so a captured call serves other lengths; how the work
+ * is divided follows from max_pages (a table no wider than the longest sequence may become is
+ * best) and, on the device, from the lengths.  Partial results lie in the workspace (0 bytes where
+ * none is needed) and are joined in a fixed order: the same lengths give the same bits.
  * ------------------------------------------------------------------------------------ */
 typedef struct gdn_paged_problem {
     int32_t num_seqs;
@@ -317,8 +320,9 @@ gdn_status gdn_paged_attn_decode(const gdn_paged_problem* p, const void* q, void
  * row, with w = weight + weight_offset:
  *     s = x + residual (x itself without a residual),   r = 1 / sqrt(mean(s^2) + eps),
  *     y = r s w;   sum = s, rounded to dtype (y comes from the unrounded s)
- * With out_dtype GDN_E4M3, y / scale is rounded to nearest even in 8 bits, with one fp32 scale
- * per row (group = 0) or per `group` consecutive values of a row (y_scale [rows, dim / group]):
+ * With out_dtype GDN_E4M3, y / scale (the product with 1 / scale in fp32) is rounded to nearest
+ * even in 8 bits, with one fp32 scale per row (group = 0) or per `group` consecutive values of a
+ * row (y_scale [rows, dim / group]):
  *     scale = max(max |y| / 448, 2^-126)
  * A row with infinities or NaN gets NaN in that row alone.
  * sum may be x or residual (in place), y may be x; NULL sum: not returned.
