@@ -36,6 +36,8 @@ gdn_status fail(gdn_status st, const char* fmt, ...) {
     gdn::set_last_error(buf);
     return st;
 }
+// No C++ exception crosses the C ABI: the launches' tables of kernel attributes allocate.
+gdn_status no_host_memory() { return fail(GDN_ERR_CUDA, "out of host memory"); }
 gdn_status done(cudaError_t e) {
     if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "CUDA error: %s", cudaGetErrorString(e));
     gdn::set_last_error("");
@@ -145,7 +147,7 @@ extern "C" {
 gdn_status gdn_recurrent_step(const gdn_step_problem* problem, const void* q, const void* k,
                               const void* v, const float* g, const float* beta, const float* A_log,
                               const float* dt_bias, const float* state_in, float* state_out,
-                              void* o, void* stream) {
+                              void* o, void* stream) try {
     if (!problem) return fail(GDN_ERR_INVALID_ARG, "problem is NULL");
     gdn::StepArgs A{*problem, q, k, v, g, beta, A_log, dt_bias, state_in, state_out, o, 0};
     gdn_step_problem& p = A.p;
@@ -164,22 +166,26 @@ gdn_status gdn_recurrent_step(const gdn_step_problem* problem, const void* q, co
     if ((A_log == nullptr) != (dt_bias == nullptr)) return fail(GDN_ERR_INVALID_ARG, "A_log and dt_bias go together");
     if (p.num_seqs == 0) return done(cudaSuccess);
     return done(gdn::launch_step(A, static_cast<cudaStream_t>(stream)));
+} catch (...) {
+    return no_host_memory();
 }
 
-gdn_status gdn_paged_attn_workspace_size(const gdn_paged_problem* problem, size_t* bytes) {
+gdn_status gdn_paged_attn_workspace_size(const gdn_paged_problem* problem, size_t* bytes) try {
     if (!problem) return fail(GDN_ERR_INVALID_ARG, "problem is NULL");
     if (!bytes) return fail(GDN_ERR_INVALID_ARG, "bytes is NULL");
     gdn_paged_problem p = *problem;
     TRY(check_paged(p));
     *bytes = p.num_seqs > 0 ? gdn::paged_plan(p).bytes : 0;
     return done(cudaSuccess);
+} catch (...) {
+    return no_host_memory();
 }
 
 gdn_status gdn_paged_attn_decode(const gdn_paged_problem* problem, const void* q, void* k_cache,
                                  void* v_cache, const int32_t* page_table, const int32_t* seq_lens,
                                  const void* k_new, const void* v_new, const float* k_scale,
                                  const float* v_scale, void* o, float* lse, void* workspace,
-                                 size_t workspace_bytes, void* stream) {
+                                 size_t workspace_bytes, void* stream) try {
     if (!problem) return fail(GDN_ERR_INVALID_ARG, "problem is NULL");
     gdn::PagedArgs A{};
     A.p = *problem;
@@ -223,10 +229,12 @@ gdn_status gdn_paged_attn_decode(const gdn_paged_problem* problem, const void* q
     A.part_ml = reinterpret_cast<float2*>(ws + plan.off_ml);
     A.part = reinterpret_cast<float*>(ws + plan.off_part);
     return done(gdn::launch_paged(A, static_cast<cudaStream_t>(stream)));
+} catch (...) {
+    return no_host_memory();
 }
 
 gdn_status gdn_rmsnorm_fwd(const gdn_norm_problem* problem, const void* x, const void* residual,
-                           const void* weight, void* y, float* y_scale, void* sum, void* stream) {
+                           const void* weight, void* y, float* y_scale, void* sum, void* stream) try {
     if (!problem) return fail(GDN_ERR_INVALID_ARG, "problem is NULL");
     gdn::NormArgs A{};
     A.p = *problem;
@@ -249,20 +257,24 @@ gdn_status gdn_rmsnorm_fwd(const gdn_norm_problem* problem, const void* x, const
     A.y_scale = y_scale;
     A.sum = sum;
     return done(gdn::launch_norm_fwd(A, static_cast<cudaStream_t>(stream)));
+} catch (...) {
+    return no_host_memory();
 }
 
-gdn_status gdn_rmsnorm_bwd_workspace_size(const gdn_norm_problem* problem, size_t* bytes) {
+gdn_status gdn_rmsnorm_bwd_workspace_size(const gdn_norm_problem* problem, size_t* bytes) try {
     if (!problem) return fail(GDN_ERR_INVALID_ARG, "problem is NULL");
     if (!bytes) return fail(GDN_ERR_INVALID_ARG, "bytes is NULL");
     gdn_norm_problem p = *problem;
     TRY(check_norm(p, true));
     *bytes = size_t(gdn::norm_bwd_parts(p)) * p.dim * sizeof(float);
     return done(cudaSuccess);
+} catch (...) {
+    return no_host_memory();
 }
 
 gdn_status gdn_rmsnorm_bwd(const gdn_norm_problem* problem, const void* s, const void* weight,
                            const void* dy, const void* dsum, void* dx, float* dweight,
-                           void* workspace, size_t workspace_bytes, void* stream) {
+                           void* workspace, size_t workspace_bytes, void* stream) try {
     if (!problem) return fail(GDN_ERR_INVALID_ARG, "problem is NULL");
     gdn::NormArgs A{};
     A.p = *problem;
@@ -289,6 +301,8 @@ gdn_status gdn_rmsnorm_bwd(const gdn_norm_problem* problem, const void* s, const
     A.dweight = dweight;
     A.part = static_cast<float*>(workspace);
     return done(gdn::launch_norm_bwd(A, static_cast<cudaStream_t>(stream)));
+} catch (...) {
+    return no_host_memory();
 }
 
 }  // extern "C"

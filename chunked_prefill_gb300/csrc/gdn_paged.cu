@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(PT, D == 256 ? 2 : 4) k_paged(const PagedArgs 
         const int32_t* table = A.table + n * p.table_stride;
         float* kc = static_cast<float*>(A.k_cache) + hk * p.k_head_stride;
         float* vc = static_cast<float*>(A.v_cache) + hk * p.v_head_stride;
-        if (A.k_new && R.len > 0 && end == tiles) {  // every block of heads writes the same bits before it reads them
+        if (A.k_new && R.fits && end == tiles) {  // every block of heads writes the same bits before it reads them
             const int at = R.len - 1, page = table[A.page_div.of(at)], slot = at - A.page_div.of(at) * p.page_size;
             if (page >= 0 && page < p.num_pages) {
                 const int64_t from = n * p.new_stride + int64_t(hk) * D;

@@ -22,6 +22,7 @@ constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 // which is first down to a multiple of 16 (a tile's rows then share a page of 16 k tokens).
 struct Range {
     int len, first, base;
+    bool fits;  // in the table: a new token has a place
     __device__ __forceinline__ int tiles(int tok) const {  // one at least: an empty row is written too
         const int64_t n = (int64_t(len) - base + tok - 1) / tok;
         return n > 1 ? int(n) : 1;
@@ -32,6 +33,7 @@ __device__ __forceinline__ Range range_of(const PagedArgs& A, int n) {
     Range R;
     const int64_t len = A.lens[n];
     R.len = int(len < 0 ? 0 : len < cap ? len : cap);
+    R.fits = len > 0 && len <= cap;
     R.first = A.p.window > 0 && R.len > A.p.window ? R.len - A.p.window : 0;
     R.base = R.first & ~15;
     return R;

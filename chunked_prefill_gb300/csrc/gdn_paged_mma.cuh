@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(Tile<C, D, SOLO>::T, Tile<C, D, SOLO>::CTAS) k
 #pragma unroll
             for (int b = 0; b < TT; ++b) first[i][b] = page_at(i, b);
 
-        if (A.k_new && R.len > 0 && end == tiles_n) {  // every block of heads writes the same bits before it reads them
+        if (A.k_new && R.fits && end == tiles_n) {  // every block of heads writes the same bits before it reads them
             const int at = R.len - 1, page = table[A.page_div.of(at)], slot = slot_of(at);
             if (page >= 0 && page < p.num_pages) {
                 C* kd = kc + page * p.k_page_stride + slot * p.k_token_stride;

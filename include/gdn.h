@@ -280,7 +280,7 @@ gdn_status gdn_recurrent_step(const gdn_step_problem* p, const void* q, const vo
  * A sequence of length 0 gets o = 0 and lse = -inf.  Whatever lies in slots outside
  * [first, len) is not used, NaN or not.  Page numbers outside [0, num_pages) are not read: the tokens of
  * such a page count as masked (and a new token there is not written); a length past
- * max_pages * page_size is cut to it.
+ * max_pages * page_size is cut to it (and its new token not written).
  *
  * Caches of any page size and strides; features contiguous; D = 64, 128 or 256.  Lengths, pages
  * and tables are read on the device alone, so a captured call serves other lengths; how the work

@@ -238,3 +238,19 @@ def test_shapes_alternate():
             rx, rw, sx, sw = decode.norm_bwd(np64(d["x"]), np64(d["weight"]), np64(d["dy"]), np64(d["dsum"]))
             close(dx, rx, sx, BF, eps_of(dim))
             assert (np.abs(np64(dw) - rw) <= ((64 + rows) * 2.0 ** -24 + 4 * eps_of(dim)) * sw + 1e-38).all()
+
+
+def test_rows_past_32_bit_offsets():
+    """More than 2^31 values: the last rows are those of a call on them alone, in every direction."""
+    from chunked_prefill_gb300 import gdn
+    dim, rows, tail = 16384, 131080, 24
+    assert rows * dim > 2 ** 31
+    x = torch.randn(rows, dim, device="cuda", dtype=BF)
+    w = torch.randn(dim, device="cuda", dtype=BF)
+    y, _ = gdn.rms_norm(x, w)
+    assert torch.equal(y[-tail:], gdn.rms_norm(x[-tail:].contiguous(), w)[0])
+    y8, scale, _ = gdn.rms_norm_quant(x, w, group=128)
+    z8, zscale, _ = gdn.rms_norm_quant(x[-tail:].contiguous(), w, group=128)
+    assert torch.equal(y8[-tail:].view(torch.uint8), z8.view(torch.uint8)) and torch.equal(scale[-tail:], zscale)
+    dx, _ = gdn.gdn_rmsnorm_bwd(x, w, y)
+    assert torch.equal(dx[-tail:], gdn.gdn_rmsnorm_bwd(x[-tail:].contiguous(), w, y[-tail:].contiguous())[0])

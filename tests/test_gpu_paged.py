@@ -292,3 +292,18 @@ def test_many_sequences_and_many_heads():
         lens[0] = most
         x = make(lens, 8, 8, 64, 32, BF, seed=most)
         check(x, *call(x))
+
+
+def test_a_new_token_past_the_table_is_not_written():
+    x = make([48, 20], 4, 2, 128, 16, BF, seed=19)
+    x["table"] = x["table"][:, :3].contiguous()
+    x["table"][1, 2] = 0
+    x["lens"][0] = 49  # the table holds 48
+    k, v = x["k"].clone(), x["v"].clone()
+    new = torch.randn(2, 2, 128, device="cuda").to(BF)
+    got = call(x, k_new=new, v_new=new)
+    at = (int(x["table"][1, 1]), 3)
+    k[at], v[at] = new[1], new[1]
+    for a, b in ((x["k"], k), (x["v"], v)):
+        assert torch.equal(torch.nan_to_num(a, nan=-7.0), torch.nan_to_num(b, nan=-7.0))
+    check(x, *got)
