@@ -71,8 +71,10 @@ struct PagedShape {
 };
 PagedShape paged_shape_bf16(int D);
 PagedShape paged_shape_f8(int D);
+PagedShape paged_shape_fp32(int D, int G);
 cudaError_t launch_paged_bf16(const PagedArgs& A, const PagedPlan& plan, cudaStream_t st);
 cudaError_t launch_paged_f8(const PagedArgs& A, const PagedPlan& plan, cudaStream_t st);
+cudaError_t launch_paged_fp32(const PagedArgs& A, const PagedPlan& plan, cudaStream_t st);
 cudaError_t launch_paged(const PagedArgs& A, cudaStream_t st);
 
 struct NormArgs {

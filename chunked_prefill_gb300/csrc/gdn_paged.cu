@@ -28,7 +28,7 @@
 // tokens and paired by byte permutes).  The weights are rounded to bf16 (fp16 for 8-bit caches) for the second
 // product, 2^-9 (2^-12) of each on average, while their sum l adds them unrounded in fp32.
 //
-// fp32: k_paged, on the CUDA cores.
+// fp32: k_paged_fp32 (gdn_paged_fp32.cu), on the CUDA cores.
 //
 // Measured (of the copy bandwidth measured on the same GPUs): 64 sequences of up to 8192 tokens, 32 / 8 heads,
 // 128 features, bf16, 162 us (6.7 TB/s, 1.00); 128 of up to 16384, 64 / 8, 8 bits, 316 us (6.7 TB/s, 1.00); one
@@ -39,222 +39,11 @@
 namespace gdn {
 namespace {
 
-// ------------------------------------------------------------------------------- fp32
-constexpr int PT = 128;   // threads
-constexpr int PW = PT / 32;
-constexpr int GB = 4;     // query heads per block of heads
-constexpr int PU = 4;     // tokens a warp takes at a time
-constexpr int PTOK = 32;  // tokens to a tile of the list
-
-template <int E>
-__device__ __forceinline__ void load_row(const float* p, float (&x)[E]) {
-    if constexpr (E == 2) {
-        *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(p);
-    } else {
-#pragma unroll
-        for (int b = 0; b < E / 4; ++b) *reinterpret_cast<float4*>(x + 4 * b) = *reinterpret_cast<const float4*>(p + 4 * b);
-    }
-}
-// 16 values a lane, summed over the warp: lane l gets value l / 2 (bit 4 of the lane is bit 3 of the value).
-__device__ __forceinline__ float sum16(float (&v)[16]) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int n = 8; n > 0; n >>= 1) {
-        const bool up = lane & (2 * n);
-#pragma unroll
-        for (int i = 0; i < n; ++i) {
-            const float keep = up ? v[i + n] : v[i], give = up ? v[i] : v[i + n];
-            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, 2 * n);
-        }
-    }
-    return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
-}
-
-// A warp takes 4 tokens at a time, a lane D / 32 features of their rows and of 4 query heads.  The 16
-// scores are summed across the warp so that each ends up in two lanes (16 exchanges instead of 80), which
-// alone work out its weight; the next 4 tokens' rows are requested meanwhile.
-template <int D>
-__global__ void __launch_bounds__(PT, D == 256 ? 2 : 4) k_paged(const PagedArgs A) {
-    constexpr int E = D / 32;
-    __shared__ __align__(16) float acc_s[PW][GB][D], res_s[GB][D];
-    __shared__ float ml_s[PW][GB][2];
-    __shared__ float2 res_ml[GB];
-    const gdn_paged_problem& p = A.p;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int G = p.Hq / p.Hkv, nb = (G + GB - 1) / GB;
-    tc::pdl_launch_dependents();
-    Part P = find_part<PT>(A, PTOK, 1);
-    const Part P0 = P;
-    if (A.cluster > 1 && tid < GB) res_ml[tid] = make_float2(-INFINITY, 0.f);
-    for (int64_t pos = P.lo; pos < P.hi;) {
-        const int n = P.n, block = P.head * A.groups + P.group, hk = block / nb, hb = (block % nb) * GB;
-        const Range R = range_of(A, n);
-        const int tiles = R.tiles(PTOK), end = int(min(int64_t(tiles), P.at + (P.hi - pos)));
-        const bool whole = P.at == 0 && end == tiles, began = P.at > 0;
-        const int start = R.base + P.at * PTOK;
-        const int t0 = max(R.first, start), t1 = end == tiles ? R.len : R.base + end * PTOK;
-        pos += end - P.at;
-        P.at = 0;
-        if (++P.head == A.heads) P.head = 0, ++P.n;
-
-        const float ks = A.k_scale ? A.k_scale[hk] : 1.f, vs = A.v_scale ? A.v_scale[hk] : 1.f;
-        const int32_t* table = A.table + n * p.table_stride;
-        float* kc = static_cast<float*>(A.k_cache) + hk * p.k_head_stride;
-        float* vc = static_cast<float*>(A.v_cache) + hk * p.v_head_stride;
-        if (A.k_new && R.fits && end == tiles) {  // every block of heads writes the same bits before it reads them
-            const int at = R.len - 1, page = table[A.page_div.of(at)], slot = at - A.page_div.of(at) * p.page_size;
-            if (page >= 0 && page < p.num_pages) {
-                const int64_t from = n * p.new_stride + int64_t(hk) * D;
-                for (int i = tid; i < D; i += PT) {
-                    kc[page * p.k_page_stride + slot * p.k_token_stride + i] = to_cache<float>(static_cast<const float*>(A.k_new)[from + i], ks);
-                    vc[page * p.v_page_stride + slot * p.v_token_stride + i] = to_cache<float>(static_cast<const float*>(A.v_new)[from + i], vs);
-                }
-            }
-            __syncthreads();
-        }
-
-        // page of token t + lane % 4, or -1 where there is nothing to attend to
-        auto page_at = [&](int t) {
-            t += lane & (PU - 1);
-            if (t < t0 || t >= t1) return -1;
-            const int page = table[A.page_div.of(t)];
-            return page >= 0 && page < p.num_pages ? page : -1;
-        };
-        float kn[PU][E], vn[PU][E];
-        auto fetch = [&](int t, int pages) {
-#pragma unroll
-            for (int u = 0; u < PU; ++u) {
-                const int page = __shfl_sync(0xffffffffu, pages, u), slot = t + u - A.page_div.of(t + u) * p.page_size;
-                if (page >= 0) {
-                    load_row<E>(kc + page * p.k_page_stride + slot * p.k_token_stride + lane * E, kn[u]);
-                    load_row<E>(vc + page * p.v_page_stride + slot * p.v_token_stride + lane * E, vn[u]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < E; ++e) kn[u][e] = vn[u][e] = 0.f;
-                }
-            }
-        };
-        constexpr int HOP = PW * PU;
-        const int first = start + warp * PU;
-        int pages = page_at(first);
-        fetch(first, pages);
-        int next = page_at(first + HOP);
-
-        float q[GB][E], acc[GB][E];
-#pragma unroll
-        for (int h = 0; h < GB; ++h)
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                acc[h][e] = 0.f;
-                q[h][e] = hb + h < G ? static_cast<const float*>(A.q)[n * p.q_stride + (hk * G + hb + h) * D + lane * E + e] : 0.f;
-            }
-        const float zs = p.scale * ks * LOG2E;
-        float m = -INFINITY, l = 0.f;  // of this lane's head, bits 1 and 2 of the lane; its token: bits 3 and 4
-        for (int t = first; t < t1; t += HOP) {
-            const bool live = __shfl_sync(0xffffffffu, pages, lane >> 3) >= 0;
-            float k[PU][E], v[PU][E];
-#pragma unroll
-            for (int u = 0; u < PU; ++u)
-#pragma unroll
-                for (int e = 0; e < E; ++e) k[u][e] = kn[u][e], v[u][e] = vn[u][e];
-            pages = next;
-            fetch(t + HOP, pages);
-            next = page_at(t + 2 * HOP);
-            float z16[16];
-#pragma unroll
-            for (int u = 0; u < PU; ++u)
-#pragma unroll
-                for (int h = 0; h < GB; ++h) {
-                    float z = 0.f;
-#pragma unroll
-                    for (int e = 0; e < E; ++e) z = fmaf(q[h][e], k[u][e], z);
-                    z16[u * GB + h] = z;
-                }
-            float z = sum16(z16) * zs;
-            if (!live) z = -INFINITY;
-            float top = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 16));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-            if (__any_sync(0xffffffffu, top > m)) {
-                const float mn = fmaxf(m, top), c = mn == -INFINITY ? 1.f : exp2f(m - mn);
-                m = mn;
-                l *= c;
-#pragma unroll
-                for (int h = 0; h < GB; ++h) {
-                    const float ch = __shfl_sync(0xffffffffu, c, 2 * h);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) acc[h][e] *= ch;
-                }
-            }
-            const float w = exp2f(z - (m == -INFINITY ? 0.f : m));
-            l += w;
-#pragma unroll
-            for (int u = 0; u < PU; ++u)
-#pragma unroll
-                for (int h = 0; h < GB; ++h) {
-                    const float wu = __shfl_sync(0xffffffffu, w, 8 * u + 2 * h);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) acc[h][e] = fmaf(wu, v[u][e], acc[h][e]);
-                }
-        }
-        l += __shfl_xor_sync(0xffffffffu, l, 16);
-        l += __shfl_xor_sync(0xffffffffu, l, 8);
-#pragma unroll
-        for (int h = 0; h < GB; ++h)
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc_s[warp][h][lane * E + e] = acc[h][e];
-        if (lane < 8 && (lane & 1) == 0) {
-            ml_s[warp][lane >> 1][0] = m;
-            ml_s[warp][lane >> 1][1] = l;
-        }
-        __syncthreads();
-        for (int i = tid; i < min(GB, G - hb) * D; i += PT) {
-            const int h = i / D, d = i % D;
-            float M = -INFINITY, S = 0.f, a = 0.f;
-#pragma unroll
-            for (int g = 0; g < PW; ++g) M = fmaxf(M, ml_s[g][h][0]);
-#pragma unroll
-            for (int g = 0; g < PW; ++g) {
-                const float c = ml_s[g][h][0] == -INFINITY ? 0.f : exp2f(ml_s[g][h][0] - M);
-                S = fmaf(ml_s[g][h][1], c, S);
-                a = fmaf(acc_s[g][h][d], c, a);
-            }
-            if (A.cluster > 1) {
-                res_s[h][d] = a;
-                if (d == 0) res_ml[h] = make_float2(M, S);
-            } else if (whole) {
-                const int64_t row = int64_t(n) * p.Hq + hk * G + hb + h;
-                const bool some = S > 0.f || S != S;
-                static_cast<float*>(A.o)[row * D + d] = some ? a / S * vs : 0.f;
-                if (A.lse && d == 0) A.lse[row] = some ? (M + log2f(S)) * LN2 : -INFINITY;
-            } else {
-                const int64_t at = place_of(blockIdx.x, began, GB) + h;
-                A.part[at * D + d] = a;
-                if (d == 0) A.part_ml[at] = make_float2(M, S);
-            }
-        }
-        __syncthreads();  // the shared arrays are read before the next pair writes them
-    }
-    if (A.cluster > 1) {
-        const int block = P0.head * A.groups + P0.group, hb = (block % nb) * GB;
-        join_cluster<float, D, PT>(A, tc::smem_addr(res_s), tc::smem_addr(res_ml), P0.n, block / nb, hb, min(GB, G - hb));
-    }
-}
-
 constexpr int CLUSTER_WORK = 4096;  // features times tokens per warp that are not worth splitting
 
-template <int D> constexpr PagedShape fp32_shape() { return {PTOK, GB, 1, D == 256 ? 2 : 4}; }
 PagedShape shape_of(const gdn_paged_problem& p) {
-    if (p.dtype == GDN_FP32) return p.D == 64 ? fp32_shape<64>() : p.D == 128 ? fp32_shape<128>() : fp32_shape<256>();
+    if (p.dtype == GDN_FP32) return paged_shape_fp32(p.D, p.Hq / p.Hkv);
     return p.cache_dtype == GDN_BF16 ? paged_shape_bf16(p.D) : paged_shape_f8(p.D);
-}
-
-template <int D>
-cudaError_t launch_fp32(const PagedArgs& A, const PagedPlan& plan, cudaStream_t st) {
-    timing_begin("paged_attn", st);
-    const cudaError_t e = launch_clusters(k_paged<D>, A, plan.ctas, PT, 0, st);
-    timing_end(st);
-    if (e != cudaSuccess) return e;
-    return launch_join<float, D>(A, plan, fp32_shape<D>(), st);
 }
 
 }  // namespace
@@ -302,8 +91,7 @@ PagedPlan paged_plan(const gdn_paged_problem& p) {
 
 cudaError_t launch_paged(const PagedArgs& A, cudaStream_t st) {
     const PagedPlan plan = paged_plan(A.p);
-    if (A.p.dtype == GDN_FP32)
-        return A.p.D == 64 ? launch_fp32<64>(A, plan, st) : A.p.D == 128 ? launch_fp32<128>(A, plan, st) : launch_fp32<256>(A, plan, st);
+    if (A.p.dtype == GDN_FP32) return launch_paged_fp32(A, plan, st);
     return A.p.cache_dtype == GDN_BF16 ? launch_paged_bf16(A, plan, st) : launch_paged_f8(A, plan, st);
 }
 

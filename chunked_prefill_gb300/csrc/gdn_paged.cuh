@@ -187,6 +187,13 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// copy of 16 bytes to shared memory, zeros where !in (the address is not read then)
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory"); }
+
 // Joins the parts of the rows that several CTAs have parts of, in the list's order.  A block of 8
 // warps takes RPB rows: a warp each (8), or all 8 warps one row's parts (1: few rows, many parts).
 constexpr int JW = 8;

@@ -50,13 +50,6 @@ __device__ __forceinline__ uint32_t split_f8(float& x, float& y, float& z, float
     return a | b << 16;
 }
 
-// copy of 16 bytes to shared memory, zeros where !in (the address is not read then)
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool in) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory"); }
-
 // SOLO: a CTA of one warp per (sequence, block of heads), for many short caches.
 template <typename C, int D, bool SOLO = false> struct Tile {
     static constexpr int E = int(sizeof(C));

@@ -100,6 +100,15 @@ def test_long_sequences_split_and_joined(cache, lens):
     check(x, *call(x))
 
 
+@pytest.mark.parametrize("cache", [BF, FP8, F32])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Hq,Hkv,page,window", [(12, 1, 1, 0), (40, 1, 32, 0), (66, 2, 5, 700)])
+def test_many_heads_to_one_on_long_sequences(cache, D, Hq, Hkv, page, window):
+    """More query heads to a kv-head than a block of heads holds, split sequences, small pages."""
+    x = make([9001, 0, 733, 2, 4000], Hq, Hkv, D, page, cache, seed=Hq + D)
+    check(x, *call(x, window=window), window=window)
+
+
 @pytest.mark.parametrize("cache", [BF, FP8])
 @pytest.mark.parametrize("window", [1, 16, 100, 5000])
 def test_window(cache, window):
