@@ -149,19 +149,39 @@ __global__ void __launch_bounds__(Tile<C, D, SOLO>::T, Tile<C, D, SOLO>::CTAS) k
         // ---- this warp's tiles: tokens from start + TOK (warp + W i)
         const int tiles = all > warp ? (all - warp + W - 1) / W : 0;
         auto token_of = [&](int i) { return start + TOK * (warp + W * i); };
-        // The page(s) of block b of tile i: with TILED (a page holds whole blocks) the block's page, in
-        // every lane; else lane l has that of token l % 16.  -1 where there is nothing to attend to.
-        auto page_at = [&](int i, int b) {
-            const int tok = token_of(i) + 16 * b + (TILED ? 0 : lane & 15);
-            if (i >= tiles || tok >= t1 || (!TILED && tok < t0)) return -1;
+        // The lanes look after the page table together: of LOOK blocks of 16 tokens, one lane each with TILED (a
+        // page holds whole blocks), else a lane to each token.  A lane reads its page (AHEAD looks ahead) and
+        // works out where its rows begin and which count; the copies take the offsets from that lane.  With a
+        // look and the arithmetic in every lane for every tile, 16 sequences of up to 48828 tokens, 8 kv-heads,
+        // took 96 us instead of 77 (8 bits, 64 features, pages of 16 tokens), of up to 6103 92 us instead of 67 (bf16,
+        // 256 features, pages of one).  -1 where there is nothing to attend to.
+        constexpr int LOOK = TILED ? 32 : 2, AHEAD = TILED ? 1 : 2;
+        auto block_of = [&](int x) { return x + (TILED ? lane : lane >> 4); };
+        auto first_of = [&](int x) { return token_of(x / TT) + 16 * (x % TT) + (TILED ? 0 : lane & 15); };
+        auto page_at = [&](int from) {
+            const int x = block_of(from), tok = first_of(x);
+            if (x / TT >= tiles || tok >= t1 || (!TILED && tok < t0)) return -1;
             const int page = table[A.page_div.of(tok)];
             return page >= 0 && page < p.num_pages ? page : -1;
         };
-        int first[STAGES - 1][TT];  // of the tiles requested ahead
+        constexpr int PRO = (TT * (STAGES - 1) + LOOK - 1) / LOOK;  // looks that the tiles requested ahead need
+        int first[PRO + AHEAD];
 #pragma unroll
-        for (int i = 0; i < STAGES - 1; ++i)
-#pragma unroll
-            for (int b = 0; b < TT; ++b) first[i][b] = page_at(i, b);
+        for (int i = 0; i < PRO + AHEAD; ++i) first[i] = page_at(i * LOOK);
+        int64_t ko = 0, vo = 0;
+        uint32_t counts = 0u;  // TILED: tokens of this lane's block; else tokens of both blocks, in every lane
+        auto locate = [&](int from, int page) {
+            const int tok = first_of(block_of(from)), slot = slot_of(tok);
+            if constexpr (TILED) {
+                counts = page < 0 ? 0u : 0xffffu;
+                if (t0 > tok) counts &= 0xffffu << min(t0 - tok, 16);
+                if (t1 - tok < 16) counts &= 0xffffu >> min(16 - (t1 - tok), 16);
+            } else {
+                counts = __ballot_sync(0xffffffffu, page >= 0);
+            }
+            ko = page < 0 ? 0 : page * p.k_page_stride + slot * p.k_token_stride;
+            vo = page < 0 ? 0 : page * p.v_page_stride + slot * p.v_token_stride;
+        };
 
         if (A.k_new && R.fits && end == tiles_n) {  // every block of heads writes the same bits before it reads them
             const int at = R.len - 1, page = table[A.page_div.of(at)], slot = slot_of(at);
@@ -178,20 +198,15 @@ __global__ void __launch_bounds__(Tile<C, D, SOLO>::T, Tile<C, D, SOLO>::CTAS) k
         }
 
         // Requests the rows of block b of tile i (zeros where masked); returns which tokens count.
-        auto issue = [&](int i, int b, int stage, int pages) -> uint32_t {
-            const int tok = token_of(i) + 16 * b;
+        const C* kl = kc + copy_piece * (16 / L::E) + (TILED ? copy_row * p.k_token_stride : 0);
+        const C* vl = vc + copy_piece * (16 / L::E) + (TILED ? copy_row * p.v_token_stride : 0);
+        auto issue = [&](int i, int b, int stage) -> uint32_t {
+            const int x = (i * TT + b) % LOOK;
             const uint32_t to = copy_to + stage * L::BYTES + b * L::BLOCK;
             uint32_t valid;
             if constexpr (TILED) {
-                valid = 0u;
-                if (pages >= 0) {
-                    valid = 0xffffu;
-                    if (t0 > tok) valid &= 0xffffu << (t0 - tok);
-                    if (t1 - tok < 16) valid &= 0xffffu >> (16 - (t1 - tok));
-                }
-                const int slot = slot_of(tok) + copy_row, page = pages < 0 ? 0 : pages;
-                const C* kt = kc + (page * p.k_page_stride + slot * p.k_token_stride) + copy_piece * (16 / L::E);
-                const C* vt = vc + (page * p.v_page_stride + slot * p.v_token_stride) + copy_piece * (16 / L::E);
+                valid = __shfl_sync(0xffffffffu, counts, x);
+                const C *kt = kl + __shfl_sync(0xffffffffu, ko, x), *vt = vl + __shfl_sync(0xffffffffu, vo, x);
 #pragma unroll
                 for (int j = 0; j < 16 / RPI; ++j) {
                     const bool in = valid >> (copy_row + RPI * j) & 1;
@@ -202,35 +217,32 @@ __global__ void __launch_bounds__(Tile<C, D, SOLO>::T, Tile<C, D, SOLO>::CTAS) k
                     vt += RPI * p.v_token_stride;
                 }
             } else {
-                valid = __ballot_sync(0xffffffffu, pages >= 0) & 0xffffu;
+                valid = counts >> (16 * x) & 0xffffu;
 #pragma unroll
                 for (int j = 0; j < 16 / RPI; ++j) {
-                    const int row = copy_row + RPI * j, page = __shfl_sync(0xffffffffu, pages, row), slot = slot_of(tok + row);
-                    const C *kt = kc, *vt = vc;
-                    if (page >= 0) {
-                        kt += page * p.k_page_stride + slot * p.k_token_stride + copy_piece * (16 / L::E);
-                        vt += page * p.v_page_stride + slot * p.v_token_stride + copy_piece * (16 / L::E);
-                    }
+                    const int row = copy_row + RPI * j;
+                    const bool in = valid >> row & 1;
                     const uint32_t at = (to ^ (L::swap(RPI * j) << 4)) + RPI * j * ROW;
-                    cp_async(at, kt, page >= 0);
-                    cp_async(at + TT * L::BLOCK, vt, page >= 0);
+                    cp_async(at, kl + __shfl_sync(0xffffffffu, ko, 16 * x + row), in);
+                    cp_async(at + TT * L::BLOCK, vl + __shfl_sync(0xffffffffu, vo, 16 * x + row), in);
                 }
             }
             return valid << (16 * b);
         };
 
         uint32_t mask[STAGES];  // which tokens of the tiles in flight count, oldest first
-        int pages[TT];
 #pragma unroll
         for (int i = 0; i < STAGES - 1; ++i) {
             mask[i] = 0u;
+            if (i * TT % LOOK == 0) locate(i * TT, first[i * TT / LOOK]);
             if (i < tiles)
 #pragma unroll
-                for (int b = 0; b < TT; ++b) mask[i] |= issue(i, b, i, first[i][b]);
+                for (int b = 0; b < TT; ++b) mask[i] |= issue(i, b, i);
             cp_commit();
         }
+        int pages[AHEAD];  // of the next looks
 #pragma unroll
-        for (int b = 0; b < TT; ++b) pages[b] = page_at(STAGES - 1, b);
+        for (int i = 0; i < AHEAD; ++i) pages[i] = first[PRO + i];
 
         // ---- query fragments, of 16-feature step s: features 2t, + 1 and 8 + 2t, + 1.  8-bit caches, of
         // 32-feature step s: features 4t .. 4t + 3 and 16 + 4t .., each value the sum of two 8-bit ones of
@@ -314,12 +326,16 @@ __global__ void __launch_bounds__(Tile<C, D, SOLO>::T, Tile<C, D, SOLO>::CTAS) k
             {
                 const int next = i + STAGES - 1;
                 mask[STAGES - 1] = 0u;
+                if (next * TT % LOOK == 0) {
+                    locate(next * TT, pages[0]);
+#pragma unroll
+                    for (int j = 1; j < AHEAD; ++j) pages[j - 1] = pages[j];
+                    pages[AHEAD - 1] = page_at(next * TT + AHEAD * LOOK);
+                }
                 if (next < tiles)
 #pragma unroll
-                    for (int b = 0; b < TT; ++b) mask[STAGES - 1] |= issue(next, b, stage == 0 ? STAGES - 1 : stage - 1, pages[b]);
+                    for (int b = 0; b < TT; ++b) mask[STAGES - 1] |= issue(next, b, stage == 0 ? STAGES - 1 : stage - 1);
                 cp_commit();
-#pragma unroll
-                for (int b = 0; b < TT; ++b) pages[b] = page_at(next + 1, b);
             }
             const uint32_t kd = k_at + stage * L::BYTES;
             float s[2 * TT][4] = {};  // of 8 tokens each
