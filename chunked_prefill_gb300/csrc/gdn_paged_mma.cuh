@@ -160,9 +160,8 @@ __global__ void __launch_bounds__(Tile<C, D, SOLO>::T, Tile<C, D, SOLO>::CTAS) k
         auto first_of = [&](int x) { return token_of(x / TT) + 16 * (x % TT) + (TILED ? 0 : lane & 15); };
         auto page_at = [&](int from) {
             const int x = block_of(from), tok = first_of(x);
-            if (x / TT >= tiles || tok >= t1 || (!TILED && tok < t0)) return -1;
-            const int page = table[A.page_div.of(tok)];
-            return page >= 0 && page < p.num_pages ? page : -1;
+            const bool in = x / TT < tiles && tok < t1 && (TILED || tok >= t0);
+            return in ? __ldg(table + A.page_div.of(tok)) : -1;  // looked at in locate: the load is not waited for here
         };
         constexpr int PRO = (TT * (STAGES - 1) + LOOK - 1) / LOOK;  // looks that the tiles requested ahead need
         int first[PRO + AHEAD];
@@ -171,6 +170,7 @@ __global__ void __launch_bounds__(Tile<C, D, SOLO>::T, Tile<C, D, SOLO>::CTAS) k
         int64_t ko = 0, vo = 0;
         uint32_t counts = 0u;  // TILED: tokens of this lane's block; else tokens of both blocks, in every lane
         auto locate = [&](int from, int page) {
+            if (page >= p.num_pages) page = -1;
             const int tok = first_of(block_of(from)), slot = slot_of(tok);
             if constexpr (TILED) {
                 counts = page < 0 ? 0u : 0xffffu;
@@ -197,16 +197,24 @@ __global__ void __launch_bounds__(Tile<C, D, SOLO>::T, Tile<C, D, SOLO>::CTAS) k
             __syncthreads();
         }
 
-        // Requests the rows of block b of tile i (zeros where masked); returns which tokens count.
+        // where block b of tile i lies, and which of its tokens count
         const C* kl = kc + copy_piece * (16 / L::E) + (TILED ? copy_row * p.k_token_stride : 0);
         const C* vl = vc + copy_piece * (16 / L::E) + (TILED ? copy_row * p.v_token_stride : 0);
-        auto issue = [&](int i, int b, int stage) -> uint32_t {
-            const int x = (i * TT + b) % LOOK;
-            const uint32_t to = copy_to + stage * L::BYTES + b * L::BLOCK;
+        struct Place {
+            const C *k, *v;
             uint32_t valid;
+            int x;
+        };
+        auto place = [&](int i, int b) -> Place {
+            const int x = (i * TT + b) % LOOK;
+            if (TILED) return {kl + __shfl_sync(0xffffffffu, ko, x), vl + __shfl_sync(0xffffffffu, vo, x), __shfl_sync(0xffffffffu, counts, x), x};
+            return {kl, vl, counts >> (16 * x) & 0xffffu, x};
+        };
+        // Requests its rows (zeros where masked).
+        auto issue = [&](const Place& P, int b, int stage) {
+            const uint32_t to = copy_to + stage * L::BYTES + b * L::BLOCK, valid = P.valid;
             if constexpr (TILED) {
-                valid = __shfl_sync(0xffffffffu, counts, x);
-                const C *kt = kl + __shfl_sync(0xffffffffu, ko, x), *vt = vl + __shfl_sync(0xffffffffu, vo, x);
+                const C *kt = P.k, *vt = P.v;
 #pragma unroll
                 for (int j = 0; j < 16 / RPI; ++j) {
                     const bool in = valid >> (copy_row + RPI * j) & 1;
@@ -217,17 +225,15 @@ __global__ void __launch_bounds__(Tile<C, D, SOLO>::T, Tile<C, D, SOLO>::CTAS) k
                     vt += RPI * p.v_token_stride;
                 }
             } else {
-                valid = counts >> (16 * x) & 0xffffu;
 #pragma unroll
                 for (int j = 0; j < 16 / RPI; ++j) {
                     const int row = copy_row + RPI * j;
                     const bool in = valid >> row & 1;
                     const uint32_t at = (to ^ (L::swap(RPI * j) << 4)) + RPI * j * ROW;
-                    cp_async(at, kl + __shfl_sync(0xffffffffu, ko, 16 * x + row), in);
-                    cp_async(at + TT * L::BLOCK, vl + __shfl_sync(0xffffffffu, vo, 16 * x + row), in);
+                    cp_async(at, P.k + __shfl_sync(0xffffffffu, ko, 16 * P.x + row), in);
+                    cp_async(at + TT * L::BLOCK, P.v + __shfl_sync(0xffffffffu, vo, 16 * P.x + row), in);
                 }
             }
-            return valid << (16 * b);
         };
 
         uint32_t mask[STAGES];  // which tokens of the tiles in flight count, oldest first
@@ -237,7 +243,11 @@ __global__ void __launch_bounds__(Tile<C, D, SOLO>::T, Tile<C, D, SOLO>::CTAS) k
             if (i * TT % LOOK == 0) locate(i * TT, first[i * TT / LOOK]);
             if (i < tiles)
 #pragma unroll
-                for (int b = 0; b < TT; ++b) mask[i] |= issue(i, b, i);
+                for (int b = 0; b < TT; ++b) {
+                    const Place at = place(i, b);
+                    issue(at, b, i);
+                    mask[i] |= at.valid << (16 * b);
+                }
             cp_commit();
         }
         int pages[AHEAD];  // of the next looks
@@ -320,23 +330,31 @@ __global__ void __launch_bounds__(Tile<C, D, SOLO>::T, Tile<C, D, SOLO>::CTAS) k
         };
 
         int stage = 0;
+        Place at[TT];  // of the next tile to request
+        auto look_on = [&](int next) {
+            if (next * TT % LOOK == 0) {
+                locate(next * TT, pages[0]);
+#pragma unroll
+                for (int j = 1; j < AHEAD; ++j) pages[j - 1] = pages[j];
+                pages[AHEAD - 1] = page_at(next * TT + AHEAD * LOOK);
+            }
+#pragma unroll
+            for (int b = 0; b < TT; ++b) at[b] = place(next, b);
+        };
+        look_on(STAGES - 1);
         for (int i = 0; i < tiles; ++i) {
+            const int next = i + STAGES - 1;
             cp_wait<STAGES - 2>();
             __syncwarp();  // every lane's copies of tile i have landed, and tile i - 1 has been read
-            {
-                const int next = i + STAGES - 1;
-                mask[STAGES - 1] = 0u;
-                if (next * TT % LOOK == 0) {
-                    locate(next * TT, pages[0]);
+            mask[STAGES - 1] = 0u;
+            if (next < tiles)
 #pragma unroll
-                    for (int j = 1; j < AHEAD; ++j) pages[j - 1] = pages[j];
-                    pages[AHEAD - 1] = page_at(next * TT + AHEAD * LOOK);
+                for (int b = 0; b < TT; ++b) {
+                    issue(at[b], b, stage == 0 ? STAGES - 1 : stage - 1);
+                    mask[STAGES - 1] |= at[b].valid << (16 * b);
                 }
-                if (next < tiles)
-#pragma unroll
-                    for (int b = 0; b < TT; ++b) mask[STAGES - 1] |= issue(next, b, stage == 0 ? STAGES - 1 : stage - 1);
-                cp_commit();
-            }
+            cp_commit();
+            look_on(next + 1);
             const uint32_t kd = k_at + stage * L::BYTES;
             float s[2 * TT][4] = {};  // of 8 tokens each
 #pragma unroll
