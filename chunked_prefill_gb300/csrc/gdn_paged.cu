@@ -78,9 +78,13 @@ PagedPlan paged_plan(const gdn_paged_problem& p) {
     const bool brief = pairs >= full ? longest <= 512 : (longest / c - longest * pairs / full) * p.D <= 16384;
     r.cluster = brief && pairs * c < (1 << 30) ? c : 0;
     if (r.cluster) r.ctas = int(pairs * c);
-    // More short ones than CTAs at a time: CTAs of one warp, 8 to a multiprocessor (195 sequences of one token, 8
-    // kv-heads: 13 us instead of 26; 250 of up to 500: 45 instead of 49; of up to 1000: 94 instead of 82).
-    r.solo = p.dtype != GDN_FP32 && r.cluster == 1 && pairs > full && most * (p.D > 128 ? p.D : 128) <= 65536;
+    // More short ones than CTAs at a time: CTAs of one warp, of which 8 to 12 fit a multiprocessor, as long as there
+    // are so many that their warps alone keep it loading: 64 of them to a token and byte of a key's row, by the times
+    // of 320 to 2000 pairs of up to 32 to 2000 tokens (2000 pairs, 128 bf16 features, CTAs of one warp and of four:
+    // up to 32 tokens 10 and 19 us, 128 19 and 28, 256 32 and 35, 512 57 and 50; 512 pairs: 5.4 and 6.9, 8.9 and 8.1,
+    // 14 and 10, 31 and 17).
+    const int64_t row = int64_t(p.D) * (p.cache_dtype == GDN_E4M3 ? 1 : 2);
+    r.solo = p.dtype != GDN_FP32 && r.cluster == 1 && pairs > full && most * (row < 256 ? row : 256) <= 64 * pairs;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     r.off_ml = up(size_t(p.num_seqs + 1) * sizeof(int64_t));
     r.off_part = r.off_ml + up(size_t(r.ctas) * 2 * s.rows * sizeof(float2));

@@ -57,7 +57,7 @@ template <typename C, int D, bool SOLO = false> struct Tile {
     static constexpr int TOK = 16 * TT;                            // tokens of a tile
     static constexpr int W = SOLO ? 1 : D * E > 256 ? 2 : 4;       // warps
     static constexpr int T = 32 * W;                               // threads
-    static constexpr int CTAS = SOLO ? (D == 256 ? 4 : 8) : D == 64 && E == 2 ? 3 : 2;  // per multiprocessor
+    static constexpr int CTAS = SOLO ? (D * E > 256 ? 4 : D == 256 ? 8 : D == 128 ? 10 : 12) : D == 64 && E == 2 ? 3 : 2;  // per multiprocessor
     static constexpr int ROW = D * E;                              // bytes of a row
     static constexpr int CPR = ROW / 16;                           // 16-byte pieces of a row
     static constexpr int RPI = 32 / CPR;                           // rows per copy instruction of a warp
