@@ -10,11 +10,16 @@
 // fp32 multiply-add, so that a token's sums need no exchange within a warp and one barrier (the warps' 4
 // parts).  A token's q, k, v, gates and <k, q> are prepared by one warp, up to STEP_TOKENS tokens at a
 // time, while the state is on its way.
+// The decay of all but a sequence's last token stays a factor E of the whole state (the state is E h, u is
+// added as u / E), which spares a multiplication per value and token; E is multiplied out where it leaves
+// [2^-20, 2^20], so that h and u / E keep within 2^20 of the state's own range, and with the last token, so that
+// a single token rounds as the formula does.
 // Bound: HBM, 64 KB in and 64 KB out per (sequence, v-head).  Measured: 256 sequences x 64 v-heads, one
-// token, bf16, 306 us (7.0 TB/s of states and rows, 1.05 of the copy bandwidth measured on the same GPUs);
-// 32 x 24 from raw projections 19.6 us (floor 15.1: three waves of CTAs); 48 sequences of up to 6 tokens, 48
-// v-heads, fp32, 58 us (floor 46.8: issue slots 56 % busy, each token some 130 instructions a warp and one
-// barrier).  Not kept: two tokens to a barrier (66 us, registers spill), two columns and 16 rows a lane (58 us).
+// token, bf16, 307 us (7.0 TB/s of states and rows, 1.05 of the copy bandwidth measured on the same GPUs);
+// 32 x 24 from raw projections 18.5 us (floor 15.1: three waves of CTAs); 48 sequences of up to 6 tokens, 48
+// v-heads, fp32, 56 us (floor 46.8: each token some 115 instructions a warp and one barrier; 58 with the decay
+// multiplied into the state every token).  Not kept: two tokens to a barrier (66 us, registers spill), two columns
+// and 16 rows a lane (58 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -31,6 +36,7 @@ constexpr int ST = 128;          // threads
 constexpr int SC = 32;           // state columns per CTA
 constexpr int SR = KD / 4;       // rows of the state per thread
 constexpr int STEP_TOKENS = 8;   // tokens prepared at a time
+constexpr float LEAST = 1.f / (1 << 20);  // of the factor E
 
 // 4 consecutive values
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
@@ -96,6 +102,7 @@ __global__ void __launch_bounds__(ST, 8) k_step(const StepArgs A) {
                              : "memory");
         }
     }
+    float E = 1.f;  // the state is E h
     for (int c0 = t0; c0 < t1; c0 += STEP_TOKENS) {
         const int n = min(STEP_TOKENS, t1 - c0);
         if (c0 > t0) __syncthreads();  // the last tokens have been read
@@ -156,14 +163,26 @@ __global__ void __launch_bounds__(ST, 8) k_step(const StepArgs A) {
                 sa += red[i & 1][w][0][lane];
                 sb += red[i & 1][w][1][lane];
             }
-            const float u = gt.y * (sv[i][lane] - gt.x * sa);
-            if (warp == (i & 3)) o[int64_t(c0 + i) * p.Hv * VD] = from_f<Op>(p.scale * fmaf(gt.z, u, gt.x * sb));
-            const uint64_t u2 = tc::dup2(u), e2 = tc::dup2(gt.x);
+            const float decay = E * gt.x, u = gt.y * (sv[i][lane] - decay * sa);
+            if (warp == (i & 3)) o[int64_t(c0 + i) * p.Hv * VD] = from_f<Op>(p.scale * fmaf(gt.z, u, decay * sb));
+            if (c0 + i + 1 < t1 && decay >= LEAST && decay <= 1.f / LEAST) {
+                E = decay;
+                const uint64_t u2 = tc::dup2(__fdividef(u, decay));
 #pragma unroll
-            for (int x = 0; x < SR / 4; ++x) {
-                const ulonglong2 kx = k2[x];
-                h[2 * x] = tc::ffma2(kx.x, u2, tc::fmul2(e2, h[2 * x]));
-                h[2 * x + 1] = tc::ffma2(kx.y, u2, tc::fmul2(e2, h[2 * x + 1]));
+                for (int x = 0; x < SR / 4; ++x) {
+                    const ulonglong2 kx = k2[x];
+                    h[2 * x] = tc::ffma2(kx.x, u2, h[2 * x]);
+                    h[2 * x + 1] = tc::ffma2(kx.y, u2, h[2 * x + 1]);
+                }
+            } else {
+                E = 1.f;
+                const uint64_t u2 = tc::dup2(u), e2 = tc::dup2(decay);
+#pragma unroll
+                for (int x = 0; x < SR / 4; ++x) {
+                    const ulonglong2 kx = k2[x];
+                    h[2 * x] = tc::ffma2(kx.x, u2, tc::fmul2(e2, h[2 * x]));
+                    h[2 * x + 1] = tc::ffma2(kx.y, u2, tc::fmul2(e2, h[2 * x + 1]));
+                }
             }
         }
     }

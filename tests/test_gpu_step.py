@@ -153,6 +153,23 @@ def test_decay_to_nothing_and_full_write():
     assert rel_err(np64(new)[0, 0], want) <= FP32_TOL
 
 
+@pytest.mark.parametrize("gates", [[0.0, -0.01, -5.0, -40.0, 0.0], [-3.0], [0.7], [-100.0, 0.0], [0.0, -float("inf"), -0.5, 20.0, -20.0]])
+def test_decays_of_every_size_over_many_tokens(gates):
+    """Decays that add up past any factor kept aside of the state, down and up.  A growing state's errors
+    grow with it: each token adds at most |k_i| <= 0.3 times 1e-4 of its largest value."""
+    from chunked_prefill_gb300 import gdn
+    T = 43
+    d = inputs(T, 2, 4, 1, 12, torch.float32)
+    d["g"] = torch.tensor(gates)[torch.arange(T) % len(gates)][:, None].repeat(1, 4) * (1 + 0.1 * torch.arange(4))
+    x = cuda(d)
+    o, new = gdn.gated_delta_rule_step(x["q"], x["k"], x["v"], x["g"], x["beta"], state=x["state"].clone())
+    ro, rs = oracle(d, [0], [T], 128 ** -0.5)
+    tol = 0.3 * T * FP32_TOL
+    assert rel_err(np64(new), rs) <= tol
+    o = np64(o)[0]
+    assert all(rel_err(o[t], ro[t]) <= tol for t in range(T))
+
+
 def test_other_stream_graph_and_determinism():
     """A captured step replayed with other lengths and slots, on a stream of its own; repeated
     calls give equal bits."""
