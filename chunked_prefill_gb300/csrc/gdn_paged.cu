@@ -71,11 +71,15 @@ PagedPlan paged_plan(const gdn_paged_problem& p) {
     // distributed shared memory.  Finding a CTA's part of the list and the second kernel take 4 to 5 us, the
     // time of some 16384 / D tokens per warp; a cluster's warps have at most longest / c tokens, in an even
     // split longest * pairs / full.  Enough CTAs even themselves out, so that the list is worth its while from
-    // 512 tokens per warp on.
+    // 512 tokens per warp on.  So do clusters that reach every multiprocessor, one CTA on each loading about as
+    // much as the memory gives (24 sequences of up to 2000 tokens, 8 kv-heads, 128 features, even lengths and
+    // random ones: bf16 33 and 23 us, the list 40 and 28; 8 bits 25 and 21, the list 31 and 28).
     const int64_t pairs = int64_t(p.num_seqs) * blocks, longest = (most + s.warps - 1) / s.warps;
     int c = 1;
     while (c < 8 && pairs * c * 2 <= full && longest * p.D > int64_t(c) * CLUSTER_WORK) c *= 2;
-    const bool brief = pairs >= full ? longest <= 512 : (longest / c - longest * pairs / full) * p.D <= 16384;
+    const bool brief = pairs >= full ? longest <= 512
+                                     : (longest / c - longest * pairs / full) * p.D <= 16384 ||
+                                           (p.dtype != GDN_FP32 && pairs * c >= sm_count_cached() && longest / c * (p.D > 128 ? p.D : 128) <= 65536);
     r.cluster = brief && pairs * c < (1 << 30) ? c : 0;
     if (r.cluster) r.ctas = int(pairs * c);
     // More short ones than CTAs at a time: CTAs of one warp, of which 8 to 12 fit a multiprocessor, as long as there
