@@ -303,6 +303,43 @@ def test_many_sequences_and_many_heads():
         check(x, *call(x))
 
 
+def some_lens(N, most, seed):
+    edges = [most, 0, 1, min(15, most), min(16, most), min(17, most), most - 1]
+    gen = torch.Generator().manual_seed(seed)
+    return (edges + torch.randint(0, most + 1, (N,), generator=gen).tolist())[:N]
+
+
+@pytest.mark.parametrize("cache", [BF, FP8, F32])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("G,page,window", [(1, 16, 0), (6, 7, 0), (16, 16, 20), (12, 5, 9), (20, 32, 0)])
+def test_many_short_sequences(cache, D, G, page, window):
+    """More pairs than multiprocessors hold CTAs, of few tokens each, empty ones among them."""
+    N, Hkv = 154, 4
+    x = make(some_lens(N, 50, D + G), G * Hkv, Hkv, D, page, cache, seed=G, heads_first=G == 6)
+    check(x, *call(x, window=window), window=window)
+
+
+@pytest.mark.parametrize("cache", [BF, FP8, F32])
+@pytest.mark.parametrize("D,N,Hkv,most", [(128, 1, 2, 900), (128, 20, 2, 900), (128, 60, 2, 700), (128, 100, 2, 400), (128, 160, 2, 600),
+                                          (64, 7, 2, 1500), (64, 170, 3, 300), (256, 5, 3, 500), (256, 140, 3, 130)])
+def test_every_division_of_short_caches(cache, D, N, Hkv, most):
+    """One to eight CTAs to a (sequence, kv-head), of one warp and of several; the last CTAs of a
+    sequence have nothing where it is short."""
+    x = make(some_lens(N, most, N), 4 * Hkv, Hkv, D, 16, cache, seed=N)
+    check(x, *call(x))
+    live = torch.nonzero(x["lens"] > 0).flatten()
+    kn, vn = (torch.randn(N, Hkv, D, device="cuda").to(x["q"].dtype) for _ in range(2))
+    before = x["k"].float().clone(), x["v"].float().clone()
+    got = call(x, k_new=kn, v_new=vn)
+    check(x, *got)  # against the caches as they are now
+    t = x["lens"][live].long() - 1
+    pages = x["table"][live, t // 16].long()
+    for c, b, new, sc in ((x["k"], before[0], kn, x["ks"]), (x["v"], before[1], vn, x["vs"])):
+        row = new[live].float() / (1.0 if sc is None else sc[:, None])
+        b[pages, t % 16] = row.to(cache).float()
+        assert torch.equal(torch.nan_to_num(c.float(), nan=-7.0), torch.nan_to_num(b, nan=-7.0))
+
+
 def test_a_new_token_past_the_table_is_not_written():
     x = make([48, 20], 4, 2, 128, 16, BF, seed=19)
     x["table"] = x["table"][:, :3].contiguous()
