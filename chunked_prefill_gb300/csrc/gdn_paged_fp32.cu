@@ -32,9 +32,10 @@ template <int D, int HB> struct Fp32Tile {
     static constexpr int REP = LPR / NV;                         // lanes that get the same score
     static constexpr int CTAS = HB == 8 || D == 256 ? 2 : 4;     // per multiprocessor
     static constexpr int BYTES = 2 * PU * D * 4;                 // of a warp's step: keys, values
-    static constexpr int FIT = 196608 / CTAS / (PW * BYTES), STAGES = FIT < 8 ? FIT : 8;
-    static constexpr int SMEM = STAGES * PW * BYTES;
-    static_assert(REP >= 1 && STAGES >= 3 && (PW * NG + 1) * HB * D * 4 <= SMEM, "the groups' accumulators are joined in the ring's memory");
+    static constexpr int FIT = 196608 / CTAS / (PW * BYTES), STAGES = FIT < 4 ? FIT : 4;  // more take more time (64 features: 6 of them 5 %)
+    static constexpr int RINGS = STAGES * PW * BYTES, JOINED = (PW * NG + 1) * HB * D * 4;  // the groups' accumulators and their sum
+    static constexpr int SMEM = RINGS > JOINED ? RINGS : JOINED;
+    static_assert(REP >= 1 && STAGES >= 3, "");
 };
 
 // N values a lane, summed over 2 W lanes: lane l gets value l / REP of N = 2 W / REP.

@@ -65,7 +65,8 @@ template <typename C, int D, bool SOLO = false> struct Tile {
     static constexpr int VC = E == 1 ? ROW / (8 * VB) : 0;         // 8-bit: pieces of a value row per thread
     static constexpr int BLOCK = 16 * ROW;                         // bytes of 16 rows
     static constexpr int BYTES = 2 * TT * BLOCK;                   // of a warp's tile: K's blocks, V's blocks
-    static constexpr int FIT = (SOLO ? 196608 / CTAS : CTAS == 3 ? 65536 : 98304) / (W * BYTES), STAGES = FIT < 8 ? FIT : 8;
+    static constexpr int FIT = (SOLO ? 196608 / CTAS : CTAS == 3 ? 65536 : 98304) / (W * BYTES);
+    static constexpr int STAGES = FIT < 3 ? FIT : 3;               // more take more time (8 bits, 64 features: 6 of them 2 to 8 %)
     static constexpr int PAD = D + 4;                              // floats between rows of the joined accumulators
     static constexpr int SMEM = STAGES * W * BYTES;
     static_assert(STAGES >= 2 && W * 16 * PAD * 4 + (SOLO ? 0 : 16 * D * 4) <= SMEM, "the warps' accumulators are joined in the stages' memory");
