@@ -31,7 +31,7 @@
 // fp32: k_paged_fp32 (gdn_paged_fp32.cu), on the CUDA cores.
 //
 // Measured (of the copy bandwidth measured on the same GPUs): 64 sequences of up to 8192 tokens, 32 / 8 heads,
-// 128 features, bf16, 161 us (6.7 TB/s, 1.00); 128 of up to 16384, 64 / 8, 8 bits, 319 us (6.6 TB/s, 0.99); one
+// 128 features, bf16, 162 us (6.7 TB/s, 1.00); 128 of up to 16384, 64 / 8, 8 bits, 322 us (6.6 TB/s, 0.98); one
 // of 131071, 32 / 4, bf16, 46.7 us (5.7 TB/s, 0.86: finding the parts and the join take 5 us); 4 of up to 700,
 // 16 / 2, 256 features, the new token written, 9.1 us (latency).
 #include "gdn_paged.cuh"
