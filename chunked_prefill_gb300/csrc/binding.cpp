@@ -128,6 +128,13 @@ void need_vector(const char* name, const at::Tensor* t, at::ScalarType type, int
     if (t) need(t->scalar_type() == type && t->dim() == 1 && t->size(0) == n && t->is_contiguous(), std::string(name) + " must be a contiguous " + what);
 }
 
+// The stride of rows of which there is more than one.  The C ABI's 0 stands for contiguous rows, so an
+// expanded view (every row the same one) would be read past its end.
+int64_t apart(const char* name, int64_t stride) {
+    if (stride == 0) throw Bad{PyExc_ValueError, std::string("the rows of ") + name + " lie at a stride of 0 (an expanded view): pass a contiguous copy"};
+    return stride;
+}
+
 // Elements from one token to the next of a [B, T, ...] tensor whose last dimensions are contiguous
 // (`inner` values) and whose tokens lie at one stride.
 int64_t token_stride(const char* name, const at::Tensor& t, int64_t inner) {
@@ -138,9 +145,9 @@ int64_t token_stride(const char* name, const at::Tensor& t, int64_t inner) {
     }
     const int64_t B = t.size(0), T = t.size(1);
     if (B * T <= 1) return inner;
-    if (T == 1) return t.stride(0);
+    if (T == 1) return apart(name, t.stride(0));
     need(B == 1 || t.stride(0) == T * t.stride(1), std::string("the tokens of ") + name + " must lie at one stride");
-    return t.stride(1);
+    return apart(name, t.stride(1));
 }
 
 PyObject* step(Args& a) {
@@ -155,18 +162,6 @@ PyObject* step(Args& a) {
     need(g.dim() == 3 && g.size(0) == B && g.size(1) == T && g.size(2) == Hv && beta.sizes() == g.sizes(), "g and beta must be [B,T,Hv]");
     need(g.scalar_type() == at::kFloat && beta.scalar_type() == at::kFloat, "g and beta must be float32");
     need(B * T < (int64_t(1) << 31) && Hqk < (1 << 30) && Hv < (1 << 30) && K < (1 << 30) && V < (1 << 30), "too many tokens or heads");
-    need_cuda(q, "q", q);
-    need_cuda(q, "k", k);
-    need_cuda(q, "v", v);
-    need_cuda(q, "g", g);
-    need_cuda(q, "beta", beta);
-    need_cuda(q, "state_in", in);
-    need_cuda(q, "state_out", out);
-    need_cuda(q, "slots", slots);
-    need_cuda(q, "cu_seqlens", cu);
-    need_cuda(q, "A_log", A_log);
-    need_cuda(q, "dt_bias", bias);
-    need_cuda(q, "o", given);
     gdn_step_problem p{};
     int64_t n = B;
     if (cu) {
@@ -203,6 +198,18 @@ PyObject* step(Args& a) {
     p.v_stride = token_stride("v", v, Hv * V);
     p.g_stride = token_stride("g", g, Hv);
     p.beta_stride = token_stride("beta", beta, Hv);
+    need_cuda(q, "q", q);
+    need_cuda(q, "k", k);
+    need_cuda(q, "v", v);
+    need_cuda(q, "g", g);
+    need_cuda(q, "beta", beta);
+    need_cuda(q, "state_in", in);
+    need_cuda(q, "state_out", out);
+    need_cuda(q, "slots", slots);
+    need_cuda(q, "cu_seqlens", cu);
+    need_cuda(q, "A_log", A_log);
+    need_cuda(q, "dt_bias", bias);
+    need_cuda(q, "o", given);
     On on(q, a);
     const at::Tensor o = given ? *given : empty(v.sizes(), v.scalar_type(), v);
     check(f_step(&p, q.data_ptr(), k.data_ptr(), v.data_ptr(), ptr(g), ptr(beta), ptr(A_log), ptr(bias), ptr(in), ptr(out), o.data_ptr(), on.stream));
@@ -237,18 +244,6 @@ PyObject* paged(Args& a) {
     const int64_t N = q.size(0), Hq = q.size(1), D = q.size(2), Hkv = kc.size(2);
     need(kc.size(3) == D, "q and the caches must match in D");
     need(vc.scalar_type() == kc.scalar_type(), "k_cache and v_cache must both be bfloat16, float32 or float8_e4m3fn");
-    need_cuda(q, "q", q);
-    need_cuda(q, "k_cache", kc);
-    need_cuda(q, "v_cache", vc);
-    need_cuda(q, "page_table", table);
-    need_cuda(q, "seq_lens", lens);
-    need_cuda(q, "k_new", kn);
-    need_cuda(q, "v_new", vn);
-    need_cuda(q, "k_scale", ks);
-    need_cuda(q, "v_scale", vs);
-    need_cuda(q, "o", given);
-    need_cuda(q, "lse", lse);
-    need_cuda(q, "workspace", ws);
     need(table.scalar_type() == at::kInt && table.dim() == 2 && table.size(0) == N && (table.size(1) <= 1 || table.stride(1) == 1),
          "page_table must be int32 [N,max_pages] with contiguous rows");
     need(lens.scalar_type() == at::kInt && lens.dim() == 1 && lens.size(0) == N && lens.is_contiguous(), "seq_lens must be a contiguous int32 [N]");
@@ -265,7 +260,7 @@ PyObject* paged(Args& a) {
         rows("v_new", *vn, Hkv);
         if (N > 1) {
             need(kn->stride(0) == vn->stride(0), "k_new and v_new must have the same row stride");
-            p.new_stride = kn->stride(0);
+            p.new_stride = apart("k_new and v_new", kn->stride(0));
         }
     }
     need_vector("k_scale", ks, at::kFloat, Hkv, "float32 [Hkv]");
@@ -285,14 +280,26 @@ PyObject* paged(Args& a) {
     p.page_size = small(kc.size(1), "tokens to a page");
     p.max_pages = small(table.size(1), "pages");
     p.num_pages = kc.size(0);
-    p.q_stride = N > 1 ? q.stride(0) : 0;
-    p.table_stride = N > 1 ? table.stride(0) : 0;
+    p.q_stride = N > 1 ? apart("q", q.stride(0)) : 0;
+    p.table_stride = N > 1 && table.size(1) > 0 ? apart("page_table", table.stride(0)) : 0;
     p.k_page_stride = kc.stride(0);
     p.k_token_stride = kc.stride(1);
     p.k_head_stride = kc.stride(2);
     p.v_page_stride = vc.stride(0);
     p.v_token_stride = vc.stride(1);
     p.v_head_stride = vc.stride(2);
+    need_cuda(q, "q", q);
+    need_cuda(q, "k_cache", kc);
+    need_cuda(q, "v_cache", vc);
+    need_cuda(q, "page_table", table);
+    need_cuda(q, "seq_lens", lens);
+    need_cuda(q, "k_new", kn);
+    need_cuda(q, "v_new", vn);
+    need_cuda(q, "k_scale", ks);
+    need_cuda(q, "v_scale", vs);
+    need_cuda(q, "o", given);
+    need_cuda(q, "lse", lse);
+    need_cuda(q, "workspace", ws);
     On on(q, a);
     size_t bytes = 0;
     check(f_paged_size(&p, &bytes));
@@ -316,7 +323,7 @@ PyObject* paged(Args& a) {
 int64_t row_stride(const char* name, const at::Tensor& t) {
     if (t.is_contiguous()) return 0;
     need(t.dim() == 2 && t.stride(1) == 1, std::string(name) + " must be contiguous, or two-dimensional with contiguous rows");
-    return t.size(0) > 1 ? t.stride(0) : 0;
+    return t.size(0) > 1 ? apart(name, t.stride(0)) : 0;
 }
 void like_rows(const char* name, const at::Tensor& t, const at::Tensor& x) {
     need(t.sizes() == x.sizes() && t.scalar_type() == x.scalar_type(), std::string(name) + " must match the rows in shape and dtype");
@@ -353,15 +360,15 @@ PyObject* norm_fwd(Args& a) {
     const bool quant = a.flag();
     const int64_t group = a.integer();
     const bool want_sum = a.flag();
-    need_cuda(x, "x", x);
-    need_cuda(x, "weight", w);
-    need_cuda(x, "residual", res);
     gdn_norm_problem p = norm_problem(x, w, eps, offset);
     p.x_stride = row_stride("x", x);
     if (res) {
         like_rows("residual", *res, x);
         p.residual_stride = row_stride("residual", *res);
     }
+    need_cuda(x, "x", x);
+    need_cuda(x, "weight", w);
+    need_cuda(x, "residual", res);
     On on(x, a);
     at::Tensor total, scale;
     if (res && want_sum) total = empty(x.sizes(), x.scalar_type(), x);
@@ -383,11 +390,6 @@ PyObject* norm_bwd(Args& a) {
     const at::Tensor* dsum = a.maybe("dsum");
     const double eps = a.number(), offset = a.number();
     const at::Tensor* ws = a.maybe("workspace");
-    need_cuda(s, "s", s);
-    need_cuda(s, "weight", w);
-    need_cuda(s, "dy", dy);
-    need_cuda(s, "dsum", dsum);
-    need_cuda(s, "workspace", ws);
     gdn_norm_problem p = norm_problem(s, w, eps, offset);
     p.x_stride = row_stride("s", s);
     like_rows("dy", dy, s);
@@ -396,6 +398,11 @@ PyObject* norm_bwd(Args& a) {
         like_rows("dsum", *dsum, s);
         p.dsum_stride = row_stride("dsum", *dsum);
     }
+    need_cuda(s, "s", s);
+    need_cuda(s, "weight", w);
+    need_cuda(s, "dy", dy);
+    need_cuda(s, "dsum", dsum);
+    need_cuda(s, "workspace", ws);
     On on(s, a);
     size_t bytes = 0;
     check(f_norm_bwd_size(&p, &bytes));

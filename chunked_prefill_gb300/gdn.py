@@ -544,7 +544,7 @@ def _binding():
 def gdn_recurrent_step(q, k, v, g, beta, scale, state_in=None, state_out=None, slots=None,
                        cu_seqlens=None, A_log=None, dt_bias=None, o=None, stream=None):
     """Recurrent step through the C ABI (see include/gdn.h).  q, k [B,T,Hqk,K], v [B,T,Hv,V],
-    g, beta [B,T,Hv] fp32, each with contiguous rows at any token stride; state_in, state_out
+    g, beta [B,T,Hv] fp32, each with contiguous rows at any token stride but 0; state_in, state_out
     [num_slots,Hv,K,V] fp32 pools; slots int32 [num_seqs]; cu_seqlens int32 [num_seqs+1] with
     B = 1, else B sequences of T tokens.  Returns o [B,T,Hv,V]."""
     return (_native or _binding()).step(q, k, v, g, beta, scale, state_in, state_out, slots,

@@ -1,0 +1,81 @@
+"""What the decoding calls' Python side refuses, on the CPU: the shapes, strides and gradients of the
+arguments are looked at before their devices, so host tensors reach these checks."""
+import pytest
+import torch
+
+from chunked_prefill_gb300 import build as gbuild
+
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def gdn():
+    gbuild.build()
+    from chunked_prefill_gb300 import gdn
+    return gdn
+
+
+def step_args(B=4, T=1, Hqk=1, Hv=2):
+    z = lambda *s: torch.zeros(*s, dtype=BF)  # noqa: E731
+    return dict(q=z(B, T, Hqk, 128), k=z(B, T, Hqk, 128), v=z(B, T, Hv, 128), g=torch.zeros(B, T, Hv), beta=torch.zeros(B, T, Hv),
+                state=torch.zeros(B, Hv, 128, 128))
+
+
+def paged_args(N=3, Hq=4, Hkv=2, D=64):
+    return dict(q=torch.zeros(N, Hq, D, dtype=BF), k_cache=torch.zeros(5, 16, Hkv, D, dtype=BF), v_cache=torch.zeros(5, 16, Hkv, D, dtype=BF),
+                page_table=torch.zeros(N, 2, dtype=torch.int32), seq_lens=torch.ones(N, dtype=torch.int32))
+
+
+def one_row(t, dims=1):
+    """All rows the first one, as an expanded view."""
+    return t[(slice(0, 1),) * dims].expand(t.shape)
+
+
+@pytest.mark.parametrize("name", ["q", "k", "v", "g", "beta"])
+@pytest.mark.parametrize("B,T", [(4, 1), (1, 4), (2, 3)])
+def test_step_refuses_expanded_rows(gdn, name, B, T):
+    """A stride of 0 means contiguous rows to the C ABI: an expanded view would be read past its end."""
+    a = step_args(B, T)
+    a[name] = one_row(a[name], 2)
+    with pytest.raises(ValueError, match=f"the rows of {name} lie at a stride of 0"):
+        gdn.gated_delta_rule_step(**a)
+
+
+@pytest.mark.parametrize("name", ["q", "page_table"])
+def test_attention_refuses_expanded_rows(gdn, name):
+    a = paged_args()
+    a[name] = one_row(a[name])
+    with pytest.raises(ValueError, match=f"the rows of {name} lie at a stride of 0"):
+        gdn.paged_attention_decode(**a)
+
+
+def test_attention_refuses_an_expanded_new_token(gdn):
+    a = paged_args()
+    new = one_row(torch.zeros(3, 2, 64, dtype=BF))
+    with pytest.raises(ValueError, match="the rows of k_new and v_new lie at a stride of 0"):
+        gdn.paged_attention_decode(**a, k_new=new, v_new=new)
+
+
+@pytest.mark.parametrize("dim", [1, 8, 64])
+def test_norm_refuses_expanded_rows(gdn, dim):
+    x, w = torch.zeros(5, dim), torch.ones(dim)
+    one = one_row(torch.zeros(5, dim))
+    for name, call in (("x", lambda: gdn.rms_norm(one, w)), ("residual", lambda: gdn.rms_norm(x, w, residual=one)),
+                       ("residual", lambda: gdn.rms_norm_quant(x, w, residual=one)), ("s", lambda: gdn.gdn_rmsnorm_bwd(one, w, x)),
+                       ("dy", lambda: gdn.gdn_rmsnorm_bwd(x, w, one)), ("dsum", lambda: gdn.gdn_rmsnorm_bwd(x, w, x, dsum=one))):
+        with pytest.raises(ValueError, match=f"the rows of {name} lie at a stride of 0"):
+            call()
+
+
+def test_one_row_may_have_any_stride(gdn):
+    """A single row, and no rows, have no distance between rows: these get as far as their device."""
+    a = step_args(1, 1)
+    a["beta"] = torch.zeros(1).expand(1, 1, 2).contiguous().as_strided((1, 1, 2), (0, 0, 1))
+    with pytest.raises(ValueError, match="CUDA"):
+        gdn.gated_delta_rule_step(**a)
+    a = paged_args(N=1)
+    a["q"], a["page_table"] = a["q"].as_strided((1, 4, 64), (0, 64, 1)), a["page_table"].as_strided((1, 2), (0, 1))
+    with pytest.raises(ValueError, match="CUDA"):
+        gdn.paged_attention_decode(**a)
+    with pytest.raises(ValueError, match="CUDA"):
+        gdn.rms_norm(torch.zeros(64).as_strided((1, 64), (0, 1)), torch.ones(64))
