@@ -118,6 +118,10 @@ template <typename T = float> T* ptr(const at::Tensor& t) { return static_cast<T
 at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like) {
     return at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
 }
+// The caller's scratch: its bytes are counted from its values, which a strided or expanded view has not all of.
+void need_scratch(const at::Tensor* t) {
+    if (t) need(t->is_contiguous(), "workspace must be contiguous");
+}
 // device scratch of n bytes: the caller's where it is large enough
 at::Tensor scratch(size_t n, const at::Tensor* given, const at::Tensor& like) {
     if (n == 0) return like;  // not used
@@ -288,6 +292,7 @@ PyObject* paged(Args& a) {
     p.v_page_stride = vc.stride(0);
     p.v_token_stride = vc.stride(1);
     p.v_head_stride = vc.stride(2);
+    need_scratch(ws);
     need_cuda(q, "q", q);
     need_cuda(q, "k_cache", kc);
     need_cuda(q, "v_cache", vc);
@@ -398,6 +403,7 @@ PyObject* norm_bwd(Args& a) {
         like_rows("dsum", *dsum, s);
         p.dsum_stride = row_stride("dsum", *dsum);
     }
+    need_scratch(ws);
     need_cuda(s, "s", s);
     need_cuda(s, "weight", w);
     need_cuda(s, "dy", dy);

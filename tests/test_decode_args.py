@@ -79,3 +79,12 @@ def test_one_row_may_have_any_stride(gdn):
         gdn.paged_attention_decode(**a)
     with pytest.raises(ValueError, match="CUDA"):
         gdn.rms_norm(torch.zeros(64).as_strided((1, 64), (0, 1)), torch.ones(64))
+
+
+@pytest.mark.parametrize("ws", [torch.zeros(1, dtype=torch.uint8).expand(1 << 20), torch.zeros(1 << 12, dtype=torch.uint8)[::2]])
+def test_a_workspace_that_is_not_contiguous_is_refused(gdn, ws):
+    """A view's values need not be bytes of its own: the kernels would write past them."""
+    with pytest.raises(ValueError, match="workspace must be contiguous"):
+        gdn.paged_attention_decode(**paged_args(), workspace=ws)
+    with pytest.raises(ValueError, match="workspace must be contiguous"):
+        gdn.gdn_rmsnorm_bwd(torch.zeros(3, 8), torch.ones(8), torch.zeros(3, 8), workspace=ws)
