@@ -258,7 +258,9 @@ __global__ void __launch_bounds__(Tile<C, D, SOLO>::T, Tile<C, D, SOLO>::CTAS) k
         // ---- query fragments, of 16-feature step s: features 2t, + 1 and 8 + 2t, + 1.  8-bit caches, of
         // 32-feature step s: features 4t .. 4t + 3 and 16 + 4t .., each value the sum of two 8-bit ones of
         // the row scaled to [128, 256): exact for bf16's 8 significant bits down to 2^-9 of the row's
-        // largest value (4 bits each, the second with a sign of its own), off by 2^-18 of it below.
+        // largest value (4 bits each, the second with a sign of its own), off by 2^-18 of it below.  A row
+        // below 2^-119 is scaled by 2^126, the largest finite power that has an inverse: bf16's values, all
+        // multiples of 2^-133, are then multiples of 2^-7, and exact.
         alignas(16) uint32_t qf[QF][2 * R2];
         float zs[R2];
 #pragma unroll
@@ -279,7 +281,7 @@ __global__ void __launch_bounds__(Tile<C, D, SOLO>::T, Tile<C, D, SOLO>::CTAS) k
                 top = mag_max(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = mag_max(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 const bool fine = top > 0.f && top < INFINITY;
-                const int e = fine ? ilogbf(top) - 7 : 0;
+                const int e = fine ? max(ilogbf(top) - 7, -126) : 0;
                 const float down = fine ? ldexpf(1.f, -e) : 1.f;
                 // an infinite or NaN query makes every score NaN (as inf - inf does in the definition)
                 const float bad = top < INFINITY ? 0.f : NAN;

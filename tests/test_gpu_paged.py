@@ -353,3 +353,18 @@ def test_a_new_token_past_the_table_is_not_written():
     for a, b in ((x["k"], k), (x["v"], v)):
         assert torch.equal(torch.nan_to_num(a, nan=-7.0), torch.nan_to_num(b, nan=-7.0))
     check(x, *got)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Hq,cache,lift", [(8, FP8, 0), (8, FP8, 120), (16, FP8, 0), (16, FP8, 120), (8, BF, 0)])
+def test_queries_of_the_smallest_sizes(D, Hq, cache, lift):
+    """Query rows down to the smallest subnormal of bf16, zeros among their features; with scales of 2^lift
+    their scores are of ordinary size and have to be as exact."""
+    x = make([300, 20, 1], Hq, 1, D, 16, cache, seed=D + Hq)
+    down = torch.tensor([-112, -118, -119, -120, -121, -126, -130, -133] * 2)[:Hq]
+    q = torch.randn(3, Hq, D, generator=torch.Generator().manual_seed(5)).double() * 2.0 ** down.double()[:, None]
+    q[:, :, ::3] = 0
+    x["q"] = q.float().to(BF).cuda()
+    if x["ks"] is not None:
+        x["ks"] *= 2.0 ** lift
+    check(x, *call(x))
