@@ -666,6 +666,10 @@ def rms_norm(x, weight, residual=None, eps=1e-6, weight_offset=0.0):
 def rms_norm_quant(x, weight, residual=None, eps=1e-6, weight_offset=0.0, group=0):
     """rms_norm with y in 8 bits (float8_e4m3fn): returns (y, scale, s) with the normed row
     approximately y * scale; scale fp32 [..., 1], or [..., dim / group] with one scale to `group`
-    consecutive values."""
-    return (_native or _binding()).norm_fwd(x, weight, residual, eps, weight_offset, True, group,
-                                            True, None)
+    consecutive values.  Nothing is differentiated here: to train through it, pass the gradient
+    with respect to y * scale as gdn_rmsnorm_bwd's dy."""
+    native = _native or _binding()
+    if native.wants_grad(x, weight, residual):
+        raise RuntimeError("rms_norm_quant is not differentiable, but an argument requires a gradient: "
+                           "train with rms_norm or gdn_rmsnorm_bwd")
+    return native.norm_fwd(x, weight, residual, eps, weight_offset, True, group, True, None)

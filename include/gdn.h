@@ -330,7 +330,8 @@ gdn_status gdn_paged_attn_decode(const gdn_paged_problem* p, const void* q, void
  * gdn_rmsnorm_bwd: the gradients of <y, dy> + <sum, dsum> (dsum NULL: 0) with respect to s
  * (x and residual alike) and to weight, for the s given:
  *     dx = r (w dy - n mean(w dy n)) + dsum with n = r s;   dweight = sum over rows of dy n
- * dweight is fp32, summed in a fixed order.  Rounding y to 8 bits passes the gradient through.
+ * dweight is fp32, summed in a fixed order.  For an 8-bit y, dy is the gradient with respect to
+ * y y_scale: the rounding passes it through.
  * dx may be dy or dsum (in place).
  *
  * Pointers and strides need only the alignment of their elements here; rows whose pointers and

@@ -88,3 +88,14 @@ def test_a_workspace_that_is_not_contiguous_is_refused(gdn, ws):
         gdn.paged_attention_decode(**paged_args(), workspace=ws)
     with pytest.raises(ValueError, match="workspace must be contiguous"):
         gdn.gdn_rmsnorm_bwd(torch.zeros(3, 8), torch.ones(8), torch.zeros(3, 8), workspace=ws)
+
+
+@pytest.mark.parametrize("name", ["x", "weight", "residual"])
+def test_the_8_bit_norm_refuses_gradients(gdn, name):
+    """Its outputs carry no gradient: the residual stream would be cut without a word."""
+    a = dict(x=torch.zeros(3, 8), weight=torch.ones(8), residual=torch.zeros(3, 8))
+    a[name].requires_grad_(True)
+    with pytest.raises(RuntimeError, match="differentiable"):
+        gdn.rms_norm_quant(**a)
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):  # as far as the device
+        gdn.rms_norm_quant(**a)
