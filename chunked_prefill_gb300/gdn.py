@@ -568,7 +568,7 @@ def gated_delta_rule_step(q, k, v, g, beta, scale=None, state=None, state_out=No
             return gated_delta_rule_step(q, k, v, g, beta, scale, state, state_out, slots, cu_seqlens,
                                          A_log, dt_bias, o)
     native = _native or _binding()
-    if native.wants_grad(q, k, v, g, beta, state):
+    if native.wants_grad(q, k, v, g, beta, state, state_out, A_log, dt_bias):
         raise RuntimeError("gated_delta_rule_step is not differentiable, but an argument requires a "
                            "gradient: train with chunk_gated_delta_rule")
     if scale is None:

@@ -99,3 +99,13 @@ def test_the_8_bit_norm_refuses_gradients(gdn, name):
         gdn.rms_norm_quant(**a)
     with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):  # as far as the device
         gdn.rms_norm_quant(**a)
+
+
+@pytest.mark.parametrize("name", ["q", "k", "v", "g", "beta", "state", "state_out", "A_log", "dt_bias"])
+def test_the_step_refuses_gradients(gdn, name):
+    a = dict(step_args(), state_out=torch.zeros(4, 2, 128, 128), A_log=torch.zeros(2), dt_bias=torch.zeros(2))
+    a[name].requires_grad_(True)
+    with pytest.raises(RuntimeError, match="differentiable"):
+        gdn.gated_delta_rule_step(**a)
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+        gdn.gated_delta_rule_step(**a)
