@@ -607,7 +607,7 @@ def paged_attention_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None
     before it attends to them.  window > 0 attends to the last `window` tokens.  For inference:
     nothing is differentiated here."""
     native = _native or _binding()
-    if native.wants_grad(q, k_new, v_new):
+    if native.wants_grad(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale):
         raise RuntimeError("paged_attention_decode is not differentiable, but an argument requires "
                            "a gradient")
     if scale is None:

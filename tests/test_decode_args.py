@@ -109,3 +109,14 @@ def test_the_step_refuses_gradients(gdn, name):
         gdn.gated_delta_rule_step(**a)
     with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
         gdn.gated_delta_rule_step(**a)
+
+
+@pytest.mark.parametrize("name", ["q", "k_cache", "v_cache", "k_new", "v_new", "k_scale", "v_scale"])
+def test_attention_refuses_gradients(gdn, name):
+    new = lambda: torch.zeros(3, 2, 64, dtype=BF)  # noqa: E731
+    a = dict(paged_args(), k_new=new(), v_new=new(), k_scale=torch.ones(2), v_scale=torch.ones(2))
+    a[name].requires_grad_(True)
+    with pytest.raises(RuntimeError, match="differentiable"):
+        gdn.paged_attention_decode(**a)
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+        gdn.paged_attention_decode(**a)
