@@ -15,6 +15,7 @@ import ctypes
 import os
 
 import torch
+from torch.autograd.function import once_differentiable
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # GDN_LIB selects another in-tree build of the same library (the checked variant
@@ -640,6 +641,7 @@ class _RMSNorm(torch.autograd.Function):
         return y, total
 
     @staticmethod
+    @once_differentiable  # a second derivative is refused, not zero
     def backward(ctx, dy, dtotal):
         s, weight = ctx.saved_tensors
         dim = s.shape[-1]
@@ -655,7 +657,7 @@ def rms_norm(x, weight, residual=None, eps=1e-6, weight_offset=0.0):
     """Root-mean-square norm with the residual's addition: s = x + residual, y = s / sqrt(mean(s^2)
     + eps) * (weight + weight_offset) over the last dimension.  Returns (y, s), s None without a
     residual.  x, residual [..., dim] bf16 or fp32; weight [dim] bf16 or fp32.  Differentiable with
-    respect to x, residual and weight (the backward pass takes s as it was rounded)."""
+    respect to x, residual and weight (the backward pass takes s as it was rounded), once."""
     native = _native or _binding()
     if native.wants_grad(x, weight, residual):
         return _RMSNorm.apply(x, weight, residual, eps, weight_offset)

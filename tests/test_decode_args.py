@@ -120,3 +120,22 @@ def test_attention_refuses_gradients(gdn, name):
         gdn.paged_attention_decode(**a)
     with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
         gdn.paged_attention_decode(**a)
+
+
+def test_a_second_derivative_of_the_norm_is_refused(gdn, monkeypatch):
+    """The gradient kernel has no derivative: a penalty on the norm's gradient must not train on zeros."""
+    def fwd(x, weight, residual, eps, offset):
+        return x * torch.rsqrt(x.square().mean(-1, keepdim=True) + eps) * (weight + offset), None, None
+
+    def bwd(s, weight, dy, dsum, eps, offset):
+        with torch.enable_grad():
+            at = s.detach().requires_grad_(True)
+            return torch.autograd.grad((fwd(at, weight.detach(), None, eps, offset)[0] * dy.detach()).sum(), at)[0], torch.zeros(s.shape[-1])
+
+    monkeypatch.setattr(gdn, "gdn_rmsnorm_fwd", fwd)
+    monkeypatch.setattr(gdn, "gdn_rmsnorm_bwd", bwd)
+    x = torch.randn(3, 8, generator=torch.Generator().manual_seed(0)).requires_grad_(True)
+    y, _ = gdn.rms_norm(x, torch.ones(8))
+    (gx,) = torch.autograd.grad(y.square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        (y.sum() + gx.square().sum()).backward()
