@@ -422,13 +422,18 @@ PyObject* norm_bwd(Args& a) {
     return r;
 }
 
-// True when gradients are on and one of the arguments (tensors or None) requires one.
+// True when gradients are on and one of the arguments (tensors or None) requires one.  A forward-mode tangent
+// (level 0 is the only level there is) would be dropped, whether gradients are on or not: refused.
 PyObject* wants_grad(Args& a) {
-    if (c10::GradMode::is_enabled())
-        while (a.at < a.n) {
-            const at::Tensor* t = a.maybe("argument");
-            if (t && t->requires_grad()) Py_RETURN_TRUE;
-        }
+    const bool on = c10::GradMode::is_enabled();
+    bool wants = false;
+    while (a.at < a.n) {
+        const at::Tensor* t = a.maybe("argument");
+        if (!t) continue;
+        if (t->_fw_grad(0).defined()) throw Bad{PyExc_RuntimeError, "forward-mode differentiation is not implemented here, but an argument carries a tangent"};
+        wants |= on && t->requires_grad();
+    }
+    if (wants) Py_RETURN_TRUE;
     Py_RETURN_FALSE;
 }
 

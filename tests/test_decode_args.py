@@ -139,3 +139,17 @@ def test_a_second_derivative_of_the_norm_is_refused(gdn, monkeypatch):
     (gx,) = torch.autograd.grad(y.square().sum(), x, create_graph=True)
     with pytest.raises(RuntimeError, match="once_differentiable"):
         (y.sum() + gx.square().sum()).backward()
+
+
+@pytest.mark.parametrize("no_grad", [False, True])
+def test_forward_mode_tangents_are_refused(gdn, no_grad):
+    """No call has a forward-mode derivative: a tangent must not be dropped."""
+    step, attn = step_args(), paged_args()
+    x, w = torch.zeros(3, 8), torch.ones(8)
+    with torch.autograd.forward_ad.dual_level(), torch.set_grad_enabled(not no_grad):
+        dual = lambda t: torch.autograd.forward_ad.make_dual(t, torch.ones_like(t))  # noqa: E731
+        for call in (lambda: gdn.rms_norm(dual(x), w), lambda: gdn.rms_norm(x, dual(w)), lambda: gdn.rms_norm(x, w, residual=dual(x)),
+                     lambda: gdn.rms_norm_quant(dual(x), w), lambda: gdn.gated_delta_rule_step(**dict(step, v=dual(step["v"]))),
+                     lambda: gdn.paged_attention_decode(**dict(attn, q=dual(attn["q"])))):
+            with pytest.raises(RuntimeError, match="tangent"):
+                call()
