@@ -216,6 +216,7 @@ PyObject* step(Args& a) {
     need_cuda(q, "o", given);
     On on(q, a);
     const at::Tensor o = given ? *given : empty(v.sizes(), v.scalar_type(), v);
+    p.clear_rest = !given;  // what the allocator hands out is not a result
     check(f_step(&p, q.data_ptr(), k.data_ptr(), v.data_ptr(), ptr(g), ptr(beta), ptr(A_log), ptr(bias), ptr(in), ptr(out), o.data_ptr(), on.stream));
     return THPVariable_Wrap(o);
 }

@@ -164,7 +164,10 @@ gdn_status gdn_recurrent_step(const gdn_step_problem* problem, const void* q, co
     TRY(check_ptr("A_log", A_log, 4, true));
     TRY(check_ptr("dt_bias", dt_bias, 4, true));
     if ((A_log == nullptr) != (dt_bias == nullptr)) return fail(GDN_ERR_INVALID_ARG, "A_log and dt_bias go together");
-    if (p.num_seqs == 0) return done(cudaSuccess);
+    if (p.num_seqs == 0) {
+        const size_t bytes = size_t(p.total_tokens) * p.Hv * p.V * elem(p.dtype);
+        return done(p.clear_rest && bytes ? cudaMemsetAsync(o, 0, bytes, static_cast<cudaStream_t>(stream)) : cudaSuccess);
+    }
     return done(gdn::launch_step(A, static_cast<cudaStream_t>(stream)));
 } catch (...) {
     return no_host_memory();

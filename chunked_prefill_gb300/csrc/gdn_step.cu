@@ -69,6 +69,12 @@ __global__ void __launch_bounds__(ST, 8) k_step(const StepArgs A) {
         t1 = t0 + per;
     }
     Op* o = static_cast<Op*>(A.o) + int64_t(j) * VD + col;
+    if (p.clear_rest) {  // the first sequence's and the last one's CTAs, where there is such a token at all
+        if (s == 0)
+            for (int t = warp; t < t0; t += 4) o[int64_t(t) * p.Hv * VD] = from_f<Op>(0.f);
+        if (s == p.num_seqs - 1)
+            for (int t = t1 + warp; t < p.total_tokens; t += 4) o[int64_t(t) * p.Hv * VD] = from_f<Op>(0.f);
+    }
     const int64_t slot = p.slots ? p.slots[s] : s;
     if (slot < 0 || slot >= p.num_slots) {
         for (int t = t0 + warp; t < t1; t += 4) o[int64_t(t) * p.Hv * VD] = from_f<Op>(0.f);

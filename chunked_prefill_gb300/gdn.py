@@ -55,7 +55,8 @@ class GdnStepProblem(ctypes.Structure):
                 ("cu_seqlens", ctypes.c_void_p), ("slots", ctypes.c_void_p),
                 ("num_slots", ctypes.c_int64), ("q_stride", ctypes.c_int64),
                 ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
-                ("g_stride", ctypes.c_int64), ("beta_stride", ctypes.c_int64)]
+                ("g_stride", ctypes.c_int64), ("beta_stride", ctypes.c_int64),
+                ("clear_rest", ctypes.c_int32)]
 
 
 class GdnPagedProblem(ctypes.Structure):
@@ -547,7 +548,8 @@ def gdn_recurrent_step(q, k, v, g, beta, scale, state_in=None, state_out=None, s
     """Recurrent step through the C ABI (see include/gdn.h).  q, k [B,T,Hqk,K], v [B,T,Hv,V],
     g, beta [B,T,Hv] fp32, each with contiguous rows at any token stride but 0; state_in, state_out
     [num_slots,Hv,K,V] fp32 pools; slots int32 [num_seqs]; cu_seqlens int32 [num_seqs+1] with
-    B = 1, else B sequences of T tokens.  Returns o [B,T,Hv,V]."""
+    B = 1, else B sequences of T tokens.  Returns o [B,T,Hv,V], 0 for tokens that no sequence
+    covers (a given o keeps what it has there)."""
     return (_native or _binding()).step(q, k, v, g, beta, scale, state_in, state_out, slots,
                                         cu_seqlens, A_log, dt_bias, o, stream)
 
@@ -562,8 +564,9 @@ def gated_delta_rule_step(q, k, v, g, beta, scale=None, state=None, state_out=No
     state [num_slots,Hv,K,V] fp32 (None: zero), e.g. chunk_gated_delta_rule's final state, is
     updated in place unless state_out names another pool of the same shape; slots int32 [N] says
     which slot each sequence has (None: its own index; -1: a padding row, whose o is 0).
-    cu_seqlens int32 [N+1] (device, B = 1) packs sequences of different token counts.  For
-    inference: nothing is differentiated here."""
+    cu_seqlens int32 [N+1] (device, B = 1) packs sequences of different token counts; the o of
+    tokens that it does not cover is 0 (a given o keeps what it has there).  For inference:
+    nothing is differentiated here."""
     if stream is not None:  # what is allocated here belongs to that stream, too
         with torch.cuda.stream(stream):
             return gated_delta_rule_step(q, k, v, g, beta, scale, state, state_out, slots, cu_seqlens,

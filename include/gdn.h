@@ -240,8 +240,9 @@ gdn_status gdn_prologue_bwd(const gdn_problem* p, const void* q_raw, const void*
  * pre-activations a, b of gdn_prologue_fwd, whose formulas are applied on the way in.
  *
  * cu_seqlens is read on the device alone, so a captured graph serves every split of
- * total_tokens; offsets outside [0, total_tokens] are clamped to it.  Tokens that no sequence
- * covers get no output.  K = V = 128.
+ * total_tokens; offsets outside [0, total_tokens] are clamped to it.  Tokens before the first
+ * offset and from the last one on belong to no sequence: their o is left as it is, or set to 0
+ * with clear_rest.  K = V = 128.
  * ------------------------------------------------------------------------------------ */
 typedef struct gdn_step_problem {
     int32_t num_seqs;
@@ -255,6 +256,7 @@ typedef struct gdn_step_problem {
     /* elements from one token's row to the next, 0 for contiguous rows; a row's heads and
      * features are contiguous.  Those of q, k, v are multiples of 16 bytes. */
     int64_t q_stride, k_stride, v_stride, g_stride, beta_stride;
+    int32_t clear_rest;            /* not 0: o = 0 for tokens that no sequence covers */
 } gdn_step_problem;
 
 gdn_status gdn_recurrent_step(const gdn_step_problem* p, const void* q, const void* k,

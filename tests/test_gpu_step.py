@@ -248,3 +248,30 @@ def test_refusals():
         gdn.gated_delta_rule_step(*a, state=x["state"], scale=float("nan"))
     with pytest.raises(RuntimeError, match="differentiable"):
         gdn.gated_delta_rule_step(a[0].requires_grad_(True), *a[1:], state=x["state"])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("cu,slots", [([3, 4, 4, 9], [1, 0, 2]), ([0, 9], [0]), ([5, 6], [-1]), ([0, 0, 0], [0, 1]), ([0], [])])
+def test_tokens_of_no_sequence_get_zeros(dtype, cu, slots):
+    """Tokens before the first offset and past the last one: 0 in an o that the call makes (not what lay in
+    that memory before), untouched in a given one."""
+    from chunked_prefill_gb300 import gdn
+    T = 21
+    d = inputs(T, 2, 6, 3, 33, dtype)
+    x = cuda(d)
+    offsets = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    sl = torch.tensor(slots, dtype=torch.int32, device="cuda")
+    covered = torch.zeros(T, dtype=torch.bool, device="cuda")
+    covered[cu[0]:cu[-1]] = True
+    state, given = x["state"], torch.full_like(x["v"], 7.0)
+    poison = torch.full_like(x["v"], float("nan"))
+    del poison  # the next allocation of this size gets its memory
+    o, _ = gdn.gated_delta_rule_step(x["q"], x["k"], x["v"], x["g"], x["beta"], state=state.clone(), slots=sl, cu_seqlens=offsets)
+    assert (o[0, ~covered] == 0).all() and torch.isfinite(o).all()
+    gdn.gated_delta_rule_step(x["q"], x["k"], x["v"], x["g"], x["beta"], state=state.clone(), slots=sl, cu_seqlens=offsets, o=given)
+    assert (given[0, ~covered] == 7.0).all() and torch.equal(given[0, covered], o[0, covered])
+    live = [b - a for a, b in zip(cu, cu[1:])]
+    shifted = {k: v[cu[0]:] if k in ("q", "k", "v", "g", "beta") else v for k, v in d.items()}
+    if sum(live):
+        ro, _ = oracle(shifted, slots, live, 128 ** -0.5)
+        assert rel_err(np64(o)[0, cu[0]:cu[-1]], ro[:sum(live)]) <= OUT_TOL[dtype]
