@@ -10,6 +10,7 @@
 #include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/forward_grad.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <optional>
@@ -426,12 +427,13 @@ PyObject* norm_bwd(Args& a) {
 // True when gradients are on and one of the arguments (tensors or None) requires one.  A forward-mode tangent
 // (level 0 is the only level there is) would be dropped, whether gradients are on or not: refused.
 PyObject* wants_grad(Args& a) {
-    const bool on = c10::GradMode::is_enabled();
+    const bool on = c10::GradMode::is_enabled(), forward = torch::autograd::ForwardADLevel::try_get_by_idx(0) != nullptr;
+    if (!on && !forward) Py_RETURN_FALSE;
     bool wants = false;
     while (a.at < a.n) {
         const at::Tensor* t = a.maybe("argument");
         if (!t) continue;
-        if (t->_fw_grad(0).defined()) throw Bad{PyExc_RuntimeError, "forward-mode differentiation is not implemented here, but an argument carries a tangent"};
+        if (forward && t->_fw_grad(0).defined()) throw Bad{PyExc_RuntimeError, "forward-mode differentiation is not implemented here, but an argument carries a tangent"};
         wants |= on && t->requires_grad();
     }
     if (wants) Py_RETURN_TRUE;
