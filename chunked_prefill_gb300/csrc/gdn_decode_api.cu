@@ -140,6 +140,14 @@ gdn_status check_norm(gdn_norm_problem& p, bool backward) {
     return GDN_OK;
 }
 
+// An output may lie in an input's place where its rows do: contiguous, and of the same type.
+gdn_status check_in_place(const gdn_norm_problem& p, const char* out, const void* o, int out_dtype, const char* in, const void* i, int64_t stride) {
+    if (!o || o != i || p.rows == 0) return GDN_OK;
+    if (out_dtype != p.dtype) return fail(GDN_ERR_INVALID_ARG, "%s may be %s only in the same type", out, in);
+    if (p.rows > 1 && stride != p.dim) return fail(GDN_ERR_INVALID_ARG, "%s may be %s only where its rows are contiguous", out, in);
+    return GDN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -251,6 +259,10 @@ gdn_status gdn_rmsnorm_fwd(const gdn_norm_problem* problem, const void* x, const
     TRY(check_ptr("y", y, elem(p.out_dtype), none));
     TRY(check_ptr("y_scale", y_scale, 4, none || p.out_dtype != GDN_E4M3));
     TRY(check_ptr("sum", sum, e, true));
+    TRY(check_in_place(p, "sum", sum, p.dtype, "x", x, p.x_stride));
+    TRY(check_in_place(p, "sum", sum, p.dtype, "residual", residual, p.residual_stride));
+    TRY(check_in_place(p, "y", y, p.out_dtype, "x", x, p.x_stride));
+    TRY(check_in_place(p, "y", y, p.out_dtype, "residual", residual, p.residual_stride));
     if (none) return done(cudaSuccess);
     A.inv_dim = 1.f / float(p.dim);
     A.x = x;
@@ -291,6 +303,9 @@ gdn_status gdn_rmsnorm_bwd(const gdn_norm_problem* problem, const void* s, const
     TRY(check_ptr("dsum", dsum, e, true));
     TRY(check_ptr("dx", dx, e, none));
     TRY(check_ptr("dweight", dweight, 4));
+    TRY(check_in_place(p, "dx", dx, p.dtype, "s", s, p.x_stride));
+    TRY(check_in_place(p, "dx", dx, p.dtype, "dy", dy, p.dy_stride));
+    TRY(check_in_place(p, "dx", dx, p.dtype, "dsum", dsum, p.dsum_stride));
     const size_t need = size_t(gdn::norm_bwd_parts(p)) * p.dim * sizeof(float);
     if (!workspace || workspace_bytes < need)
         return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? workspace_bytes : size_t(0));

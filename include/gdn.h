@@ -327,14 +327,15 @@ gdn_status gdn_paged_attn_decode(const gdn_paged_problem* p, const void* q, void
  * row (y_scale [rows, dim / group]):
  *     scale = max(max |y| / 448, 2^-126)
  * A row with infinities or NaN gets NaN in that row alone.
- * sum may be x or residual (in place), y may be x; NULL sum: not returned.
+ * sum may be x or residual (in place), y of x's type may be x, where their rows are contiguous
+ * like the output's; NULL sum: not returned.
  *
  * gdn_rmsnorm_bwd: the gradients of <y, dy> + <sum, dsum> (dsum NULL: 0) with respect to s
  * (x and residual alike) and to weight, for the s given:
  *     dx = r (w dy - n mean(w dy n)) + dsum with n = r s;   dweight = sum over rows of dy n
  * dweight is fp32, summed in a fixed order.  For an 8-bit y, dy is the gradient with respect to
  * y y_scale: the rounding passes it through.
- * dx may be dy or dsum (in place).
+ * dx may be dy or dsum (in place) where their rows are contiguous.
  *
  * Pointers and strides need only the alignment of their elements here; rows whose pointers and
  * strides are all multiples of 16 bytes run faster.

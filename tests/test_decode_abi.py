@@ -115,3 +115,22 @@ def test_norm_direction_refusals(L):
     assert L.lib().gdn_rmsnorm_bwd_workspace_size(ctypes.byref(p), ctypes.byref(n)) == 0 and n.value >= 64 * 4
     assert norm(L, back=True, ws=(FAKE, n.value - 1)) == 3
     assert norm(L, rows=0, ptrs=dict(x=None, y=None)) == 0
+
+
+OTHER, THIRD = 0x40000, 0x80000
+
+
+@pytest.mark.parametrize("rows,kw,ptrs", [
+    (4, dict(x_stride=72), dict(y=OTHER, sum=FAKE)), (4, dict(x_stride=72), dict(y=FAKE)), (4, dict(residual_stride=72), dict(r=THIRD, y=OTHER, sum=THIRD)),
+    (4, dict(out_dtype=2), dict(scale=OTHER, y=FAKE)), (1, dict(out_dtype=2), dict(scale=OTHER, y=FAKE)), (4, dict(residual_stride=72), dict(r=THIRD, y=THIRD)),
+])
+def test_norm_in_place_refusals(L, rows, kw, ptrs):
+    """Outputs have contiguous rows of their own type: over an input whose rows lie elsewhere they would
+    overwrite rows that are still to be read."""
+    assert norm(L, rows=rows, ptrs=ptrs, **kw) == 1
+
+
+@pytest.mark.parametrize("kw,ptrs", [(dict(dy_stride=72), dict(dy=OTHER, dx=OTHER)), (dict(dsum_stride=72), dict(dsum=OTHER, dx=OTHER)),
+                                     (dict(x_stride=72), dict(dy=OTHER))])
+def test_norm_gradient_in_place_refusals(L, kw, ptrs):
+    assert norm(L, back=True, ptrs=ptrs, **kw) == 1
