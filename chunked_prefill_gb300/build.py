@@ -5,6 +5,7 @@ from __future__ import annotations
 
 import glob
 import os
+import platform
 import shutil
 import subprocess
 import sys
@@ -21,6 +22,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB_CHECK = os.path.join(HERE, "libgdn_check.so")
 BUILD_CHECK = os.path.join(ROOT, "_build_check")
 BINDING = os.path.join(HERE, "_binding.so")
+BINDING_FOR = os.path.join(BUILD, "_binding.txt")  # what the built one is for
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -48,9 +50,20 @@ def _stale(lib) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _binding_made_for() -> str:
+    """What _binding.so is compiled against: it can be loaded by no other torch or Python."""
+    import torch
+    return f"torch {torch.__version__} ({os.path.dirname(torch.__file__)}), {sys.implementation.cache_tag} {platform.machine()}\n"
+
+
 def _binding_stale() -> bool:
     deps = [BINDING_SRC, os.path.join(ROOT, "include", "gdn.h")]
-    return not os.path.exists(BINDING) or any(os.path.getmtime(d) > os.path.getmtime(BINDING) for d in deps)
+    if not os.path.exists(BINDING) or any(os.path.getmtime(d) > os.path.getmtime(BINDING) for d in deps):
+        return True
+    if not os.path.exists(BINDING_FOR):
+        return True
+    with open(BINDING_FOR) as f:
+        return f.read() != _binding_made_for()
 
 
 def build_binding(verbose: bool = False) -> str:
@@ -69,6 +82,9 @@ def build_binding(verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed for {BINDING_SRC}:\n{r.stderr}")
     os.replace(tmp, BINDING)
+    os.makedirs(BUILD, exist_ok=True)
+    with open(BINDING_FOR, "w") as f:
+        f.write(_binding_made_for())
     return BINDING
 
 

@@ -153,3 +153,14 @@ def test_forward_mode_tangents_are_refused(gdn, no_grad):
                      lambda: gdn.paged_attention_decode(**dict(attn, q=dual(attn["q"])))):
             with pytest.raises(RuntimeError, match="tangent"):
                 call()
+
+
+def test_the_binding_is_built_again_for_another_torch_or_python(gdn, monkeypatch):
+    assert not gbuild._binding_stale()
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", torch.__version__ + ".post1")
+        assert gbuild._binding_stale()
+    with monkeypatch.context() as m:
+        m.setattr(gbuild.sys.implementation, "cache_tag", "cpython-300")
+        assert gbuild._binding_stale()
+    assert not gbuild._binding_stale()
