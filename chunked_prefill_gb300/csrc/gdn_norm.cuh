@@ -670,20 +670,25 @@ cudaError_t bwd_out(const NormArgs& A, const Layout& L, int& parts, cudaStream_t
     }
 }
 
-// Calls f<VEC, NV, LPR, SHIFT> for the layout.
+// Calls f<VEC, NV, LPR, SHIFT> for the layout.  (The forward takes SHIFT for rows of more than 512 values alone,
+// which are more than 64 pieces: a CTA each.)
+#define NORM_CTA(F, T, FULL, SHIFT, ...)                                           \
+    do {                                                                            \
+        if (L.nv == 1) return F<T, FULL, 1, 0, SHIFT>(__VA_ARGS__);                 \
+        if (L.nv == 2) return F<T, FULL, 2, 0, SHIFT>(__VA_ARGS__);                 \
+        return F<T, FULL, 4, 0, SHIFT>(__VA_ARGS__);                                \
+    } while (0)
 #define NORM_WIDE(F, T, FULL, SHIFT, ...)                                          \
     do {                                                                            \
         if (L.lpr == 8) return F<T, FULL, 1, 8, SHIFT>(__VA_ARGS__);                \
         if (L.lpr == 16) return F<T, FULL, 1, 16, SHIFT>(__VA_ARGS__);              \
         if (L.lpr == 32 && L.nv == 1) return F<T, FULL, 1, 32, SHIFT>(__VA_ARGS__); \
         if (L.lpr == 32) return F<T, FULL, 2, 32, SHIFT>(__VA_ARGS__);              \
-        if (L.nv == 1) return F<T, FULL, 1, 0, SHIFT>(__VA_ARGS__);                 \
-        if (L.nv == 2) return F<T, FULL, 2, 0, SHIFT>(__VA_ARGS__);                 \
-        return F<T, FULL, 4, 0, SHIFT>(__VA_ARGS__);                                \
+        NORM_CTA(F, T, FULL, SHIFT, __VA_ARGS__);                                   \
     } while (0)
-#define NORM_LAYOUTS(F, T, FULL, ...)                                              \
+#define NORM_LAYOUTS(F, T, FULL, SHIFTED, ...)                                     \
     do {                                                                            \
-        if (L.shift) NORM_WIDE(F, T, FULL, true, __VA_ARGS__);                      \
+        if (L.shift) SHIFTED(F, T, FULL, true, __VA_ARGS__);                        \
         if (L.vec > 1) NORM_WIDE(F, T, FULL, false, __VA_ARGS__);                   \
         if (L.lpr == 8) return F<T, 1, 1, 8, false>(__VA_ARGS__);                   \
         if (L.lpr == 16) return F<T, 1, 1, 16, false>(__VA_ARGS__);                 \
@@ -711,7 +716,7 @@ cudaError_t fwd_type(const NormArgs& A, cudaStream_t st) {
         k_norm_fwd_loop<T><<<unsigned(p.rows), LOOP_T, 0, st>>>(A);
         return cudaGetLastError();
     }
-    NORM_LAYOUTS(fwd_out, T, (sizeof(T) == 2 ? 8 : 4), A, L, st);
+    NORM_LAYOUTS(fwd_out, T, (sizeof(T) == 2 ? 8 : 4), NORM_CTA, A, L, st);
 }
 
 int parts_of(const gdn_norm_problem& p, const Layout& L) {
@@ -734,7 +739,7 @@ cudaError_t bwd_type(const NormArgs& A, int& parts, cudaStream_t st) {
         k_norm_bwd_loop<T><<<parts, LOOP_T, 0, st>>>(A);
         return cudaGetLastError();
     }
-    NORM_LAYOUTS(bwd_out, T, (sizeof(T) == 2 ? 8 : 4), A, L, parts, st);
+    NORM_LAYOUTS(bwd_out, T, (sizeof(T) == 2 ? 8 : 4), NORM_WIDE, A, L, parts, st);
 }
 
 }  // namespace

@@ -198,7 +198,7 @@ template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.as
 // warps takes RPB rows: a warp each (8), or all 8 warps one row's parts (1: few rows, many parts).
 constexpr int JW = 8;
 template <typename Act, int D, int RPB>
-__global__ void __launch_bounds__(32 * JW) k_paged_join(const PagedArgs A, int tok, int rows, int ctas, int warps) {
+__global__ void __launch_bounds__(32 * JW) k_paged_join(const PagedArgs A, int rows, int ctas, int warps) {
     constexpr int E = D / 32;
     __shared__ float acc_s[RPB == 1 ? JW : 1][D], ml_s[RPB == 1 ? JW : 1][2];
     tc::pdl_wait();
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(32 * JW) k_paged_join(const PagedArgs A, int t
     if (c0 == c1) return;  // that CTA wrote it out
     // parts c0 .. c1; this warp's: c0 + first, first + step, ...
     const int parts = c1 - c0 + 1, first = RPB == 1 ? warp : 0, step = RPB == 1 ? JW : 1;
-    auto place = [&](int i) { return place_of((c0 + i) * A.groups + group, i > 0 || at0 < c0 * share, rows) + in; };
+    auto place = [&](int i) { return place_of((c0 + i) * A.groups + group, i > 0, rows) + in; };  // the pair begins in c0's part
     float M = -INFINITY, S = 0.f, acc[E] = {};
     // batches of parts, everything of a batch requested at once
     constexpr int NB = (D == 256 ? 4 : 8) * (RPB == 1 ? 2 : 1);
@@ -308,8 +308,8 @@ cudaError_t launch_join(const PagedArgs& A, const PagedPlan& plan, const PagedSh
     const bool many = plan.ctas > int64_t(4) * A.p.num_seqs * plan.groups * plan.heads;
     timing_begin("paged_attn_join", st);
     const cudaError_t e =
-        many ? launch_pdl(k_paged_join<Act, D, 1>, dim3(unsigned(rows)), dim3(32 * JW), 0, st, A, s.tok, s.rows, plan.ctas, s.warps)
-             : launch_pdl(k_paged_join<Act, D, JW>, dim3(unsigned((rows + JW - 1) / JW)), dim3(32 * JW), 0, st, A, s.tok, s.rows, plan.ctas, s.warps);
+        many ? launch_pdl(k_paged_join<Act, D, 1>, dim3(unsigned(rows)), dim3(32 * JW), 0, st, A, s.rows, plan.ctas, s.warps)
+             : launch_pdl(k_paged_join<Act, D, JW>, dim3(unsigned((rows + JW - 1) / JW)), dim3(32 * JW), 0, st, A, s.rows, plan.ctas, s.warps);
     timing_end(st);
     return e;
 }
