@@ -254,3 +254,30 @@ def test_rows_past_32_bit_offsets():
     assert torch.equal(y8[-tail:].view(torch.uint8), z8.view(torch.uint8)) and torch.equal(scale[-tail:], zscale)
     dx, _ = gdn.gdn_rmsnorm_bwd(x, w, y)
     assert torch.equal(dx[-tail:], gdn.gdn_rmsnorm_bwd(x[-tail:].contiguous(), w, y[-tail:].contiguous())[0])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dim", [64, 512, 1001, 2048, 20000])
+def test_rows_of_every_size_match_the_oracle(dtype, dim):
+    """Rows of 1e15, of 1 and of 1e-18 without eps, and down to subnormal ones beside it, where the 8-bit
+    scale ends at 2^-126: values, scales and gradients against the oracle, none of them lost."""
+    from chunked_prefill_gb300 import gdn
+    gen = torch.Generator().manual_seed(dim)
+    w = torch.ones(dim, dtype=dtype)
+    sizes = torch.tensor([1e15, 1.0, 1e-18])[:, None]
+    x, dy = (torch.randn(3, dim, generator=gen) * sizes).to(dtype), torch.randn(3, dim, generator=gen).to(dtype)
+    y, _ = gdn.rms_norm(x.cuda(), w.cuda(), eps=0.0)
+    ry = decode.norm(np64(x), np64(w), eps=0.0)[0]
+    close(y, ry, np.abs(ry), dtype, eps_of(dim))
+    assert (np.abs(np64(y)).max(1) > 1).all()
+    dx, _ = gdn.gdn_rmsnorm_bwd(x.cuda(), w.cuda(), dy.cuda(), eps=0.0)
+    rx, _, sx, _ = decode.norm_bwd(np64(x), np64(w), np64(dy), eps=0.0)
+    close(dx, rx, sx, dtype, eps_of(dim))
+    tiny = (torch.randn(4, dim, generator=gen) * torch.tensor([1e15, 1e-18, 1e-30, 1e-39])[:, None]).to(dtype)
+    for rows, eps in ((x, 0.0), (tiny, 1e-6)):
+        y8, scale, _ = gdn.rms_norm_quant(rows.cuda(), w.cuda(), eps=eps)
+        ry = decode.norm(np64(rows), np64(w), eps=eps)[0]
+        sc = decode.norm_scales(ry)
+        assert (np.abs(np64(scale) - sc) <= 4 * eps_of(dim) * sc).all()
+        assert (np.abs(np64(y8.float()) * sc - ry) <= 2.0 ** -4 * np.abs(ry) * (1 + 1e-3) + 2.0 ** -10 * sc * (1 + 1e-3)).all()
+        assert (np.abs(np64(y8.float())).max(1) >= 32).all()
