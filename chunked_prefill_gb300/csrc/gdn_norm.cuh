@@ -148,9 +148,7 @@ __device__ __forceinline__ void weight_piece(const gdn_norm_problem& p, const vo
     }
 }
 
-// y * inv in 8 bits, round to nearest even (|y inv| <= 448 up to rounding; NaN stays NaN).  inv = rcp(scale) for a
-// whole piece of a row: y inv is within 2^-22 of the quotient, and a division per value would be many more
-// instructions in kernels that have the issue slots 75 % busy.
+// y * inv in 8 bits, round to nearest even (|y inv| <= 448 up to rounding; NaN stays NaN).
 template <int VEC>
 __device__ __forceinline__ void store8(uint8_t* p, const float (&y)[VEC], float inv) {
     if constexpr (VEC == 1) {
@@ -170,7 +168,7 @@ __device__ __forceinline__ void store8(uint8_t* p, const float (&y)[VEC], float 
     }
 }
 
-__device__ __forceinline__ float scale_of(float mag) { return max_nan(mag / F8_MAX, F8_TINY); }
+__device__ __forceinline__ float scale_of(float mag) { return max_nan(mag * (1.f / F8_MAX), F8_TINY); }
 
 // OUT8: 0 dtype out; 1 one scale per row; 2 groups of 2^n <= 32 lanes' vectors; 3 other groups
 // (magnitudes by shared-memory maxima, whose order does not matter).

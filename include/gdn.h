@@ -322,11 +322,10 @@ gdn_status gdn_paged_attn_decode(const gdn_paged_problem* p, const void* q, void
  * row, with w = weight + weight_offset:
  *     s = x + residual (x itself without a residual),   r = 1 / sqrt(mean(s^2) + eps),
  *     y = r s w;   sum = s, rounded to dtype (y comes from the unrounded s)
- * With out_dtype GDN_E4M3, y / scale is rounded to nearest even in 8 bits, with one fp32 scale per
- * row (group = 0) or per `group` consecutive values of a row (y_scale [rows, dim / group]):
- *     scale = max(max |y| / 448, 2^-126), the quotient rounded to fp32
- * (the values as y times 1 / scale, within 2^-22 of the quotient: one that near to the middle
- * between two 8-bit values may get the other).
+ * With out_dtype GDN_E4M3, y / scale (the product with 1 / scale in fp32) is rounded to nearest
+ * even in 8 bits, with one fp32 scale per row (group = 0) or per `group` consecutive values of a
+ * row (y_scale [rows, dim / group]):
+ *     scale = max(max |y| / 448, 2^-126)
  * A row with infinities or NaN gets NaN in that row alone.
  * sum may be x or residual (in place), y of x's type may be x, where their rows are contiguous
  * like the output's; NULL sum: not returned.
