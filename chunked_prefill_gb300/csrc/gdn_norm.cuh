@@ -148,7 +148,9 @@ __device__ __forceinline__ void weight_piece(const gdn_norm_problem& p, const vo
     }
 }
 
-// y * inv in 8 bits, round to nearest even (|y inv| <= 448 up to rounding; NaN stays NaN).
+// y * inv in 8 bits, round to nearest even (|y inv| <= 448 up to rounding; NaN stays NaN).  inv = rcp(scale), once
+// for a piece of a row: within 2^-22 of the quotient; a division per value would be many more instructions where
+// the issue slots are 75 % busy.
 template <int VEC>
 __device__ __forceinline__ void store8(uint8_t* p, const float (&y)[VEC], float inv) {
     if constexpr (VEC == 1) {
@@ -168,6 +170,9 @@ __device__ __forceinline__ void store8(uint8_t* p, const float (&y)[VEC], float 
     }
 }
 
+// mag / 448 as a product (a division takes the same time and lies within 2^-24 instead of 2^-23 of it, but torch's
+// own division of a GPU tensor by 448 is this product: 40 M values in groups of 128 agree with torch's to 2.4e-4 of
+// their norm, with a division to 3.9e-4, and both are 0.026 off the exact values, the 8 bits' own rounding).
 __device__ __forceinline__ float scale_of(float mag) { return max_nan(mag * (1.f / F8_MAX), F8_TINY); }
 
 // OUT8: 0 dtype out; 1 one scale per row; 2 groups of 2^n <= 32 lanes' vectors; 3 other groups

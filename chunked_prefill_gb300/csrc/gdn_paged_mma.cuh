@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(Tile<C, D, SOLO>::T, Tile<C, D, SOLO>::CTAS) k
         // 32-feature step s: features 4t .. 4t + 3 and 16 + 4t .., each value the sum of two 8-bit ones of
         // the row scaled to [128, 256): exact for bf16's 8 significant bits down to 2^-9 of the row's
         // largest value (4 bits each, the second with a sign of its own), off by 2^-18 of it below.  A row
-        // below 2^-119 is scaled by 2^126, the largest finite power that has an inverse: bf16's values, all
+        // below 2^-119 is scaled by 2^126 (beyond 2^127 the factor would be infinite): bf16's values, all
         // multiples of 2^-133, are then multiples of 2^-7, and exact.
         alignas(16) uint32_t qf[QF][2 * R2];
         float zs[R2];

@@ -608,8 +608,10 @@ def paged_attention_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None
     e4m3 (with fp32 scales [Hkv]) under bf16 queries, fp32 under fp32 ones; page_table int32
     [N,max_pages]; seq_lens int32 [N], the new token counted.  k_new, v_new [N,Hkv,D]: the new
     token's key and value, which the call then writes to position seq_lens - 1 of the caches
-    before it attends to them.  window > 0 attends to the last `window` tokens.  For inference:
-    nothing is differentiated here."""
+    before it attends to them.  window > 0 attends to the last `window` tokens.  The weights are
+    rounded to bf16 (fp16 under e4m3 caches) for their product with v under bf16 queries, their
+    sum is not; a table no wider than the longest sequence may become is best, for the work is
+    divided by its width.  For inference: nothing is differentiated here."""
     native = _native or _binding()
     if native.wants_grad(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale):
         raise RuntimeError("paged_attention_decode is not differentiable, but an argument requires "
@@ -671,8 +673,9 @@ def rms_norm(x, weight, residual=None, eps=1e-6, weight_offset=0.0):
 def rms_norm_quant(x, weight, residual=None, eps=1e-6, weight_offset=0.0, group=0):
     """rms_norm with y in 8 bits (float8_e4m3fn): returns (y, scale, s) with the normed row
     approximately y * scale; scale fp32 [..., 1], or [..., dim / group] with one scale to `group`
-    consecutive values.  Nothing is differentiated here: to train through it, pass the gradient
-    with respect to y * scale as gdn_rmsnorm_bwd's dy."""
+    consecutive values: max |y| / 448, not below 2^-126, by a product with 1 / 448 as torch
+    divides a GPU tensor by a number, and y by one with 1 / scale.  Nothing is differentiated here:
+    to train through it, pass the gradient with respect to y * scale as gdn_rmsnorm_bwd's dy."""
     native = _native or _binding()
     if native.wants_grad(x, weight, residual):
         raise RuntimeError("rms_norm_quant is not differentiable, but an argument requires a gradient: "

@@ -226,7 +226,9 @@ gdn_status gdn_prologue_bwd(const gdn_problem* p, const void* q_raw, const void*
  * per sequence, or the few drafted ones that a verification pass runs) from the states that a
  * prefill (gdn_chunk_fwd's ht) or an earlier step left.  Per sequence, v-head and token
  *     u = beta (v - e^g h^T k),   h <- e^g h + k u^T,   o = scale h^T q
- * which is the recurrence at the top of this file for h = S^T.  Arithmetic and states are fp32.
+ * which is the recurrence at the top of this file for h = S^T.  Arithmetic and states are fp32;
+ * between a sequence's tokens the decay may be kept as a factor in [2^-20, 2^20] beside the state,
+ * with u divided by it (to 2^-22 of u), multiplied out with the last token.
  *
  * The states live in pools [num_slots, Hv, K, V] fp32: sequence s reads slot slots[s] of
  * state_in (NULL: zero states) and writes the same slot of state_out (NULL: not returned).
@@ -279,6 +281,12 @@ gdn_status gdn_recurrent_step(const gdn_step_problem* p, const void* q, const vo
  * share the page of that position.
  * 8-bit caches hold k / k_scale[j] and v / v_scale[j]; NULL scales are 1.
  *
+ * Scores, softmax statistics and sums are fp32.  With bf16 queries the weights e^{z - max} are
+ * rounded to bf16 (8-bit caches: to fp16, as 2^14 e^{z - max}) for their product with v; the sum
+ * that o is divided by, and lse, take them unrounded.  Under 8-bit caches a query value is the sum
+ * of two 8-bit ones: exact down to 2^-9 of its row's largest, within 2^-18 of that one below.
+ * Under fp32 caches nothing is rounded below fp32.
+ *
  * A sequence of length 0 gets o = 0 and lse = -inf.  Whatever lies in slots outside
  * [first, len) is not used, NaN or not.  Page numbers outside [0, num_pages) are not read: the tokens of
  * such a page count as masked (and a new token there is not written); a length past
@@ -322,10 +330,12 @@ gdn_status gdn_paged_attn_decode(const gdn_paged_problem* p, const void* q, void
  * row, with w = weight + weight_offset:
  *     s = x + residual (x itself without a residual),   r = 1 / sqrt(mean(s^2) + eps),
  *     y = r s w;   sum = s, rounded to dtype (y comes from the unrounded s)
- * With out_dtype GDN_E4M3, y / scale (the product with 1 / scale in fp32) is rounded to nearest
- * even in 8 bits, with one fp32 scale per row (group = 0) or per `group` consecutive values of a
- * row (y_scale [rows, dim / group]):
+ * With out_dtype GDN_E4M3, y / scale is rounded to nearest even in 8 bits, with one fp32 scale per
+ * row (group = 0) or per `group` consecutive values of a row (y_scale [rows, dim / group]):
  *     scale = max(max |y| / 448, 2^-126)
+ * Both quotients are products with reciprocals: the scale is within 2^-23 of max |y| / 448, and
+ * y / scale within 2^-22 of itself before it is rounded, so that a value that near to the middle
+ * between two 8-bit ones may get the other.
  * A row with infinities or NaN gets NaN in that row alone.
  * sum may be x or residual (in place), y of x's type may be x, where their rows are contiguous
  * like the output's; NULL sum: not returned.
