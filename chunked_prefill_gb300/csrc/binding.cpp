@@ -1,4 +1,4 @@
-// Native argument marshalling of the decoding operators for Python: checks tensors, fills the C
+// Native argument marshalling of the decoding operators, of attention over prompts and of the paged cache's operators for Python: checks tensors, fills the C
 // ABI's problem structures and calls libgdn.so.  A decoding step is made of many calls that take a
 // few microseconds on the GPU, and the same checks written in Python cost 20 to 30 us a call.
 // Nothing is computed here.  The library's functions are handed over by address (bind), so that this
@@ -13,8 +13,12 @@
 #include <torch/csrc/autograd/forward_grad.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
+#include <initializer_list>
 #include <optional>
 #include <string>
+#include <type_traits>
+#include <utility>
 
 #include "../../include/gdn.h"
 
@@ -37,6 +41,14 @@ decltype(&gdn_paged_attn_decode) f_paged;
 decltype(&gdn_rmsnorm_fwd) f_norm_fwd;
 decltype(&gdn_rmsnorm_bwd_workspace_size) f_norm_bwd_size;
 decltype(&gdn_rmsnorm_bwd) f_norm_bwd;
+decltype(&gdn_prompt_attn_fwd) f_prompt_fwd;
+decltype(&gdn_prompt_attn_bwd_workspace_size) f_prompt_bwd_size;
+decltype(&gdn_prompt_attn_bwd) f_prompt_bwd;
+decltype(&gdn_paged_attn_tree_workspace_size) f_tree_size;
+decltype(&gdn_paged_attn_tree) f_tree;
+decltype(&gdn_paged_cache_write) f_write;
+decltype(&gdn_page_table_extend) f_extend;
+decltype(&gdn_page_table_trim) f_trim;
 PyObject* on_error;  // called with a status that is not GDN_OK; raises
 
 void check(gdn_status st) {
@@ -424,6 +436,263 @@ PyObject* norm_bwd(Args& a) {
     return r;
 }
 
+// A tuple of new references.
+PyObject* tuple(std::initializer_list<at::Tensor> ts) {
+    PyObject* r = PyTuple_New(Py_ssize_t(ts.size()));
+    if (!r) throw Bad{nullptr, ""};
+    Py_ssize_t i = 0;
+    for (const at::Tensor& t : ts) PyTuple_SET_ITEM(r, i++, THPVariable_Wrap(t));
+    return r;
+}
+// lse: a tensor, None, or True for a new one
+const at::Tensor* lse_of(Args& a, bool& make) {
+    make = a.at < a.n && a.a[a.at] == Py_True;
+    if (make) {
+        ++a.at;
+        return nullptr;
+    }
+    return a.maybe("lse");
+}
+
+gdn_prompt_problem prompt_problem(const at::Tensor& q, const at::Tensor& k, const at::Tensor& v, double scale, int64_t window, const at::Tensor* cu, const at::Tensor* cu_k) {
+    need(q.dim() == 4 && k.dim() == 4 && v.sizes() == k.sizes() && k.size(0) == q.size(0) && k.size(3) == q.size(3) && q.size(2) > 0 && k.size(2) > 0,
+         "q must be [B,T,Hq,D], k and v [B,Tk,Hkv,D]");
+    need(k.scalar_type() == q.scalar_type() && v.scalar_type() == q.scalar_type(), "q, k and v must match in dtype");
+    const int64_t B = q.size(0);
+    gdn_prompt_problem p{};
+    int64_t n = B;
+    if (cu) {
+        need(B == 1, "cu_seqlens needs B == 1");
+        need(cu->scalar_type() == at::kInt && cu->dim() == 1 && cu->numel() >= 1 && cu->is_contiguous(), "cu_seqlens must be a contiguous int32 [num_seqs+1]");
+        n = cu->numel() - 1;
+        need(cu_k || k.size(1) == q.size(1), "without cu_seqlens_k there must be as many keys as queries");
+    }
+    if (cu_k) {
+        need(cu, "cu_seqlens_k needs cu_seqlens");
+        need_vector("cu_seqlens_k", cu_k, at::kInt, n + 1, "int32 [num_seqs+1]");
+    }
+    need(window >= 0 && window < (int64_t(1) << 31), "window must be >= 0, and below 2^31");
+    p.num_seqs = small(n, "sequences");
+    p.total_q = small(B * q.size(1), "tokens");
+    p.total_k = small(B * k.size(1), "tokens");
+    p.Hq = small(q.size(2), "heads");
+    p.Hkv = small(k.size(2), "heads");
+    p.D = small(q.size(3), "features");
+    p.dtype = code(q, "q, k and v");
+    p.scale = float(scale);
+    p.window = int32_t(window);
+    p.cu_seqlens = ptr<int32_t>(cu);
+    p.cu_seqlens_k = ptr<int32_t>(cu_k);
+    p.q_stride = token_stride("q", q, int64_t(p.Hq) * p.D);
+    p.k_stride = token_stride("k", k, int64_t(p.Hkv) * p.D);
+    p.v_stride = token_stride("v", v, int64_t(p.Hkv) * p.D);
+    need_cuda(q, "q", q);
+    need_cuda(q, "k", k);
+    need_cuda(q, "v", v);
+    need_cuda(q, "cu_seqlens", cu);
+    need_cuda(q, "cu_seqlens_k", cu_k);
+    return p;
+}
+void need_like(const char* name, const at::Tensor& t, const at::Tensor& q, const char* what) {
+    need(t.sizes() == q.sizes() && t.scalar_type() == q.scalar_type() && t.is_contiguous(), std::string(name) + " must be contiguous and match " + what);
+}
+void need_lse(const char* name, const at::Tensor* t, const at::Tensor& q) {
+    if (t)
+        need(t->dim() == 3 && t->sizes() == q.sizes().slice(0, 3) && t->scalar_type() == at::kFloat && t->is_contiguous(), std::string(name) + " must be a contiguous float32 [B,T,Hq]");
+}
+
+PyObject* prompt_fwd(Args& a) {
+    const at::Tensor &q = a.tensor("q"), &k = a.tensor("k"), &v = a.tensor("v");
+    const double scale = a.number();
+    const int64_t window = a.integer();
+    const at::Tensor *cu = a.maybe("cu_seqlens"), *cu_k = a.maybe("cu_seqlens_k"), *given = a.maybe("o");
+    bool make_lse;
+    const at::Tensor* lse = lse_of(a, make_lse);
+    if (given) need_like("o", *given, q, "q");
+    need_lse("lse", lse, q);
+    gdn_prompt_problem p = prompt_problem(q, k, v, scale, window, cu, cu_k);
+    need_cuda(q, "o", given);
+    need_cuda(q, "lse", lse);
+    On on(q, a);
+    const at::Tensor o = given ? *given : empty(q.sizes(), q.scalar_type(), q);
+    p.clear_rest = !given;
+    at::Tensor new_lse;
+    if (make_lse) {
+        new_lse = empty(q.sizes().slice(0, 3), at::kFloat, q);
+        if (given && cu) new_lse.fill_(-INFINITY);  // what the allocator hands out is not a result
+        lse = &new_lse;
+    }
+    check(f_prompt_fwd(&p, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), ptr(lse), on.stream));
+    return make_lse ? tuple({o, new_lse}) : THPVariable_Wrap(o);
+}
+
+PyObject* prompt_bwd(Args& a) {
+    const at::Tensor &q = a.tensor("q"), &k = a.tensor("k"), &v = a.tensor("v"), &o = a.tensor("o"), &lse = a.tensor("lse"), &dO = a.tensor("do");
+    const at::Tensor* dlse = a.maybe("dlse");
+    const double scale = a.number();
+    const int64_t window = a.integer();
+    const at::Tensor *cu = a.maybe("cu_seqlens"), *cu_k = a.maybe("cu_seqlens_k"), *ws = a.maybe("workspace");
+    need_like("o", o, q, "q");
+    need_like("do", dO, q, "q");
+    need_lse("lse", &lse, q);
+    need_lse("dlse", dlse, q);
+    gdn_prompt_problem p = prompt_problem(q, k, v, scale, window, cu, cu_k);
+    need_scratch(ws);
+    need_cuda(q, "o", o);
+    need_cuda(q, "lse", lse);
+    need_cuda(q, "do", dO);
+    need_cuda(q, "dlse", dlse);
+    need_cuda(q, "workspace", ws);
+    On on(q, a);
+    p.clear_rest = 1;
+    size_t bytes = 0;
+    check(f_prompt_bwd_size(&p, &bytes));
+    const at::Tensor work = scratch(bytes, ws, q), dq = empty(q.sizes(), q.scalar_type(), q), dk = empty(k.sizes(), q.scalar_type(), q), dv = empty(k.sizes(), q.scalar_type(), q);
+    check(f_prompt_bwd(&p, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), ptr(lse), dO.data_ptr(), ptr(dlse), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                       bytes ? work.data_ptr() : nullptr, bytes ? size_t(work.numel()) * work.element_size() : 0, on.stream));
+    return tuple({dq, dk, dv});
+}
+
+// The strides of a pair of caches [num_pages,page_size,Hkv,D] into a problem.
+template <typename P> void cache_strides(P& p, const at::Tensor& kc, const at::Tensor& vc) {
+    need(kc.stride(3) == 1 && vc.stride(3) == 1, "the features of the caches must be contiguous");
+    p.cache_dtype = cache_code(kc);
+    p.page_size = small(kc.size(1), "tokens to a page");
+    p.num_pages = kc.size(0);
+    p.k_page_stride = kc.stride(0);
+    p.k_token_stride = kc.stride(1);
+    p.k_head_stride = kc.stride(2);
+    p.v_page_stride = vc.stride(0);
+    p.v_token_stride = vc.stride(1);
+    p.v_head_stride = vc.stride(2);
+}
+void need_table(const at::Tensor& table, int64_t N) {
+    need(table.scalar_type() == at::kInt && table.dim() == 2 && table.size(0) == N && (table.size(1) <= 1 || table.stride(1) == 1),
+         "page_table must be int32 [N,max_pages] with contiguous rows");
+}
+
+PyObject* tree(Args& a) {
+    const at::Tensor &q = a.tensor("q"), &kn = a.tensor("k_new"), &vn = a.tensor("v_new"), &kc = a.tensor("k_cache"), &vc = a.tensor("v_cache"), &table = a.tensor("page_table"),
+                     &lens = a.tensor("seq_lens"), &parents = a.tensor("parents");
+    const double scale = a.number();
+    const at::Tensor *ks = a.maybe("k_scale"), *vs = a.maybe("v_scale");
+    const int64_t window = a.integer();
+    const at::Tensor* given = a.maybe("o");
+    bool make_lse;
+    const at::Tensor* lse = lse_of(a, make_lse);
+    const at::Tensor* ws = a.maybe("workspace");
+    need(q.dim() == 4 && kc.dim() == 4 && vc.sizes() == kc.sizes(), "q must be [N,T,Hq,D], k_cache and v_cache [num_pages,page_size,Hkv,D]");
+    const int64_t N = q.size(0), T = q.size(1), Hq = q.size(2), D = q.size(3), Hkv = kc.size(2);
+    need(kc.size(3) == D, "q and the caches must match in D");
+    need(vc.scalar_type() == kc.scalar_type(), "k_cache and v_cache must both be bfloat16, float32 or float8_e4m3fn");
+    need(T > 0 && Hq > 0 && Hkv > 0, "there must be drafted tokens and heads");
+    need(kn.dim() == 4 && kn.size(0) == N && kn.size(1) == T && kn.size(2) == Hkv && kn.size(3) == D && vn.sizes() == kn.sizes() &&
+             kn.scalar_type() == q.scalar_type() && vn.scalar_type() == q.scalar_type(),
+         "k_new and v_new must be [N,T," + std::to_string(Hkv) + ",D] of q's dtype");
+    need_table(table, N);
+    need(lens.scalar_type() == at::kInt && lens.dim() == 1 && lens.size(0) == N && lens.is_contiguous(), "seq_lens must be a contiguous int32 [N]");
+    need(parents.scalar_type() == at::kInt && parents.dim() == 2 && parents.size(0) == N && parents.size(1) == T && parents.is_contiguous(), "parents must be a contiguous int32 [N,T]");
+    need_vector("k_scale", ks, at::kFloat, Hkv, "float32 [Hkv]");
+    need_vector("v_scale", vs, at::kFloat, Hkv, "float32 [Hkv]");
+    if (given) need_like("o", *given, q, "q");
+    need_lse("lse", lse, q);
+    need(window >= 0 && window < (int64_t(1) << 31), "window must be >= 0, and below 2^31");
+    gdn_tree_problem p{};
+    p.num_seqs = small(N, "sequences");
+    p.T = small(T, "drafted tokens");
+    p.Hq = small(Hq, "heads");
+    p.Hkv = small(Hkv, "heads");
+    p.D = small(D, "features");
+    p.dtype = code(q, "q");
+    p.scale = float(scale);
+    p.window = int32_t(window);
+    p.max_pages = small(table.size(1), "pages");
+    p.q_stride = token_stride("q", q, Hq * D);
+    p.k_new_stride = token_stride("k_new", kn, Hkv * D);
+    p.v_new_stride = token_stride("v_new", vn, Hkv * D);
+    p.table_stride = N > 1 && table.size(1) > 0 ? apart("page_table", table.stride(0)) : 0;
+    cache_strides(p, kc, vc);
+    need_scratch(ws);
+    for (const auto& [name, t] : {std::pair{"q", &q}, {"k_new", &kn}, {"v_new", &vn}, {"k_cache", &kc}, {"v_cache", &vc}, {"page_table", &table}, {"seq_lens", &lens}, {"parents", &parents},
+                                  {"k_scale", ks}, {"v_scale", vs}, {"o", given}, {"lse", lse}, {"workspace", ws}})
+        need_cuda(q, name, t);
+    On on(q, a);
+    size_t bytes = 0;
+    check(f_tree_size(&p, &bytes));
+    const at::Tensor work = scratch(bytes, ws, q), o = given ? *given : empty(q.sizes(), q.scalar_type(), q);
+    at::Tensor new_lse;
+    if (make_lse) {
+        new_lse = empty(q.sizes().slice(0, 3), at::kFloat, q);
+        lse = &new_lse;
+    }
+    check(f_tree(&p, q.data_ptr(), kn.data_ptr(), vn.data_ptr(), kc.data_ptr(), vc.data_ptr(), ptr<int32_t>(table), ptr<int32_t>(lens), ptr<int32_t>(parents), ptr(ks), ptr(vs), o.data_ptr(),
+                 ptr(lse), bytes ? work.data_ptr() : nullptr, bytes ? size_t(work.numel()) * work.element_size() : 0, on.stream));
+    return make_lse ? tuple({o, new_lse}) : THPVariable_Wrap(o);
+}
+
+PyObject* cache_write(Args& a) {
+    const at::Tensor &k = a.tensor("k"), &v = a.tensor("v"), &kc = a.tensor("k_cache"), &vc = a.tensor("v_cache"), &slots = a.tensor("slots");
+    const at::Tensor *rows = a.maybe("rows"), *ks = a.maybe("k_scale"), *vs = a.maybe("v_scale");
+    need(kc.dim() == 4 && vc.sizes() == kc.sizes(), "k_cache and v_cache must be [num_pages,page_size,Hkv,D]");
+    need(vc.scalar_type() == kc.scalar_type(), "k_cache and v_cache must both be bfloat16, float32 or float8_e4m3fn");
+    const int64_t Hkv = kc.size(2), D = kc.size(3);
+    need((k.dim() == 3 || k.dim() == 4) && k.size(-2) == Hkv && k.size(-1) == D && v.sizes() == k.sizes() && v.scalar_type() == k.scalar_type() && Hkv > 0 && D > 0,
+         "k and v must be [rows,Hkv,D] or [B,T,Hkv,D], with the caches' heads and features, of one dtype");
+    need(slots.scalar_type() == at::kLong && slots.dim() == 1 && slots.is_contiguous(), "slots must be a contiguous int64 [count]");
+    gdn_cache_problem p{};
+    p.count = slots.numel();
+    p.num_rows = k.numel() / (Hkv * D);
+    need_vector("rows", rows, at::kInt, p.count, "int32 [count]");
+    need(rows || p.count <= p.num_rows, std::to_string(p.count) + " slots for " + std::to_string(p.num_rows) + " rows");
+    need_vector("k_scale", ks, at::kFloat, Hkv, "float32 [Hkv]");
+    need_vector("v_scale", vs, at::kFloat, Hkv, "float32 [Hkv]");
+    p.Hkv = small(Hkv, "heads");
+    p.D = small(D, "features");
+    p.dtype = code(k, "k and v");
+    cache_strides(p, kc, vc);
+    p.k_stride = token_stride("k", k.dim() == 4 ? k : k.unsqueeze(0), Hkv * D);
+    p.v_stride = token_stride("v", v.dim() == 4 ? v : v.unsqueeze(0), Hkv * D);
+    for (const auto& [name, t] : {std::pair{"k", &k}, {"v", &v}, {"k_cache", &kc}, {"v_cache", &vc}, {"slots", &slots}, {"rows", rows}, {"k_scale", ks}, {"v_scale", vs}}) need_cuda(k, name, t);
+    On on(k, a);
+    check(f_write(&p, k.data_ptr(), v.data_ptr(), kc.data_ptr(), vc.data_ptr(), ptr<int64_t>(slots), ptr<int32_t>(rows), ptr(ks), ptr(vs), on.stream));
+    Py_RETURN_NONE;
+}
+
+struct TableCall {
+    const at::Tensor &table, &lens, &change, &stack, &free;
+    gdn_table_problem p;
+    TableCall(Args& a, const char* what) : table(a.tensor("page_table")), lens(a.tensor("seq_lens")), change(a.tensor(what)), stack(a.tensor("free_pages")), free(a.tensor("num_free")), p{} {
+        const int64_t page = a.integer(), N = lens.dim() == 1 ? lens.size(0) : 0;
+        need(lens.scalar_type() == at::kInt && lens.dim() == 1 && lens.is_contiguous(), "seq_lens must be a contiguous int32 [N]");
+        need_table(table, N);
+        need_vector(what, &change, at::kInt, N, "int32 [N]");
+        need(stack.scalar_type() == at::kInt && stack.dim() == 1 && stack.is_contiguous(), "free_pages must be a contiguous int32 vector");
+        need_vector("num_free", &free, at::kInt, 1, "int32 [1]");
+        need(page > 0 && page < (int64_t(1) << 31), "page_size must be positive");
+        p.num_seqs = small(N, "sequences");
+        p.max_pages = small(table.size(1), "pages");
+        p.page_size = int32_t(page);
+        p.stack_size = small(stack.numel(), "pages");
+        p.table_stride = N > 1 && table.size(1) > 0 ? apart("page_table", table.stride(0)) : 0;
+        for (const auto& [name, t] : {std::pair{"page_table", &table}, {"seq_lens", &lens}, {what, &change}, {"free_pages", &stack}, {"num_free", &free}}) need_cuda(lens, name, t);
+    }
+};
+PyObject* table_extend(Args& a) {
+    TableCall c(a, "new_lens");
+    c.p.total = a.integer();
+    need(c.p.total >= 0, "total must be >= 0");
+    On on(c.lens, a);
+    const at::Tensor slots = empty({c.p.total}, at::kLong, c.lens), cu = empty({int64_t(c.p.num_seqs) + 1}, at::kInt, c.lens);
+    check(f_extend(&c.p, ptr<int32_t>(c.table), ptr<int32_t>(c.lens), ptr<int32_t>(c.change), ptr<int32_t>(c.stack), ptr<int32_t>(c.free), ptr<int64_t>(slots), ptr<int32_t>(cu), on.stream));
+    return tuple({slots, cu});
+}
+PyObject* table_trim(Args& a) {
+    TableCall c(a, "keep_lens");
+    On on(c.lens, a);
+    check(f_trim(&c.p, ptr<int32_t>(c.table), ptr<int32_t>(c.lens), ptr<int32_t>(c.change), ptr<int32_t>(c.stack), ptr<int32_t>(c.free), on.stream));
+    Py_RETURN_NONE;
+}
+
 // True when gradients are on and one of the arguments (tensors or None) requires one.  A forward-mode tangent
 // (level 0 is the only level there is) would be dropped, whether gradients are on or not: refused.
 PyObject* wants_grad(Args& a) {
@@ -441,17 +710,25 @@ PyObject* wants_grad(Args& a) {
 }
 
 PyObject* bind(Args& a) {
-    void* at[6];
-    for (void*& p : at) {
-        p = PyLong_AsVoidPtr(a.next());
+    auto next = [&](auto& f) {
+        void* p = PyLong_AsVoidPtr(a.next());
         if (!p) throw Bad{PyExc_ValueError, "a function's address is missing"};
-    }
-    f_step = reinterpret_cast<decltype(f_step)>(at[0]);
-    f_paged_size = reinterpret_cast<decltype(f_paged_size)>(at[1]);
-    f_paged = reinterpret_cast<decltype(f_paged)>(at[2]);
-    f_norm_fwd = reinterpret_cast<decltype(f_norm_fwd)>(at[3]);
-    f_norm_bwd_size = reinterpret_cast<decltype(f_norm_bwd_size)>(at[4]);
-    f_norm_bwd = reinterpret_cast<decltype(f_norm_bwd)>(at[5]);
+        f = reinterpret_cast<std::remove_reference_t<decltype(f)>>(p);
+    };
+    next(f_step);
+    next(f_paged_size);
+    next(f_paged);
+    next(f_norm_fwd);
+    next(f_norm_bwd_size);
+    next(f_norm_bwd);
+    next(f_prompt_fwd);
+    next(f_prompt_bwd_size);
+    next(f_prompt_bwd);
+    next(f_tree_size);
+    next(f_tree);
+    next(f_write);
+    next(f_extend);
+    next(f_trim);
     PyObject* f = a.next();
     Py_INCREF(f);
     Py_XDECREF(on_error);
@@ -474,7 +751,8 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
 }
 
 #define METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&call<&name>)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {METHOD(bind), METHOD(step), METHOD(paged), METHOD(norm_fwd), METHOD(norm_bwd), METHOD(wants_grad), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {METHOD(bind), METHOD(step), METHOD(paged), METHOD(norm_fwd), METHOD(norm_bwd), METHOD(prompt_fwd), METHOD(prompt_bwd), METHOD(tree), METHOD(cache_write),
+                          METHOD(table_extend), METHOD(table_trim), METHOD(wants_grad), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -1,0 +1,286 @@
+// A paged key-value cache's own operators (include/gdn.h): keys and values written to slots, and the page
+// tables kept on the device from the requests' lengths.
+//
+// gdn_paged_cache_write moves every value once: bound by HBM for a prompt, by the launch for a few tokens.
+// A thread takes 16-byte pieces of the output, four at a time (their rows and slots are asked for together);
+// a block has as many tokens as give its 256 threads four pieces each, or one.
+//
+// gdn_page_table_extend and _trim are latency: one launch, in which every CTA sums the requests' needs for
+// itself (a scan over up to 8 requests a thread) and keeps the sums in shared memory, so that the tokens and
+// pages can be dealt out evenly, each finding its request by bisection.  Only lengths and the count of free
+// pages are both read and written; a cluster barrier lies between.  Clusters of 8 CTAs from 4096 tokens on,
+// one CTA below.
+#include "gdn_attn.h"
+#include "gdn_paged.cuh"
+
+namespace gdn {
+namespace {
+
+// ---- writing the cache
+constexpr int WT = 256, WU = 4;
+
+struct WriteShape {
+    int tokens;             // of a block
+    int pieces, half;       // of a token; of its keys
+    FastDiv by_pieces, by_half, by_row, by_page;
+};
+
+// A: the rows' type, C: the cache's.  PV values make 16 bytes of the cache.
+template <typename A, typename C>
+__global__ void __launch_bounds__(WT) k_cache_write(const CacheArgs G, const WriteShape S) {
+    constexpr int PV = 16 / int(sizeof(C)), LV = PV * int(sizeof(A)) / 16;  // 16-byte loads of a piece
+    const gdn_cache_problem& p = G.p;
+    const int64_t token0 = int64_t(blockIdx.x) * S.tokens, places = p.num_pages * p.page_size;
+    const int items = int(min(int64_t(S.tokens), p.count - token0)) * S.pieces;
+    for (int i0 = threadIdx.x; i0 < items; i0 += WT * WU) {
+        uint4 raw[WU][LV];
+        C* to[WU];
+        float scale[WU];
+#pragma unroll
+        for (int u = 0; u < WU; ++u) {
+            const int i = i0 + u * WT;
+            to[u] = nullptr;
+            scale[u] = 1.f;
+            if (i >= items) continue;
+            const int t = S.by_pieces.of(i), r = i - t * S.pieces, second = S.by_half.of(r), at = r - second * S.half;
+            const int head = S.by_row.of(at), d = (at - head * (p.D / PV)) * PV;
+            const int64_t n = token0 + t, row = G.rows ? G.rows[n] : n, slot = G.slots[n];
+            if (slot < 0 || slot >= places || row < 0 || row >= p.num_rows) continue;
+            const int64_t page = slot >> 31 ? slot / p.page_size : S.by_page.of(int(slot)), in = slot - page * p.page_size;
+            const A* from = static_cast<const A*>(second ? G.v : G.k) + row * (second ? p.v_stride : p.k_stride) + int64_t(head) * p.D + d;
+            to[u] = static_cast<C*>(second ? G.v_cache : G.k_cache) + page * (second ? p.v_page_stride : p.k_page_stride) +
+                    in * (second ? p.v_token_stride : p.k_token_stride) + head * (second ? p.v_head_stride : p.k_head_stride) + d;
+            const float* s = second ? G.v_scale : G.k_scale;
+            if (s) scale[u] = s[head];
+#pragma unroll
+            for (int l = 0; l < LV; ++l) raw[u][l] = reinterpret_cast<const uint4*>(from)[l];
+        }
+#pragma unroll
+        for (int u = 0; u < WU; ++u) {
+            if (!to[u]) continue;
+            alignas(16) C out[PV];
+#pragma unroll
+            for (int l = 0; l < LV; ++l) {
+                const A* x = reinterpret_cast<const A*>(&raw[u][l]);
+#pragma unroll
+                for (int e = 0; e < PV / LV; ++e) out[l * (PV / LV) + e] = to_cache<C>(to_f(x[e]), scale[u]);
+            }
+            *reinterpret_cast<uint4*>(to[u]) = *reinterpret_cast<const uint4*>(out);
+        }
+    }
+}
+
+template <typename A, typename C>
+cudaError_t write_as(const CacheArgs& G, cudaStream_t st) {
+    constexpr int PV = 16 / int(sizeof(C));
+    WriteShape S;
+    S.half = G.p.Hkv * (G.p.D / PV);
+    S.pieces = 2 * S.half;
+    S.tokens = S.pieces >= WT * WU ? 1 : WT * WU / S.pieces;
+    // fewer tokens to a block where that is what gives every multiprocessor one
+    while (S.tokens > 1 && (G.p.count + S.tokens - 1) / S.tokens < sm_count_cached() && S.tokens * S.pieces > WT) S.tokens = (S.tokens + 1) / 2;
+    S.by_pieces.set(uint32_t(S.pieces));
+    S.by_half.set(uint32_t(S.half));
+    S.by_row.set(uint32_t(G.p.D / PV));
+    S.by_page.set(uint32_t(G.p.page_size));
+    timing_begin("paged_cache_write", st);
+    k_cache_write<A, C><<<unsigned((G.p.count + S.tokens - 1) / S.tokens), WT, 0, st>>>(G, S);
+    timing_end(st);
+    return cudaGetLastError();
+}
+
+// ---- page tables
+constexpr int TT_ = 1024, TPER = TABLE_SEQS / TT_;
+
+// What a CTA keeps of a request: extend: its first new token, its length before, the place on the stack of
+// its first new page (downwards), the pages that it takes (-1: refused); trim: pages given by the requests
+// after it, -, its columns before, and kept.
+struct Request {
+    int first, len, place, pages;
+};
+
+__device__ __forceinline__ int64_t warp_sum_upto(int64_t x) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    return x;
+}
+// The sum of x over the threads before this one; total: over all.
+__device__ __forceinline__ int64_t sum_before(int64_t x, int64_t* wsum, int64_t& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t upto = warp_sum_upto(x);
+    if (lane == 31) wsum[warp] = upto;
+    __syncthreads();
+    const int64_t w = warp_sum_upto(wsum[lane]);
+    total = __shfl_sync(0xffffffffu, w, 31);
+    const int64_t before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+    __syncthreads();
+    return (warp ? before : 0) + upto - x;
+}
+__device__ __forceinline__ int stack_top(const TableArgs& A) {
+    const int f = *A.free;
+    return f < 0 ? 0 : f < A.p.stack_size ? f : A.p.stack_size;
+}
+__device__ __forceinline__ int64_t length_of(const TableArgs& A, int n) {
+    const int64_t len = A.lens[n], cap = int64_t(A.p.max_pages) * A.p.page_size;
+    return len < 0 ? 0 : len < cap ? len : cap;
+}
+__device__ __forceinline__ uint32_t ctas_of_cluster() {
+    uint32_t x;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(x));
+    return x;
+}
+__device__ __forceinline__ void cluster_barrier(bool several) {
+    if (several)
+        cluster_sync();
+    else
+        __syncthreads();
+}
+
+__global__ void __launch_bounds__(TT_) k_table_extend(const TableArgs A, const FastDiv by_page) {
+    extern __shared__ Request req[];
+    __shared__ int64_t wsum[32];
+    const gdn_table_problem& p = A.p;
+    const int tid = threadIdx.x, N = p.num_seqs, per = (N + TT_ - 1) / TT_, n0 = min(N, tid * per), n1 = min(N, n0 + per);
+    const int ps = p.page_size, top = stack_top(A);
+    const int64_t cap = int64_t(p.max_pages) * ps;
+    auto pages_of = [&](int64_t len) { return by_page.of(int(len + ps - 1)); };  // of at most cap tokens
+    int64_t tokens = 0, pages = 0;
+    for (int n = n0; n < n1; ++n) {
+        const int64_t len = length_of(A, n), more = max(A.change[n], 0);
+        tokens += more;
+        if (len + more <= cap) pages += pages_of(len + more) - pages_of(len);
+    }
+    int64_t all, all_pages;
+    int64_t at = sum_before(tokens, wsum, all), taken = sum_before(pages, wsum, all_pages);
+    int64_t mine = 0;  // pages that this thread's requests get
+    for (int n = n0; n < n1; ++n) {
+        const int64_t len = length_of(A, n), more = max(A.change[n], 0);
+        const bool fits = len + more <= cap;
+        const int64_t need = fits ? pages_of(len + more) - pages_of(len) : 0;
+        const bool granted = fits && (need == 0 || taken + need <= top);
+        req[n] = {int(min(at, int64_t(0x7fffffff))), int(len), granted ? int(top - 1 - taken) : 0, granted ? int(need) : -1};
+        if (granted) mine += need;
+        at += more;
+        taken += need;
+    }
+    int64_t given;
+    sum_before(mine, wsum, given);
+    const int ctas = int(gridDim.x), cta = int(blockIdx.x);  // one cluster
+    cluster_barrier(ctas > 1);  // the requests are in shared memory; every CTA has read lengths and count
+    if (cta == 0) {
+        for (int n = tid; n < N; n += TT_) {
+            const Request r = req[n];
+            A.cu[n] = r.first;
+            if (r.pages >= 0) A.lens[n] = r.len + max(A.change[n], 0);
+        }
+        if (tid == 0) {
+            A.cu[N] = int(min(all, int64_t(0x7fffffff)));
+            *A.free = int(top - given);
+        }
+    }
+    // pages, a warp to a request
+    for (int n = cta * (TT_ / 32) + (tid >> 5); n < N; n += ctas * (TT_ / 32)) {
+        const Request r = req[n];
+        const int had = pages_of(r.len);
+        for (int i = tid & 31; i < r.pages; i += 32) A.table[n * p.table_stride + had + i] = A.stack[r.place - i];
+    }
+    // slots
+    const int64_t tokens_all = min(all, p.total);
+    for (int64_t t = int64_t(cta) * TT_ + tid; t < p.total; t += int64_t(ctas) * TT_) {
+        int64_t slot = -1;
+        if (t < tokens_all) {
+            int lo = 0, hi = N;  // the last request that begins at or before t
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (req[mid].first <= t)
+                    lo = mid;
+                else
+                    hi = mid;
+            }
+            const Request r = req[lo];
+            if (r.pages >= 0) {
+                const int pos = r.len + int(t - r.first), column = by_page.of(pos), had = pages_of(r.len);
+                const int page = column < had ? A.table[lo * p.table_stride + column] : A.stack[r.place - (column - had)];
+                slot = int64_t(page) * ps + (pos - column * ps);
+            }
+        }
+        A.slots[t] = slot;
+    }
+}
+
+__global__ void __launch_bounds__(TT_) k_table_trim(const TableArgs A, const FastDiv by_page) {
+    extern __shared__ Request req[];
+    __shared__ int64_t wsum[32];
+    const gdn_table_problem& p = A.p;
+    const int tid = threadIdx.x, N = p.num_seqs, per = (N + TT_ - 1) / TT_, n0 = min(N, tid * per), n1 = min(N, n0 + per);
+    const int top = stack_top(A);
+    auto pages_of = [&](int64_t len) { return by_page.of(int(len + p.page_size - 1)); };
+    int64_t pages = 0;
+    for (int n = n0; n < n1; ++n) {
+        const int64_t len = length_of(A, n), keep = min(len, int64_t(max(A.change[n], 0)));
+        pages += pages_of(len) - pages_of(keep);
+    }
+    int64_t all, before = sum_before(pages, wsum, all);
+    for (int n = n0; n < n1; ++n) {
+        const int64_t len = length_of(A, n), keep = min(len, int64_t(max(A.change[n], 0)));
+        const int has = pages_of(len), kept = pages_of(keep);
+        before += has - kept;
+        req[n] = {int(all - before), int(keep), has, kept};
+    }
+    const int ctas = int(gridDim.x), cta = int(blockIdx.x);
+    cluster_barrier(ctas > 1);
+    if (cta == 0) {
+        for (int n = tid; n < N; n += TT_) A.lens[n] = req[n].len;
+        if (tid == 0) *A.free = int(min(top + all, int64_t(p.stack_size)));
+    }
+    for (int n = cta * (TT_ / 32) + (tid >> 5); n < N; n += ctas * (TT_ / 32)) {
+        const Request r = req[n];
+        for (int c = r.pages + (tid & 31); c < r.place; c += 32) {
+            const int64_t to = int64_t(top) + r.first + (r.place - 1 - c);
+            if (to < p.stack_size) A.stack[to] = A.table[n * p.table_stride + c];
+        }
+    }
+}
+
+cudaError_t launch_table(void (*kern)(const TableArgs, const FastDiv), const char* name, const TableArgs& A, int64_t work, cudaStream_t st) {
+    const int smem = A.p.num_seqs * int(sizeof(Request));
+    cudaError_t e = smem_attr(kern, TABLE_SEQS * int(sizeof(Request)));
+    if (e != cudaSuccess) return e;
+    FastDiv by_page;
+    by_page.set(uint32_t(A.p.page_size));
+    cudaLaunchConfig_t cfg = {};
+    const unsigned ctas = work > 4096 ? 8 : 1;
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(TT_);
+    cfg.dynamicSmemBytes = size_t(smem);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = ctas > 1 ? 1 : 0;
+    timing_begin(name, st);
+    e = cudaLaunchKernelEx(&cfg, kern, A, by_page);
+    timing_end(st);
+    return e;
+}
+
+}  // namespace
+
+cudaError_t launch_cache_write(const CacheArgs& A, cudaStream_t st) {
+    if (A.p.dtype == GDN_FP32) return write_as<float, float>(A, st);
+    return A.p.cache_dtype == GDN_BF16 ? write_as<__nv_bfloat16, __nv_bfloat16>(A, st) : write_as<__nv_bfloat16, __nv_fp8_e4m3>(A, st);
+}
+cudaError_t launch_table_extend(const TableArgs& A, cudaStream_t st) {
+    return launch_table(k_table_extend, "page_table_extend", A, A.p.total, st);
+}
+cudaError_t launch_table_trim(const TableArgs& A, cudaStream_t st) {
+    return launch_table(k_table_trim, "page_table_trim", A, int64_t(A.p.num_seqs) * 8, st);
+}
+
+}  // namespace gdn

@@ -54,8 +54,8 @@ __device__ __forceinline__ int64_t share_of(int64_t total, int parts, int warps)
     return (quotient(total + parts - 1, parts) + warps - 1) & ~int64_t(warps - 1);
 }
 // CTA 0 also leaves the number of tiles before each sequence (per block of heads) in A.before.
-template <int T>
-__device__ Part find_part(const PagedArgs& A, int tok, int warps) {
+template <int T, typename Args>
+__device__ Part find_part(const Args& A, int tok, int warps) {
     if (A.cluster) {  // a cluster of CTAs per (sequence, block of heads), equal parts of its tiles
         const int pair = blockIdx.x / A.cluster, r = blockIdx.x % A.cluster, blocks = A.groups * A.heads, n = pair / blocks, b = pair % blocks;
         const int tiles = range_of(A, n).tiles(tok), share = ((tiles + A.cluster - 1) / A.cluster + warps - 1) / warps * warps;

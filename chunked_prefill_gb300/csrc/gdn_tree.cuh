@@ -1,0 +1,130 @@
+// What the kernels of attention of drafted trees over a paged cache share (see gdn_tree.cu).
+#pragma once
+#include "gdn_attn.cuh"
+
+namespace gdn {
+
+// Sequence n's cached tokens: those that a drafted token may attend to are [first, len).  Its tiles are those
+// of `tok` cached tokens from base on, and one more: the drafted tokens.
+struct TreeRange {
+    int len, first, base;
+    __device__ __forceinline__ int cached(int tok) const { return (len - base + tok - 1) / tok; }
+    __device__ __forceinline__ int tiles(int tok) const { return cached(tok) + 1; }
+};
+static __device__ __forceinline__ TreeRange range_of(const TreeArgs& A, int n) {
+    const int64_t cap = int64_t(A.p.max_pages) * A.p.page_size, len = A.lens[n];
+    TreeRange R;
+    R.len = int(len < 0 ? 0 : len < cap ? len : cap);
+    R.first = A.p.window > 0 && R.len >= A.p.window ? R.len - A.p.window + 1 : 0;
+    R.base = min(R.first & ~15, R.len);
+    return R;
+}
+
+namespace {
+
+// Which drafted tokens (bits) a drafted token attends to, and its number of ancestors; none and -1 where
+// there is no such token.
+struct Tree {
+    uint64_t sees[64];
+    int depth[64];
+};
+// By the first 64 threads of the CTA; the caller synchronises.
+__device__ __forceinline__ void read_tree(const TreeArgs& A, int n, Tree& tree) {
+    const int t = threadIdx.x;
+    if (t >= 64) return;
+    uint64_t sees = 0;
+    int depth = -1;
+    if (t < A.p.T) {
+        const int32_t* parents = A.parents + int64_t(n) * A.p.T;
+        int at = t;
+        while (at >= 0) {
+            ++depth;
+            if (A.p.window == 0 || depth < A.p.window) sees |= uint64_t(1) << at;
+            const int up = parents[at];
+            if (up < -1 || up >= at) {
+                sees = 0, depth = -1;
+                break;
+            }
+            at = up;
+        }
+    }
+    tree.sees[t] = sees;
+    tree.depth[t] = depth;
+}
+// The first cached token that a drafted token `depth` deep attends to.
+__device__ __forceinline__ int first_cached(const TreeArgs& A, const TreeRange& R, int depth) {
+    const int64_t f = int64_t(R.len) + depth - A.p.window + 1;
+    return A.p.window > 0 && f > 0 ? int(min(f, int64_t(R.len))) : 0;
+}
+
+// Joins the parts of the rows that several CTAs have parts of, in the list's order: a warp to a row.
+template <typename Act, int D>
+__global__ void __launch_bounds__(256) k_tree_join(const TreeArgs A, int rows, int tok, int ctas) {
+    constexpr int E = D / 32, NB = D == 256 ? 4 : 8;
+    tc::pdl_wait();
+    const gdn_tree_problem& p = A.p;
+    const int lane = threadIdx.x & 31, per = p.T * p.Hq;
+    const int64_t row = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (row >= int64_t(p.num_seqs) * per) return;
+    const int n = int(quotient(row, per)), rest = int(row - int64_t(n) * per), t = rest / p.Hq, h = rest - t * p.Hq;
+    const int G = p.Hq / p.Hkv, r = t * G + h % G, nb = (p.T * G + rows - 1) / rows;
+    const int block = (h / G) * nb + r / rows, in = r % rows, head = block / A.groups, group = block % A.groups;
+    const int64_t before = A.before[n], tiles = A.before[n + 1] - before;
+    const int64_t share = share_of(A.before[p.num_seqs] * A.heads, ctas / A.groups, 1);
+    const int64_t at0 = before * A.heads + head * tiles, at1 = at0 + tiles;
+    const int c0 = int(quotient(at0, share)), c1 = int(quotient(at1 - 1, share));
+    if (c0 == c1) return;  // that CTA wrote it out
+    const int parts = c1 - c0 + 1;
+    float M = -INFINITY, S = 0.f, acc[E] = {};
+    for (int i0 = 0; i0 < parts; i0 += NB) {  // batches of parts, everything of a batch requested at once
+        float2 ml[NB];
+        float x[NB][E];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const int i = i0 + b;
+            ml[b] = make_float2(-INFINITY, 0.f);
+            if (i < parts) {
+                const int64_t at = place_of((c0 + i) * A.groups + group, i > 0, rows) + in;
+                ml[b] = A.part_ml[at];
+#pragma unroll
+                for (int e = 0; e < E; ++e) x[b][e] = A.part[at * D + 32 * e + lane];
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; ++e) x[b][e] = 0.f;
+            }
+        }
+        float top = M;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) top = fmaxf(top, ml[b].x);
+        const float c = M == -INFINITY ? 0.f : ex2(M - top);
+        M = top;
+        S *= c;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] *= c;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            if (ml[b].x == -INFINITY && ml[b].y == 0.f) continue;  // that part has none of this row's keys
+            const float w = ml[b].x == -INFINITY ? 1.f : ex2(ml[b].x - M);
+            S = fmaf(ml[b].y, w, S);
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(x[b][e], w, acc[e]);
+        }
+    }
+    const bool some = S > 0.f || S != S;
+    const float f = some ? 1.f / S : 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) static_cast<Act*>(A.o)[row * D + 32 * e + lane] = from_f<Act>(acc[e] * f);
+    if (A.lse && lane == 0) A.lse[row] = some ? (M + log2f(S)) * LN2 : -INFINITY;
+}
+
+template <typename Act, int D>
+cudaError_t launch_tree_join(const TreeArgs& A, const TreePlan& plan, cudaStream_t st) {
+    const int64_t rows = int64_t(A.p.num_seqs) * A.p.T * A.p.Hq;
+    timing_begin("tree_attn_join", st);
+    const cudaError_t e = launch_pdl(k_tree_join<Act, D>, dim3(unsigned((rows + 7) / 8)), dim3(256), 0, st, A, plan.rows, plan.tok, plan.ctas);
+    timing_end(st);
+    return e;
+}
+
+}  // namespace
+}  // namespace gdn

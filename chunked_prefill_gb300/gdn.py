@@ -82,12 +82,49 @@ class GdnNormProblem(ctypes.Structure):
                 ("dsum_stride", ctypes.c_int64)]
 
 
+class GdnPromptProblem(ctypes.Structure):
+    """Mirror of ``gdn_prompt_problem``."""
+    _fields_ = ([(n, ctypes.c_int32) for n in ("num_seqs", "total_q", "total_k", "Hq", "Hkv", "D", "dtype")] +
+                [("scale", ctypes.c_float), ("window", ctypes.c_int32), ("clear_rest", ctypes.c_int32),
+                 ("cu_seqlens", ctypes.c_void_p), ("cu_seqlens_k", ctypes.c_void_p)] +
+                [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride")])
+
+
+_CACHE_STRIDES = [(f"{c}_{n}_stride", ctypes.c_int64) for c in "kv" for n in ("page", "token", "head")]
+
+
+class GdnTreeProblem(ctypes.Structure):
+    """Mirror of ``gdn_tree_problem``."""
+    _fields_ = ([(n, ctypes.c_int32) for n in ("num_seqs", "T", "Hq", "Hkv", "D", "dtype", "cache_dtype")] +
+                [("scale", ctypes.c_float)] + [(n, ctypes.c_int32) for n in ("window", "page_size", "max_pages")] +
+                [(n, ctypes.c_int64) for n in ("num_pages", "q_stride", "k_new_stride", "v_new_stride", "table_stride")] +
+                _CACHE_STRIDES)
+
+
+class GdnCacheProblem(ctypes.Structure):
+    """Mirror of ``gdn_cache_problem``."""
+    _fields_ = ([("count", ctypes.c_int64), ("num_rows", ctypes.c_int64)] +
+                [(n, ctypes.c_int32) for n in ("Hkv", "D", "dtype", "cache_dtype", "page_size")] +
+                [(n, ctypes.c_int64) for n in ("num_pages", "k_stride", "v_stride")] + _CACHE_STRIDES)
+
+
+class GdnTableProblem(ctypes.Structure):
+    """Mirror of ``gdn_table_problem``."""
+    _fields_ = ([(n, ctypes.c_int32) for n in ("num_seqs", "max_pages", "page_size", "stack_size")] +
+                [("total", ctypes.c_int64), ("table_stride", ctypes.c_int64)])
+
+
 class GdnKernelTime(ctypes.Structure):
     """Mirror of ``gdn_kernel_time``."""
     _fields_ = [("name", ctypes.c_char * 48), ("launches", ctypes.c_int32),
                 ("total_ms", ctypes.c_float)]
 
 
+# what _binding.so calls, in the order in which it takes the addresses
+_BOUND = ("gdn_recurrent_step", "gdn_paged_attn_workspace_size", "gdn_paged_attn_decode", "gdn_rmsnorm_fwd",
+          "gdn_rmsnorm_bwd_workspace_size", "gdn_rmsnorm_bwd", "gdn_prompt_attn_fwd",
+          "gdn_prompt_attn_bwd_workspace_size", "gdn_prompt_attn_bwd", "gdn_paged_attn_tree_workspace_size",
+          "gdn_paged_attn_tree", "gdn_paged_cache_write", "gdn_page_table_extend", "gdn_page_table_trim")
 _lib = None
 
 
@@ -120,8 +157,17 @@ def lib():
         L.gdn_rmsnorm_fwd.argtypes = [N] + [vp] * 7
         L.gdn_rmsnorm_bwd_workspace_size.argtypes = [N, ctypes.POINTER(ctypes.c_size_t)]
         L.gdn_rmsnorm_bwd.argtypes = [N] + [vp] * 7 + [ctypes.c_size_t, vp]
-        for f in ("gdn_recurrent_step", "gdn_paged_attn_workspace_size", "gdn_paged_attn_decode",
-                  "gdn_rmsnorm_fwd", "gdn_rmsnorm_bwd_workspace_size", "gdn_rmsnorm_bwd"):
+        Q, R, C, T = (ctypes.POINTER(c) for c in (GdnPromptProblem, GdnTreeProblem, GdnCacheProblem, GdnTableProblem))
+        size = ctypes.POINTER(ctypes.c_size_t)
+        L.gdn_prompt_attn_fwd.argtypes = [Q] + [vp] * 6
+        L.gdn_prompt_attn_bwd_workspace_size.argtypes = [Q, size]
+        L.gdn_prompt_attn_bwd.argtypes = [Q] + [vp] * 11 + [ctypes.c_size_t, vp]
+        L.gdn_paged_attn_tree_workspace_size.argtypes = [R, size]
+        L.gdn_paged_attn_tree.argtypes = [R] + [vp] * 13 + [ctypes.c_size_t, vp]
+        L.gdn_paged_cache_write.argtypes = [C] + [vp] * 9
+        L.gdn_page_table_extend.argtypes = [T] + [vp] * 8
+        L.gdn_page_table_trim.argtypes = [T] + [vp] * 6
+        for f in _BOUND:
             getattr(L, f).restype = ctypes.c_int
         for f in ("gdn_chunk_fwd_workspace_size", "gdn_chunk_bwd_workspace_size",
                   "gdn_chunk_fwd", "gdn_chunk_bwd", "gdn_chunk_layout", "gdn_chunk_fwd_saved",
@@ -536,9 +582,7 @@ def _binding():
             raise RuntimeError(f"{path} is missing: build it with "
                                "`python -m chunked_prefill_gb300.build` (no fallback exists)")
         from chunked_prefill_gb300 import _binding as B
-        B.bind(*(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
-            "gdn_recurrent_step", "gdn_paged_attn_workspace_size", "gdn_paged_attn_decode",
-            "gdn_rmsnorm_fwd", "gdn_rmsnorm_bwd_workspace_size", "gdn_rmsnorm_bwd")), _check)
+        B.bind(*(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in _BOUND), _check)
         _native = B
     return _native
 
@@ -681,3 +725,113 @@ def rms_norm_quant(x, weight, residual=None, eps=1e-6, weight_offset=0.0, group=
         raise RuntimeError("rms_norm_quant is not differentiable, but an argument requires a gradient: "
                            "train with rms_norm or gdn_rmsnorm_bwd")
     return native.norm_fwd(x, weight, residual, eps, weight_offset, True, group, True, None)
+
+
+# ------------------------------------------------------------- prompts and the paged cache
+def gdn_prompt_attn_fwd(q, k, v, scale, window=0, cu_seqlens=None, cu_seqlens_k=None, o=None, lse=None, stream=None):
+    """Causal attention over prompts through the C ABI (see include/gdn.h).  q [B,T,Hq,D], k and v
+    [B,Tk,Hkv,D], each with contiguous rows at any token stride but 0.  Returns o, with lse=True
+    (o, lse [B,T,Hq] fp32); an lse tensor is written."""
+    return (_native or _binding()).prompt_fwd(q, k, v, scale, window, cu_seqlens, cu_seqlens_k, o, lse, stream)
+
+
+def gdn_prompt_attn_bwd(q, k, v, o, lse, do, scale, window=0, cu_seqlens=None, cu_seqlens_k=None, dlse=None,
+                        workspace=None, stream=None):
+    """Gradients of <o, do> + <lse, dlse> from the forward's o and lse: (dq, dk, dv)."""
+    return (_native or _binding()).prompt_bwd(q, k, v, o, lse, do, dlse, scale, window, cu_seqlens, cu_seqlens_k,
+                                              workspace, stream)
+
+
+class _PromptAttention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, scale, window, cu_seqlens, cu_seqlens_k):
+        ctx.set_materialize_grads(False)  # an unused lse has no gradient to read
+        o, lse = gdn_prompt_attn_fwd(q, k, v, scale, window, cu_seqlens, cu_seqlens_k, lse=True)
+        ctx.save_for_backward(q, k, v, o, lse, cu_seqlens, cu_seqlens_k)
+        ctx.scale, ctx.window = scale, window
+        return o, lse
+
+    @staticmethod
+    @once_differentiable  # a second derivative is refused, not zero
+    def backward(ctx, do, dlse):
+        q, k, v, o, lse, cu, cu_k = ctx.saved_tensors
+        do = torch.zeros_like(o) if do is None else do.contiguous()
+        dlse = None if dlse is None else dlse.contiguous()
+        return (*gdn_prompt_attn_bwd(q, k, v, o, lse, do, ctx.scale, ctx.window, cu, cu_k, dlse), None, None, None, None)
+
+
+def prompt_attention(q, k, v, scale=None, window=0, cu_seqlens=None, cu_seqlens_k=None, return_lse=False):
+    """Causal attention over whole prompts, grouped heads, for packed sequences of different lengths: o like q,
+    or (o, lse [B,T,Hq] fp32) with return_lse.
+
+    q [B,T,Hq,D]; k, v [B,Tk,Hkv,D], bf16 or fp32, D = 64, 128 or 256, each with contiguous rows at any token
+    stride but 0 (views of a fused projection's rows).  cu_seqlens int32 [N+1] (device, B = 1) packs sequences;
+    cu_seqlens_k theirs of the keys where a sequence has other numbers of keys than of queries.  The last query
+    stands at the last key: more keys than queries are a prompt's last part with the earlier keys given.
+    window > 0 attends to the last `window` keys.  Queries that see no key, and rows that no sequence
+    covers, get o = 0 and lse = -inf.  With bf16 the weights are rounded to bf16 for their product with v, their
+    sum is not.  Differentiable with respect to q, k and v, once."""
+    native = _native or _binding()
+    if scale is None:
+        scale = q.shape[-1] ** -0.5
+    if native.wants_grad(q, k, v):
+        o, lse = _PromptAttention.apply(q, k, v, scale, window, cu_seqlens, cu_seqlens_k)
+        return (o, lse) if return_lse else o
+    return native.prompt_fwd(q, k, v, scale, window, cu_seqlens, cu_seqlens_k, None, True if return_lse else None, None)
+
+
+def gdn_paged_attn_tree(q, k_new, v_new, k_cache, v_cache, page_table, seq_lens, parents, scale, k_scale=None,
+                        v_scale=None, window=0, o=None, lse=None, workspace=None, stream=None):
+    """Attention of a tree of drafted tokens through the C ABI (see include/gdn.h).  Returns o, with lse=True
+    (o, lse); an lse tensor is written."""
+    return (_native or _binding()).tree(q, k_new, v_new, k_cache, v_cache, page_table, seq_lens, parents, scale,
+                                        k_scale, v_scale, window, o, lse, workspace, stream)
+
+
+def paged_attention_tree(q, k_new, v_new, k_cache, v_cache, page_table, seq_lens, parents, scale=None, k_scale=None,
+                         v_scale=None, window=0, return_lse=False, o=None, workspace=None, stream=None):
+    """Attention of a tree of drafted tokens per sequence over its paged key-value cache, to verify all
+    branches in one call: o [N,T,Hq,D], or (o, lse [N,T,Hq] fp32) with return_lse.
+
+    q [N,T,Hq,D] and k_new, v_new [N,T,Hkv,D]: the drafted tokens', 1 <= T <= 64.  parents int32 [N,T]: the
+    drafted token that each follows (below its own index), -1: the cached ones; anything else: no such token
+    (o = 0, lse = -inf).  A token attends to the seq_lens[n] cached tokens, its ancestors and itself, with
+    window > 0 to the last `window` positions up to its own.  Caches, page_table, scales and types as in
+    paged_attention_decode, but seq_lens does not count the drafted tokens and nothing is written to the
+    cache (paged_cache_write does that with the accepted ones).  For inference: nothing is differentiated."""
+    native = _native or _binding()
+    if native.wants_grad(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale):
+        raise RuntimeError("paged_attention_tree is not differentiable, but an argument requires a gradient")
+    if scale is None:
+        scale = q.shape[-1] ** -0.5
+    return native.tree(q, k_new, v_new, k_cache, v_cache, page_table, seq_lens, parents, scale, k_scale, v_scale,
+                       window, o, True if return_lse else None, workspace, stream)
+
+
+def paged_cache_write(k, v, k_cache, v_cache, slots, rows=None, k_scale=None, v_scale=None, stream=None):
+    """Keys and values into a paged cache: row rows[i] (i without rows) of k and v [rows,Hkv,D] or [B,T,Hkv,D]
+    to slot slots[i] (int64, page * page_size + offset, as page_table_extend gives them; negative: skipped) of
+    the caches [num_pages,page_size,Hkv,D], divided by the scales [Hkv] and rounded to the cache's type (clamped
+    to +-448 in 8 bits).  rows int32 picks the accepted ones of drafted tokens.  Two rows may not have the same
+    slot.  Nothing is differentiated here."""
+    native = _native or _binding()
+    if native.wants_grad(k, v, k_cache, v_cache, k_scale, v_scale):
+        raise RuntimeError("paged_cache_write is not differentiable, but an argument requires a gradient")
+    native.cache_write(k, v, k_cache, v_cache, slots, rows, k_scale, v_scale, stream)
+
+
+def page_table_extend(page_table, seq_lens, new_lens, free_pages, num_free, page_size, total, stream=None):
+    """Room in the paged cache for new_lens[n] more tokens of every sequence, on the device: pages are taken
+    from the top of the stack free_pages[:num_free] in the sequences' order, page_table [N,max_pages], seq_lens [N]
+    and num_free [1] (all int32) are updated in place.  Returns (slots int64 [total], cu_seqlens int32 [N+1]): the
+    new tokens' places in the cache, packed by the sums of new_lens.  A sequence whose pages are not there, or
+    whose length would not fit its row, is refused: its length and row stay and its slots are -1, as are those
+    behind the last token.  See gdn_page_table_extend in include/gdn.h."""
+    return (_native or _binding()).table_extend(page_table, seq_lens, new_lens, free_pages, num_free, page_size, total, stream)
+
+
+def page_table_trim(page_table, seq_lens, keep_lens, free_pages, num_free, page_size, stream=None):
+    """Cuts every sequence to keep_lens[n] tokens (0: gives it up) and puts the pages that it then does not
+    need back on the stack, so that it undoes page_table_extend; seq_lens, free_pages and num_free are updated in
+    place."""
+    (_native or _binding()).table_trim(page_table, seq_lens, keep_lens, free_pages, num_free, page_size, stream)

@@ -58,7 +58,7 @@ typedef enum {
 } gdn_status;
 
 /* GDN_E4M3 (8 bits: 1 sign, 4 exponent, 3 mantissa bits, no infinities) only where an entry
- * point names it: a cache of gdn_paged_attn_decode, the output of gdn_rmsnorm_fwd. */
+ * point names it: a paged cache, the output of gdn_rmsnorm_fwd. */
 typedef enum { GDN_BF16 = 0, GDN_FP32 = 1, GDN_E4M3 = 2 } gdn_dtype;
 
 /* Intra-GPU context parallelism over chunk ranges (FlashQLA pages, "AutoCP" section: when
@@ -371,6 +371,153 @@ gdn_status gdn_rmsnorm_bwd_workspace_size(const gdn_norm_problem* p, size_t* byt
 gdn_status gdn_rmsnorm_bwd(const gdn_norm_problem* p, const void* s, const void* weight,
                            const void* dy, const void* dsum, void* dx, float* dweight,
                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * Causal attention over whole prompts, and its gradient (the full-attention layers of a model that
+ * interleaves them with gated-delta-rule layers).  Per sequence of Lq queries and Lk keys and query
+ * head h, with kv-head j = h / (Hq / Hkv): query i stands at position i + Lk - Lq and attends to the
+ * keys t of [max(0, position - window + 1), position] (from 0 without a window):
+ *     z_it = scale <q_i, k_t>,   o_i = sum_t softmax(z_i)_t v_t,   lse_i = log sum_t e^{z_it}
+ * Lk = Lq is a whole prompt; Lk > Lq its last part, the earlier keys given with it; with Lk < Lq the
+ * first Lq - Lk queries see nothing.  A query that sees nothing gets o = 0, lse = -inf and no gradient.
+ *
+ *   q, o, dO, dq  [total_q, Hq, D]     k, v, dk, dv  [total_k, Hkv, D]     lse, dlse  [total_q, Hq] fp32
+ * Sequences are packed: queries [cu_seqlens[n], cu_seqlens[n+1]), keys by cu_seqlens_k (NULL: by
+ * cu_seqlens, with total_k = total_q); without cu_seqlens there are num_seqs of equal lengths.  Both are
+ * read on the device alone, and cut to [0, total], so a captured call serves other lengths; sequences must
+ * not overlap.  Rows that no sequence covers are left as they were (clear_rest = 0), or get o = 0, lse = -inf
+ * and gradients of 0 (clear_rest = 1).  What lies there, NaN or not, is not used.
+ *
+ * gdn_prompt_attn_bwd: the gradients of <o, dO> + <lse, dlse> (dlse NULL: 0) with respect to q, k and v,
+ * from the forward's o and lse; dk and dv are summed over the query heads that share a kv-head.
+ *
+ * Scores, softmax statistics, sums and gradients are held in fp32.  With bf16 the weights e^{z - m} (m the
+ * running maximum, or up to 8 log 2 below it) are rounded to bf16 for their product with v, while the sum
+ * that o is divided by, and lse, take them unrounded; in the gradient, softmax(z) and the gradient of z are
+ * rounded to bf16 for the products with dO, q and k.  With fp32 nothing is rounded below fp32.
+ * A value v_t that is infinite or NaN reaches the queries that attend to t and no others.  In the gradient
+ * such a value, or one in q, k, o or dO, may reach the other rows of its sequence within the same 128.
+ * ------------------------------------------------------------------------------------ */
+typedef struct gdn_prompt_problem {
+    int32_t num_seqs;
+    int32_t total_q, total_k;      /* rows of q and of k and v */
+    int32_t Hq, Hkv;               /* query heads, a multiple of the kv-heads */
+    int32_t D;                     /* 64, 128 or 256 */
+    int32_t dtype;                 /* gdn_dtype of q, k, v, o and their gradients: bf16 or fp32 */
+    float scale;                   /* finite and > 0 */
+    int32_t window;                /* keys attended to, 0 for all */
+    int32_t clear_rest;
+    const int32_t* cu_seqlens;     /* device [num_seqs+1], or NULL; 4-byte aligned */
+    const int32_t* cu_seqlens_k;
+    /* elements from one token's row to the next, 0 for contiguous rows; a row's heads and features are
+     * contiguous.  Multiples of 16 bytes. */
+    int64_t q_stride, k_stride, v_stride;
+} gdn_prompt_problem;
+
+gdn_status gdn_prompt_attn_fwd(const gdn_prompt_problem* p, const void* q, const void* k, const void* v,
+                               void* o, float* lse /* NULL: not returned */, void* stream);
+
+gdn_status gdn_prompt_attn_bwd_workspace_size(const gdn_prompt_problem* p, size_t* bytes);
+
+gdn_status gdn_prompt_attn_bwd(const gdn_prompt_problem* p, const void* q, const void* k, const void* v,
+                               const void* o, const float* lse, const void* dO, const float* dlse,
+                               void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * Attention of a tree of drafted tokens over a paged key-value cache (their verification: all branches
+ * in one call).  Sequence n has seq_lens[n] tokens in its pages, as in gdn_paged_attn_decode, but none of
+ * the drafted ones, and up to T drafted tokens whose keys and values are k_new and v_new.  parents[n][t]
+ * is the drafted token that t follows, below t; -1: t follows the cached tokens; anything else: there is
+ * no token t (its o is 0, its lse -inf, and a token that follows it is none either).
+ * Token t attends to the cached tokens, its ancestors and itself.  With a window it attends to positions above its own, seq_lens[n] +
+ * (number of its ancestors), less window.
+ * k_scale and v_scale are those of the cache; k_new and v_new are used as given.  Nothing is written to
+ * the cache: the accepted tokens are by gdn_paged_cache_write.
+ *
+ * Types, scales, roundings, lengths past the table, page numbers out of range and slots without tokens: as
+ * in gdn_paged_attn_decode, but that query values are not split under 8-bit caches (keys and values are widened to
+ * bf16, exactly, and weights rounded to bf16).  1 <= T <= 64.
+ * ------------------------------------------------------------------------------------ */
+typedef struct gdn_tree_problem {
+    int32_t num_seqs;
+    int32_t T;                     /* drafted tokens of a sequence, at most */
+    int32_t Hq, Hkv, D;
+    int32_t dtype, cache_dtype;
+    float scale;
+    int32_t window;
+    int32_t page_size, max_pages;
+    int64_t num_pages;
+    int64_t q_stride, k_new_stride, v_new_stride; /* elements between tokens (0: contiguous), sequence n's at n T */
+    int64_t table_stride;
+    int64_t k_page_stride, k_token_stride, k_head_stride;
+    int64_t v_page_stride, v_token_stride, v_head_stride;
+} gdn_tree_problem;
+
+gdn_status gdn_paged_attn_tree_workspace_size(const gdn_tree_problem* p, size_t* bytes);
+
+gdn_status gdn_paged_attn_tree(const gdn_tree_problem* p, const void* q, const void* k_new, const void* v_new,
+                               const void* k_cache, const void* v_cache, const int32_t* page_table,
+                               const int32_t* seq_lens, const int32_t* parents, /* [num_seqs, T] */
+                               const float* k_scale, const float* v_scale, void* o, /* [num_seqs, T, Hq, D] */
+                               float* lse, /* [num_seqs, T, Hq] or NULL */
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * Keys and values into a paged cache.  For i < count, row rows[i] (i itself where rows is NULL) of k and v
+ * goes to slot slots[i] % page_size of page slots[i] / page_size, as k / k_scale[j] and v / v_scale[j] rounded
+ * to the cache's type (in 8 bits clamped to +-448, NaN kept; NULL scales: 1).  Slots outside
+ * [0, num_pages page_size) and rows outside [0, num_rows) are skipped.  Two rows of a call may not have the
+ * same slot: which values stay is not defined then.
+ * ------------------------------------------------------------------------------------ */
+typedef struct gdn_cache_problem {
+    int64_t count, num_rows;
+    int32_t Hkv, D;                /* D a multiple of 16 */
+    int32_t dtype, cache_dtype;    /* as in gdn_paged_problem */
+    int32_t page_size;
+    int64_t num_pages;
+    int64_t k_stride, v_stride;    /* elements between rows (0: contiguous); multiples of 16 bytes */
+    int64_t k_page_stride, k_token_stride, k_head_stride;
+    int64_t v_page_stride, v_token_stride, v_head_stride;
+} gdn_cache_problem;
+
+gdn_status gdn_paged_cache_write(const gdn_cache_problem* p, const void* k, const void* v, void* k_cache,
+                                 void* v_cache, const int64_t* slots /* 8-byte aligned */, const int32_t* rows,
+                                 const float* k_scale, const float* v_scale, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * Page tables on the device.  Row n of page_table [num_seqs, max_pages] lists the pages of sequence n, which
+ * has seq_lens[n] tokens and thus ceil(seq_lens[n] / page_size) pages; free_pages[0 .. *num_free) are the
+ * pages that no sequence has, a stack with its top at the end.  All of it is device memory, updated in place.
+ *
+ * gdn_page_table_extend makes room for new_lens[n] more tokens of every sequence.  In the sequences' order,
+ * a sequence that needs m pages more takes the top m (its next column the topmost) and its length grows, if
+ *   its length then fits the table's row, and
+ *   m = 0, or the stack has as many pages as the sequences up to it need that fit their rows;
+ * otherwise it is refused: its length and row stay.  Outputs: cu_seqlens [num_seqs+1], the sums of new_lens,
+ * and slots [total]: for the new token cu_seqlens[n] + i of sequence n the slot page * page_size + offset of its position in
+ * the cache, -1 where the sequence was refused and behind the last token.  Tokens behind `total` get no slot.
+ *
+ * gdn_page_table_trim cuts every sequence to keep_lens[n] tokens (longer ones stay as they are) and puts the
+ * pages that it then does not need on the stack, the last sequence's first and of each the last column's
+ * first, so that it undoes an extension.  0 gives up the sequence; the table's row is left as it was.
+ * Pages that the stack has no place for (stack_size) are dropped.
+ *
+ * Negative lengths count as 0, and *num_free is cut to [0, stack_size]; a cached length past the table's row
+ * counts as the row's.  Page numbers are copied as they are.  num_seqs <= 8192.  Integer work: exact.
+ * ------------------------------------------------------------------------------------ */
+typedef struct gdn_table_problem {
+    int32_t num_seqs, max_pages, page_size;
+    int32_t stack_size;            /* places in free_pages */
+    int64_t total;                 /* places in slots */
+    int64_t table_stride;          /* elements between rows of page_table (0: contiguous) */
+} gdn_table_problem;
+
+gdn_status gdn_page_table_extend(const gdn_table_problem* p, int32_t* page_table, int32_t* seq_lens,
+                                 const int32_t* new_lens, int32_t* free_pages, int32_t* num_free,
+                                 int64_t* slots, int32_t* cu_seqlens, void* stream);
+gdn_status gdn_page_table_trim(const gdn_table_problem* p, const int32_t* page_table, int32_t* seq_lens,
+                               const int32_t* keep_lens, int32_t* free_pages, int32_t* num_free, void* stream);
 
 /* ------------------------------------------------------------------------------------
  * Per-kernel timing (instrumentation for benchmarks; not needed for computation).
