@@ -25,6 +25,9 @@ struct PromptArgs {
 size_t prompt_bwd_workspace(const gdn_prompt_problem& p);
 cudaError_t launch_prompt_fwd_simt(const PromptArgs& A, cudaStream_t st);
 cudaError_t launch_prompt_bwd_simt(const PromptArgs& A, cudaStream_t st);
+// bf16, on the tensor cores
+cudaError_t launch_prompt_fwd_tc(const PromptArgs& A, cudaStream_t st);
+int prompt_fwd_status();  // not 0 where a wait of an earlier launch gave up (reads and clears it; synchronises)
 cudaError_t launch_prompt_stat(const PromptArgs& A, cudaStream_t st);
 
 struct TreeArgs {

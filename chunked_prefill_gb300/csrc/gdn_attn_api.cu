@@ -128,7 +128,8 @@ gdn_status gdn_prompt_attn_fwd(const gdn_prompt_problem* problem, const void* q,
     A.v = v;
     A.o = o;
     A.lse = lse;
-    return done(gdn::launch_prompt_fwd_simt(A, static_cast<cudaStream_t>(stream)));
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return done(A.p.dtype == GDN_FP32 ? gdn::launch_prompt_fwd_simt(A, st) : gdn::launch_prompt_fwd_tc(A, st));
 } catch (...) {
     return no_host_memory();
 }

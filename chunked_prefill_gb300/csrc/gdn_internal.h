@@ -38,6 +38,9 @@ bool make_map(CUtensorMap* m, const void* base, int H, int64_t T_total);
 // [rows, 128] bf16 (rows of 256 bytes), box 64 x 128 (one 64-column block of a 128-row
 // tile), 128-byte swizzle.
 bool make_rows_map(CUtensorMap* m, const void* base, int64_t rows);
+// [tokens, H, D] bf16 with `stride` elements between tokens, viewed as (d, head, token), box 64 x 1 x rows,
+// 128-byte swizzle.
+bool make_tokens_map(CUtensorMap* m, const void* base, int D, int H, int64_t tokens, int64_t stride, int rows);
 // Chunk-parallel preparation of the tensor-core path into P.prep: per (chunk, v-head) one
 // record of P.prep_stride bytes holding W' = -T diag(beta e) K (bf16 64 x 128, two
 // 128-byte-swizzled 64-column blocks), TU = T diag(beta) and P (bf16 64 x 64, swizzled), and
