@@ -28,6 +28,9 @@ cudaError_t launch_prompt_bwd_simt(const PromptArgs& A, cudaStream_t st);
 // bf16, on the tensor cores
 cudaError_t launch_prompt_fwd_tc(const PromptArgs& A, cudaStream_t st);
 int prompt_fwd_status();  // not 0 where a wait of an earlier launch gave up (reads and clears it; synchronises)
+cudaError_t launch_prompt_bwd_tc(const PromptArgs& A, cudaStream_t st);
+int prompt_bwd_parts(const gdn_prompt_problem& p);
+int prompt_bwd_status();
 cudaError_t launch_prompt_stat(const PromptArgs& A, cudaStream_t st);
 
 struct TreeArgs {

@@ -181,7 +181,18 @@ gdn_status gdn_prompt_attn_bwd(const gdn_prompt_problem* problem, const void* q,
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = gdn::launch_prompt_stat(A, st);
     if (e != cudaSuccess) return done(e);
-    return done(gdn::launch_prompt_bwd_simt(A, st));
+    return done(A.p.dtype == GDN_FP32 ? gdn::launch_prompt_bwd_simt(A, st) : gdn::launch_prompt_bwd_tc(A, st));
+} catch (...) {
+    return no_host_memory();
+}
+
+gdn_status gdn_attn_device_status(void* stream) try {
+    const cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return done(e);
+    const int fwd = gdn::prompt_fwd_status(), bwd = gdn::prompt_bwd_status();
+    if (fwd < 0 || bwd < 0) return done(cudaGetLastError());
+    if (fwd || bwd) return fail(GDN_ERR_TIMEOUT, "a device-side wait gave up (%s%s )", fwd ? " forward" : "", bwd ? " backward" : "");
+    return done(cudaSuccess);
 } catch (...) {
     return no_host_memory();
 }

@@ -237,7 +237,10 @@ cudaError_t bwd(const PromptArgs& A, cudaStream_t st) {
 
 }  // namespace
 
-size_t prompt_bwd_workspace(const gdn_prompt_problem& p) { return size_t((int64_t(p.total_q) + 127) / 128 * 128) * p.Hq * sizeof(float2); }
+size_t prompt_bwd_workspace(const gdn_prompt_problem& p) {
+    const int parts = prompt_bwd_parts(p);
+    return size_t((int64_t(p.total_q) + 127) / 128 * 128) * p.Hq * sizeof(float2) + (parts > 1 ? size_t(2) * parts * p.total_k * p.Hkv * p.D * sizeof(float) : 0);
+}
 
 cudaError_t launch_prompt_stat(const PromptArgs& A, cudaStream_t st) {
     const int64_t rows = int64_t(A.p.total_q) * A.p.Hq;

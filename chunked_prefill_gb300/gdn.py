@@ -174,6 +174,8 @@ def lib():
                   "gdn_chunk_bwd_saved", "gdn_prologue_fwd", "gdn_prologue_bwd_workspace_size",
                   "gdn_prologue_bwd"):
             getattr(L, f).restype = ctypes.c_int
+        L.gdn_attn_device_status.argtypes = [vp]
+        L.gdn_attn_device_status.restype = ctypes.c_int
         L.gdn_device_status.argtypes = [vp, vp]
         L.gdn_device_status.restype = ctypes.c_int
         L.gdn_debug_wait_timeout.argtypes = [vp, ctypes.c_int32, vp]
@@ -198,6 +200,12 @@ def gdn_device_status(workspace, stream=None) -> int:
     GDN_ERR_BOUNDS when a checked build skipped an out-of-range store, or GDN_ERR_TIMEOUT
     when a device-side wait of that call gave up (see include/gdn.h)."""
     return lib().gdn_device_status(_ptr(workspace), _stream(stream))
+
+
+def gdn_attn_device_status(stream=None) -> int:
+    """Wait for the stream: GDN_OK, or GDN_ERR_TIMEOUT when a device-side wait of an attention call over
+    prompts or drafted trees has given up since the last time (see include/gdn.h)."""
+    return lib().gdn_attn_device_status(_stream(stream))
 
 
 def gdn_debug_wait_timeout(workspace, limit_us: int, stream=None):

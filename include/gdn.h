@@ -424,6 +424,12 @@ gdn_status gdn_prompt_attn_bwd(const gdn_prompt_problem* p, const void* q, const
                                void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes,
                                void* stream);
 
+/* Waits in the tensor-core kernels of the attention over prompts and of drafted trees are bounded like those
+ * of the chunked rule (2 s; see "Device-side failure report"), but leave their mark in the library: this waits
+ * for `stream` and returns GDN_OK, or GDN_ERR_TIMEOUT where a wait of such a call on the current device has given
+ * up since it was last asked (that call's outputs are not valid).  Not to be called while a stream is captured. */
+gdn_status gdn_attn_device_status(void* stream);
+
 /* ------------------------------------------------------------------------------------
  * Attention of a tree of drafted tokens over a paged key-value cache (their verification: all branches
  * in one call).  Sequence n has seq_lens[n] tokens in its pages, as in gdn_paged_attn_decode, but none of

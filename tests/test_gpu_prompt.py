@@ -331,3 +331,8 @@ def test_broadcast_leaves_sum_their_gradients(gdn):
         gdn.prompt_attention(q[b:b + 1], leaf, v[b:b + 1]).sum().backward()
         parts.append(leaf.grad)
     assert torch.allclose(k.grad, parts[0] + parts[1], rtol=1e-6, atol=1e-6)
+
+
+def test_no_wait_gave_up(gdn):
+    run(gdn, make([(200, 300), (77, 77)], 4, 2, 128))
+    assert gdn.gdn_attn_device_status() == gdn.GDN_OK
