@@ -58,8 +58,10 @@ TreePlan tree_plan(const gdn_tree_problem& p);
 struct TreeShape {
     int rows, tok, ctas;
 };
-TreeShape tree_shape_simt(int D);
-cudaError_t launch_tree_simt(const TreeArgs& A, const TreePlan& plan, cudaStream_t st);
+cudaError_t launch_tree_bf16(const TreeArgs& A, const TreePlan& plan, cudaStream_t st);
+cudaError_t launch_tree_f8(const TreeArgs& A, const TreePlan& plan, cudaStream_t st);
+int tree_status_bf16();
+int tree_status_f8();
 cudaError_t launch_tree(const TreeArgs& A, cudaStream_t st);
 
 struct CacheArgs {

@@ -189,9 +189,10 @@ gdn_status gdn_prompt_attn_bwd(const gdn_prompt_problem* problem, const void* q,
 gdn_status gdn_attn_device_status(void* stream) try {
     const cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return done(e);
-    const int fwd = gdn::prompt_fwd_status(), bwd = gdn::prompt_bwd_status();
-    if (fwd < 0 || bwd < 0) return done(cudaGetLastError());
-    if (fwd || bwd) return fail(GDN_ERR_TIMEOUT, "a device-side wait gave up (%s%s )", fwd ? " forward" : "", bwd ? " backward" : "");
+    const int fwd = gdn::prompt_fwd_status(), bwd = gdn::prompt_bwd_status(), t16 = gdn::tree_status_bf16(), t8 = gdn::tree_status_f8();
+    if (fwd < 0 || bwd < 0 || t16 < 0 || t8 < 0) return done(cudaGetLastError());
+    if (fwd || bwd || t16 || t8)
+        return fail(GDN_ERR_TIMEOUT, "a device-side wait gave up (prompt%s%s, tree%s%s)", fwd ? " forward" : "", bwd ? " backward" : "", t16 ? " bf16" : "", t8 ? " 8 bits" : "");
     return done(cudaSuccess);
 } catch (...) {
     return no_host_memory();

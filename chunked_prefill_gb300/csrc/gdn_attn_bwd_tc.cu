@@ -328,6 +328,7 @@ __global__ void __launch_bounds__(Bwd<D, KEYS>::T, 1) k_prompt_bwd_tc(const Prom
 #pragma unroll 1
         for (int c = 0; c < cols; c += 32) {
             float x[32];
+            __syncwarp();
             if (NT > 0 && ok) {
                 tc::tmem_ld32(acc + c, x);
                 tc::tmem_ld_wait();
@@ -335,8 +336,8 @@ __global__ void __launch_bounds__(Bwd<D, KEYS>::T, 1) k_prompt_bwd_tc(const Prom
 #pragma unroll
                 for (int e = 0; e < 32; ++e) x[e] = 0.f;
             }
-            if (r >= rows) continue;
-            if (KEYS && parts > 1) {
+            if (r >= rows) {
+            } else if (KEYS && parts > 1) {
                 float* to32 = partial + ((int64_t(is_dv ? 0 : 1) * parts + part) * p.total_k * p.Hkv + out) * D + col0 + c;
 #pragma unroll
                 for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(to32 + e) = make_float4(x[e] * f, x[e + 1] * f, x[e + 2] * f, x[e + 3] * f);
@@ -429,11 +430,6 @@ int prompt_bwd_parts(const gdn_prompt_problem& p) {
 
 cudaError_t launch_prompt_bwd_tc(const PromptArgs& A, cudaStream_t st) { return A.p.D == 64 ? both<64>(A, st) : A.p.D == 128 ? both<128>(A, st) : both<256>(A, st); }
 
-int prompt_bwd_status() {
-    int x = 0, zero = 0;
-    if (cudaMemcpyFromSymbol(&x, g_gave_up, sizeof(x)) != cudaSuccess) return -1;
-    if (x) cudaMemcpyToSymbol(g_gave_up, &zero, sizeof(zero));
-    return x;
-}
+int prompt_bwd_status() { return take_gave_up(); }
 
 }  // namespace gdn

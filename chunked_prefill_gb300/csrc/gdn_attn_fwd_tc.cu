@@ -350,6 +350,7 @@ __global__ void __launch_bounds__(Fwd<D>::T, 1)
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
             float x[32];
+            __syncwarp();
             if (steps > 0 && ok) {
                 tc::tmem_ld32(mine + L::O + w * D + c, x);
                 tc::tmem_ld_wait();
@@ -408,11 +409,6 @@ cudaError_t launch_d(const PromptArgs& A, cudaStream_t st) {
 
 cudaError_t launch_prompt_fwd_tc(const PromptArgs& A, cudaStream_t st) { return A.p.D == 64 ? launch_d<64>(A, st) : A.p.D == 128 ? launch_d<128>(A, st) : launch_d<256>(A, st); }
 
-int prompt_fwd_status() {
-    int x = 0, zero = 0;
-    if (cudaMemcpyFromSymbol(&x, g_gave_up, sizeof(x)) != cudaSuccess) return -1;
-    if (x) cudaMemcpyToSymbol(g_gave_up, &zero, sizeof(zero));
-    return x;
-}
+int prompt_fwd_status() { return take_gave_up(); }
 
 }  // namespace gdn

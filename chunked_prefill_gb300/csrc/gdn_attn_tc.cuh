@@ -10,6 +10,14 @@ namespace {
 // Every wait of these kernels is bounded (2 s): one that gives up sets this, and the CTA winds down.
 __device__ int g_gave_up;
 
+// Whether one gave up since the last time; -1 where that cannot be asked.
+inline int take_gave_up() {
+    int x = 0, zero = 0;
+    if (cudaMemcpyFromSymbol(&x, g_gave_up, sizeof(x)) != cudaSuccess) return -1;
+    if (x && cudaMemcpyToSymbol(g_gave_up, &zero, sizeof(zero)) != cudaSuccess) return -1;
+    return x;
+}
+
 // a wait by a whole warp
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t phase) { return __all_sync(0xffffffffu, tc::mbar_wait(bar, phase)); }
 

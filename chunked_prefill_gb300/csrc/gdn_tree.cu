@@ -7,6 +7,8 @@
 // part of its group's list.  A block that lies in one CTA's part is written out by it; of others every CTA
 // leaves (accumulator, maximum, sum), and a second kernel joins them in the list's order.
 // v_scale goes into the weights of the cached tokens, so that drafted ones join them as they are.
+//
+// bf16 and 8-bit caches: k_tree_tc (gdn_tree_tc.cuh), on the tensor cores.  fp32: k_tree_simt, here.
 #include "gdn_attn_simt.cuh"
 #include "gdn_tree.cuh"
 
@@ -17,7 +19,7 @@ namespace {
 constexpr int TB = 64;
 template <int D> constexpr int tree_smem() { return (3 * TB * (D + 4) + TB * (TB + 4)) * 4; }
 
-template <typename Act, typename C, int D>
+template <int D>
 __global__ void __launch_bounds__(ST) k_tree_simt(const TreeArgs A) {
     constexpr int MI = TB / 16;
     extern __shared__ __align__(16) float sm[];
@@ -41,7 +43,7 @@ __global__ void __launch_bounds__(ST) k_tree_simt(const TreeArgs A) {
         for (int i = tid; i < TB * (D / 4); i += ST) {
             const int r = i / (D / 4), d = i % (D / 4) * 4, t = (r0 + r) / G, g = (r0 + r) % G;
             *reinterpret_cast<float4*>(Q + r * (D + 4) + d) =
-                r0 + r < all_rows ? ldg4(static_cast<const Act*>(A.q) + (int64_t(n) * p.T + t) * p.q_stride + int64_t(hk * G + g) * D + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+                r0 + r < all_rows ? ldg4(static_cast<const float*>(A.q) + (int64_t(n) * p.T + t) * p.q_stride + int64_t(hk * G + g) * D + d) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
         __syncthreads();
         float acc[MI][D / 16] = {}, m[MI], l[MI] = {};
@@ -59,8 +61,8 @@ __global__ void __launch_bounds__(ST) k_tree_simt(const TreeArgs A) {
             const bool drafted = tile == tiles - 1;
             const int t0 = R.base + tile * TB;
             if (drafted) {
-                load_rows<TB, D>(K, static_cast<const Act*>(A.k_new) + int64_t(n) * p.T * p.k_new_stride + int64_t(hk) * D, p.k_new_stride, p.T);
-                load_rows<TB, D>(V, static_cast<const Act*>(A.v_new) + int64_t(n) * p.T * p.v_new_stride + int64_t(hk) * D, p.v_new_stride, p.T);
+                load_rows<TB, D>(K, static_cast<const float*>(A.k_new) + int64_t(n) * p.T * p.k_new_stride + int64_t(hk) * D, p.k_new_stride, p.T);
+                load_rows<TB, D>(V, static_cast<const float*>(A.v_new) + int64_t(n) * p.T * p.v_new_stride + int64_t(hk) * D, p.v_new_stride, p.T);
             } else {
                 if (tid < TB) {
                     const int t = t0 + tid, page = t < R.len ? A.table[n * p.table_stride + A.page_div.of(t)] : -1;
@@ -73,8 +75,8 @@ __global__ void __launch_bounds__(ST) k_tree_simt(const TreeArgs A) {
                     float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
                     if (page >= 0) {
                         const int in = t - A.page_div.of(t) * p.page_size;
-                        k = ldg4(static_cast<const C*>(A.k_cache) + page * p.k_page_stride + in * p.k_token_stride + hk * p.k_head_stride + d);
-                        v = ldg4(static_cast<const C*>(A.v_cache) + page * p.v_page_stride + in * p.v_token_stride + hk * p.v_head_stride + d);
+                        k = ldg4(static_cast<const float*>(A.k_cache) + page * p.k_page_stride + in * p.k_token_stride + hk * p.k_head_stride + d);
+                        v = ldg4(static_cast<const float*>(A.v_cache) + page * p.v_page_stride + in * p.v_token_stride + hk * p.v_head_stride + d);
                     }
                     *reinterpret_cast<float4*>(K + r * (D + 4) + d) = k;
                     *reinterpret_cast<float4*>(V + r * (D + 4) + d) = v;
@@ -111,7 +113,7 @@ __global__ void __launch_bounds__(ST) k_tree_simt(const TreeArgs A) {
                 const int64_t at = (int64_t(n) * p.T + r / G) * p.Hq + hk * G + r % G;
 #pragma unroll
                 for (int v = 0; v < D / 64; ++v)
-                    st4(static_cast<Act*>(A.o) + at * D + 64 * v + 4 * tx, acc[i][4 * v] * f, acc[i][4 * v + 1] * f, acc[i][4 * v + 2] * f, acc[i][4 * v + 3] * f);
+                    st4(static_cast<float*>(A.o) + at * D + 64 * v + 4 * tx, acc[i][4 * v] * f, acc[i][4 * v + 1] * f, acc[i][4 * v + 2] * f, acc[i][4 * v + 3] * f);
                 if (A.lse && tx == 0) A.lse[at] = some ? (m[i] + log2f(sum)) * LN2 : -INFINITY;
             } else {
                 const int64_t at = place_of(blockIdx.x, began, TB) + ty + 16 * i;
@@ -124,31 +126,26 @@ __global__ void __launch_bounds__(ST) k_tree_simt(const TreeArgs A) {
     }
 }
 
-template <typename Act, typename C, int D>
+template <int D>
 cudaError_t simt(const TreeArgs& A, const TreePlan& plan, cudaStream_t st) {
-    cudaError_t e = smem_attr(k_tree_simt<Act, C, D>, tree_smem<D>());
+    cudaError_t e = smem_attr(k_tree_simt<D>, tree_smem<D>());
     if (e != cudaSuccess) return e;
     timing_begin("tree_attn", st);
-    k_tree_simt<Act, C, D><<<plan.ctas, ST, tree_smem<D>(), st>>>(A);
+    k_tree_simt<D><<<plan.ctas, ST, tree_smem<D>(), st>>>(A);
     timing_end(st);
     e = cudaGetLastError();
-    return e != cudaSuccess ? e : launch_tree_join<Act, D>(A, plan, st);
+    return e != cudaSuccess ? e : launch_tree_join<float, D>(A, plan, st);
 }
-template <typename Act, typename C>
-cudaError_t simt_type(const TreeArgs& A, const TreePlan& plan, cudaStream_t st) {
-    return A.p.D == 64 ? simt<Act, C, 64>(A, plan, st) : A.p.D == 128 ? simt<Act, C, 128>(A, plan, st) : simt<Act, C, 256>(A, plan, st);
+
+TreeShape shape_of(const gdn_tree_problem& p) {
+    if (p.dtype == GDN_FP32) return {TB, TB, p.D == 64 ? 2 : 1};
+    return {p.D <= 128 && p.T * (p.Hq / p.Hkv) > 128 ? 256 : 128, p.D == 256 ? 64 : 128, 1};
 }
 
 }  // namespace
 
-TreeShape tree_shape_simt(int D) { return {TB, TB, D == 64 ? 2 : 1}; }
-cudaError_t launch_tree_simt(const TreeArgs& A, const TreePlan& plan, cudaStream_t st) {
-    if (A.p.dtype == GDN_FP32) return simt_type<float, float>(A, plan, st);
-    return A.p.cache_dtype == GDN_BF16 ? simt_type<__nv_bfloat16, __nv_bfloat16>(A, plan, st) : simt_type<__nv_bfloat16, __nv_fp8_e4m3>(A, plan, st);
-}
-
 TreePlan tree_plan(const gdn_tree_problem& p) {
-    const TreeShape s = tree_shape_simt(p.D);
+    const TreeShape s = shape_of(p);
     TreePlan r;
     r.rows = s.rows;
     r.tok = s.tok;
@@ -169,6 +166,10 @@ TreePlan tree_plan(const gdn_tree_problem& p) {
     return r;
 }
 
-cudaError_t launch_tree(const TreeArgs& A, cudaStream_t st) { return launch_tree_simt(A, tree_plan(A.p), st); }
+cudaError_t launch_tree(const TreeArgs& A, cudaStream_t st) {
+    const TreePlan plan = tree_plan(A.p);
+    if (A.p.dtype == GDN_BF16) return A.p.cache_dtype == GDN_BF16 ? launch_tree_bf16(A, plan, st) : launch_tree_f8(A, plan, st);
+    return A.p.D == 64 ? simt<64>(A, plan, st) : A.p.D == 128 ? simt<128>(A, plan, st) : simt<256>(A, plan, st);
+}
 
 }  // namespace gdn

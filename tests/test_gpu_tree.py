@@ -155,6 +155,30 @@ def test_a_bad_value_reaches_only_those_who_see_it(gdn, cache):
         assert not torch.isfinite(ob[0, sees][:, :2, 7]).any()
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_every_8_bit_value(gdn, D):
+    """A cached token that takes all the weight: its value comes back as it is, each of the 256."""
+    every = torch.arange(256, dtype=torch.uint8, device="cuda").view(FP8)
+    N = 256 // min(D, 256)
+    v = every.view(torch.uint8).view(N, 1, 1, D).expand(N, 4, 1, D).contiguous().view(FP8)
+    k = torch.full((N, 4, 1, D), 8.0, device="cuda").to(FP8)
+    q = torch.full((N, 1, 1, D), 8.0, device="cuda", dtype=BF)
+    table = torch.arange(N, dtype=torch.int32, device="cuda").view(N, 1)
+    one = torch.ones(N, dtype=torch.int32, device="cuda")
+    o = gdn.paged_attention_tree(q, -q, torch.ones_like(q), k, v, table, one, one[:, None] * -1)  # the drafted token's weight: 0
+    want = every.float()
+    got = o.float().flatten()
+    assert torch.equal(torch.isnan(got), torch.isnan(want)) and torch.equal(torch.nan_to_num(got), torch.nan_to_num(want))
+
+
+@pytest.mark.parametrize("factor", [0.0, -1.0])
+def test_scales_that_are_zero_or_negative(gdn, factor):
+    x = make([300, 5, 0], 4, 4, 2, 64, 16, FP8, seed=11)
+    x["ks"] = x["ks"] * factor
+    x["vs"] = x["vs"] * factor
+    check(x, *call(gdn, x))
+
+
 def test_pages_out_of_range_and_long_lengths(gdn):
     x = make([100, 100, 64], 3, 4, 2, 64, 16, seed=6)
     x["table"][0, 2] = -1
@@ -227,3 +251,9 @@ def test_long_offsets(gdn):
     want = call(gdn, small)
     got = call(gdn, dict(small, k=k, v=v, table=far))
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_no_wait_gave_up(gdn):
+    for cache in (BF, FP8):
+        call(gdn, make([500, 0, 77], 9, 8, 2, 128, 16, cache))
+    assert gdn.gdn_attn_device_status() == gdn.GDN_OK
