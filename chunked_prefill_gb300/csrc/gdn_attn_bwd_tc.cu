@@ -124,20 +124,20 @@ __global__ void __launch_bounds__(Bwd<D, KEYS>::T, 1) k_prompt_bwd_tc(const Prom
             int tails = 0, n0 = 0, n1 = 0;
             for (int i = 0; i < NT; ++i) {
                 const int head = KEYS ? h0 + i / per_head : hk, at = str_at + tile_row(i);
-                if (i >= L::N0 && !(ok = tc::mbar_wait(&sh.empty0[i % L::N0], (i / L::N0 - 1) & 1))) break;
+                if (i >= L::N0 && !(ok = bounded_wait(&sh.empty0[i % L::N0], (i / L::N0 - 1) & 1))) break;
                 tc::mbar_expect_tx(&sh.full0[i % L::N0], L::STR);
                 for (int c = 0; c < D / 64; ++c) tc::tma_load_3d(mem + 2 * L::RES + (i % L::N0) * L::STR + c * (BN * 128), &M.str0, &sh.full0[i % L::N0], c * 64, head, at);
                 ++n0;
-                if (i >= L::N1 && !(ok = tc::mbar_wait(&sh.empty1[i % L::N1], (i / L::N1 - 1) & 1))) break;
+                if (i >= L::N1 && !(ok = bounded_wait(&sh.empty1[i % L::N1], (i / L::N1 - 1) & 1))) break;
                 tc::mbar_expect_tx(&sh.full1[i % L::N1], L::STR);
                 for (int c = 0; c < D / 64; ++c) tc::tma_load_3d(mem + 2 * L::RES + (L::N0 + i % L::N1) * L::STR + c * (BN * 128), &M.str1, &sh.full1[i % L::N1], c * 64, head, at);
                 ++n1;
                 if (tail(i)) tc::mbar_arrive(&sh.issued[tails++ & 3]);
             }
             if (!ok) {  // the copies in flight land before the CTA ends
-                for (int i = max(0, n0 - L::N0); i < n0; ++i) tc::mbar_wait(&sh.full0[i % L::N0], (i / L::N0) & 1);
-                for (int i = max(0, n1 - L::N1); i < n1; ++i) tc::mbar_wait(&sh.full1[i % L::N1], (i / L::N1) & 1);
-                tc::mbar_wait(&sh.res_full, 0);
+                for (int i = max(0, n0 - L::N0); i < n0; ++i) bounded_wait(&sh.full0[i % L::N0], (i / L::N0) & 1);
+                for (int i = max(0, n1 - L::N1); i < n1; ++i) bounded_wait(&sh.full1[i % L::N1], (i / L::N1) & 1);
+                bounded_wait(&sh.res_full, 0);
             }
         }
     } else if (warp == 10) {  // ---- the streamed queries' statistics, and rows behind the sequence
@@ -189,23 +189,23 @@ __global__ void __launch_bounds__(Bwd<D, KEYS>::T, 1) k_prompt_bwd_tc(const Prom
             auto s0 = [&](int i) { return ring0 + (i % L::N0) * L::STR; };
             auto s1 = [&](int i) { return ring1 + (i % L::N1) * L::STR; };
             auto first = [&](int i) {
-                ok = ok && tc::mbar_wait(&sh.full0[i % L::N0], (i / L::N0) & 1);
+                ok = ok && bounded_wait(&sh.full0[i % L::N0], (i / L::N0) & 1);
                 if (ok) scores(base, s0(i), L::S, &sh.s_ready);
             };
             auto second = [&](int i) {
-                ok = ok && tc::mbar_wait(&sh.full1[i % L::N1], (i / L::N1) & 1);
+                ok = ok && bounded_wait(&sh.full1[i % L::N1], (i / L::N1) & 1);
                 if (!ok) return;
                 scores(base + L::RES, s1(i), L::DP, &sh.dp_ready);
                 if (!KEYS) tc::commit(&sh.empty1[i % L::N1]);
             };
             int tails = 0;
-            ok = tc::mbar_wait(&sh.res_full, 0);
+            ok = bounded_wait(&sh.res_full, 0);
             first(0);
             second(0);
             for (int i = 0; i < NT && ok; ++i) {
-                if (!(ok = tc::mbar_wait(&sh.p_ready, i & 1))) break;
+                if (!(ok = bounded_wait(&sh.p_ready, i & 1))) break;
                 if (tail(i)) {
-                    if (!(ok = tc::mbar_wait(&sh.clean[tails & 3], (tails >> 2) & 1))) break;
+                    if (!(ok = bounded_wait(&sh.clean[tails & 3], (tails >> 2) & 1))) break;
                     ++tails;
                 }
                 if (KEYS) {
@@ -213,13 +213,13 @@ __global__ void __launch_bounds__(Bwd<D, KEYS>::T, 1) k_prompt_bwd_tc(const Prom
                     tc::commit(&sh.empty1[i % L::N1]);
                 }
                 if (i + 1 < NT) first(i + 1);
-                if (!(ok = ok && tc::mbar_wait(&sh.ds_ready, i & 1))) break;
+                if (!(ok = ok && bounded_wait(&sh.ds_ready, i & 1))) break;
                 sum(L::DP, s0(i), L::OUT1, i > 0);
                 tc::commit(&sh.empty0[i % L::N0]);
                 if (i + 1 < NT) second(i + 1);
             }
             tc::commit(ok ? &sh.done : &sh.drain);
-            if (!ok) tc::mbar_wait(&sh.drain, 0);  // the products in flight end before tensor memory is freed
+            if (!ok) bounded_wait(&sh.drain, 0);  // the products in flight end before tensor memory is freed
         }
     }
     if (warp < 8) {  // ---- weights: thread to a row, warpgroup to half of the columns

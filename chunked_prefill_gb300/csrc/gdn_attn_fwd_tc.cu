@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(Fwd<D>::T, 1)
             in_order<NQ>(k, [&](bool value, int j) {
                 for (int c = 0; c < NC; ++c, ++n) {
                     const int slot = n % SLOTS;
-                    if (n >= SLOTS && !tc::mbar_wait(&sh.empty[slot], (n / SLOTS - 1) & 1)) return ok = false;
+                    if (n >= SLOTS && !bounded_wait(&sh.empty[slot], (n / SLOTS - 1) & 1)) return ok = false;
                     tc::mbar_expect_tx(&sh.full[slot], L::PIECE);
                     for (int b = 0; b < DC / 64; ++b)
                         tc::tma_load_3d(base + NQ * L::QT + slot * L::PIECE + b * 16384, value ? &vm : &km, &sh.full[slot], c * DC + b * 64, hk, s.k0 + j * 128);
@@ -160,8 +160,8 @@ __global__ void __launch_bounds__(Fwd<D>::T, 1)
                 return true;
             });
             if (!ok) {  // the copies in flight land before the CTA ends
-                for (int i = n < SLOTS ? 0 : n - SLOTS; i < n; ++i) tc::mbar_wait(&sh.full[i % SLOTS], (i / SLOTS) & 1);
-                tc::mbar_wait(&sh.q_full, 0);
+                for (int i = n < SLOTS ? 0 : n - SLOTS; i < n; ++i) bounded_wait(&sh.full[i % SLOTS], (i / SLOTS) & 1);
+                bounded_wait(&sh.q_full, 0);
             }
         }
     } else if (warp == NQ * 4 + 2) {  // ---- cleaning
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(Fwd<D>::T, 1)
             int cleaned = 0;
             auto full = [&](bool value, int j, int c) {
                 const int n = place_in_ring<NQ>(k, value, j) * NC + c;
-                return ok = ok && tc::mbar_wait(&sh.full[n % SLOTS], (n / SLOTS) & 1);
+                return ok = ok && bounded_wait(&sh.full[n % SLOTS], (n / SLOTS) & 1);
             };
             auto at = [&](bool value, int j, int c) { return ring + (place_in_ring<NQ>(k, value, j) * NC + c) % SLOTS * L::PIECE; };
             auto release = [&](bool value, int j) {
@@ -215,21 +215,21 @@ __global__ void __launch_bounds__(Fwd<D>::T, 1)
 #pragma unroll
                     for (int x = 0; x < 128; x += 16) tc::mma_bf16_ta(tmem + L::O + w * D + c * DC, tmem + buf * 128 + x / 2, desc_mn<128>(b, x), IO, more || x > 0);
                 }
-                tc::commit(&sh.pv_done[w]);
+                tc::commit(&sh.pv_done[buf]);
             };
-            ok = tc::mbar_wait(&sh.q_full, 0);
+            ok = bounded_wait(&sh.q_full, 0);
             if (NQ == 2) {
                 for (int w = 0; w < NQ; ++w)
                     if (ok && k.in(w, k.lo)) scores(w, k.lo, w);
                 release(false, k.lo);
                 for (int j = k.lo; j < k.hi && ok; ++j) {
                     if (special(p, s, k, j)) {
-                        ok = tc::mbar_wait(&sh.clean[cleaned], 0);
+                        ok = bounded_wait(&sh.clean[cleaned], 0);
                         ++cleaned;
                     }
                     for (int w = 0; w < NQ && ok; ++w) {
                         if (k.in(w, j)) {
-                            ok = tc::mbar_wait(&sh.p_ready[w], (j - k.begin[w]) & 1);
+                            ok = bounded_wait(&sh.p_ready[w], (j - k.begin[w]) & 1);
                             if (ok) values(w, j, w, j > k.begin[w]);
                         }
                         if (ok && j + 1 < k.hi && k.in(w, j + 1)) scores(w, j + 1, w);
@@ -245,10 +245,10 @@ __global__ void __launch_bounds__(Fwd<D>::T, 1)
                 for (int j = k.lo; j < k.hi && ok; ++j) {
                     const int i = j - k.lo;
                     if (special(p, s, k, j)) {
-                        ok = tc::mbar_wait(&sh.clean[cleaned], 0);
+                        ok = bounded_wait(&sh.clean[cleaned], 0);
                         ++cleaned;
                     }
-                    ok = ok && tc::mbar_wait(&sh.p_ready[i & 1], (i >> 1) & 1);
+                    ok = ok && bounded_wait(&sh.p_ready[i & 1], (i >> 1) & 1);
                     if (ok) values(0, j, i & 1, j > k.lo);
                     release(true, j);
                     if (ok && j + 2 < k.hi) {
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(Fwd<D>::T, 1)
             }
             if (!ok) {  // the products in flight end before tensor memory is freed
                 tc::commit(&sh.drain);
-                tc::mbar_wait(&sh.drain, 0);
+                bounded_wait(&sh.drain, 0);
             }
         }
     }
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(Fwd<D>::T, 1)
             if (__any_sync(0xffffffffu, top > m + 8.f)) {
                 if (i > 0) {
                     const float f = top == -INFINITY ? 1.f : ex2(m - top);
-                    if (!(ok = warp_wait(&sh.pv_done[w], (i - 1) & 1))) break;
+                    if (!(ok = warp_wait(&sh.pv_done[NQ == 2 ? w : (i - 1) & 1], (NQ == 2 ? i - 1 : (i - 1) >> 1) & 1))) break;
                     tc::fence_after_sync();
 #pragma unroll 1
                     for (int c = 0; c < D; c += 32) {
@@ -336,10 +336,10 @@ __global__ void __launch_bounds__(Fwd<D>::T, 1)
         }
         const int steps = k.end[w] - k.begin[w];
         if (ok && steps > 0) {
-            // with one query tile the scores run two tiles ahead: the last product but one may not be done yet, and its
-            // phase has to be passed first
-            if (NQ == 1 && steps > 1) ok = warp_wait(&sh.pv_done[w], steps & 1);
-            ok = ok && warp_wait(&sh.pv_done[w], (steps - 1) & 1);
+            // With one query tile the scores run two tiles ahead and the last two products may both be open, or both done:
+            // each has a barrier of its own, for a phase that another has followed can no longer be waited for.
+            const int l_tile = steps - 1;
+            ok = ok && warp_wait(&sh.pv_done[NQ == 2 ? w : l_tile & 1], (NQ == 2 ? l_tile : l_tile >> 1) & 1);
             tc::fence_after_sync();
         }
         const bool some = ok && (l > 0.f || l != l);

@@ -18,8 +18,19 @@ inline int take_gave_up() {
     return x;
 }
 
-// a wait by a whole warp
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t phase) { return __all_sync(0xffffffffu, tc::mbar_wait(bar, phase)); }
+// A wait that gives up after 4e9 cycles (2 s).
+__device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t phase) {
+    if (tc::mbar_try_wait(bar, phase)) return true;
+    const long long t0 = clock64();
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i)
+            if (tc::mbar_try_wait(bar, phase)) return true;
+        if (clock64() - t0 > 4000000000ll) return false;
+    }
+}
+// by a whole warp
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t phase) { return __all_sync(0xffffffffu, bounded_wait(bar, phase)); }
 
 // 32 lanes x 32 columns from v[0 .. 31]
 __device__ __forceinline__ void tmem_st32u(uint32_t taddr, const uint32_t* v) {
