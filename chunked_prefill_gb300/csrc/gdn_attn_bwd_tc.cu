@@ -171,55 +171,65 @@ __global__ void __launch_bounds__(Bwd<D, KEYS>::T, 1) k_prompt_bwd_tc(const Prom
             }
         }
     } else if (warp == 8) {  // ---- products
-        if (lane == 0) {
+        {
+            const bool el = elected();
+            const uint32_t tm = same(tmem);
+            const int NTu = same(NT), tail_from = same(per_head - (tail(per_head - 1) ? 1 : 0)), per_u = same(per_head), half_u = same(half);
             constexpr uint32_t IS = tc::make_idesc(128, BN, 0, 0), IO = tc::make_idesc(128, ND, 0, 1);
             auto scores = [&](uint32_t res, uint32_t str, uint32_t to, uint64_t* bar) {
                 tc::fence_after_sync();
+                const uint64_t a = desc_k<128>(res, 0), b = desc_k<BN>(str, 0);
+                if (el) {
 #pragma unroll
-                for (int x = 0; x < D; x += 16) tc::mma_bf16(tmem + to, desc_k<128>(res, x), desc_k<BN>(str, x), IS, x > 0);
-                tc::commit(bar);
+                    for (int x = 0; x < D; x += 16) tc::mma_bf16(tm + to, step_k<128>(a, x), step_k<BN>(b, x), IS, x > 0);
+                    tc::commit(bar);
+                }
             };
             // columns [0, CW) of the left operand lie at `from`, the others BN / 2 columns on
             auto sum = [&](uint32_t from, uint32_t str, uint32_t to, bool more) {
                 tc::fence_after_sync();
+                const uint64_t b = desc_mn<BN>(str + half_u * (ND / 64) * (BN * 128), 0);
+                if (el)
 #pragma unroll
-                for (int x = 0; x < BN; x += 16)
-                    tc::mma_bf16_ta(tmem + to, tmem + from + (x < CW ? 0 : CW) + (x % CW) / 2, desc_mn<BN>(str + half * (ND / 64) * (BN * 128), x), IO, more || x > 0);
+                    for (int x = 0; x < BN; x += 16) tc::mma_bf16_ta(tm + to, tm + from + (x < CW ? 0 : CW) + (x % CW) / 2, step_mn(b, x), IO, more || x > 0);
             };
             auto s0 = [&](int i) { return ring0 + (i % L::N0) * L::STR; };
             auto s1 = [&](int i) { return ring1 + (i % L::N1) * L::STR; };
             auto first = [&](int i) {
-                ok = ok && bounded_wait(&sh.full0[i % L::N0], (i / L::N0) & 1);
+                ok = ok && warp_spin(&sh.full0[i % L::N0], (i / L::N0) & 1);
                 if (ok) scores(base, s0(i), L::S, &sh.s_ready);
             };
             auto second = [&](int i) {
-                ok = ok && bounded_wait(&sh.full1[i % L::N1], (i / L::N1) & 1);
+                ok = ok && warp_spin(&sh.full1[i % L::N1], (i / L::N1) & 1);
                 if (!ok) return;
                 scores(base + L::RES, s1(i), L::DP, &sh.dp_ready);
-                if (!KEYS) tc::commit(&sh.empty1[i % L::N1]);
+                if (!KEYS && el) tc::commit(&sh.empty1[i % L::N1]);
             };
             int tails = 0;
-            ok = bounded_wait(&sh.res_full, 0);
+            ok = warp_spin(&sh.res_full, 0);
             first(0);
             second(0);
-            for (int i = 0; i < NT && ok; ++i) {
-                if (!(ok = bounded_wait(&sh.p_ready, i & 1))) break;
-                if (tail(i)) {
-                    if (!(ok = bounded_wait(&sh.clean[tails & 3], (tails >> 2) & 1))) break;
+            int in_head = 0;
+            for (int i = 0; i < NTu && ok; ++i) {
+                if (!(ok = warp_spin(&sh.p_ready, i & 1))) break;
+                const bool is_tail = in_head >= tail_from;
+                if (++in_head == per_u) in_head = 0;
+                if (is_tail) {
+                    if (!(ok = warp_spin(&sh.clean[tails & 3], (tails >> 2) & 1))) break;
                     ++tails;
                 }
                 if (KEYS) {
                     sum(L::S, s1(i), L::OUT0, i > 0);
-                    tc::commit(&sh.empty1[i % L::N1]);
+                    if (el) tc::commit(&sh.empty1[i % L::N1]);
                 }
-                if (i + 1 < NT) first(i + 1);
-                if (!(ok = ok && bounded_wait(&sh.ds_ready, i & 1))) break;
+                if (i + 1 < NTu) first(i + 1);
+                if (!(ok = ok && warp_spin(&sh.ds_ready, i & 1))) break;
                 sum(L::DP, s0(i), L::OUT1, i > 0);
-                tc::commit(&sh.empty0[i % L::N0]);
-                if (i + 1 < NT) second(i + 1);
+                if (el) tc::commit(&sh.empty0[i % L::N0]);
+                if (i + 1 < NTu) second(i + 1);
             }
-            tc::commit(ok ? &sh.done : &sh.drain);
-            if (!ok) bounded_wait(&sh.drain, 0);  // the products in flight end before tensor memory is freed
+            if (el) tc::commit(ok ? &sh.done : &sh.drain);
+            if (!ok) warp_spin(&sh.drain, 0);  // the products in flight end before tensor memory is freed
         }
     }
     if (warp < 8) {  // ---- weights: thread to a row, warpgroup to half of the columns
@@ -343,8 +353,7 @@ __global__ void __launch_bounds__(Bwd<D, KEYS>::T, 1) k_prompt_bwd_tc(const Prom
                 for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(to32 + e) = make_float4(x[e] * f, x[e + 1] * f, x[e + 2] * f, x[e + 3] * f);
             } else {
                 __nv_bfloat16* to16 = static_cast<__nv_bfloat16*>(KEYS ? (is_dv ? A.dv : A.dk) : A.dq) + out * D + col0 + c;
-                store_bf16x16(to16, x, f);
-                store_bf16x16(to16 + 16, x + 16, f);
+                store_bf16x32(to16, x, f, wide_aligned(to16));
             }
         }
     }

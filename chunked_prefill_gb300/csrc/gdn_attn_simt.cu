@@ -66,21 +66,40 @@ __global__ void __launch_bounds__(ST) k_prompt_fwd_simt(const PromptArgs A) {
     }
 }
 
-// ---- the queries' statistics for the gradient: a warp to a (row, head)
-template <typename T>
+// ---- the queries' statistics for the gradient: a block to 64 rows of a head, D / 8 lanes (fp32: D / 4) to a row, so that
+// the statistics' rows are written whole
+template <typename T, int D>
 __global__ void __launch_bounds__(256) k_prompt_stat(const PromptArgs A) {
+    constexpr int V = 16 / int(sizeof(T)), LPR = D / V < 32 ? D / V : 32, PER = D / V / LPR, R = 256 / LPR, U = 64 / R;  // rows at a time, times
     const gdn_prompt_problem& p = A.p;
-    const int64_t at = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (at >= int64_t(p.total_q) * p.Hq) return;
-    const T *o = static_cast<const T*>(A.o_in) + at * p.D, *g = static_cast<const T*>(A.dO) + at * p.D;
-    float sum = 0.f;
-    for (int d = lane * 2; d < p.D; d += 64) sum = fmaf(to_f(o[d]), to_f(g[d]), fmaf(to_f(o[d + 1]), to_f(g[d + 1]), sum));
+    const int h = blockIdx.x % p.Hq, row0 = int(blockIdx.x / p.Hq) * 64, r = threadIdx.x / LPR, lane = threadIdx.x % LPR;
+    uint4 o[U * PER], g[U * PER];
 #pragma unroll
-    for (int w = 16; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-    if (lane == 0) {
-        const int64_t row = at / p.Hq, h = at - row * p.Hq;
-        A.stat[h * A.stat_rows + row] = make_float2(A.lse_in[at] * LOG2E, sum - (A.dlse ? A.dlse[at] : 0.f));
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int x = 0; x < PER; ++x) {
+            const int row = row0 + r + R * u;
+            const int64_t at = (int64_t(row) * p.Hq + h) * D + (x * LPR + lane) * V;
+            const bool in = row < p.total_q;
+            o[u * PER + x] = in ? *reinterpret_cast<const uint4*>(static_cast<const T*>(A.o_in) + at) : make_uint4(0u, 0u, 0u, 0u);
+            g[u * PER + x] = in ? *reinterpret_cast<const uint4*>(static_cast<const T*>(A.dO) + at) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        float sum = 0.f;
+#pragma unroll
+        for (int x = 0; x < PER; ++x) {
+            const T *a = reinterpret_cast<const T*>(&o[u * PER + x]), *b = reinterpret_cast<const T*>(&g[u * PER + x]);
+#pragma unroll
+            for (int e = 0; e < V; ++e) sum = fmaf(to_f(a[e]), to_f(b[e]), sum);
+        }
+#pragma unroll
+        for (int w = LPR / 2; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+        const int row = row0 + r + R * u;
+        if (lane == 0 && row < p.total_q) {
+            const int64_t at = int64_t(row) * p.Hq + h;
+            A.stat[h * A.stat_rows + row] = make_float2(A.lse_in[at] * LOG2E, sum - (A.dlse ? A.dlse[at] : 0.f));
+        }
     }
 }
 
@@ -243,13 +262,15 @@ size_t prompt_bwd_workspace(const gdn_prompt_problem& p) {
 }
 
 cudaError_t launch_prompt_stat(const PromptArgs& A, cudaStream_t st) {
-    const int64_t rows = int64_t(A.p.total_q) * A.p.Hq;
-    if (rows == 0) return cudaSuccess;
+    const int64_t blocks = (int64_t(A.p.total_q) + 63) / 64 * A.p.Hq;
+    if (blocks == 0) return cudaSuccess;
     timing_begin("prompt_attn_stat", st);
+    auto go = [&](auto kern) { kern<<<unsigned(blocks), 256, 0, st>>>(A); };
+    using B = __nv_bfloat16;
     if (A.p.dtype == GDN_FP32)
-        k_prompt_stat<float><<<unsigned((rows + 7) / 8), 256, 0, st>>>(A);
+        A.p.D == 64 ? go(k_prompt_stat<float, 64>) : A.p.D == 128 ? go(k_prompt_stat<float, 128>) : go(k_prompt_stat<float, 256>);
     else
-        k_prompt_stat<__nv_bfloat16><<<unsigned((rows + 7) / 8), 256, 0, st>>>(A);
+        A.p.D == 64 ? go(k_prompt_stat<B, 64>) : A.p.D == 128 ? go(k_prompt_stat<B, 128>) : go(k_prompt_stat<B, 256>);
     timing_end(st);
     return cudaGetLastError();
 }

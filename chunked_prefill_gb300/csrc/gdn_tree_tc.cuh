@@ -298,43 +298,52 @@ __global__ void __launch_bounds__(TreeTc<C, D, NQ>::T, 1) k_tree_tc(const TreeAr
             push((which >= 0 ? 1 + which : 0) | (drafted ? 4 : 0) | (queries ? 8 : 0));
         }
     } else if (warp == 8) {  // ---- products
-        if (lane == 0) {
+        {
+            const bool el = elected();
+            const uint32_t tm = same(tmem);
             constexpr uint32_t IS = tc::make_idesc(128, TOK, 0, 0), IO = tc::make_idesc(128, D, 0, 1);
             int g = 0, pair = 0;  // tiles and pairs before
             while (ok && it.next<L::ROWS, TOK>(A, nb)) {
-                const int nt = it.end - it.begin;
+                const int nt = same(it.end - it.begin);
                 auto slot_at = [&](int i, int value) { return ring + (2 * (g + i) + value) % SLOTS * L::SLOT; };
                 auto full = [&](int i, int value) {
                     const int n = 2 * (g + i) + value;
-                    return ok = ok && bounded_wait(&sh.full[n % SLOTS], (n / SLOTS) & 1);
+                    return ok = ok && warp_wait(&sh.full[n % SLOTS], (n / SLOTS) & 1);
                 };
-                auto release = [&](int i, int value) { tc::commit(&sh.empty[(2 * (g + i) + value) % SLOTS]); };
+                auto release = [&](int i, int value) {
+                    if (el) tc::commit(&sh.empty[(2 * (g + i) + value) % SLOTS]);
+                };
                 auto scores = [&](int w, int i) {
                     if (!full(i, 0)) return;
                     tc::fence_after_sync();
                     const int buf = NQ == 2 ? w : (g + i) & 1;
-                    const uint32_t a = q_at + w * (128 * D * 2), b = slot_at(i, 0);
+                    const uint64_t a = desc_k<128>(q_at + w * (128 * D * 2), 0), b = desc_k<TOK>(slot_at(i, 0), 0);
+                    if (el) {
 #pragma unroll
-                    for (int x = 0; x < D; x += 16) tc::mma_bf16(tmem + L::S + buf * TOK, desc_k<128>(a, x), desc_k<TOK>(b, x), IS, x > 0);
-                    tc::commit(&sh.s_ready[buf]);
+                        for (int x = 0; x < D; x += 16) tc::mma_bf16(tm + L::S + buf * TOK, step_k<128>(a, x), step_k<TOK>(b, x), IS, x > 0);
+                        tc::commit(&sh.s_ready[buf]);
+                    }
                     if (w == NQ - 1) {
                         release(i, 0);
-                        if (i == nt - 1) tc::commit(&sh.q_empty);
+                        if (i == nt - 1 && el) tc::commit(&sh.q_empty);
                     }
                 };
                 auto values = [&](int w, int i) {
                     const int buf = NQ == 2 ? w : (g + i) & 1;
-                    ok = ok && bounded_wait(&sh.p_ready[buf], (NQ == 2 ? g + i : (g + i) >> 1) & 1);
-                    if (i == 0 && w == 0 && pair > 0) ok = ok && bounded_wait(&sh.o_free, (pair - 1) & 1);
+                    ok = ok && warp_wait(&sh.p_ready[buf], (NQ == 2 ? g + i : (g + i) >> 1) & 1);
+                    if (i == 0 && w == 0 && pair > 0) ok = ok && warp_wait(&sh.o_free, (pair - 1) & 1);
                     if (!full(i, 1)) return;
                     tc::fence_after_sync();
-                    const uint32_t b = slot_at(i, 1);
+                    const uint64_t b = desc_mn<TOK>(slot_at(i, 1), 0);
+                    if (el) {
 #pragma unroll
-                    for (int x = 0; x < TOK; x += 16) tc::mma_bf16_ta(tmem + L::O + w * D, tmem + L::S + buf * TOK + x / L::CW * L::CW + x % L::CW / 2, desc_mn<TOK>(b, x), IO, i > 0 || x > 0);
-                    tc::commit(&sh.pv_done[buf]);
+                        for (int x = 0; x < TOK; x += 16)
+                            tc::mma_bf16_ta(tm + L::O + w * D, tm + L::S + buf * TOK + x / L::CW * L::CW + x % L::CW / 2, step_mn(b, x), IO, i > 0 || x > 0);
+                        tc::commit(&sh.pv_done[buf]);
+                    }
                     if (w == NQ - 1) release(i, 1);
                 };
-                ok = bounded_wait(&sh.q_full, pair & 1);
+                ok = warp_wait(&sh.q_full, pair & 1);
                 if (NQ == 2) {
                     for (int w = 0; w < NQ && ok; ++w) scores(w, 0);
                     for (int i = 0; i < nt && ok; ++i)
@@ -353,8 +362,8 @@ __global__ void __launch_bounds__(TreeTc<C, D, NQ>::T, 1) k_tree_tc(const TreeAr
                 ++pair;
             }
             if (!ok) {  // the products in flight end before tensor memory is freed
-                tc::commit(&sh.drain);
-                bounded_wait(&sh.drain, 0);
+                if (el) tc::commit(&sh.drain);
+                warp_wait(&sh.drain, 0);
             }
         }
     } else {  // ---- weights: thread to a row
@@ -548,8 +557,7 @@ __global__ void __launch_bounds__(TreeTc<C, D, NQ>::T, 1) k_tree_tc(const TreeAr
                     }
                 if (r >= all_rows) {
                 } else if (whole) {
-                    store_bf16x16(static_cast<__nv_bfloat16*>(A.o) + out * D + c, x, f);
-                    store_bf16x16(static_cast<__nv_bfloat16*>(A.o) + out * D + c + 16, x + 16, f);
+                    store_bf16x32(static_cast<__nv_bfloat16*>(A.o) + out * D + c, x, f, wide_aligned(A.o));
                 } else {
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(A.part + at * D + c + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
