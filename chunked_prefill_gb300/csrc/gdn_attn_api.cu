@@ -76,7 +76,7 @@ gdn_status check_cache(gdn_cache_problem& p) {
     if (p.count > 0x7fffffff) return fail(GDN_ERR_UNSUPPORTED, "more than 2^31 - 1 rows in one call");
     if (p.Hkv <= 0 || p.D <= 0) return fail(GDN_ERR_INVALID_ARG, "Hkv and D must be positive");
     if (p.D % 16) return fail(GDN_ERR_UNSUPPORTED, "D (%d) must be a multiple of 16", p.D);
-    if (int64_t(p.Hkv) * p.D > (1 << 24)) return fail(GDN_ERR_UNSUPPORTED, "rows of more than 2^24 values");
+    if (int64_t(p.Hkv) * p.D > (1 << 20)) return fail(GDN_ERR_UNSUPPORTED, "rows of more than 2^20 values");
     TRY(check_types(p.dtype, p.cache_dtype));
     if (p.page_size <= 0) return fail(GDN_ERR_INVALID_ARG, "page_size must be positive");
     const int64_t act = 16 / int64_t(elem(p.dtype));

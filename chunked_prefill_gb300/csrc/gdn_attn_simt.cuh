@@ -10,25 +10,13 @@ namespace {
 constexpr int ST = 256;
 
 __device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 ldg4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 ldg4(const __nv_bfloat16* p) {
-    const uint2 r = *reinterpret_cast<const uint2*>(p);
-    return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u), __uint_as_float(r.y << 16), __uint_as_float(r.y & 0xffff0000u));
-}
-__device__ __forceinline__ float4 ldg4(const __nv_fp8_e4m3* p) {
-    const uint32_t r = *reinterpret_cast<const uint32_t*>(p);
-    const __half2 a = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(r & 0xffffu), __NV_E4M3), b = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(r >> 16), __NV_E4M3);
-    const float2 x = __half22float2(a), y = __half22float2(b);
-    return make_float4(x.x, x.y, y.x, y.y);
-}
-
 // rows [0, R) of D values at `stride` into dst, zeros from `valid` on
-template <int R, int D, typename T>
-__device__ __forceinline__ void load_rows(float* dst, const T* src, int64_t stride, int valid) {
+template <int R, int D>
+__device__ __forceinline__ void load_rows(float* dst, const float* src, int64_t stride, int valid) {
 #pragma unroll 4
     for (int i = threadIdx.x; i < R * (D / 4); i += ST) {
         const int r = i / (D / 4), d = i % (D / 4) * 4;
-        *reinterpret_cast<float4*>(dst + r * (D + 4) + d) = r < valid ? ldg4(src + r * stride + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<float4*>(dst + r * (D + 4) + d) = r < valid ? ld4(src + r * stride + d) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 }
 
@@ -59,14 +47,14 @@ __device__ __forceinline__ void mul_nt(float (&c)[MI][NJ], const float* A, const
     }
 }
 
-// c[i][4 v + e] += sum_n P(ty + 16 i, n) V[n][64 v + 4 tx + e] over n < N, with P(r, n) = P[r ld + n], or
+// c[i][4 v + e] += sum_n P(ty + 16 i, n) V[n][64 v + 4 tx + e] over n < count, with P(r, n) = P[r ld + n], or
 // P[n ld + r] where TRANS.  counts(i, n): of a masked tile, whether row i's product with n counts at all
 // (a weight of 0 would make NaN of an infinite value).
-template <int MI, int N, int D, bool TRANS, bool MASKED, typename F>
-__device__ __forceinline__ void mul_add(float (&c)[MI][D / 16], const float* P, int ld, const float* V, F counts) {
+template <int MI, int D, bool TRANS, bool MASKED, typename F>
+__device__ __forceinline__ void mul_add(float (&c)[MI][D / 16], int count, const float* P, int ld, const float* V, F counts) {
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-#pragma unroll 2
-    for (int n = 0; n < N; ++n) {
+#pragma unroll 4
+    for (int n = 0; n < count; ++n) {
         float p[MI];
 #pragma unroll
         for (int i = 0; i < MI; ++i) p[i] = TRANS ? P[n * ld + ty + 16 * i] : P[(ty + 16 * i) * ld + n];
@@ -98,10 +86,6 @@ __device__ __forceinline__ float row_sum(float x) {
 }
 
 __device__ __forceinline__ void st4(float* p, float a, float b, float c, float d) { *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d); }
-__device__ __forceinline__ void st4(__nv_bfloat16* p, float a, float b, float c, float d) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(tc::pack_bf16(a, b), tc::pack_bf16(c, d));
-}
-
 // One step of a running softmax over a tile of BN keys: z scores in units of log 2 (-inf where masked), in
 // place of which the weights are left at P [BM][BN + 4]; statistics and accumulators follow.
 template <int MI, int NJ, int DV>

@@ -2,8 +2,7 @@
 // tables kept on the device from the requests' lengths.
 //
 // gdn_paged_cache_write moves every value once: bound by HBM for a prompt, by the launch for a few tokens.
-// A thread takes 16-byte pieces of the output, four at a time (their rows and slots are asked for together);
-// a block has as many tokens as give its 256 threads four pieces each, or one.
+// Up to 32 lanes have a token, whose slot and row they look up once, and four 16-byte pieces of the output each.
 //
 // gdn_page_table_extend and _trim are latency: one launch, in which every CTA sums the requests' needs for
 // itself (a scan over up to 8 requests a thread) and keeps the sums in shared memory, so that the tokens and
@@ -20,9 +19,9 @@ namespace {
 constexpr int WT = 256, WU = 4;
 
 struct WriteShape {
-    int tokens;             // of a block
-    int pieces, half;       // of a token; of its keys
-    FastDiv by_pieces, by_half, by_row, by_page;
+    int lanes;          // of a token
+    int pieces, half;   // of a token; of its keys
+    FastDiv by_row, by_page;
 };
 
 // x / s to the nearest: the quotient's estimate x r with r = 1 / s to the nearest, corrected by its exact remainder (Markstein,
@@ -38,26 +37,28 @@ template <typename A, typename C>
 __global__ void __launch_bounds__(WT) k_cache_write(const CacheArgs G, const WriteShape S) {
     constexpr int PV = 16 / int(sizeof(C)), LV = PV * int(sizeof(A)) / 16;  // 16-byte loads of a piece
     const gdn_cache_problem& p = G.p;
-    const int64_t token0 = int64_t(blockIdx.x) * S.tokens, places = p.num_pages * p.page_size;
-    const int items = int(min(int64_t(S.tokens), p.count - token0)) * S.pieces;
-    for (int i0 = threadIdx.x; i0 < items; i0 += WT * WU) {
+    const int per = WT / S.lanes, lane = threadIdx.x & (S.lanes - 1);
+    const int64_t n = int64_t(blockIdx.x) * per + threadIdx.x / S.lanes;
+    if (n >= p.count) return;
+    const int64_t row = G.rows ? G.rows[n] : n, slot = G.slots[n];
+    if (slot < 0 || slot >= p.num_pages * p.page_size || row < 0 || row >= p.num_rows) return;
+    const int64_t page = slot >> 31 ? slot / p.page_size : S.by_page.of(int(slot)), in = slot - page * p.page_size;
+    {
+        const A *k = static_cast<const A*>(G.k) + row * p.k_stride, *v = static_cast<const A*>(G.v) + row * p.v_stride;
+        C *kc = static_cast<C*>(G.k_cache) + page * p.k_page_stride + in * p.k_token_stride, *vc = static_cast<C*>(G.v_cache) + page * p.v_page_stride + in * p.v_token_stride;
         uint4 raw[WU][LV];
         C* to[WU];
         float scale[WU];
 #pragma unroll
         for (int u = 0; u < WU; ++u) {
-            const int i = i0 + u * WT;
+            const int r = (int(blockIdx.y) * WU + u) * S.lanes + lane;
             to[u] = nullptr;
             scale[u] = 1.f;
-            if (i >= items) continue;
-            const int t = S.by_pieces.of(i), r = i - t * S.pieces, second = S.by_half.of(r), at = r - second * S.half;
-            const int head = S.by_row.of(at), d = (at - head * (p.D / PV)) * PV;
-            const int64_t n = token0 + t, row = G.rows ? G.rows[n] : n, slot = G.slots[n];
-            if (slot < 0 || slot >= places || row < 0 || row >= p.num_rows) continue;
-            const int64_t page = slot >> 31 ? slot / p.page_size : S.by_page.of(int(slot)), in = slot - page * p.page_size;
-            const A* from = static_cast<const A*>(second ? G.v : G.k) + row * (second ? p.v_stride : p.k_stride) + int64_t(head) * p.D + d;
-            to[u] = static_cast<C*>(second ? G.v_cache : G.k_cache) + page * (second ? p.v_page_stride : p.k_page_stride) +
-                    in * (second ? p.v_token_stride : p.k_token_stride) + head * (second ? p.v_head_stride : p.k_head_stride) + d;
+            if (r >= S.pieces) continue;
+            const bool second = r >= S.half;
+            const int at = second ? r - S.half : r, head = S.by_row.of(at), d = (at - head * (p.D / PV)) * PV;
+            const A* from = (second ? v : k) + head * p.D + d;
+            to[u] = (second ? vc + head * p.v_head_stride : kc + head * p.k_head_stride) + d;
             const float* s = second ? G.v_scale : G.k_scale;
             if (s) scale[u] = s[head];
 #pragma unroll
@@ -97,15 +98,14 @@ cudaError_t write_as(const CacheArgs& G, cudaStream_t st) {
     WriteShape S;
     S.half = G.p.Hkv * (G.p.D / PV);
     S.pieces = 2 * S.half;
-    S.tokens = S.pieces >= WT * WU ? 1 : WT * WU / S.pieces;
-    // fewer tokens to a block where that is what gives every multiprocessor one
-    while (S.tokens > 1 && (G.p.count + S.tokens - 1) / S.tokens < sm_count_cached() && S.tokens * S.pieces > WT) S.tokens = (S.tokens + 1) / 2;
-    S.by_pieces.set(uint32_t(S.pieces));
-    S.by_half.set(uint32_t(S.half));
+    S.lanes = 32;
+    while (S.lanes > 2 && S.lanes / 2 >= S.pieces) S.lanes /= 2;
     S.by_row.set(uint32_t(G.p.D / PV));
     S.by_page.set(uint32_t(G.p.page_size));
+    const int per = WT / S.lanes;
+    const dim3 grid(unsigned((G.p.count + per - 1) / per), unsigned((S.pieces + WU * S.lanes - 1) / (WU * S.lanes)));
     timing_begin("paged_cache_write", st);
-    k_cache_write<A, C><<<unsigned((G.p.count + S.tokens - 1) / S.tokens), WT, 0, st>>>(G, S);
+    k_cache_write<A, C><<<grid, WT, 0, st>>>(G, S);
     timing_end(st);
     return cudaGetLastError();
 }

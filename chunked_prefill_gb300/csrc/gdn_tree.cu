@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(ST) k_tree_simt(const TreeArgs A) {
         for (int i = tid; i < TB * (D / 4); i += ST) {
             const int r = i / (D / 4), d = i % (D / 4) * 4, t = (r0 + r) / G, g = (r0 + r) % G;
             *reinterpret_cast<float4*>(Q + r * (D + 4) + d) =
-                r0 + r < all_rows ? ldg4(static_cast<const float*>(A.q) + (int64_t(n) * p.T + t) * p.q_stride + int64_t(hk * G + g) * D + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+                r0 + r < all_rows ? ld4(static_cast<const float*>(A.q) + (int64_t(n) * p.T + t) * p.q_stride + int64_t(hk * G + g) * D + d) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
         __syncthreads();
         float acc[MI][D / 16] = {}, m[MI], l[MI] = {};
@@ -75,8 +75,8 @@ __global__ void __launch_bounds__(ST) k_tree_simt(const TreeArgs A) {
                     float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
                     if (page >= 0) {
                         const int in = t - A.page_div.of(t) * p.page_size;
-                        k = ldg4(static_cast<const float*>(A.k_cache) + page * p.k_page_stride + in * p.k_token_stride + hk * p.k_head_stride + d);
-                        v = ldg4(static_cast<const float*>(A.v_cache) + page * p.v_page_stride + in * p.v_token_stride + hk * p.v_head_stride + d);
+                        k = ld4(static_cast<const float*>(A.k_cache) + page * p.k_page_stride + in * p.k_token_stride + hk * p.k_head_stride + d);
+                        v = ld4(static_cast<const float*>(A.v_cache) + page * p.v_page_stride + in * p.v_token_stride + hk * p.v_head_stride + d);
                     }
                     *reinterpret_cast<float4*>(K + r * (D + 4) + d) = k;
                     *reinterpret_cast<float4*>(V + r * (D + 4) + d) = v;
@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(ST) k_tree_simt(const TreeArgs A) {
                 for (int i = tid; i < TB * TB; i += ST) P[(i / TB) * (TB + 4) + i % TB] *= vs;
                 __syncthreads();
             }
-            mul_add<MI, TB, D, false, true>(acc, P, TB + 4, V, counts);
+            mul_add<MI, D, false, true>(acc, TB, P, TB + 4, V, counts);
         }
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
