@@ -63,6 +63,7 @@ gdn_status check_tree(gdn_tree_problem& p) {
     if (p.page_size <= 0) return fail(GDN_ERR_INVALID_ARG, "page_size must be positive");
     if (int64_t(p.max_pages) * p.page_size > 0x7ffe0000) return fail(GDN_ERR_UNSUPPORTED, "max_pages * page_size above 2^31 tokens");
     if (p.num_seqs > 65535) return fail(GDN_ERR_UNSUPPORTED, "more than 65535 sequences in one call");
+    if (p.num_pages > 0x7ffffffe) return fail(GDN_ERR_UNSUPPORTED, "2^31 - 1 pages or more");
     const int64_t act = 16 / int64_t(elem(p.dtype));
     TRY(check_stride("q_stride", p.q_stride, int64_t(p.Hq) * p.D, act));
     TRY(check_stride("k_new_stride", p.k_new_stride, int64_t(p.Hkv) * p.D, act));

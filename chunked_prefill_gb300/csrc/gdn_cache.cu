@@ -111,7 +111,7 @@ cudaError_t write_as(const CacheArgs& G, cudaStream_t st) {
 }
 
 // ---- page tables
-constexpr int TT_ = 1024, TPER = TABLE_SEQS / TT_;
+constexpr int TT_ = 1024;
 
 // What a CTA keeps of a request: extend: its first new token, its length before, the place on the stack of
 // its first new page (downwards), the pages that it takes (-1: refused); trim: pages given by the requests
@@ -148,11 +148,6 @@ __device__ __forceinline__ int stack_top(const TableArgs& A) {
 __device__ __forceinline__ int64_t length_of(const TableArgs& A, int n) {
     const int64_t len = A.lens[n], cap = int64_t(A.p.max_pages) * A.p.page_size;
     return len < 0 ? 0 : len < cap ? len : cap;
-}
-__device__ __forceinline__ uint32_t ctas_of_cluster() {
-    uint32_t x;
-    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(x));
-    return x;
 }
 __device__ __forceinline__ void cluster_barrier(bool several) {
     if (several)
@@ -205,7 +200,7 @@ __global__ void __launch_bounds__(TT_) k_table_extend(const TableArgs A, const F
             *A.free = int(top - given);
         }
     }
-    if (!FILL) return;
+    if constexpr (!FILL) return;
     // pages, a warp to a request
     for (int n = cta * (TT_ / 32) + (tid >> 5); n < N; n += ctas * (TT_ / 32)) {
         const Request r = req[n];

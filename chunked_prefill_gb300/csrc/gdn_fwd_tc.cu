@@ -1812,6 +1812,20 @@ bool make_tokens_map(CUtensorMap* m, const void* base, int D, int H, int64_t tok
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_pages_map(CUtensorMap* m, const void* base, int bytes, int D, int H, int page_size, int64_t pages, int64_t head, int64_t token, int64_t page, int rows) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    // the stride of a dimension of one has no meaning, and need not be one that a map may have
+    const int64_t dense = int64_t(D) * bytes;
+    const cuuint64_t dims[4] = {cuuint64_t(D), cuuint64_t(H), cuuint64_t(page_size), cuuint64_t(pages > 0 ? pages : 1)};
+    const cuuint64_t strides[3] = {cuuint64_t(H > 1 ? head * bytes : dense), cuuint64_t(page_size > 1 ? token * bytes : dense), cuuint64_t(pages > 1 ? page * bytes : dense)};
+    const cuuint32_t box[4] = {cuuint32_t(bytes == 1 ? D : 64), 1, cuuint32_t(rows), 1};
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    return fn(m, bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, bytes == 1 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 #ifdef GDN_TRACE
 extern "C" int gdn_debug_trace(unsigned long long* out) {
     return int(cudaMemcpyFromSymbol(out, g_trace, sizeof(g_trace)));

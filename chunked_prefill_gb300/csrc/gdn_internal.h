@@ -41,6 +41,9 @@ bool make_rows_map(CUtensorMap* m, const void* base, int64_t rows);
 // [tokens, H, D] bf16 with `stride` elements between tokens, viewed as (d, head, token), box 64 x 1 x rows,
 // 128-byte swizzle.
 bool make_tokens_map(CUtensorMap* m, const void* base, int D, int H, int64_t tokens, int64_t stride, int rows);
+// A paged cache's pages, bf16 (bytes = 2: box 64 x 1 x rows x 1, 128-byte swizzle) or 8 bits (1: D x 1 x rows x 1, no
+// swizzle), viewed as (d, head, token of the page, page); strides in elements.
+bool make_pages_map(CUtensorMap* m, const void* base, int bytes, int D, int H, int page_size, int64_t pages, int64_t head, int64_t token, int64_t page, int rows);
 // Chunk-parallel preparation of the tensor-core path into P.prep: per (chunk, v-head) one
 // record of P.prep_stride bytes holding W' = -T diag(beta e) K (bf16 64 x 128, two
 // 128-byte-swizzled 64-column blocks), TU = T diag(beta) and P (bf16 64 x 64, swizzled), and

@@ -6,9 +6,11 @@
 // a thread to a row makes weights of it in place, O += P V with P read from tensor memory, O rescaled only where a
 // maximum has grown by more than 2^8.  A row is read twice from tensor memory, once for its maximum, in pieces of 32
 // values: the registers are the loading warps'.
-// Pages lie anywhere, so those warps copy rows in 16-byte pieces (cp.async) straight into the swizzled tiles that the
-// tensor cores read; of 8-bit caches into a ring of their own, from where every thread widens the pieces it copied
-// itself to bf16 (exactly).  Tokens without a page, and those behind the sequence, become zeros.
+// Pages lie anywhere, but their rows are at regular distances: TMA brings pieces of up to 16 tokens (the largest power of
+// two that divides the page size), issued by the lanes of one warp, straight into the swizzled tiles that the tensor cores
+// read; of 8-bit caches into a ring of their own, from where six warps widen them to bf16 (exactly).  A page number out of
+// range is replaced by one past the last, which TMA reads as zeros.  (Copied by cp.async, in 16-byte pieces by 128 to 224
+// threads, 32 sequences of up to 8192 tokens took 190 us: a tile's addresses alone kept those threads busy.)
 // Where some row masks a token that others see (drafted tokens, the edge of a window) infinite and NaN values are made
 // zeros, for a weight of 0 would make NaN of them, and are added at the end to the rows that see them.
 // Bound: HBM, up to some 128 rows to a kv-head with bf16; the tensor cores and the widening beyond.
@@ -25,23 +27,28 @@ template <typename C, int D, int NQ> struct TreeTc {
     static constexpr int ROWS = NQ * 128;
     static constexpr int QB = ROWS * D * 2;              // bytes of the queries
     static constexpr int SLOT = TOK * D * 2;             // of a tile of keys or values
-    static constexpr int NL = 224, NLW = NL / 32;        // loading threads, warps: with the others 16 warps, 128 registers a thread
-    static constexpr int STG = E == 1 ? 3 : 0, STGB = TOK * D;    // 8-bit tiles on their way
-    static constexpr int FIT = (228352 - QB - STG * STGB) / SLOT, SLOTS = FIT < 6 ? FIT : 6;
-    static constexpr int LAG = 1;                         // tiles requested ahead of the one handed over
+    static constexpr int NH = E == 1 ? 6 : 2;            // helping warps: widening; cleaning
+    static constexpr int STG = E == 1 ? 3 : 0, STGB = TOK * (D < 128 ? 128 : D);  // 8-bit tiles on their way (a piece begins at 128 bytes)
+    static constexpr int FIT = (225280 - QB - STG * STGB) / SLOT, SLOTS = FIT < 8 ? FIT : 8;
     static constexpr int SMEM = 1024 + QB + SLOTS * SLOT + STG * STGB;
-    static constexpr int T = 256 + 32 + NL;               // 8 warps of weights, then products, loads
+    static constexpr int T = 256 + 64 + 32 * NH;          // 8 warps of weights, then products, loads, helping ones
     static constexpr int CW = NQ == 2 ? TOK : TOK / 2;   // columns of a thread: with one tile of rows the two warpgroups share them
     static constexpr int S = 0, O = 2 * TOK;             // tensor memory columns
-    static constexpr int CPR = D * E / 16, PIECES = TOK * CPR, U = (PIECES + NL - 1) / NL;  // 16-byte pieces of a row, of a tile, of a thread at most
     static_assert(SLOTS >= 3 && O + NQ * D <= 512, "");
 };
+constexpr int CLEAN = 8;  // tiles of values to be cleaned on their way at a time: each holds a place in the ring
 
-template <int TOK> struct TreeShared {
-    uint64_t full[6], empty[6], q_full, q_empty, s_ready[2], p_ready[2], pv_done[2], o_free, met[4], drain;
-    int64_t off[2][TOK][2];
+struct TreeMaps {
+    CUtensorMap k, v, k_new, v_new;
+};
+
+struct TreeShared {
+    uint64_t full[8], empty[8], stage_full[4], stage_empty[4], issued[CLEAN], clean[CLEAN], q_full, q_empty, s_ready[2], p_ready[2], pv_done[2], o_free, met[4], drain;
     uint32_t counts[8][4];   // which tokens of a cached tile count
-    uint32_t bad[4][3][4];   // of the last pairs: tokens of the first two cached tiles and of the drafted ones with bad values
+    // Of the last pairs (more than the ring holds): which had infinite or NaN values, and of the first two cached tiles and the
+    // drafted tokens which tokens, as each helping warp found them.
+    int bad_pair[8];
+    uint32_t bad[8][3][6][4];
     float shared[2][2][128]; // what a row's two threads tell one another
     uint32_t tmem;
 };
@@ -58,12 +65,12 @@ __device__ __forceinline__ void widen(uint32_t v, uint32_t& lo, uint32_t& hi) {
 }
 // the bytes that are NaN, in their uppermost bits
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t v) { return ((v & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
-__device__ __forceinline__ void widen_nan(uint32_t v, uint32_t& lo, uint32_t& hi) {
-    const uint32_t nan = nan_bytes(v);
-    if (nan & 0x80u) lo |= 0x00007fffu;
-    if (nan & 0x8000u) lo |= 0x7fff0000u;
-    if (nan & 0x800000u) hi |= 0x00007fffu;
-    if (nan & 0x80000000u) hi |= 0x7fff0000u;
+__device__ __forceinline__ void widen_nan(uint32_t v, uint32_t& lo, uint32_t& hi, bool zero) {
+    const uint32_t nan = nan_bytes(v), to = zero ? 0u : 0x7fff7fffu;
+    if (nan & 0x80u) lo = (lo & 0xffff0000u) | (to & 0xffffu);
+    if (nan & 0x8000u) lo = (lo & 0xffffu) | (to & 0xffff0000u);
+    if (nan & 0x800000u) hi = (hi & 0xffff0000u) | (to & 0xffffu);
+    if (nan & 0x80000000u) hi = (hi & 0xffffu) | (to & 0xffff0000u);
 }
 
 // The (sequence, block) pairs of a CTA's part of the list, one after another.
@@ -89,12 +96,50 @@ struct Pairs {
     }
 };
 
+__device__ __forceinline__ void mark(uint32_t (&bad)[4], int row) {
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+        if (row >> 5 == w) bad[w] |= 1u << (row & 31);
+}
+// By one of `parts` warps: of a swizzled tile of R rows x D bf16 values, rows outside [from, to) become zeros, and with
+// `values` infinite and NaN values of the others too, their rows marked in `bad`.  As clean_tile.
+template <int R, int D>
+__device__ __forceinline__ void clean_rows(uint32_t tile, int from, int to, int part, int parts, bool values, uint32_t (&bad)[4]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int i0 = 8 * part; i0 < R * D / 256; i0 += 8 * parts) {  // 4 rows of 64 columns at a time
+        const uint32_t at = tile + i0 * 512 + lane * 16;
+        const int row0 = (i0 * 4 + (lane >> 3)) % R;
+        uint32_t any = 0;
+        if (values) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const uint4 v = tc::lds128(at + x * 512);
+                any |= ((v.x & 0x7f807f80u) + 0x00800080u) | ((v.y & 0x7f807f80u) + 0x00800080u) | ((v.z & 0x7f807f80u) + 0x00800080u) | ((v.w & 0x7f807f80u) + 0x00800080u);
+            }
+        }
+        if (!(any & 0x80008000u) && row0 >= from && row0 + 28 < to) continue;
+#pragma unroll 1
+        for (int x = 0; x < 8; ++x) {
+            const int row = row0 + 4 * x;
+            const uint4 v = tc::lds128(at + x * 512);
+            if (row < from || row >= to) {
+                tc::sts128(at + x * 512, make_uint4(0u, 0u, 0u, 0u));
+            } else if (values && (bad_pair(v.x) || bad_pair(v.y) || bad_pair(v.z) || bad_pair(v.w))) {
+                tc::sts128(at + x * 512, make_uint4(clean_pair(v.x), clean_pair(v.y), clean_pair(v.z), clean_pair(v.w)));
+                mark(bad, row);
+            }
+        }
+    }
+}
+
+// log_rows: of the pieces of a page that are copied at a time, 2^log_rows rows
 template <typename C, int D, int NQ>
-__global__ void __launch_bounds__(TreeTc<C, D, NQ>::T, 1) k_tree_tc(const TreeArgs A) {
+__global__ void __launch_bounds__(TreeTc<C, D, NQ>::T, 1) k_tree_tc(const TreeArgs A, const __grid_constant__ TreeMaps M, int log_rows) {
     using L = TreeTc<C, D, NQ>;
-    constexpr int TOK = L::TOK, SLOTS = L::SLOTS, NL = L::NL;
+    constexpr int TOK = L::TOK, SLOTS = L::SLOTS, NH = L::NH, STG = L::STG ? L::STG : 1;
     extern __shared__ unsigned char raw[];
-    __shared__ __align__(16) TreeShared<TOK> sh;
+    __shared__ __align__(16) TreeShared sh;
     const gdn_tree_problem& p = A.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = p.Hq / p.Hkv, all_rows = p.T * G, nb = (all_rows + L::ROWS - 1) / L::ROWS;
     tc::pdl_launch_dependents();
@@ -106,10 +151,18 @@ __global__ void __launch_bounds__(TreeTc<C, D, NQ>::T, 1) k_tree_tc(const TreeAr
     if (warp == 8) tc::tmem_alloc(&sh.tmem, 512);
     if (tid == 0) {
         for (int i = 0; i < SLOTS; ++i) {
-            tc::mbar_init(&sh.full[i], L::NLW);
+            tc::mbar_init(&sh.full[i], L::E == 1 ? NH : 1);
             tc::mbar_init(&sh.empty[i], 1);
         }
-        tc::mbar_init(&sh.q_full, L::NLW);
+        for (int i = 0; i < 4; ++i) {
+            tc::mbar_init(&sh.stage_full[i], 1);
+            tc::mbar_init(&sh.stage_empty[i], NH);
+        }
+        for (int i = 0; i < CLEAN; ++i) {
+            tc::mbar_init(&sh.issued[i], 1);
+            tc::mbar_init(&sh.clean[i], NH);
+        }
+        tc::mbar_init(&sh.q_full, 8);
         tc::mbar_init(&sh.q_empty, 1);
         for (int b = 0; b < 2; ++b) {
             tc::mbar_init(&sh.s_ready[b], 1);
@@ -120,6 +173,7 @@ __global__ void __launch_bounds__(TreeTc<C, D, NQ>::T, 1) k_tree_tc(const TreeAr
         for (int i = 0; i < 4; ++i) tc::mbar_init(&sh.met[i], 2);
         tc::mbar_init(&sh.drain, 1);
         tc::mbar_fence_init();
+        for (int i = 0; i < 8; ++i) sh.bad_pair[i] = -1;
     }
     tc::fence_before_sync();
     __syncthreads();
@@ -127,188 +181,194 @@ __global__ void __launch_bounds__(TreeTc<C, D, NQ>::T, 1) k_tree_tc(const TreeAr
     const uint32_t tmem = sh.tmem;
     bool ok = true;
 
-    if (warp > 8) {  // ---- loads
-        const int lt = tid - 288;
-        // where piece u of this thread goes: row, piece of the row
-        auto row_of = [&](int u) { return (lt + NL * u) / L::CPR; };
-        auto piece_of = [&](int u) { return (lt + NL * u) % L::CPR; };
-        auto swizzled = [&](uint32_t slot, int row, int pc) { return slot + (pc >> 3) * (TOK * 128) + row * 128 + (((pc & 7) ^ (row & 7)) << 4); };
-        auto hand_over = [&](uint64_t* bar) {
-            tc::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(bar);
-        };
-        // infinite and NaN values out of a piece that has just been read
-        auto clean = [&](uint4& x, int row, uint32_t (*bad)[4], int which) {
-            if (!(bad_pair(x.x) || bad_pair(x.y) || bad_pair(x.z) || bad_pair(x.w))) return false;
-            x = make_uint4(clean_pair(x.x), clean_pair(x.y), clean_pair(x.z), clean_pair(x.w));
-            atomicOr(&bad[which][row >> 5], 1u << (row & 31));
-            return true;
-        };
-        int issued = 0, handed = 0, pair = -1, tile_count = -1;
-        uint64_t codes = 0;  // of the groups on their way, oldest lowest: 4 bits, 1 + which tile of values to clean; 0: none; + 4: bf16 already; + 8: the pair's queries with them
-        uint32_t bads = 0;   // their pairs' places in sh.bad, 2 bits each
-        auto finish = [&]() {  // the oldest group
-            const int n = handed++, code = int(codes & 15), which = (code & 3) - 1, slot = n % SLOTS;
-            uint32_t(*bad)[4] = sh.bad[bads & 3];
-            codes >>= 4;
-            bads >>= 2;
-            const uint32_t to = ring + slot * L::SLOT;
-            if (L::E == 1 && !(code & 4)) {
-                if (n >= SLOTS && ok) ok = warp_wait(&sh.empty[slot], (n / SLOTS - 1) & 1);
-                if (!ok) return;
-                // not unrolled further: the loading warps' code and the weights' share the instruction cache (8 times: 450
-                // cycles to a piece)
-#pragma unroll 2
-                for (int u = 0; u < L::U; ++u) {
-                    if (u * NL + lt >= L::PIECES) break;
-                    const uint4 v = tc::lds128(stage + n % (L::STG ? L::STG : 1) * L::STGB + (u * NL + lt) * 16);
-                    uint4 a, b;
-                    widen(v.x, a.x, a.y);
-                    widen(v.y, a.z, a.w);
-                    widen(v.z, b.x, b.y);
-                    widen(v.w, b.z, b.w);
-                    const uint32_t nan = nan_bytes(v.x) | nan_bytes(v.y) | nan_bytes(v.z) | nan_bytes(v.w);
-                    if (nan) {
-                        widen_nan(v.x, a.x, a.y);
-                        widen_nan(v.y, a.z, a.w);
-                        widen_nan(v.z, b.x, b.y);
-                        widen_nan(v.w, b.z, b.w);
-                    }
-                    const int row = row_of(u), pc = piece_of(u);
-                    tc::sts128(swizzled(to, row, 2 * pc), a);
-                    tc::sts128(swizzled(to, row, 2 * pc + 1), b);
-                }
-            }
-            if (which >= 0) {  // this thread's pieces, as it has just written them
-                const int pieces = L::E == 1 && !(code & 4) ? L::CPR : D / 8, wide = L::E == 1 && !(code & 4) ? 2 : 1;
-#pragma unroll 1
-                for (int i = lt; i < TOK * pieces; i += NL)
-#pragma unroll 1
-                    for (int x = 0; x < wide; ++x) {
-                        const int row = i / pieces;
-                        const uint32_t at = swizzled(to, row, i % pieces * wide + x);
-                        uint4 y = tc::lds128(at);
-                        if (clean(y, row, bad, which)) tc::sts128(at, y);
-                    }
-            }
-            if (code & 8) hand_over(&sh.q_full);
-            hand_over(&sh.full[slot]);
-        };
-        auto push = [&](int code) {
-            codes |= uint64_t(code) << (4 * (issued - handed));
-            bads |= uint32_t(pair & 3) << (2 * (issued - handed));
-            ++issued;
-        };
-        // One loop over all tiles of keys and of values, and one place where a tile is handed over and one where it is
-        // requested: the code of both is long, and copies of it would not stay in the instruction cache.
-        int page = -1, tile = 0, value = 1;
-        bool more = true;
-        it.end = 0;
-        for (;;) {
-            bool first = false, drafted = false;
-            if ((value ^= 1) == 0) {
-                if (++tile >= it.end) {
-                    more = it.next<L::ROWS, TOK>(A, nb);
-                    tile = it.begin;
-                    if (more) {
-                        first = true;
-                        ++pair;
-                    }
-                }
-                if (more) {
-                    const int32_t* table = A.table + it.n * p.table_stride;
-                    auto page_at = [&](int x) {  // of this thread's token
-                        const int t = it.R.base + x * TOK + lt;
-                        return lt < TOK && x < it.tiles - 1 && t < it.R.len && t >= it.R.first ? __ldg(table + A.page_div.of(t)) : -1;
-                    };
-                    if (first) {
-                        page = page_at(tile);
-                        if (lt < 12) sh.bad[pair & 3][lt >> 2][lt & 3] = 0;  // its last use was four pairs ago
-                    }
-                    ++tile_count;
-                    if (tile < it.tiles - 1 && lt < TOK) {
-                        const int t = it.R.base + tile * TOK + lt, in = t - A.page_div.of(t) * p.page_size;
-                        const bool good = page >= 0 && page < p.num_pages;
-                        sh.off[tile_count & 1][lt][0] = good ? page * p.k_page_stride + in * p.k_token_stride + it.hk * p.k_head_stride : -1;
-                        sh.off[tile_count & 1][lt][1] = good ? page * p.v_page_stride + in * p.v_token_stride + it.hk * p.v_head_stride : -1;
-                        const uint32_t votes = __ballot_sync(0xffffffffu, good);
-                        if (lane == 0) sh.counts[tile_count & 7][lt >> 5] = votes;
-                    }
-                    if (tile + 1 < it.end) page = page_at(tile + 1);
-                    tc::named_sync(1, NL);
-                }
-            }
-            drafted = tile == it.tiles - 1;
-            const bool queries = value == 1 && tile == it.begin;  // come with the pair's first values
-            // How many tiles may be on their way: none at the end, or before drafted tokens' under 8 bits (copied to their
-            // place at once); one before the queries of another pair, for their place is free only when the pair before has
-            // its last tiles.
-            int left = L::LAG;
-            if (!more || (drafted && L::E == 1 && value == 0)) {
-                left = 0;
-                cp_wait<0>();
-            } else if (queries && pair > 0) {
-                left = 1;
-                cp_wait<1>();
-            } else {
-                cp_wait<L::LAG>();
-            }
-#pragma unroll 1
-            while (issued - handed > left) finish();
-            if (!more) break;
-            const int n = issued, slot = n % SLOTS, which = !value ? -1 : drafted ? 2 : p.window > 0 && tile < 2 ? tile : -1;
-            if (queries && pair > 0 && ok) ok = warp_wait(&sh.q_empty, (pair - 1) & 1);
-            if ((L::E == 2 || drafted) && n >= SLOTS && ok) ok = warp_wait(&sh.empty[slot], (n / SLOTS - 1) & 1);
-            if (queries && ok) {
-                constexpr int CPR = D / 8;
-#pragma unroll 2
-                for (int i = lt; i < L::ROWS * CPR; i += NL) {
-                    const int row = i / CPR, pc = i % CPR, r = it.r0 + row, t = r / G, g = r - t * G;
-                    const bool in = r < all_rows;
-                    cp_async(q_at + (row >> 7) * (128 * D * 2) + (pc >> 3) * 16384 + (row & 127) * 128 + (((pc & 7) ^ (row & 7)) << 4),
-                             static_cast<const __nv_bfloat16*>(A.q) + (in ? (int64_t(it.n) * p.T + t) * p.q_stride + int64_t(it.hk * G + g) * D + pc * 8 : 0), in);
-                }
-            }
-            if (ok && drafted) {
-                constexpr int CPR = D / 8;
-                const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(value ? A.v_new : A.k_new) + int64_t(it.hk) * D;
-                const int64_t stride = value ? p.v_new_stride : p.k_new_stride;
-#pragma unroll 4
-                for (int i = lt; i < TOK * CPR; i += NL) {
-                    const int row = i / CPR, pc = i % CPR;
-                    const bool in = row < p.T;
-                    cp_async(swizzled(ring + slot * L::SLOT, row, pc), from + (in ? (int64_t(it.n) * p.T + row) * stride + pc * 8 : 0), in);
-                }
-            } else if (ok) {
-                // the addresses first, the copies back to back
-                const C* from = static_cast<const C*>(value ? A.v_cache : A.k_cache);
-                int64_t off[L::U];
+    // Tile `tile` of the pair: where its tokens that count lie in it, whether its values are cleaned of infinities and NaN (and
+    // which of sh.bad says of what: -1), and whether anything is to be done about them at all.
+    auto bounds = [&](int tile, int& from, int& to, int& which) {
+        const int t0 = it.R.base + tile * TOK;
+        const bool drafted = tile == it.tiles - 1;
+        from = drafted ? 0 : it.R.first - t0;
+        to = drafted ? p.T : it.R.len - t0;
+        which = drafted ? 2 : p.window > 0 && tile < 2 ? tile : -1;
+        return which >= 0 || from > 0 || to < TOK;
+    };
+
+    if (warp == 9) {  // ---- loads
+        const int log_pieces = (TOK == 128 ? 7 : 6) - log_rows, pieces = 1 << log_pieces;
+        int n = 0, cleaned = 0, tiles = 0;
+        if (lane == 0) {
+            prefetch_map(&M.k);
+            prefetch_map(&M.v);
+            prefetch_map(&M.k_new);
+            prefetch_map(&M.v_new);
+        }
+        const int nowhere = int(p.num_pages > 0 ? p.num_pages : 1);
+        while (ok && it.next<L::ROWS, TOK>(A, nb)) {
+            const int32_t* table = A.table + it.n * p.table_stride;
+            auto page_at = [&](int tile, int piece) {
+                const int t = it.R.base + tile * TOK + (piece << log_rows);
+                return piece < pieces && tile < it.tiles - 1 && t < it.R.len && t + (1 << log_rows) > it.R.first ? __ldg(table + A.page_div.of(t)) : -1;
+            };
+            int page[4], next[4];  // of this lane's pieces
 #pragma unroll
-                for (int u = 0; u < L::U; ++u) off[u] = u * NL + lt < L::PIECES ? sh.off[tile_count & 1][row_of(u)][value] : -1;
+            for (int x = 0; x < 4; ++x) next[x] = page_at(it.begin, lane + 32 * x);
+            for (int tile = it.begin; tile < it.end && ok; ++tile, ++tiles) {
+                const bool drafted = tile == it.tiles - 1;
 #pragma unroll
-                for (int u = 0; u < L::U; ++u) {
-                    if (u * NL + lt >= L::PIECES) break;
-                    const int row = row_of(u), pc = piece_of(u);
-                    const uint32_t to = L::E == 1 ? stage + n % (L::STG ? L::STG : 1) * L::STGB + (u * NL + lt) * 16 : swizzled(ring + slot * L::SLOT, row, pc);
-                    cp_async(to, from + (off[u] < 0 ? 0 : off[u] + pc * (16 / L::E)), off[u] >= 0);
+                for (int x = 0; x < 4; ++x) page[x] = next[x];
+                if (tile + 1 < it.end)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) next[x] = page_at(tile + 1, lane + 32 * x);
+                if (!drafted) {
+                    // which tokens count: a lane to a word of 32, which is 2 to 32 pieces of the 32 that one vote covers
+                    const int per = 32 >> log_rows, first = lane * per;
+                    uint32_t good = 0, word = 0;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const uint32_t votes = __ballot_sync(0xffffffffu, page[x] >= 0 && page[x] < p.num_pages);
+                        if (first >> 5 == x) good = votes;
+                    }
+                    if (lane < TOK / 32) {
+                        for (int y = 0; y < per; ++y)
+                            if (good >> ((first + y) & 31) & 1) word |= ((1u << (1 << log_rows)) - 1) << (y << log_rows);
+                        const int skip = it.R.first - (it.R.base + tile * TOK + lane * 32), left = it.R.len - (it.R.base + tile * TOK + lane * 32);
+                        if (skip > 0) word &= skip < 32 ? 0xffffffffu << skip : 0u;
+                        if (left < 32) word &= left > 0 ? 0xffffffffu >> (32 - left) : 0u;
+                        sh.counts[tiles & 7][lane] = word;
+                    }
+                }
+                __syncwarp();
+                for (int value = 0; value < 2 && ok; ++value, ++n) {
+                    const int slot = n % SLOTS, st = n % STG;
+                    const uint32_t to = ring + slot * L::SLOT;
+                    uint64_t* bar = L::E == 1 ? &sh.stage_full[st] : &sh.full[slot];
+                    if (L::E == 1 && n >= STG) ok = warp_wait(&sh.stage_empty[st], (n / STG - 1) & 1);
+                    if ((L::E == 2 || drafted) && n >= SLOTS) ok = ok && warp_wait(&sh.empty[slot], (n / SLOTS - 1) & 1);
+                    if (!ok) break;
+                    if (lane == 0) tc::mbar_expect_tx(bar, drafted ? L::SLOT : TOK * D * L::E);
+                    __syncwarp();
+                    if (drafted) {
+                        if (lane < D / 64) {
+                            const int row = it.n * p.T;
+                            tc::tma_load_4d(to + lane * (TOK * 128), value ? &M.v_new : &M.k_new, bar, lane * 64, it.hk, row, 0);
+                            if (TOK == 128) tc::tma_load_4d(to + lane * (TOK * 128) + 64 * 128, value ? &M.v_new : &M.k_new, bar, lane * 64, it.hk, p.num_seqs * p.T, 0);  // zeros
+                        }
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const int piece = lane + 32 * x;
+                            if (piece >= pieces) continue;
+                            const int t = it.R.base + tile * TOK + (piece << log_rows), in = t - A.page_div.of(t) * p.page_size;
+                            const int pg = page[x] >= 0 && page[x] < p.num_pages ? page[x] : nowhere;
+                            if (L::E == 1) {
+                                const int each = D << log_rows;
+                                tc::tma_load_4d(stage + st * L::STGB + piece * (each < 128 ? 128 : each), value ? &M.v : &M.k, bar, 0, it.hk, in, pg);
+                            } else {
+#pragma unroll
+                                for (int c = 0; c < D / 64; ++c)
+                                    tc::tma_load_4d(to + c * (TOK * 128) + (piece << (log_rows + 7)), value ? &M.v : &M.k, bar, c * 64, it.hk, in, pg);
+                            }
+                        }
+                    }
+                    int from, till, which;
+                    if (L::E == 2 && value && bounds(tile, from, till, which)) {
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive(&sh.issued[cleaned % CLEAN]);
+                        ++cleaned;
+                    }
                 }
             }
-            cp_commit();
-            push((which >= 0 ? 1 + which : 0) | (drafted ? 4 : 0) | (queries ? 8 : 0));
+        }
+        if (!ok)  // the copies in flight land before the CTA ends
+            for (int i = max(0, n - (L::E == 1 ? STG : SLOTS)); i < n; ++i) warp_wait(L::E == 1 ? &sh.stage_full[i % STG] : &sh.full[i % SLOTS], (i / (L::E == 1 ? STG : SLOTS)) & 1);
+    } else if (warp > 9) {  // ---- helping warps
+        const int part = warp - 10, lt = tid - 320;
+        int n = 0, cleaned = 0, pair = 0;
+        while (ok && it.next<L::ROWS, TOK>(A, nb)) {
+            for (int tile = it.begin; tile < it.end && ok; ++tile) {
+                const bool drafted = tile == it.tiles - 1;
+                int from, to, which;
+                const bool some = bounds(tile, from, to, which);
+                for (int value = 0; value < 2 && ok; ++value, ++n) {
+                    const int slot = n % SLOTS, st = n % STG;
+                    const uint32_t at = ring + slot * L::SLOT;
+                    uint32_t bad[4] = {};
+                    const bool here = value && some;
+                    if (L::E == 1) {
+                        ok = warp_wait(&sh.stage_full[st], (n / STG) & 1);
+                        if (!drafted && n >= SLOTS) ok = ok && warp_wait(&sh.empty[slot], (n / SLOTS - 1) & 1);
+                        if (!ok) break;
+                        if (drafted) {
+                            if (here) clean_rows<TOK, D>(at, from, to, part, NH, which >= 0, bad);
+                        } else {
+                            constexpr int CPR = D / 16;
+                            const int each = D << log_rows, pitch = each < 128 ? 128 : each;
+                            // not unrolled further: these warps' code and the weights' share the instruction cache
+#pragma unroll 2
+                            for (int i = lt; i < TOK * CPR; i += 32 * NH) {
+                                const int row = i / CPR, pc = i % CPR;
+                                const uint4 v = tc::lds128(stage + st * L::STGB + (row >> log_rows) * pitch + (row & ((1 << log_rows) - 1)) * D + pc * 16);
+                                uint4 a, b;
+                                widen(v.x, a.x, a.y);
+                                widen(v.y, a.z, a.w);
+                                widen(v.z, b.x, b.y);
+                                widen(v.w, b.z, b.w);
+                                if (nan_bytes(v.x) | nan_bytes(v.y) | nan_bytes(v.z) | nan_bytes(v.w)) {  // the only values without an end
+                                    if (here && which >= 0 && row >= from && row < to) mark(bad, row);
+                                    const bool zero = here && which >= 0;
+                                    widen_nan(v.x, a.x, a.y, zero);
+                                    widen_nan(v.y, a.z, a.w, zero);
+                                    widen_nan(v.z, b.x, b.y, zero);
+                                    widen_nan(v.w, b.z, b.w, zero);
+                                }
+                                if (here && (row < from || row >= to)) a = b = make_uint4(0u, 0u, 0u, 0u);
+                                const uint32_t block = at + (2 * pc >> 3) * (TOK * 128) + row * 128;
+                                tc::sts128(block + (((2 * pc & 7) ^ (row & 7)) << 4), a);
+                                tc::sts128(block + (((2 * pc + 1 & 7) ^ (row & 7)) << 4), b);
+                            }
+                        }
+                    } else if (here) {
+                        ok = warp_wait(&sh.issued[cleaned % CLEAN], (cleaned / CLEAN) & 1);  // from then on the slot's barrier is in this tile's phase
+                        ok = ok && warp_wait(&sh.full[slot], (n / SLOTS) & 1);
+                        if (!ok) break;
+                        clean_rows<TOK, D>(at, from, to, part, NH, which >= 0, bad);
+                    }
+                    if (here && which >= 0) {
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            bad[w] = __reduce_or_sync(0xffffffffu, bad[w]);
+                            if (lane == 0) sh.bad[pair & 7][which][part][w] = bad[w];
+                        }
+                        if (lane == 0 && (bad[0] | bad[1] | bad[2] | bad[3])) sh.bad_pair[pair & 7] = pair;
+                    }
+                    if (L::E == 1 || here) {
+                        tc::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (L::E == 1) {
+                                tc::mbar_arrive(&sh.full[slot]);
+                                tc::mbar_arrive(&sh.stage_empty[st]);
+                            } else {
+                                tc::mbar_arrive(&sh.clean[cleaned % CLEAN]);
+                            }
+                        }
+                        ++cleaned;
+                    }
+                }
+            }
+            ++pair;
         }
     } else if (warp == 8) {  // ---- products
         {
             const bool el = elected();
             const uint32_t tm = same(tmem);
             constexpr uint32_t IS = tc::make_idesc(128, TOK, 0, 0), IO = tc::make_idesc(128, D, 0, 1);
-            int g = 0, pair = 0;  // tiles and pairs before
+            int g = 0, pair = 0, cleaned = 0;  // tiles and pairs before, tiles of values cleaned
             while (ok && it.next<L::ROWS, TOK>(A, nb)) {
                 const int nt = same(it.end - it.begin);
                 auto slot_at = [&](int i, int value) { return ring + (2 * (g + i) + value) % SLOTS * L::SLOT; };
                 auto full = [&](int i, int value) {
                     const int n = 2 * (g + i) + value;
-                    return ok = ok && warp_wait(&sh.full[n % SLOTS], (n / SLOTS) & 1);
+                    return ok = ok && warp_spin(&sh.full[n % SLOTS], (n / SLOTS) & 1);
                 };
                 auto release = [&](int i, int value) {
                     if (el) tc::commit(&sh.empty[(2 * (g + i) + value) % SLOTS]);
@@ -330,9 +390,17 @@ __global__ void __launch_bounds__(TreeTc<C, D, NQ>::T, 1) k_tree_tc(const TreeAr
                 };
                 auto values = [&](int w, int i) {
                     const int buf = NQ == 2 ? w : (g + i) & 1;
-                    ok = ok && warp_wait(&sh.p_ready[buf], (NQ == 2 ? g + i : (g + i) >> 1) & 1);
-                    if (i == 0 && w == 0 && pair > 0) ok = ok && warp_wait(&sh.o_free, (pair - 1) & 1);
+                    ok = ok && warp_spin(&sh.p_ready[buf], (NQ == 2 ? g + i : (g + i) >> 1) & 1);
+                    if (i == 0 && w == 0 && pair > 0) ok = ok && warp_spin(&sh.o_free, (pair - 1) & 1);
                     if (!full(i, 1)) return;
+                    if (L::E == 2 && w == 0) {
+                        int from, to, which;
+                        if (bounds(it.begin + i, from, to, which)) {
+                            ok = warp_spin(&sh.clean[cleaned % CLEAN], (cleaned / CLEAN) & 1);
+                            ++cleaned;
+                        }
+                    }
+                    if (!ok) return;
                     tc::fence_after_sync();
                     const uint64_t b = desc_mn<TOK>(slot_at(i, 1), 0);
                     if (el) {
@@ -343,7 +411,7 @@ __global__ void __launch_bounds__(TreeTc<C, D, NQ>::T, 1) k_tree_tc(const TreeAr
                     }
                     if (w == NQ - 1) release(i, 1);
                 };
-                ok = warp_wait(&sh.q_full, pair & 1);
+                ok = warp_spin(&sh.q_full, pair & 1);
                 if (NQ == 2) {
                     for (int w = 0; w < NQ && ok; ++w) scores(w, 0);
                     for (int i = 0; i < nt && ok; ++i)
@@ -363,7 +431,7 @@ __global__ void __launch_bounds__(TreeTc<C, D, NQ>::T, 1) k_tree_tc(const TreeAr
             }
             if (!ok) {  // the products in flight end before tensor memory is freed
                 if (el) tc::commit(&sh.drain);
-                warp_wait(&sh.drain, 0);
+                warp_spin(&sh.drain, 0);
             }
         }
     } else {  // ---- weights: thread to a row
@@ -382,6 +450,24 @@ __global__ void __launch_bounds__(TreeTc<C, D, NQ>::T, 1) k_tree_tc(const TreeAr
             ok = ok && warp_wait(&sh.met[warp & 3], met & 1);
             return sh.shared[met++ & 1][half ^ 1][lane_row];
         };
+        // The queries of a pair, when the scores of the one before are made.
+        auto load_queries = [&](const Pairs& x, int before) {
+            if (before > 0) ok = ok && warp_wait(&sh.q_empty, (before - 1) & 1);
+            constexpr int CPR = D / 8;
+#pragma unroll 4
+            for (int i = tid; i < L::ROWS * CPR && ok; i += 256) {
+                const int row = i / CPR, pc = i % CPR, r = x.r0 + row, t = r / G;
+                uint4 q = make_uint4(0u, 0u, 0u, 0u);
+                if (r < all_rows) q = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(A.q) + (int64_t(x.n) * p.T + t) * p.q_stride + int64_t(x.hk * G + r - t * G) * D + pc * 8);
+                tc::sts128(q_at + (row >> 7) * (128 * D * 2) + (pc >> 3) * 16384 + (row & 127) * 128 + (((pc & 7) ^ (row & 7)) << 4), q);
+            }
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&sh.q_full);
+        };
+        Pairs ahead = it;
+        ahead.next<L::ROWS, TOK>(A, nb);
+        load_queries(ahead, 0);
         while (ok && it.next<L::ROWS, TOK>(A, nb)) {
             const int r = it.r0 + my_row, t = r / G, nt = it.end - it.begin;
             // what this row's drafted token attends to
@@ -509,6 +595,7 @@ __global__ void __launch_bounds__(TreeTc<C, D, NQ>::T, 1) k_tree_tc(const TreeAr
                 tc::unpk2(fadd2(sum[0], sum[1]), a, b);
                 l += a + b;
             }
+            if (ok && ahead.next<L::ROWS, TOK>(A, nb)) load_queries(ahead, pair + 1);
             // With one tile of rows the scores run two tiles ahead and the last two products may both be open, or both done:
             // each has a barrier of its own, for a phase that another has followed can no longer be waited for.
             const int last = g + nt - 1;
@@ -524,9 +611,7 @@ __global__ void __launch_bounds__(TreeTc<C, D, NQ>::T, 1) k_tree_tc(const TreeAr
             const float f = !whole ? 1.f : some ? 1.f / l : 0.f;
             const int64_t out = (int64_t(it.n) * p.T + t) * p.Hq + it.hk * G + (r - t * G), at = place_of(blockIdx.x, it.begin > 0, L::ROWS) + my_row;
             constexpr int OW = NQ == 2 ? D : D / 2;
-            uint32_t any_bad = 0;
-#pragma unroll
-            for (int x = 0; x < 12; ++x) any_bad |= sh.bad[pair & 3][x >> 2][x & 3];
+            const bool any_bad = sh.bad_pair[pair & 7] == pair;  // written before the last product
 #pragma unroll 1
             for (int c = half * OW; c < (half + 1) * OW; c += 32) {
                 float x[32];
@@ -539,7 +624,11 @@ __global__ void __launch_bounds__(TreeTc<C, D, NQ>::T, 1) k_tree_tc(const TreeAr
                 if (any_bad && live)  // infinite and NaN values that this row sees
                     for (int b = 0; b < 3 * TOK; ++b) {
                         const int which = b / TOK, token = b % TOK, cached = it.R.base + which * TOK + token;
-                        if (!(sh.bad[pair & 3][which][token >> 5] >> (token & 31) & 1)) continue;
+                        // of the tiles that this CTA has
+                        if (which == 2 ? it.end < it.tiles : !(p.window > 0 && which >= it.begin && which < it.end && which < it.tiles - 1)) continue;
+                        uint32_t bits = 0;
+                        for (int h = 0; h < NH; ++h) bits |= sh.bad[pair & 7][which][h][token >> 5];
+                        if (!(bits >> (token & 31) & 1)) continue;
                         if (which < 2 ? cached < first : !(sees >> token & 1)) continue;
                         const int page = which < 2 ? A.table[it.n * p.table_stride + A.page_div.of(cached)] : 0;
                         for (int e = 0; e < 32; ++e) {
@@ -586,10 +675,21 @@ __global__ void __launch_bounds__(TreeTc<C, D, NQ>::T, 1) k_tree_tc(const TreeAr
 template <typename C, int D, int NQ>
 cudaError_t tree_tc(const TreeArgs& A, const TreePlan& plan, cudaStream_t st) {
     using L = TreeTc<C, D, NQ>;
+    const gdn_tree_problem& p = A.p;
+    int log_rows = 0;
+    while (log_rows < 4 && p.page_size % (2 << log_rows) == 0) ++log_rows;
+    TreeMaps m;
+    const int64_t rows = int64_t(p.num_seqs) * p.T;
+    const bool none = p.num_pages == 0 || !A.k_cache || !A.v_cache;  // read nowhere
+    const void *k = none ? A.k_new : A.k_cache, *v = none ? A.v_new : A.v_cache;
+    if (!make_pages_map(&m.k, k, L::E, D, none ? 1 : p.Hkv, none ? 1 : p.page_size, none ? 1 : p.num_pages, p.k_head_stride, p.k_token_stride, p.k_page_stride, 1 << log_rows) ||
+        !make_pages_map(&m.v, v, L::E, D, none ? 1 : p.Hkv, none ? 1 : p.page_size, none ? 1 : p.num_pages, p.v_head_stride, p.v_token_stride, p.v_page_stride, 1 << log_rows) ||
+        !make_pages_map(&m.k_new, A.k_new, 2, D, p.Hkv, int(rows), 1, D, p.k_new_stride, 0, 64) || !make_pages_map(&m.v_new, A.v_new, 2, D, p.Hkv, int(rows), 1, D, p.v_new_stride, 0, 64))
+        return cudaErrorInvalidValue;
     cudaError_t e = smem_attr(k_tree_tc<C, D, NQ>, L::SMEM);
     if (e != cudaSuccess) return e;
     timing_begin("tree_attn", st);
-    k_tree_tc<C, D, NQ><<<plan.ctas, L::T, L::SMEM, st>>>(A);
+    k_tree_tc<C, D, NQ><<<plan.ctas, L::T, L::SMEM, st>>>(A, m, log_rows);
     timing_end(st);
     e = cudaGetLastError();
     return e != cudaSuccess ? e : launch_tree_join<__nv_bfloat16, D>(A, plan, st);
