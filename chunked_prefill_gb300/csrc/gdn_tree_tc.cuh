@@ -27,12 +27,16 @@ template <typename C, int D, int NQ> struct TreeTc {
     static constexpr int ROWS = NQ * 128;
     static constexpr int QB = ROWS * D * 2;              // bytes of the queries
     static constexpr int SLOT = TOK * D * 2;             // of a tile of keys or values
-    static constexpr int NH = E == 1 ? 6 : 2;            // helping warps: widening; cleaning
+    // A piece takes the warp that requests it some 120 cycles (tree of 16, 32 sequences, bf16, by one warp: 158 us): keys and values of
+    // bf16, whose rows are two pieces or more, by a warp each.
+    static constexpr int NLW = E == 1 ? 1 : 2;           // loading warps
+    static constexpr int NH = E == 1 ? 6 : 1;            // helping warps: widening; cleaning
     static constexpr int STG = E == 1 ? 3 : 0, STGB = TOK * (D < 128 ? 128 : D);  // 8-bit tiles on their way (a piece begins at 128 bytes)
     static constexpr int FIT = (225280 - QB - STG * STGB) / SLOT, SLOTS = FIT < 8 ? FIT : 8;
     static constexpr int SMEM = 1024 + QB + SLOTS * SLOT + STG * STGB;
-    static constexpr int T = 256 + 64 + 32 * NH;          // 8 warps of weights, then products, loads, helping ones
+    static constexpr int T = 256 + 32 + 32 * (NLW + NH);  // 8 warps of weights, then products, loads, helping ones
     static constexpr int CW = NQ == 2 ? TOK : TOK / 2;   // columns of a thread: with one tile of rows the two warpgroups share them
+    static constexpr int PIECE = CW < 64 ? CW : 64;      // of which a thread holds so many at a time
     static constexpr int S = 0, O = 2 * TOK;             // tensor memory columns
     static_assert(SLOTS >= 3 && O + NQ * D <= 512, "");
 };
@@ -192,9 +196,10 @@ __global__ void __launch_bounds__(TreeTc<C, D, NQ>::T, 1) k_tree_tc(const TreeAr
         return which >= 0 || from > 0 || to < TOK;
     };
 
-    if (warp == 9) {  // ---- loads
+    if (warp > 8 && warp < 9 + L::NLW) {  // ---- loads
+        const int mine = warp - 9;  // keys or values, where a warp has one of them
         const int log_pieces = (TOK == 128 ? 7 : 6) - log_rows, pieces = 1 << log_pieces;
-        int n = 0, cleaned = 0, tiles = 0;
+        int cleaned = 0, tiles = 0;
         if (lane == 0) {
             prefetch_map(&M.k);
             prefetch_map(&M.v);
@@ -202,12 +207,14 @@ __global__ void __launch_bounds__(TreeTc<C, D, NQ>::T, 1) k_tree_tc(const TreeAr
             prefetch_map(&M.v_new);
         }
         const int nowhere = int(p.num_pages > 0 ? p.num_pages : 1);
+        const bool el = elected();
         while (ok && it.next<L::ROWS, TOK>(A, nb)) {
             const int32_t* table = A.table + it.n * p.table_stride;
             auto page_at = [&](int tile, int piece) {
                 const int t = it.R.base + tile * TOK + (piece << log_rows);
                 return piece < pieces && tile < it.tiles - 1 && t < it.R.len && t + (1 << log_rows) > it.R.first ? __ldg(table + A.page_div.of(t)) : -1;
             };
+            const int hk = same(it.hk);
             int page[4], next[4];  // of this lane's pieces
 #pragma unroll
             for (int x = 0; x < 4; ++x) next[x] = page_at(it.begin, lane + 32 * x);
@@ -233,18 +240,18 @@ __global__ void __launch_bounds__(TreeTc<C, D, NQ>::T, 1) k_tree_tc(const TreeAr
                         const int skip = it.R.first - (it.R.base + tile * TOK + lane * 32), left = it.R.len - (it.R.base + tile * TOK + lane * 32);
                         if (skip > 0) word &= skip < 32 ? 0xffffffffu << skip : 0u;
                         if (left < 32) word &= left > 0 ? 0xffffffffu >> (32 - left) : 0u;
-                        sh.counts[tiles & 7][lane] = word;
+                        if (mine == 0) sh.counts[tiles & 7][lane] = word;
                     }
                 }
                 __syncwarp();
-                for (int value = 0; value < 2 && ok; ++value, ++n) {
-                    const int slot = n % SLOTS, st = n % STG;
+                for (int value = mine; value < (L::NLW == 2 ? mine + 1 : 2) && ok; ++value) {
+                    const int n = 2 * tiles + value, slot = n % SLOTS, st = n % STG;
                     const uint32_t to = ring + slot * L::SLOT;
                     uint64_t* bar = L::E == 1 ? &sh.stage_full[st] : &sh.full[slot];
                     if (L::E == 1 && n >= STG) ok = warp_wait(&sh.stage_empty[st], (n / STG - 1) & 1);
                     if ((L::E == 2 || drafted) && n >= SLOTS) ok = ok && warp_wait(&sh.empty[slot], (n / SLOTS - 1) & 1);
                     if (!ok) break;
-                    if (lane == 0) tc::mbar_expect_tx(bar, drafted ? L::SLOT : TOK * D * L::E);
+                    if (el) tc::mbar_expect_tx(bar, drafted ? L::SLOT : TOK * D * L::E);
                     __syncwarp();
                     if (drafted) {
                         if (lane < D / 64) {
@@ -253,19 +260,28 @@ __global__ void __launch_bounds__(TreeTc<C, D, NQ>::T, 1) k_tree_tc(const TreeAr
                             if (TOK == 128) tc::tma_load_4d(to + lane * (TOK * 128) + 64 * 128, value ? &M.v_new : &M.k_new, bar, lane * 64, it.hk, p.num_seqs * p.T, 0);  // zeros
                         }
                     } else {
+                        // one piece after another by one lane: addresses that differ between the lanes of an instruction cost
+                        // a turn of the warp each, 100 cycles (tree of 16, 32 sequences: 163 us)
+                        const CUtensorMap* map = value ? &M.v : &M.k;
+                        const uint32_t first = L::E == 1 ? stage + st * L::STGB : to, each = D << log_rows, step = L::E == 1 ? (each < 128 ? 128 : each) : 128u << log_rows;
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
-                            const int piece = lane + 32 * x;
-                            if (piece >= pieces) continue;
-                            const int t = it.R.base + tile * TOK + (piece << log_rows), in = t - A.page_div.of(t) * p.page_size;
-                            const int pg = page[x] >= 0 && page[x] < p.num_pages ? page[x] : nowhere;
-                            if (L::E == 1) {
-                                const int each = D << log_rows;
-                                tc::tma_load_4d(stage + st * L::STGB + piece * (each < 128 ? 128 : each), value ? &M.v : &M.k, bar, 0, it.hk, in, pg);
-                            } else {
+                            if (32 * x >= pieces) break;
+                            const int t = it.R.base + tile * TOK + ((lane + 32 * x) << log_rows), my_in = t - A.page_div.of(t) * p.page_size;
+                            const int my_page = page[x] >= 0 && page[x] < p.num_pages ? page[x] : nowhere;
+                            const int some = min(32, pieces - 32 * x);
+#pragma unroll 1
+                            for (int y = 0; y < some; ++y) {
+                                const int pg = __shfl_sync(0xffffffffu, my_page, y), in = __shfl_sync(0xffffffffu, my_in, y);
+                                const uint32_t at = first + (32 * x + y) * step;
+                                if (el) {
+                                    if (L::E == 1) {
+                                        tc::tma_load_4d(at, map, bar, 0, hk, in, pg);
+                                    } else {
 #pragma unroll
-                                for (int c = 0; c < D / 64; ++c)
-                                    tc::tma_load_4d(to + c * (TOK * 128) + (piece << (log_rows + 7)), value ? &M.v : &M.k, bar, c * 64, it.hk, in, pg);
+                                        for (int c = 0; c < D / 64; ++c) tc::tma_load_4d(at + c * (TOK * 128), map, bar, c * 64, hk, in, pg);
+                                    }
+                                }
                             }
                         }
                     }
@@ -278,10 +294,12 @@ __global__ void __launch_bounds__(TreeTc<C, D, NQ>::T, 1) k_tree_tc(const TreeAr
                 }
             }
         }
-        if (!ok)  // the copies in flight land before the CTA ends
-            for (int i = max(0, n - (L::E == 1 ? STG : SLOTS)); i < n; ++i) warp_wait(L::E == 1 ? &sh.stage_full[i % STG] : &sh.full[i % SLOTS], (i / (L::E == 1 ? STG : SLOTS)) & 1);
-    } else if (warp > 9) {  // ---- helping warps
-        const int part = warp - 10, lt = tid - 320;
+        if (!ok) {  // the copies in flight land before the CTA ends
+            const int n = 2 * tiles + 2, ringed = L::E == 1 ? STG : SLOTS;
+            for (int i = max(0, n - ringed); i < n; ++i) warp_wait(L::E == 1 ? &sh.stage_full[i % STG] : &sh.full[i % SLOTS], (i / ringed) & 1);
+        }
+    } else if (warp > 8) {  // ---- helping warps
+        const int part = warp - 9 - L::NLW, lt = part * 32 + lane;
         int n = 0, cleaned = 0, pair = 0;
         while (ok && it.next<L::ROWS, TOK>(A, nb)) {
             for (int tile = it.begin; tile < it.end && ok; ++tile) {
@@ -300,13 +318,20 @@ __global__ void __launch_bounds__(TreeTc<C, D, NQ>::T, 1) k_tree_tc(const TreeAr
                         if (drafted) {
                             if (here) clean_rows<TOK, D>(at, from, to, part, NH, which >= 0, bad);
                         } else {
-                            constexpr int CPR = D / 16;
-                            const int each = D << log_rows, pitch = each < 128 ? 128 : each;
+                            // A thread's pieces lie in one place of rows 24 (256 features: 12) apart: both addresses only grow.  (Rows of 64
+                            // bytes in pieces of one row have 128 bytes each.)
+                            constexpr int CPR = D / 16, STEP = 32 * NH / CPR;
+                            static_assert(STEP * CPR == 32 * NH || L::E != 1, "");
+                            const int row0 = lt / CPR, pc = lt % CPR, pitch = D == 64 && log_rows == 0 ? 128 : D;
+                            uint32_t src = stage + st * L::STGB + row0 * pitch + pc * 16, dst = at + (2 * pc >> 3) * (TOK * 128) + row0 * 128;
+                            // The second block of 64 columns takes its pieces' halves the other way round: 8 lanes then write distinct banks.
+                            uint32_t lo = ((2 * pc & 7) ^ (row0 & 7)) << 4 ^ (pc & 4 ? 16 : 0), hi = lo ^ 16;
+                            const uint32_t swap = pc & 4 ? 8 : 0;
                             // not unrolled further: these warps' code and the weights' share the instruction cache
 #pragma unroll 2
-                            for (int i = lt; i < TOK * CPR; i += 32 * NH) {
-                                const int row = i / CPR, pc = i % CPR;
-                                const uint4 v = tc::lds128(stage + st * L::STGB + (row >> log_rows) * pitch + (row & ((1 << log_rows) - 1)) * D + pc * 16);
+                            for (int row = row0; row < TOK; row += STEP, src += STEP * pitch, dst += STEP * 128) {
+                                const uint2 v0 = tc::lds64(src + swap), v1 = tc::lds64(src + (swap ^ 8));
+                                const uint4 v = make_uint4(v0.x, v0.y, v1.x, v1.y);
                                 uint4 a, b;
                                 widen(v.x, a.x, a.y);
                                 widen(v.y, a.z, a.w);
@@ -321,9 +346,9 @@ __global__ void __launch_bounds__(TreeTc<C, D, NQ>::T, 1) k_tree_tc(const TreeAr
                                     widen_nan(v.w, b.z, b.w, zero);
                                 }
                                 if (here && (row < from || row >= to)) a = b = make_uint4(0u, 0u, 0u, 0u);
-                                const uint32_t block = at + (2 * pc >> 3) * (TOK * 128) + row * 128;
-                                tc::sts128(block + (((2 * pc & 7) ^ (row & 7)) << 4), a);
-                                tc::sts128(block + (((2 * pc + 1 & 7) ^ (row & 7)) << 4), b);
+                                tc::sts128(dst + lo, a);
+                                tc::sts128(dst + hi, b);
+                                if (STEP % 8) lo ^= (STEP % 8) << 4, hi ^= (STEP % 8) << 4;  // 4
                             }
                         }
                     } else if (here) {
@@ -406,7 +431,7 @@ __global__ void __launch_bounds__(TreeTc<C, D, NQ>::T, 1) k_tree_tc(const TreeAr
                     if (el) {
 #pragma unroll
                         for (int x = 0; x < TOK; x += 16)
-                            tc::mma_bf16_ta(tm + L::O + w * D, tm + L::S + buf * TOK + x / L::CW * L::CW + x % L::CW / 2, step_mn(b, x), IO, i > 0 || x > 0);
+                            tc::mma_bf16_ta(tm + L::O + w * D, tm + L::S + buf * TOK + x / L::PIECE * L::PIECE + x % L::PIECE / 2, step_mn(b, x), IO, i > 0 || x > 0);
                         tc::commit(&sh.pv_done[buf]);
                     }
                     if (w == NQ - 1) release(i, 1);
@@ -439,7 +464,7 @@ __global__ void __launch_bounds__(TreeTc<C, D, NQ>::T, 1) k_tree_tc(const TreeAr
         // threads then exchange maxima, and at the end sums.
         const int wg = warp >> 2, w = NQ == 2 ? wg : 0, half = NQ == 2 ? 0 : wg, lane_row = tid & 127, my_row = NQ == 2 ? tid : lane_row;
         const uint32_t mine = tmem + (uint32_t(warp & 3) << 21);
-        constexpr int CW = L::CW, PIECE = CW < 64 ? CW : 64;
+        constexpr int CW = L::CW, PIECE = L::PIECE;
         int g = 0, pair = 0, met = 0;
         // The other half's value of the row.  A place is written again only after the next exchange, before which the
         // other thread has read it.
@@ -583,8 +608,8 @@ __global__ void __launch_bounds__(TreeTc<C, D, NQ>::T, 1) k_tree_tc(const TreeAr
                             tc::unpk2(tc::fmul2(tc::pk2(a, b), vf2), a, b);
                             wts[(c - y) / 2] = __uint_as_float(tc::pack_bf16(a, b));
                         }
-                        // columns [c, c + 2) of the weights in place of the scores' column c / 2
-                        tc::tmem_st16(at + (PIECE * x + y) / 2, wts);
+                        // columns [c, c + 2) of a piece's weights in place of its scores' column c / 2
+                        tc::tmem_st16(at + PIECE * x + y / 2, wts);
                     }
                 }
                 tc::tmem_st_wait();
