@@ -508,8 +508,10 @@ PyObject* prompt_fwd(Args& a) {
     const at::Tensor *cu = a.maybe("cu_seqlens"), *cu_k = a.maybe("cu_seqlens_k"), *given = a.maybe("o");
     bool make_lse;
     const at::Tensor* lse = lse_of(a, make_lse);
+    const bool want_rest = a.flag();
     if (given) need_like("o", *given, q, "q");
     need_lse("lse", lse, q);
+    need(!want_rest || make_lse, "rest comes with lse=True");
     gdn_prompt_problem p = prompt_problem(q, k, v, scale, window, cu, cu_k);
     need_cuda(q, "o", given);
     need_cuda(q, "lse", lse);
@@ -522,8 +524,11 @@ PyObject* prompt_fwd(Args& a) {
         if (given && cu) new_lse.fill_(-INFINITY);  // what the allocator hands out is not a result
         lse = &new_lse;
     }
-    check(f_prompt_fwd(&p, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), ptr(lse), on.stream));
-    return make_lse ? tuple({o, new_lse}) : THPVariable_Wrap(o);
+    const bool rest = want_rest && p.dtype == GDN_BF16;
+    const at::Tensor o_rest = rest ? empty(q.sizes(), q.scalar_type(), q) : at::Tensor();
+    check(f_prompt_fwd(&p, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), ptr(lse), rest ? o_rest.data_ptr() : nullptr, on.stream));
+    if (!make_lse) return THPVariable_Wrap(o);
+    return !want_rest ? tuple({o, new_lse}) : tuple_of(o, &new_lse, rest ? &o_rest : nullptr);
 }
 
 PyObject* prompt_bwd(Args& a) {
@@ -531,8 +536,9 @@ PyObject* prompt_bwd(Args& a) {
     const at::Tensor* dlse = a.maybe("dlse");
     const double scale = a.number();
     const int64_t window = a.integer();
-    const at::Tensor *cu = a.maybe("cu_seqlens"), *cu_k = a.maybe("cu_seqlens_k"), *ws = a.maybe("workspace");
+    const at::Tensor *cu = a.maybe("cu_seqlens"), *cu_k = a.maybe("cu_seqlens_k"), *rest = a.maybe("o_rest"), *ws = a.maybe("workspace");
     need_like("o", o, q, "q");
+    if (rest) need_like("o_rest", *rest, q, "q");
     need_like("do", dO, q, "q");
     need_lse("lse", &lse, q);
     need_lse("dlse", dlse, q);
@@ -540,6 +546,7 @@ PyObject* prompt_bwd(Args& a) {
     need_scratch(ws);
     need_cuda(q, "o", o);
     need_cuda(q, "lse", lse);
+    need_cuda(q, "o_rest", rest);
     need_cuda(q, "do", dO);
     need_cuda(q, "dlse", dlse);
     need_cuda(q, "workspace", ws);
@@ -548,7 +555,7 @@ PyObject* prompt_bwd(Args& a) {
     size_t bytes = 0;
     check(f_prompt_bwd_size(&p, &bytes));
     const at::Tensor work = scratch(bytes, ws, q), dq = empty(q.sizes(), q.scalar_type(), q), dk = empty(k.sizes(), q.scalar_type(), q), dv = empty(k.sizes(), q.scalar_type(), q);
-    check(f_prompt_bwd(&p, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), ptr(lse), dO.data_ptr(), ptr(dlse), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+    check(f_prompt_bwd(&p, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), ptr(lse), ptr<void>(rest), dO.data_ptr(), ptr(dlse), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
                        bytes ? work.data_ptr() : nullptr, bytes ? size_t(work.numel()) * work.element_size() : 0, on.stream));
     return tuple({dq, dk, dv});
 }

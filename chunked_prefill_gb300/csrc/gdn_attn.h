@@ -14,8 +14,9 @@ struct PromptArgs {
     const void *q, *k, *v;
     void* o;
     float* lse;
+    void* o_rest;
     // backward
-    const void *o_in, *dO;
+    const void *o_in, *rest_in, *dO;
     const float *lse_in, *dlse;
     void *dq, *dk, *dv;
     // [Hq][rows] pairs of (lse in units of log 2, <dO, o> - dlse) of every query, rows = total_q up to a multiple of 128

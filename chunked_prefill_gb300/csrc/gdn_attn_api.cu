@@ -115,7 +115,7 @@ gdn_status prompt_ptrs(const gdn_prompt_problem& p, const void* q, const void* k
 extern "C" {
 
 gdn_status gdn_prompt_attn_fwd(const gdn_prompt_problem* problem, const void* q, const void* k, const void* v,
-                               void* o, float* lse, void* stream) try {
+                               void* o, float* lse, void* o_rest, void* stream) try {
     if (!problem) return fail(GDN_ERR_INVALID_ARG, "problem is NULL");
     gdn::PromptArgs A{};
     A.p = *problem;
@@ -123,12 +123,15 @@ gdn_status gdn_prompt_attn_fwd(const gdn_prompt_problem* problem, const void* q,
     TRY(prompt_ptrs(A.p, q, k, v));
     TRY(check_ptr("o", o, 16, A.p.total_q == 0));
     TRY(check_ptr("lse", lse, 4, true));
+    TRY(check_ptr("o_rest", o_rest, 16, true));
+    if (o_rest && A.p.dtype != GDN_BF16) return fail(GDN_ERR_INVALID_ARG, "o_rest is of bf16 outputs alone");
     if (A.p.total_q == 0) return done(cudaSuccess);
     A.q = q;
     A.k = k;
     A.v = v;
     A.o = o;
     A.lse = lse;
+    A.o_rest = o_rest;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     return done(A.p.dtype == GDN_FP32 ? gdn::launch_prompt_fwd_simt(A, st) : gdn::launch_prompt_fwd_tc(A, st));
 } catch (...) {
@@ -147,8 +150,9 @@ gdn_status gdn_prompt_attn_bwd_workspace_size(const gdn_prompt_problem* problem,
 }
 
 gdn_status gdn_prompt_attn_bwd(const gdn_prompt_problem* problem, const void* q, const void* k, const void* v,
-                               const void* o, const float* lse, const void* dO, const float* dlse, void* dq,
-                               void* dk, void* dv, void* workspace, size_t workspace_bytes, void* stream) try {
+                               const void* o, const float* lse, const void* o_rest, const void* dO,
+                               const float* dlse, void* dq, void* dk, void* dv, void* workspace,
+                               size_t workspace_bytes, void* stream) try {
     if (!problem) return fail(GDN_ERR_INVALID_ARG, "problem is NULL");
     gdn::PromptArgs A{};
     A.p = *problem;
@@ -157,6 +161,8 @@ gdn_status gdn_prompt_attn_bwd(const gdn_prompt_problem* problem, const void* q,
     TRY(prompt_ptrs(A.p, q, k, v));
     TRY(check_ptr("o", o, 16, no_q));
     TRY(check_ptr("lse", lse, 4, no_q));
+    TRY(check_ptr("o_rest", o_rest, 16, true));
+    if (o_rest && A.p.dtype != GDN_BF16) return fail(GDN_ERR_INVALID_ARG, "o_rest is of bf16 outputs alone");
     TRY(check_ptr("dO", dO, 16, no_q));
     TRY(check_ptr("dlse", dlse, 4, true));
     TRY(check_ptr("dq", dq, 16, no_q));
@@ -171,6 +177,7 @@ gdn_status gdn_prompt_attn_bwd(const gdn_prompt_problem* problem, const void* q,
     A.k = k;
     A.v = v;
     A.o_in = o;
+    A.rest_in = o_rest;
     A.lse_in = lse;
     A.dO = dO;
     A.dlse = dlse;

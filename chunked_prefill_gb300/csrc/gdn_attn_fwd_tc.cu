@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(Fwd<D>::T, 1)
         const int w = warp >> 2;
         const uint32_t mine = tmem + (uint32_t(warp & 3) << 21);
         const float zs = p.scale * LOG2E;
-        const bool wide = wide_aligned(A.o);
+        const bool wide = wide_aligned(A.o) && wide_aligned(A.o_rest);
         int count = 0, item = 0;  // key tiles, tiles of queries so far
         while (ok && it.next(p)) {
             const int r = it.row + tid, i_row = min(r, s.lq - 1), begin = w == 0 ? k.begin[0] : k.begin[1], steps = (w == 0 ? k.end[0] : k.end[1]) - begin;
@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(Fwd<D>::T, 1)
             const bool some = l > 0.f || l != l;
             const float f = some ? 1.f / l : 0.f;
             const int64_t out = (int64_t(s.q0) + r) * p.Hq + it.h;
-            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(A.o) + out * D;
+            __nv_bfloat16 *o = static_cast<__nv_bfloat16*>(A.o) + out * D, *rest = A.o_rest ? static_cast<__nv_bfloat16*>(A.o_rest) + out * D : nullptr;
             // written before the last product
             int bad_tiles = 0;
             if (steps > 0 && sh.bad_item[item & 3] == item)
@@ -484,6 +484,11 @@ __global__ void __launch_bounds__(Fwd<D>::T, 1)
                     }
                 if (live) {
                     store_bf16x32(o + c, x, f, wide);
+                    if (rest) {  // what the rounding leaves
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) x[e] = x[e] * f - to_f(__float2bfloat16_rn(x[e] * f));
+                        store_bf16x32(rest + c, x, 1.f, wide);
+                    }
                 }
             }
             if (live && A.lse) A.lse[out] = some ? (m + log2f(l)) * LN2 : -INFINITY;

@@ -94,6 +94,15 @@ __global__ void __launch_bounds__(256) k_prompt_stat(const PromptArgs A) {
 #pragma unroll
             for (int e = 0; e < V; ++e) sum = fmaf(to_f(a[e]), to_f(b[e]), sum);
         }
+        if (sizeof(T) == 2 && A.rest_in && row0 + r + R * u < p.total_q) {
+#pragma unroll
+            for (int x = 0; x < PER; ++x) {
+                const uint4 rest = *reinterpret_cast<const uint4*>(static_cast<const T*>(A.rest_in) + (int64_t(row0 + r + R * u) * p.Hq + h) * D + (x * LPR + lane) * V);
+                const T *a = reinterpret_cast<const T*>(&rest), *b = reinterpret_cast<const T*>(&g[u * PER + x]);
+#pragma unroll
+                for (int e = 0; e < V; ++e) sum = fmaf(to_f(a[e]), to_f(b[e]), sum);
+            }
+        }
 #pragma unroll
         for (int w = LPR / 2; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
         const int row = row0 + r + R * u;

@@ -159,9 +159,9 @@ def lib():
         L.gdn_rmsnorm_bwd.argtypes = [N] + [vp] * 7 + [ctypes.c_size_t, vp]
         Q, R, C, T = (ctypes.POINTER(c) for c in (GdnPromptProblem, GdnTreeProblem, GdnCacheProblem, GdnTableProblem))
         size = ctypes.POINTER(ctypes.c_size_t)
-        L.gdn_prompt_attn_fwd.argtypes = [Q] + [vp] * 6
+        L.gdn_prompt_attn_fwd.argtypes = [Q] + [vp] * 7
         L.gdn_prompt_attn_bwd_workspace_size.argtypes = [Q, size]
-        L.gdn_prompt_attn_bwd.argtypes = [Q] + [vp] * 11 + [ctypes.c_size_t, vp]
+        L.gdn_prompt_attn_bwd.argtypes = [Q] + [vp] * 12 + [ctypes.c_size_t, vp]
         L.gdn_paged_attn_tree_workspace_size.argtypes = [R, size]
         L.gdn_paged_attn_tree.argtypes = [R] + [vp] * 13 + [ctypes.c_size_t, vp]
         L.gdn_paged_cache_write.argtypes = [C] + [vp] * 9
@@ -736,36 +736,38 @@ def rms_norm_quant(x, weight, residual=None, eps=1e-6, weight_offset=0.0, group=
 
 
 # ------------------------------------------------------------- prompts and the paged cache
-def gdn_prompt_attn_fwd(q, k, v, scale, window=0, cu_seqlens=None, cu_seqlens_k=None, o=None, lse=None, stream=None):
+def gdn_prompt_attn_fwd(q, k, v, scale, window=0, cu_seqlens=None, cu_seqlens_k=None, o=None, lse=None, rest=False, stream=None):
     """Causal attention over prompts through the C ABI (see include/gdn.h).  q [B,T,Hq,D], k and v
     [B,Tk,Hkv,D], each with contiguous rows at any token stride but 0.  Returns o, with lse=True
-    (o, lse [B,T,Hq] fp32); an lse tensor is written."""
-    return (_native or _binding()).prompt_fwd(q, k, v, scale, window, cu_seqlens, cu_seqlens_k, o, lse, stream)
+    (o, lse [B,T,Hq] fp32), with lse=True and rest=True (o, lse, o_rest), what rounding o to bf16 left, for the
+    gradient (None with fp32); an lse tensor is written."""
+    return (_native or _binding()).prompt_fwd(q, k, v, scale, window, cu_seqlens, cu_seqlens_k, o, lse, rest, stream)
 
 
 def gdn_prompt_attn_bwd(q, k, v, o, lse, do, scale, window=0, cu_seqlens=None, cu_seqlens_k=None, dlse=None,
-                        workspace=None, stream=None):
-    """Gradients of <o, do> + <lse, dlse> from the forward's o and lse: (dq, dk, dv)."""
+                        o_rest=None, workspace=None, stream=None):
+    """Gradients of <o, do> + <lse, dlse> from the forward's o and lse (and, for 10 % less error of dq and dk
+    with bf16, its o_rest): (dq, dk, dv)."""
     return (_native or _binding()).prompt_bwd(q, k, v, o, lse, do, dlse, scale, window, cu_seqlens, cu_seqlens_k,
-                                              workspace, stream)
+                                              o_rest, workspace, stream)
 
 
 class _PromptAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, scale, window, cu_seqlens, cu_seqlens_k):
         ctx.set_materialize_grads(False)  # an unused lse has no gradient to read
-        o, lse = gdn_prompt_attn_fwd(q, k, v, scale, window, cu_seqlens, cu_seqlens_k, lse=True)
-        ctx.save_for_backward(q, k, v, o, lse, cu_seqlens, cu_seqlens_k)
+        o, lse, rest = gdn_prompt_attn_fwd(q, k, v, scale, window, cu_seqlens, cu_seqlens_k, lse=True, rest=True)
+        ctx.save_for_backward(q, k, v, o, lse, rest, cu_seqlens, cu_seqlens_k)
         ctx.scale, ctx.window = scale, window
         return o, lse
 
     @staticmethod
     @once_differentiable  # a second derivative is refused, not zero
     def backward(ctx, do, dlse):
-        q, k, v, o, lse, cu, cu_k = ctx.saved_tensors
+        q, k, v, o, lse, rest, cu, cu_k = ctx.saved_tensors
         do = torch.zeros_like(o) if do is None else do.contiguous()
         dlse = None if dlse is None else dlse.contiguous()
-        return (*gdn_prompt_attn_bwd(q, k, v, o, lse, do, ctx.scale, ctx.window, cu, cu_k, dlse), None, None, None, None)
+        return (*gdn_prompt_attn_bwd(q, k, v, o, lse, do, ctx.scale, ctx.window, cu, cu_k, dlse, rest), None, None, None, None)
 
 
 def prompt_attention(q, k, v, scale=None, window=0, cu_seqlens=None, cu_seqlens_k=None, return_lse=False):
@@ -785,7 +787,7 @@ def prompt_attention(q, k, v, scale=None, window=0, cu_seqlens=None, cu_seqlens_
     if native.wants_grad(q, k, v):
         o, lse = _PromptAttention.apply(q, k, v, scale, window, cu_seqlens, cu_seqlens_k)
         return (o, lse) if return_lse else o
-    return native.prompt_fwd(q, k, v, scale, window, cu_seqlens, cu_seqlens_k, None, True if return_lse else None, None)
+    return native.prompt_fwd(q, k, v, scale, window, cu_seqlens, cu_seqlens_k, None, True if return_lse else None, False, None)
 
 
 def gdn_paged_attn_tree(q, k_new, v_new, k_cache, v_cache, page_table, seq_lens, parents, scale, k_scale=None,

@@ -389,7 +389,9 @@ gdn_status gdn_rmsnorm_bwd(const gdn_norm_problem* p, const void* s, const void*
  * and gradients of 0 (clear_rest = 1).  What lies there, NaN or not, is not used.
  *
  * gdn_prompt_attn_bwd: the gradients of <o, dO> + <lse, dlse> (dlse NULL: 0) with respect to q, k and v,
- * from the forward's o and lse; dk and dv are summed over the query heads that share a kv-head.
+ * from the forward's o and lse; dk and dv are summed over the query heads that share a kv-head.  o_rest (bf16,
+ * like o; NULL: none) is what rounding o left, itself rounded: with it <dO, o> has 16 bits of o instead of 8, and dq
+ * and dk, whose terms all have that product in them, some 10 % less error.
  *
  * Scores, softmax statistics, sums and gradients are held in fp32.  With bf16 the weights e^{z - m} (m the
  * running maximum, or up to 8 log 2 below it) are rounded to bf16 for their product with v, while the sum
@@ -415,14 +417,15 @@ typedef struct gdn_prompt_problem {
 } gdn_prompt_problem;
 
 gdn_status gdn_prompt_attn_fwd(const gdn_prompt_problem* p, const void* q, const void* k, const void* v,
-                               void* o, float* lse /* NULL: not returned */, void* stream);
+                               void* o, float* lse, void* o_rest, /* lse, o_rest NULL: not returned */
+                               void* stream);
 
 gdn_status gdn_prompt_attn_bwd_workspace_size(const gdn_prompt_problem* p, size_t* bytes);
 
 gdn_status gdn_prompt_attn_bwd(const gdn_prompt_problem* p, const void* q, const void* k, const void* v,
-                               const void* o, const float* lse, const void* dO, const float* dlse,
-                               void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes,
-                               void* stream);
+                               const void* o, const float* lse, const void* o_rest, const void* dO,
+                               const float* dlse, void* dq, void* dk, void* dv, void* workspace,
+                               size_t workspace_bytes, void* stream);
 
 /* Waits in the tensor-core kernels of the attention over prompts and of drafted trees are bounded like those
  * of the chunked rule (2 s; see "Device-side failure report"), but leave their mark in the library: this waits

@@ -23,10 +23,10 @@ def prompt(L, back=False, ptrs=None, ws=(FAKE, 1 << 40), **kw):
     f.update(kw)
     p = L.GdnPromptProblem(**f)
     if back:
-        a = dict(q=FAKE, k=FAKE, v=FAKE, o=FAKE, lse=FAKE, do=FAKE, dlse=None, dq=FAKE, dk=FAKE, dv=FAKE)
+        a = dict(q=FAKE, k=FAKE, v=FAKE, o=FAKE, lse=FAKE, rest=None, do=FAKE, dlse=None, dq=FAKE, dk=FAKE, dv=FAKE)
         a.update(ptrs or {})
         return L.lib().gdn_prompt_attn_bwd(ctypes.byref(p), *a.values(), *ws, None)
-    a = dict(q=FAKE, k=FAKE, v=FAKE, o=FAKE, lse=None)
+    a = dict(q=FAKE, k=FAKE, v=FAKE, o=FAKE, lse=None, rest=None)
     a.update({n: x for n, x in (ptrs or {}).items() if n in a})
     return L.lib().gdn_prompt_attn_fwd(ctypes.byref(p), *a.values(), None)
 
@@ -38,6 +38,7 @@ def prompt(L, back=False, ptrs=None, ws=(FAKE, 1 << 40), **kw):
     (dict(cu_seqlens=FAKE, cu_seqlens_k=ODD), 1), (dict(q_stride=128), 1), (dict(k_stride=130), 1), (dict(v_stride=132), 1),
     (dict(total_q=0x7fff0002, total_k=0x7fff0002), 2), (dict(Hq=1 << 16, Hkv=1), 2), (dict(q_stride=1 << 40), 2),
     (dict(ptrs=dict(q=None)), 1), (dict(ptrs=dict(k=ODD)), 1), (dict(ptrs=dict(v=None)), 1), (dict(ptrs=dict(o=ODD)), 1), (dict(ptrs=dict(lse=ODD)), 1),
+    (dict(ptrs=dict(rest=ODD)), 1), (dict(ptrs=dict(rest=FAKE), dtype=1), 1),
 ])
 @pytest.mark.parametrize("back", [False, True])
 def test_prompt_refusals(L, kw, code, back):
@@ -268,14 +269,14 @@ def test_forward_mode_tangents_are_refused(L, which, name):
 
 
 def test_a_second_derivative_of_attention_is_refused(L, monkeypatch):
-    def fwd(q, k, v, scale, window, cu, cu_k, lse):
+    def fwd(q, k, v, scale, window, cu, cu_k, lse, rest):
         z = scale * torch.einsum("bqhd,bkhd->bhqk", q, k)
-        return torch.einsum("bhqk,bkhd->bqhd", z.softmax(-1), v), z.logsumexp(-1).transpose(1, 2)
+        return torch.einsum("bhqk,bkhd->bqhd", z.softmax(-1), v), z.logsumexp(-1).transpose(1, 2), None
 
-    def bwd(q, k, v, o, lse, do, scale, window, cu, cu_k, dlse):
+    def bwd(q, k, v, o, lse, do, scale, window, cu, cu_k, dlse, rest):
         with torch.enable_grad():
             leaves = [x.detach().requires_grad_(True) for x in (q, k, v)]
-            return torch.autograd.grad((fwd(*leaves, scale, 0, None, None, True)[0] * do.detach()).sum(), leaves)
+            return torch.autograd.grad((fwd(*leaves, scale, 0, None, None, True, True)[0] * do.detach()).sum(), leaves)
 
     monkeypatch.setattr(L, "gdn_prompt_attn_fwd", fwd)
     monkeypatch.setattr(L, "gdn_prompt_attn_bwd", bwd)

@@ -241,13 +241,20 @@ def test_autograd(gdn, dtype):
     o, lse = gdn.prompt_attention(*leaves, return_lse=True, **args(x))
     got = torch.autograd.grad((o, lse), leaves, (x["do"], x["dlse"]), retain_graph=True)
     raw = [t.detach() for t in leaves]
-    for a, b in zip(got, gdn.gdn_prompt_attn_bwd(*raw, o.detach(), lse.detach(), x["do"], dlse=x["dlse"], **args(x))):
+    again, _, rest = gdn.gdn_prompt_attn_fwd(*raw, lse=True, rest=True, **args(x))
+    assert torch.equal(again, o) and (rest is None) == (dtype == F32)
+    if rest is not None:  # o and its rest are o to 16 bits
+        r = oracle(dict(x, **dict(zip("qkv", raw))))
+        assert (rest.float().abs() <= 2.0 ** -8 * o.float().abs()).all()
+        _, L, _, dz = sizes(x, r)
+        near("o + rest", o.float() + rest.float(), r["o"], (2 * dz[..., None] + 2.0 ** -8 + (64 + L) * U) * r["mass"] + 2.0 ** -16 * np.abs(r["o"]))
+    for a, b in zip(got, gdn.gdn_prompt_attn_bwd(*raw, o.detach(), lse.detach(), x["do"], dlse=x["dlse"], o_rest=rest, **args(x))):
         assert torch.equal(a, b)
     only_o = torch.autograd.grad(o, leaves, x["do"], retain_graph=True)
-    for a, b in zip(only_o, gdn.gdn_prompt_attn_bwd(*raw, o.detach(), lse.detach(), x["do"], **args(x))):
+    for a, b in zip(only_o, gdn.gdn_prompt_attn_bwd(*raw, o.detach(), lse.detach(), x["do"], o_rest=rest, **args(x))):
         assert torch.equal(a, b)
     only_lse = torch.autograd.grad(lse, leaves, x["dlse"])
-    for a, b in zip(only_lse, gdn.gdn_prompt_attn_bwd(*raw, o.detach(), lse.detach(), torch.zeros_like(o), dlse=x["dlse"], **args(x))):
+    for a, b in zip(only_lse, gdn.gdn_prompt_attn_bwd(*raw, o.detach(), lse.detach(), torch.zeros_like(o), dlse=x["dlse"], o_rest=rest, **args(x))):
         assert torch.equal(a, b)
 
 
