@@ -3,10 +3,12 @@ layer between RMS norms, random weights.
 
     python examples/hybrid_decode.py
 
-The prompt goes through the fused prologue and the chunked rule; every further token through one
-step of the recurrent rule per layer (activations fused in), one new token against the paged
-key-value cache (written by the same call) and the norms with the residual's addition, the last
-one in 8 bits with a scale per row.  The plain products in between are torch's.
+The prompt goes through the fused prologue and the chunked rule, or causal attention and its keys and
+values into the paged cache; every further token through one step of the recurrent rule per layer
+(activations fused in), one new token against the paged key-value cache (written by the same call) and
+the norms with the residual's addition, the last one in 8 bits with a scale per row.  The page table is
+kept on the device: the captured step takes a page for itself where a sequence needs one.  The plain
+products in between are torch's.
 """
 from __future__ import annotations
 
@@ -101,13 +103,10 @@ class HybridModel:
                 pool[slots.long()] = state
             else:
                 q, k, v = self._attention_inputs(w, y)
+                o = gdn.prompt_attention(q, k, v)
                 at = torch.arange(T, device=self.device)
-                page = table[:, at // c.page].long()
-                pool[0][page, at % c.page], pool[1][page, at % c.page] = k, v
-                G = c.heads // c.kv_heads
-                z = torch.einsum("nqhd,nkhd->nhqk", q.float(), k.float().repeat_interleave(G, 2)) * c.head_dim ** -0.5
-                z = z.masked_fill(at[None, :] > at[:, None], float("-inf"))
-                o = torch.einsum("nhqk,nkhd->nqhd", z.softmax(-1), v.float().repeat_interleave(G, 2)).to(c.dtype)
+                slots_k = (table[:, at // c.page].long() * c.page + at % c.page).flatten()
+                gdn.paged_cache_write(k, v, pool[0], pool[1], slots_k)
             x = o.flatten(2) @ w["out"]
         return self._logits(x[:, -1], residual[:, -1])
 
@@ -140,10 +139,14 @@ def main():
     prompt = torch.randint(0, cfg.vocab, (N, T), generator=gen, device="cuda")
     pools = model.new_cache(slots=N + 2, pages=N * max_pages)
     slots = torch.tensor([3, 0, 5, 1], dtype=torch.int32, device="cuda")
-    table = torch.randperm(N * max_pages, generator=gen, device="cuda").to(torch.int32).view(N, max_pages)
+    # no sequence has a page yet, all are on the stack; room for the prompts
+    table, lens = torch.zeros(N, max_pages, dtype=torch.int32, device="cuda"), torch.zeros(N, dtype=torch.int32, device="cuda")
+    stack = torch.randperm(N * max_pages, generator=gen, device="cuda").to(torch.int32)
+    free = torch.tensor([N * max_pages], dtype=torch.int32, device="cuda")
+    gdn.page_table_extend(table, lens, torch.full_like(lens, T), stack, free, cfg.page, N * T)
     logits = model.prefill(prompt, pools, slots, table)
     token = logits.argmax(-1)
-    lens = torch.full((N,), T, dtype=torch.int32, device="cuda")
+    one = torch.ones_like(lens)
 
     # the step as a captured graph: lengths, slots and pages are read on the device
     side = torch.cuda.Stream()
@@ -153,7 +156,7 @@ def main():
         model.decode(token, kept, slots, table, lens + 1)  # warm-up on copies
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph, stream=side):
-            lens += 1
+            gdn.page_table_extend(table, lens, one, stack, free, cfg.page, N)  # lens count the new token then
             token.copy_(model.decode(token, pools, slots, table, lens).argmax(-1))
     torch.cuda.current_stream().wait_stream(side)
     out = [token.clone()]
