@@ -83,7 +83,12 @@ gdn_status check_cache(gdn_cache_problem& p) {
     const int64_t act = 16 / int64_t(elem(p.dtype));
     TRY(check_stride("k_stride", p.k_stride, int64_t(p.Hkv) * p.D, act));
     TRY(check_stride("v_stride", p.v_stride, int64_t(p.Hkv) * p.D, act));
-    return check_cache_strides(16 / int64_t(elem(p.cache_dtype)), p.k_page_stride, p.k_token_stride, p.k_head_stride, p.v_page_stride, p.v_token_stride, p.v_head_stride);
+    TRY(check_cache_strides(16 / int64_t(elem(p.cache_dtype)), p.k_page_stride, p.k_token_stride, p.k_head_stride, p.v_page_stride, p.v_token_stride, p.v_head_stride));
+    // a head, token or page that stands for several would be written by each
+    if ((p.num_pages > 1 && !(p.k_page_stride && p.v_page_stride)) || (p.page_size > 1 && !(p.k_token_stride && p.v_token_stride)) ||
+        (p.Hkv > 1 && !(p.k_head_stride && p.v_head_stride)))
+        return fail(GDN_ERR_INVALID_ARG, "a cache that is written to must not have strides of 0");
+    return GDN_OK;
 }
 
 gdn_status check_table(gdn_table_problem& p) {

@@ -477,7 +477,8 @@ gdn_status gdn_paged_attn_tree(const gdn_tree_problem* p, const void* q, const v
  * goes to slot slots[i] % page_size of page slots[i] / page_size, as k / k_scale[j] and v / v_scale[j] rounded
  * to the cache's type (in 8 bits clamped to +-448, NaN kept; NULL scales: 1).  Slots outside
  * [0, num_pages page_size) and rows outside [0, num_rows) are skipped.  Two rows of a call may not have the
- * same slot: which values stay is not defined then.
+ * same slot: which values stay is not defined then.  Strides of the caches are not 0 where there is more than one
+ * page, token or head.
  * ------------------------------------------------------------------------------------ */
 typedef struct gdn_cache_problem {
     int64_t count, num_rows;

@@ -111,11 +111,17 @@ def write(L, ptrs=None, **kw):
     (dict(count=-1), 1), (dict(num_rows=-1), 1), (dict(num_pages=-1), 1), (dict(count=1 << 32), 2), (dict(Hkv=0), 1), (dict(D=0), 1), (dict(D=72), 2),
     (dict(dtype=1), 1), (dict(cache_dtype=1), 1), (dict(page_size=0), 1), (dict(k_stride=64), 1), (dict(v_stride=130), 1), (dict(k_head_stride=4), 1),
     (dict(v_token_stride=-128), 1), (dict(Hkv=1 << 20), 2),
+    (dict(k_page_stride=0), 1), (dict(v_page_stride=0), 1), (dict(k_token_stride=0), 1), (dict(v_token_stride=0), 1), (dict(k_head_stride=0), 1), (dict(v_head_stride=0), 1),
     (dict(ptrs=dict(k=None)), 1), (dict(ptrs=dict(v=ODD)), 1), (dict(ptrs=dict(kc=None)), 1), (dict(ptrs=dict(vc=ODD)), 1), (dict(ptrs=dict(slots=FAKE + 4)), 1),
     (dict(ptrs=dict(slots=None)), 1), (dict(ptrs=dict(rows=ODD)), 1), (dict(ptrs=dict(ks=ODD)), 1), (dict(ptrs=dict(vs=ODD)), 1),
 ])
 def test_write_refusals(L, kw, code):
     assert write(L, **kw) == code and L.lib().gdn_last_error()
+
+
+def test_write_to_caches_of_one_of_each_has_no_strides_to_check(L):
+    assert write(L, num_pages=1, page_size=1, Hkv=1, count=0, k_stride=64, v_stride=64, k_page_stride=0, v_page_stride=0, k_token_stride=0, v_token_stride=0,
+                 k_head_stride=0, v_head_stride=0) == 0
 
 
 def test_write_of_nothing_is_fine(L):
