@@ -525,7 +525,7 @@ cudaError_t launch_d(const PromptArgs& A, cudaStream_t st) {
     // turns does.  Short ones take turns, for the overlap of one tile's end with the next one's begin.  32 / 8 heads, 128 features,
     // turns and one each: 16 x 512 tokens 93 and 110 us, 8 x 2048 299 and 317, 2 x 8192 802 and 783, 1 x 32768 (16 / 4) 2782 and 2694.
     const int64_t all = tiles * p.Hq, sms = sm_count_cached();
-    const bool turns = p.total_k / p.num_seqs <= 4096;
+    const bool turns = p.num_seqs == 0 || p.total_k / p.num_seqs <= 4096 || all > 0x7fffffff;  // a grid has 2^31 - 1 CTAs at most
     timing_begin("prompt_attn_fwd", st);
     k_prompt_fwd_tc<D><<<unsigned(turns && all > sms ? sms : all), L::T, L::SMEM, st>>>(A, q, k, v, int(tiles));
     timing_end(st);

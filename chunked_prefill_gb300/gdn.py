@@ -766,6 +766,8 @@ class _PromptAttention(torch.autograd.Function):
     def backward(ctx, do, dlse):
         q, k, v, o, lse, rest, cu, cu_k = ctx.saved_tensors
         do = torch.zeros_like(o) if do is None else do.contiguous()
+        if do.data_ptr() % 16:  # a part of a flat buffer, as of torch.cat's gradient
+            do = do.clone()
         dlse = None if dlse is None else dlse.contiguous()
         return (*gdn_prompt_attn_bwd(q, k, v, o, lse, do, ctx.scale, ctx.window, cu, cu_k, dlse, rest), None, None, None, None)
 
@@ -780,7 +782,10 @@ def prompt_attention(q, k, v, scale=None, window=0, cu_seqlens=None, cu_seqlens_
     stands at the last key: more keys than queries are a prompt's last part with the earlier keys given.
     window > 0 attends to the last `window` keys.  Queries that see no key, and rows that no sequence
     covers, get o = 0 and lse = -inf.  With bf16 the weights are rounded to bf16 for their product with v, their
-    sum is not.  Differentiable with respect to q, k and v, once."""
+    sum is not.  Differentiable with respect to q, k and v, once.
+
+    Forward and backward can be captured into a CUDA graph.  As for every function of autograd, leaves whose
+    gradients are captured may then not be held by a graph of autograd from outside the capture."""
     native = _native or _binding()
     if scale is None:
         scale = q.shape[-1] ** -0.5

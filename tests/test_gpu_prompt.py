@@ -134,6 +134,17 @@ def test_lengths_and_heads(gdn, dtype, D, Hq, Hkv):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("front,behind", [(0, 0), (0, 300), (5, 0)])
+def test_no_sequence_at_all(gdn, dtype, front, behind):
+    """Offsets of one element: rows, but no sequence that covers them."""
+    x = make([], 4, 2, 128, dtype, front=front, behind=behind)
+    o, lse, grads = run(gdn, x)
+    assert o.shape == x["q"].shape and (o == 0).all() and torch.isneginf(lse).all()
+    for g, t in zip(grads, (x["q"], x["k"], x["v"])):
+        assert g.shape == t.shape and (g == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("window", [1, 2, 63, 64, 65, 128, 200, 1 << 30])
 def test_window(gdn, dtype, window):
     check(gdn, make([(300, 300), (130, 400), (5, 2), (0, 3), (400, 130)], 4, 2, 64, dtype, seed=window % 97), window)
@@ -312,6 +323,79 @@ def test_captured_calls_serve_other_lengths(gdn, dtype):
         r = oracle(z, 0, True)
         check_fwd(z, r, out[0], out[1])
         check_bwd(z, r, *out[2])
+
+
+def test_captured_forward_and_gradient(gdn):
+    """Autograd's own forward and backward in a graph, of leaves that were made for it."""
+    x, y = (make([(190, 190), (66, 66)], 4, 2, 64, seed=s) for s in (1, 2))
+    leaves = [x[n].clone().requires_grad_(True) for n in ("q", "k", "v")]
+    do, cu = x["do"].clone(), x["cu_seqlens"]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+
+    def step():
+        o, lse = gdn.prompt_attention(*leaves, scale=x["scale"], cu_seqlens=cu, return_lse=True)
+        return o, lse, torch.autograd.grad(o, leaves, do)
+
+    with torch.cuda.stream(side):
+        step()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            o, lse, grads = step()
+    torch.cuda.current_stream().wait_stream(side)
+    for z in (y, x):
+        with torch.no_grad():
+            for t, n in zip(leaves, ("q", "k", "v")):
+                t.copy_(z[n])
+        do.copy_(z["do"])
+        graph.replay()
+        torch.cuda.synchronize()
+        r = oracle(z, 0, True)
+        check_fwd(z, r, o, lse)
+        check_bwd(z, r, *grads)
+
+
+def test_a_gradient_that_begins_anywhere(gdn):
+    """The gradient of a concatenation of flat tensors is a view at any offset."""
+    x = make([(70, 70)], 2, 2, 64)
+    grads = []
+    for odd in (0, 3):
+        leaf = x["v"].clone().requires_grad_(True)
+        o = gdn.prompt_attention(x["q"], x["k"], leaf)
+        w = torch.cat([x["do"].new_zeros(odd), x["do"].flatten()])
+        (torch.cat([o.new_zeros(odd), o.flatten()]) * w).sum().backward()
+        grads.append(leaf.grad)
+    assert torch.equal(*grads)
+
+
+def test_two_calls_at_once(gdn):
+    """Calls on two streams, and two captured graphs with a workspace each, replayed together."""
+    xs = [make([(900, 900), (300, 500)], 4, 2, 128, seed=s) for s in (1, 2)]
+    want = [run(gdn, x) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+
+    def same(got):
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1]) and all(torch.equal(a, b) for a, b in zip(g[2], w[2]))
+
+    torch.cuda.synchronize()
+    for _ in range(5):
+        outs = []
+        for x, st in zip(xs, streams):
+            with torch.cuda.stream(st):
+                outs.append(run(gdn, x))
+        same(outs)
+    graphs, outs = [], []
+    for x, st in zip(xs, streams):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=st):
+            outs.append(run(gdn, x))
+    for _ in range(5):
+        for graph, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                graph.replay()
+        same(outs)
 
 
 def test_on_another_stream(gdn):

@@ -239,6 +239,32 @@ def test_repeated_calls_and_workspaces_give_the_same_bits(gdn):
         assert torch.equal(again[0], o) and torch.equal(again[1], lse)
 
 
+def test_two_calls_at_once(gdn):
+    """On two streams, and as two captured graphs that share a workspace and run one after the other."""
+    xs = [make([3000, 40, 900], 9, 8, 2, 128, 16, seed=s) for s in (1, 2)]
+    want = [call(gdn, x) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        outs = []
+        for x, st in zip(xs, streams):
+            with torch.cuda.stream(st):
+                outs.append(call(gdn, x))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for g, w in zip(outs, want) for a, b in zip(g, w))
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    graphs, outs = [], []
+    for x in xs:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=streams[0]):
+            outs.append(call(gdn, x, workspace=ws))
+    with torch.cuda.stream(streams[0]):
+        for graph in graphs * 3:
+            graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for g, w in zip(outs, want) for a, b in zip(g, w))
+
+
 def test_long_offsets(gdn):
     """Pages whose offsets pass 32 bits of elements."""
     pages, page, Hkv, D = (1 << 31) // (64 * 128) + 40, 64, 1, 128
