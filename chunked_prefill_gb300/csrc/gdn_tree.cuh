@@ -58,15 +58,15 @@ __device__ __forceinline__ int first_cached(const TreeArgs& A, const TreeRange& 
 }
 
 // Joins the parts of the rows that several CTAs have parts of, in the list's order: a warp to a row.  A (sequence, block)
-// that several have is found at the border between the first and the second of them: blocks (CTA, 8 of its first block's
-// rows), of which those whose CTA is a second one work.  (A warp to every row of the output: 66 us for 64 sequences of 31
-// drafted tokens and 64 heads, with 150 borders among 512 blocks.)
+// that several have is found at the border between the first and the second of them: blocks (CTA, 8 rows at a
+// time of its first block), of which those whose CTA is a second one work.  (A warp to every row of the output: 66 us for
+// 64 sequences of 31 drafted tokens and 64 heads, with 150 borders among 512 blocks.)
 template <typename Act, int D>
 __global__ void __launch_bounds__(256) k_tree_join(const TreeArgs A, int rows, int ctas) {
     constexpr int E = D / 32, NB = D == 256 ? 4 : 8;
     tc::pdl_wait();
     const gdn_tree_problem& p = A.p;
-    const int lane = threadIdx.x & 31, cta = blockIdx.x, group = cta % A.groups, c = cta / A.groups, in = blockIdx.y * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, cta = blockIdx.x, group = cta % A.groups, c = cta / A.groups;
     const int64_t share = share_of(A.before[p.num_seqs] * A.heads, ctas / A.groups, 1), lo = c * share;
     if (c == 0 || lo >= A.before[p.num_seqs] * A.heads) return;
     int n = 0, end = p.num_seqs;  // the last sequence that begins at or before lo: 32 candidates a round
@@ -80,58 +80,64 @@ __global__ void __launch_bounds__(256) k_tree_join(const TreeArgs A, int rows, i
     const int head = int(quotient(rest, tiles));
     const int64_t at0 = before * A.heads + head * tiles, at1 = at0 + tiles;
     const int c0 = int(quotient(at0, share)), c1 = int(quotient(at1 - 1, share));
-    const int G = p.Hq / p.Hkv, all_rows = p.T * G, nb = (all_rows + rows - 1) / rows, block = head * A.groups + group, hk = block / nb, r = (block - hk * nb) * rows + in;
-    if (at0 == lo || c0 != c - 1 || r >= all_rows) return;  // begins here, or joined at an earlier border
-    const int t = r / G;
-    const int64_t row = (int64_t(n) * p.T + t) * p.Hq + hk * G + (r - t * G);
+    const int G = p.Hq / p.Hkv, all_rows = p.T * G, nb = (all_rows + rows - 1) / rows, block = head * A.groups + group, hk = block / nb;
+    if (at0 == lo || c0 != c - 1) return;  // begins here, or joined at an earlier border
     const int parts = c1 - c0 + 1;
-    float M = -INFINITY, S = 0.f, acc[E] = {};
-    for (int i0 = 0; i0 < parts; i0 += NB) {  // batches of parts, everything of a batch requested at once
-        float2 ml[NB];
-        float x[NB][E];
+#pragma unroll 1
+    for (int in = blockIdx.y * 8 + (threadIdx.x >> 5); in < rows; in += gridDim.y * 8) {
+        const int r = (block - hk * nb) * rows + in, t = r / G;
+        if (r >= all_rows) return;
+        const int64_t row = (int64_t(n) * p.T + t) * p.Hq + hk * G + (r - t * G);
+        float M = -INFINITY, S = 0.f, acc[E] = {};
+        for (int i0 = 0; i0 < parts; i0 += NB) {  // batches of parts, everything of a batch requested at once
+            float2 ml[NB];
+            float x[NB][E];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            const int i = i0 + b;
-            ml[b] = make_float2(-INFINITY, 0.f);
-            if (i < parts) {
-                const int64_t at = place_of((c0 + i) * A.groups + group, i > 0, rows) + in;
-                ml[b] = A.part_ml[at];
+            for (int b = 0; b < NB; ++b) {
+                const int i = i0 + b;
+                ml[b] = make_float2(-INFINITY, 0.f);
+                if (i < parts) {
+                    const int64_t at = place_of((c0 + i) * A.groups + group, i > 0, rows) + in;
+                    ml[b] = A.part_ml[at];
 #pragma unroll
-                for (int e = 0; e < E; ++e) x[b][e] = A.part[at * D + 32 * e + lane];
-            } else {
+                    for (int e = 0; e < E; ++e) x[b][e] = A.part[at * D + 32 * e + lane];
+                } else {
 #pragma unroll
-                for (int e = 0; e < E; ++e) x[b][e] = 0.f;
+                    for (int e = 0; e < E; ++e) x[b][e] = 0.f;
+                }
+            }
+            float top = M;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) top = fmaxf(top, ml[b].x);
+            const float c = M == -INFINITY ? 0.f : ex2(M - top);
+            M = top;
+            S *= c;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] *= c;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                if (ml[b].x == -INFINITY && ml[b].y == 0.f) continue;  // that part has none of this row's keys
+                const float w = ml[b].x == -INFINITY ? 1.f : ex2(ml[b].x - M);
+                S = fmaf(ml[b].y, w, S);
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] = fmaf(x[b][e], w, acc[e]);
             }
         }
-        float top = M;
+        const bool some = S > 0.f || S != S;
+        const float f = some ? 1.f / S : 0.f;
 #pragma unroll
-        for (int b = 0; b < NB; ++b) top = fmaxf(top, ml[b].x);
-        const float c = M == -INFINITY ? 0.f : ex2(M - top);
-        M = top;
-        S *= c;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] *= c;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            if (ml[b].x == -INFINITY && ml[b].y == 0.f) continue;  // that part has none of this row's keys
-            const float w = ml[b].x == -INFINITY ? 1.f : ex2(ml[b].x - M);
-            S = fmaf(ml[b].y, w, S);
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = fmaf(x[b][e], w, acc[e]);
-        }
+        for (int e = 0; e < E; ++e) static_cast<Act*>(A.o)[row * D + 32 * e + lane] = from_f<Act>(acc[e] * f);
+        if (A.lse && lane == 0) A.lse[row] = some ? (M + log2f(S)) * LN2 : -INFINITY;
     }
-    const bool some = S > 0.f || S != S;
-    const float f = some ? 1.f / S : 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) static_cast<Act*>(A.o)[row * D + 32 * e + lane] = from_f<Act>(acc[e] * f);
-    if (A.lse && lane == 0) A.lse[row] = some ? (M + log2f(S)) * LN2 : -INFINITY;
 }
 
 template <typename Act, int D>
 cudaError_t launch_tree_join(const TreeArgs& A, const TreePlan& plan, cudaStream_t st) {
     const int rows = A.p.T * (A.p.Hq / A.p.Hkv) < plan.rows ? A.p.T * (A.p.Hq / A.p.Hkv) : plan.rows;
+    // Up to 64 rows each warp has one; above, four in turn, for most CTAs find no work: 248 rows to a kv-head 37 and 26 us.
+    const int blocks = rows <= 64 ? (rows + 7) / 8 : (rows + 31) / 32;
     timing_begin("tree_attn_join", st);
-    const cudaError_t e = launch_pdl(k_tree_join<Act, D>, dim3(unsigned(plan.ctas), unsigned((rows + 7) / 8)), dim3(256), 0, st, A, plan.rows, plan.ctas);
+    const cudaError_t e = launch_pdl(k_tree_join<Act, D>, dim3(unsigned(plan.ctas), unsigned(blocks)), dim3(256), 0, st, A, plan.rows, plan.ctas);
     timing_end(st);
     return e;
 }
