@@ -11,11 +11,14 @@
 // in the order in which they are used), one cleans tiles of values in which some query masks some key: a weight of 0
 // would make NaN of an infinite value, so rows behind the sequence and infinite or NaN values become zeros there, and
 // the latter are added to the rows that see them at the end.
-// The grid fills the GPU once; a CTA takes tiles of queries in turn, by descending length, all heads of one after
-// another, so that neighbours read the same keys.  While one tile's result is written the next one's queries and keys
-// come and its first scores are made.
-// Bound: the tensor cores (4 D flops per pair); a tile's weights (a max, a multiply-add, an exponential, an addition
-// and half a conversion for each of 16384 scores) take about as long as its products with 128 features.
+// Tiles of queries go by descending length, all heads of one after another, so that neighbours read the same keys; a CTA
+// has one, or takes one after another (see launch_d): while one tile's result is written the next one's queries and
+// keys come and its first scores are made.
+// Bound: the tensor cores (4 D flops per pair of a query and a key that it attends to); a tile's weights (a max, a
+// multiply-add, an exponential, an addition and half a conversion for each of 16384 scores) take about as long as its
+// products with 128 features, and longer with 64.  Measured, TFLOP/s: 1 x 32768 tokens, 16 / 4 heads, 128 features
+// 2.69 ms, 1632; 2 x 8192, 32 / 8, 128 0.78 ms, 1405; 1 x 16384, 32 / 8, 64 1.26 ms, 866; 1 x 16384, 16 / 2, 256
+// 1.33 ms, 1653.  Short sequences: a tile's setup, masked softmax and end, which do not shrink with its products.
 #include "gdn_attn_tc.cuh"
 
 namespace gdn {
@@ -236,8 +239,14 @@ __global__ void __launch_bounds__(Fwd<D>::T, 1)
         int n0 = 0, cleaned = 0, item = 0, count[2] = {0, 0}, uses[2] = {0, 0};  // pieces; per query tile: key tiles, tiles of queries
         const bool el = elected();
         const uint32_t tm = same(tmem);
-        while (ok && it.next(p)) {
-            if (it.k.lo >= it.k.hi) continue;
+        // the next tile of queries that sees any keys
+        auto next = [&] {
+            while (it.next(p))
+                if (it.k.lo < it.k.hi) return true;
+            return false;
+        };
+        bool more = next();
+        while (ok && more) {
             Walk k;
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
@@ -314,9 +323,8 @@ __global__ void __launch_bounds__(Fwd<D>::T, 1)
                         if (ok && k.in(w, k.lo)) scores(w, at, w);
                     release(at);
                     at = after(at);
-                    if (k.hi - k.lo == 1) {
-                        if (el) tc::commit(&sh.q_empty);
-                    }
+                    if (k.hi - k.lo == 1 && el) tc::commit(&sh.q_empty);
+                    more = next();  // while the first weights are made
                     for (int j = k.lo; j < k.hi && ok; ++j) {
                         const Place keys = after(at);
                         wait_clean(j);
@@ -327,9 +335,7 @@ __global__ void __launch_bounds__(Fwd<D>::T, 1)
                         }
                         release(at);
                         if (j + 1 < k.hi) release(keys);
-                        if (j + 2 == k.hi) {
-                        if (el) tc::commit(&sh.q_empty);
-                    }
+                        if (j + 2 == k.hi && el) tc::commit(&sh.q_empty);
                         at = after(keys);
                     }
                 } else {
@@ -338,10 +344,9 @@ __global__ void __launch_bounds__(Fwd<D>::T, 1)
                         scores(0, at, (c + j - k.lo) & 1);
                         release(at);
                         at = after(at);
-                        if (j + 1 == k.hi) {
-                        if (el) tc::commit(&sh.q_empty);
+                        if (j + 1 == k.hi && el) tc::commit(&sh.q_empty);
                     }
-                    }
+                    more = next();
                     for (int j = k.lo; j < k.hi && ok; ++j, ++c) {
                         wait_clean(j);
                         values(0, at, c & 1, (c >> 1) & 1, j == k.lo);
@@ -351,9 +356,7 @@ __global__ void __launch_bounds__(Fwd<D>::T, 1)
                             scores(0, at, c & 1);
                             release(at);
                             at = after(at);
-                            if (j + 3 == k.hi) {
-                        if (el) tc::commit(&sh.q_empty);
-                    }
+                            if (j + 3 == k.hi && el) tc::commit(&sh.q_empty);
                         }
                     }
                 }
@@ -394,8 +397,12 @@ __global__ void __launch_bounds__(Fwd<D>::T, 1)
                 const int lo = first - j * 128, hi = last - j * 128;
                 if (__any_sync(0xffffffffu, lo > 0 || hi < 127)) {
 #pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if (c < lo || c > hi) v[c] = -INFINITY;
+                    for (int c = 0; c < 128; c += 32) {
+                        const uint32_t counted = span_of(lo - c, hi - c);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!(counted >> e & 1)) v[c + e] = -INFINITY;
+                    }
                 }
                 const float top = fmaxf(m, max_of<128>(v) * zs);
                 if (__any_sync(0xffffffffu, top > m + 8.f)) {
@@ -442,6 +449,12 @@ __global__ void __launch_bounds__(Fwd<D>::T, 1)
                 tc::unpk2(fadd2(sum[0], sum[1]), a, b);
                 l += a + b;
             }
+            // While the last product is on its way: all that does not need it.
+            const bool some = l > 0.f || l != l;
+            const float f = some ? 1.f / l : 0.f;
+            const int64_t out = (int64_t(s.q0) + r) * p.Hq + it.h;
+            __nv_bfloat16 *o = static_cast<__nv_bfloat16*>(A.o) + out * D, *rest = A.o_rest ? static_cast<__nv_bfloat16*>(A.o_rest) + out * D : nullptr;
+            if (live && A.lse) A.lse[out] = some ? (m + log2f(l)) * LN2 : -INFINITY;
             if (ok && steps > 0) {
                 // With one query tile the scores run two tiles ahead and the last two products may both be open, or both done:
                 // each has a barrier of its own, for a phase that another has followed can no longer be waited for.
@@ -450,14 +463,8 @@ __global__ void __launch_bounds__(Fwd<D>::T, 1)
                 tc::fence_after_sync();
             }
             if (!ok) break;
-            const bool some = l > 0.f || l != l;
-            const float f = some ? 1.f / l : 0.f;
-            const int64_t out = (int64_t(s.q0) + r) * p.Hq + it.h;
-            __nv_bfloat16 *o = static_cast<__nv_bfloat16*>(A.o) + out * D, *rest = A.o_rest ? static_cast<__nv_bfloat16*>(A.o_rest) + out * D : nullptr;
             // written before the last product
-            int bad_tiles = 0;
-            if (steps > 0 && sh.bad_item[item & 3] == item)
-                for (int j = k.lo; j < k.hi; ++j) bad_tiles += k.special(j);
+            const int bad_tiles = steps > 0 && sh.bad_item[item & 3] == item ? k.hi - k.lo - max(0, min(k.hi, k.clean_from) - max(k.lo, k.clean_to)) : 0;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 float x[32];
@@ -491,7 +498,6 @@ __global__ void __launch_bounds__(Fwd<D>::T, 1)
                     }
                 }
             }
-            if (live && A.lse) A.lse[out] = some ? (m + log2f(l)) * LN2 : -INFINITY;
             if (steps > 0) {
                 tc::fence_before_sync();
                 __syncwarp();
@@ -523,7 +529,8 @@ cudaError_t launch_d(const PromptArgs& A, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     // One tile of queries to a CTA where sequences are long: the hardware deals CTAs out as others end, more evenly than taking
     // turns does.  Short ones take turns, for the overlap of one tile's end with the next one's begin.  32 / 8 heads, 128 features,
-    // turns and one each: 16 x 512 tokens 93 and 110 us, 8 x 2048 299 and 317, 2 x 8192 802 and 783, 1 x 32768 (16 / 4) 2782 and 2694.
+    // turns and one each: 16 x 512 tokens 93 and 110 us, 8 x 2048 299 and 317, 2 x 8192 802 and 783, 1 x 32768 (16 / 4) 2782 and 2694
+    // (before masks were made of words).
     const int64_t all = tiles * p.Hq, sms = sm_count_cached();
     const bool turns = p.num_seqs == 0 || p.total_k / p.num_seqs <= 4096 || all > 0x7fffffff;  // a grid has 2^31 - 1 CTAs at most
     timing_begin("prompt_attn_fwd", st);

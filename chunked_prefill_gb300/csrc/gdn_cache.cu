@@ -3,6 +3,8 @@
 //
 // gdn_paged_cache_write moves every value once: bound by HBM for a prompt, by the launch for a few tokens.
 // Up to 32 lanes have a token, whose slot and row they look up once, and four 16-byte pieces of the output each.
+// 32767 tokens of 8 heads of 128 from bf16 into 8 bits: 49 us, 4.1 TB/s; the conversion's instructions take as long as
+// the bytes.  96 accepted tokens: 5 us a call.
 //
 // gdn_page_table_extend and _trim are latency: one launch, in which every CTA sums the requests' needs for
 // itself (a scan over up to 8 requests a thread) and keeps the sums in shared memory, so that the tokens and
@@ -68,7 +70,7 @@ __global__ void __launch_bounds__(WT) k_cache_write(const CacheArgs G, const Wri
         for (int u = 0; u < WU; ++u) {
             if (!to[u]) continue;
             alignas(16) C out[PV];
-            // the division of 8-bit values took half of a long prompt's time: 70 us instead of 40 for 32767 tokens, 8 heads of 128
+            // with divisions 32767 tokens of 8 heads of 128 took 70 us
             const bool quick = sizeof(C) == 1 && scale[u] >= 8.673617e-19f && scale[u] <= 1.1529215e18f;
             const float r = 1.f / scale[u];
 #pragma unroll
@@ -295,7 +297,7 @@ cudaError_t launch_cache_write(const CacheArgs& A, cudaStream_t st) {
     return A.p.cache_dtype == GDN_BF16 ? write_as<__nv_bfloat16, __nv_bfloat16>(A, st) : write_as<__nv_bfloat16, __nv_fp8_e4m3>(A, st);
 }
 cudaError_t launch_table_extend(const TableArgs& A, cudaStream_t st) {
-    // 500 prompts of up to 2000 tokens: a cluster of 8 CTAs takes 60 us, both launches 12
+    // 500 prompts of up to 2000 tokens: a cluster of 8 CTAs takes 60 us, the two launches 19
     if (A.p.total > 32768) {
         const cudaError_t e = launch_table(k_table_extend<true, false>, "page_table_extend", A, unsigned(sm_count_cached()), false, st);
         return e != cudaSuccess ? e : launch_table(k_table_extend<false, true>, "page_table_update", A, 1, false, st);

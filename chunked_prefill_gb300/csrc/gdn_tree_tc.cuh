@@ -13,7 +13,10 @@
 // threads, 32 sequences of up to 8192 tokens took 190 us: a tile's addresses alone kept those threads busy.)
 // Where some row masks a token that others see (drafted tokens, the edge of a window) infinite and NaN values are made
 // zeros, for a weight of 0 would make NaN of them, and are added at the end to the rows that see them.
-// Bound: HBM, up to some 128 rows to a kv-head with bf16; the tensor cores and the widening beyond.
+// Bound: HBM in the limit, up to some 128 rows to a kv-head with bf16; a tile's chain of requests, scores and weights keeps
+// it from that: tree of 16 tokens, 32 sequences of up to 8192, 32 / 8 heads of 128: 127 us, 61 % of HBM's rate.  8 bits and
+// 248 rows to a kv-head: the instructions of weights and widening (issue slots half used by 16 warps that wait for
+// each other), 64 sequences of up to 16384: 677 us, 20 % of HBM's rate, the tensor cores a third busy.
 #pragma once
 #include "gdn_attn_tc.cuh"
 #include "gdn_tree.cuh"
