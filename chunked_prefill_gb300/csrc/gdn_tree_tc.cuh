@@ -4,8 +4,9 @@
 // and values (more than 128 rows, up to 128 features), and walks over its part of the list of tiles of 128 cached tokens
 // (64 with 256 features).  As in the attention over prompts: S = Q K^T into tensor memory, a warpgroup per tile of rows and
 // a thread to a row makes weights of it in place, O += P V with P read from tensor memory, O rescaled only where a
-// maximum has grown by more than 2^8.  A row is read twice from tensor memory, once for its maximum, in pieces of 32
-// values: the registers are the loading warps'.
+// maximum has grown by more than 2^8.  A row is read twice from tensor memory, once for its maximum, in pieces of 64
+// values: the registers are the helping warps' (a piece kept for its weights, with 168 of them: 628 us instead of 540 for 64 sequences of
+// up to 16384 tokens, 8 bits).  With two tiles of rows the product begins with the first piece's weights.
 // Pages lie anywhere, but their rows are at regular distances: TMA brings pieces of up to 16 tokens (the largest power of
 // two that divides the page size), issued by the lanes of one warp, straight into the swizzled tiles that the tensor cores
 // read; of 8-bit caches into a ring of their own, from where six warps widen them to bf16 (exactly).  A page number out of
@@ -16,7 +17,7 @@
 // Bound: HBM in the limit, up to some 128 rows to a kv-head with bf16; a tile's chain of requests, scores and weights keeps
 // it from that: tree of 16 tokens, 32 sequences of up to 8192, 32 / 8 heads of 128: 127 us, 61 % of HBM's rate.  8 bits and
 // 248 rows to a kv-head: the instructions of weights and widening (issue slots half used by 16 warps that wait for
-// each other), 64 sequences of up to 16384: 677 us, 20 % of HBM's rate, the tensor cores a third busy.
+// each other), 64 sequences of up to 16384: 544 us, 25 % of HBM's rate.
 #pragma once
 #include "gdn_attn_tc.cuh"
 #include "gdn_tree.cuh"
@@ -50,8 +51,8 @@ struct TreeMaps {
 };
 
 struct TreeShared {
-    uint64_t full[8], empty[8], stage_full[4], stage_empty[4], issued[CLEAN], clean[CLEAN], q_full, q_empty, s_ready[2], p_ready[2], pv_done[2], o_free, met[4], drain;
-    uint32_t counts[8][4];   // which tokens of a cached tile count
+    uint64_t p_half[2], full[8], empty[8], stage_full[4], stage_empty[4], issued[CLEAN], clean[CLEAN], q_full, q_empty, s_ready[2], p_ready[2], pv_done[2], o_free, met[4], drain;
+    alignas(16) uint32_t counts[8][4];   // which tokens of a cached tile count
     // Of the last pairs (more than the ring holds): which had infinite or NaN values, and of the first two cached tiles and the
     // drafted tokens which tokens, as each helping warp found them.
     int bad_pair[8];
@@ -175,6 +176,7 @@ __global__ void __launch_bounds__(TreeTc<C, D, NQ>::T, 1) k_tree_tc(const TreeAr
         tc::mbar_init(&sh.q_empty, 1);
         for (int b = 0; b < 2; ++b) {
             tc::mbar_init(&sh.s_ready[b], 1);
+            tc::mbar_init(&sh.p_half[b], 4);
             tc::mbar_init(&sh.p_ready[b], NQ == 2 ? 4 : 8);
             tc::mbar_init(&sh.pv_done[b], 1);
         }
@@ -419,7 +421,7 @@ __global__ void __launch_bounds__(TreeTc<C, D, NQ>::T, 1) k_tree_tc(const TreeAr
                 };
                 auto values = [&](int w, int i) {
                     const int buf = NQ == 2 ? w : (g + i) & 1;
-                    ok = ok && warp_spin(&sh.p_ready[buf], (NQ == 2 ? g + i : (g + i) >> 1) & 1);
+                    ok = ok && warp_spin(NQ == 2 ? &sh.p_half[buf] : &sh.p_ready[buf], (NQ == 2 ? g + i : (g + i) >> 1) & 1);
                     if (i == 0 && w == 0 && pair > 0) ok = ok && warp_spin(&sh.o_free, (pair - 1) & 1);
                     if (!full(i, 1)) return;
                     if (L::E == 2 && w == 0) {
@@ -430,14 +432,21 @@ __global__ void __launch_bounds__(TreeTc<C, D, NQ>::T, 1) k_tree_tc(const TreeAr
                         }
                     }
                     if (!ok) return;
-                    tc::fence_after_sync();
                     const uint64_t b = desc_mn<TOK>(slot_at(i, 1), 0);
-                    if (el) {
+                    constexpr int FIRST = NQ == 2 ? TOK / 2 : TOK;  // with two tiles of rows the weights come in two halves
+                    auto product = [&](int from) {
+                        tc::fence_after_sync();
+                        if (el)
 #pragma unroll
-                        for (int x = 0; x < TOK; x += 16)
-                            tc::mma_bf16_ta(tm + L::O + w * D, tm + L::S + buf * TOK + x / L::PIECE * L::PIECE + x % L::PIECE / 2, step_mn(b, x), IO, i > 0 || x > 0);
-                        tc::commit(&sh.pv_done[buf]);
+                            for (int x = 0; x < FIRST; x += 16)
+                                tc::mma_bf16_ta(tm + L::O + w * D, tm + L::S + buf * TOK + (from + x) / L::PIECE * L::PIECE + (from + x) % L::PIECE / 2, step_mn(b, from + x), IO, i > 0 || from + x > 0);
+                    };
+                    product(0);
+                    if (NQ == 2) {
+                        if (!(ok = warp_spin(&sh.p_ready[buf], (g + i) & 1))) return;
+                        product(FIRST);
                     }
+                    if (el) tc::commit(&sh.pv_done[buf]);
                     if (w == NQ - 1) release(i, 1);
                 };
                 ok = warp_spin(&sh.q_full, pair & 1);
@@ -535,10 +544,9 @@ __global__ void __launch_bounds__(TreeTc<C, D, NQ>::T, 1) k_tree_tc(const TreeAr
                     const int skip = first - (it.R.base + tile * TOK + 32 * y);
                     return sh.counts[at_tile & 7][y] & (skip <= 0 ? 0xffffffffu : skip < 32 ? 0xffffffffu << skip : 0u);
                 };
-                uint32_t all = see(0);
-#pragma unroll
-                for (int x = 1; x < CW / 32; ++x) all &= see(x);
-                const bool some_masked = __any_sync(0xffffffffu, all != 0xffffffffu);
+                const uint4 counted_all = *reinterpret_cast<const uint4*>(sh.counts[at_tile & 7]);
+                const uint32_t all = TOK == 128 ? counted_all.x & counted_all.y & counted_all.z & counted_all.w : counted_all.x & counted_all.y;
+                const bool some_masked = __any_sync(0xffffffffu, drafted || all != 0xffffffffu || first > it.R.base + tile * TOK);
                 // a scale of 0 makes all scores alike: so does this one, and masked ones stay infinite
                 float zs = p.scale * (drafted ? 1.f : ks) * LOG2E;
                 if (zs == 0.f) zs = 1.17549435e-38f;
@@ -615,11 +623,11 @@ __global__ void __launch_bounds__(TreeTc<C, D, NQ>::T, 1) k_tree_tc(const TreeAr
                         // columns [c, c + 2) of a piece's weights in place of its scores' column c / 2
                         tc::tmem_st16(at + PIECE * x + y / 2, wts);
                     }
+                    tc::tmem_st_wait();
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(x + 1 < CW / PIECE ? &sh.p_half[buf] : &sh.p_ready[buf]);  // the product begins with the first half
                 }
-                tc::tmem_st_wait();
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&sh.p_ready[buf]);
                 float a, b;
                 tc::unpk2(fadd2(sum[0], sum[1]), a, b);
                 l += a + b;
