@@ -164,6 +164,7 @@ __global__ void __launch_bounds__(TT_) k_table_extend(const TableArgs A, const F
     extern __shared__ Request req[];
     __shared__ int64_t wsum[32];
     const gdn_table_problem& p = A.p;
+    if (!UPDATE) tc::pdl_launch_dependents();  // the other launch sums alongside: what it reads is written by itself alone
     const int tid = threadIdx.x, N = p.num_seqs, per = (N + TT_ - 1) / TT_, n0 = min(N, tid * per), n1 = min(N, n0 + per);
     const int ps = p.page_size, top = stack_top(A);
     const int64_t cap = int64_t(p.max_pages) * ps;
@@ -191,6 +192,7 @@ __global__ void __launch_bounds__(TT_) k_table_extend(const TableArgs A, const F
     sum_before(mine, wsum, given);
     const int ctas = int(gridDim.x), cta = int(blockIdx.x);  // one cluster where one launch does both
     cluster_barrier(FILL && UPDATE && ctas > 1);  // the requests are in shared memory; every CTA has read lengths and count
+    if (!FILL) tc::pdl_wait();  // all CTAs of the launch before have ended
     if (UPDATE && cta == 0) {
         for (int n = tid; n < N; n += TT_) {
             const Request r = req[n];
@@ -267,7 +269,8 @@ __global__ void __launch_bounds__(TT_) k_table_trim(const TableArgs A, const Fas
     }
 }
 
-cudaError_t launch_table(void (*kern)(const TableArgs, const FastDiv), const char* name, const TableArgs& A, unsigned ctas, bool cluster, cudaStream_t st) {
+// after: begins while the launch before, of the same kernel's other half, is at work
+cudaError_t launch_table(void (*kern)(const TableArgs, const FastDiv), const char* name, const TableArgs& A, unsigned ctas, bool cluster, cudaStream_t st, bool after = false) {
     const int smem = A.p.num_seqs * int(sizeof(Request));
     cudaError_t e = smem_attr(kern, TABLE_SEQS * int(sizeof(Request)));
     if (e != cudaSuccess) return e;
@@ -282,8 +285,12 @@ cudaError_t launch_table(void (*kern)(const TableArgs, const FastDiv), const cha
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = ctas;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    if (after) {
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+    }
     cfg.attrs = attr;
-    cfg.numAttrs = cluster && ctas > 1 ? 1 : 0;
+    cfg.numAttrs = after || (cluster && ctas > 1) ? 1 : 0;
     timing_begin(name, st);
     e = cudaLaunchKernelEx(&cfg, kern, A, by_page);
     timing_end(st);
@@ -297,10 +304,10 @@ cudaError_t launch_cache_write(const CacheArgs& A, cudaStream_t st) {
     return A.p.cache_dtype == GDN_BF16 ? write_as<__nv_bfloat16, __nv_bfloat16>(A, st) : write_as<__nv_bfloat16, __nv_fp8_e4m3>(A, st);
 }
 cudaError_t launch_table_extend(const TableArgs& A, cudaStream_t st) {
-    // 500 prompts of up to 2000 tokens: a cluster of 8 CTAs takes 60 us, the two launches 19
+    // 500 prompts of up to 2000 tokens: a cluster of 8 CTAs takes 60 us, the two launches, the second summing beside the first, 15
     if (A.p.total > 32768) {
         const cudaError_t e = launch_table(k_table_extend<true, false>, "page_table_extend", A, unsigned(sm_count_cached()), false, st);
-        return e != cudaSuccess ? e : launch_table(k_table_extend<false, true>, "page_table_update", A, 1, false, st);
+        return e != cudaSuccess ? e : launch_table(k_table_extend<false, true>, "page_table_update", A, 1, false, st, true);
     }
     return launch_table(k_table_extend<true, true>, "page_table_extend", A, A.p.total > 4096 ? 8 : 1, true, st);
 }
