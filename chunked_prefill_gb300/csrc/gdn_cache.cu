@@ -2,9 +2,9 @@
 // tables kept on the device from the requests' lengths.
 //
 // gdn_paged_cache_write moves every value once: bound by HBM for a prompt, by the launch for a few tokens.
-// Up to 32 lanes have a token, whose slot and row they look up once, and four 16-byte pieces of the output each.
-// 32767 tokens of 8 heads of 128 from bf16 into 8 bits: 49 us, 4.1 TB/s; the conversion's instructions take as long as
-// the bytes.  96 accepted tokens: 5 us a call.
+// Up to 32 lanes have a token, whose slot and row they look up once, and two 16-byte pieces of the output each.
+// 32767 tokens of 8 heads of 128 from bf16 into 8 bits: 45 us, 4.5 TB/s; the conversion's instructions beside the
+// bytes.  96 accepted tokens: 5 us a call.
 //
 // gdn_page_table_extend and _trim are latency: one launch, in which every CTA sums the requests' needs for
 // itself (a scan over up to 8 requests a thread) and keeps the sums in shared memory, so that the tokens and
@@ -18,7 +18,9 @@ namespace gdn {
 namespace {
 
 // ---- writing the cache
-constexpr int WT = 256, WU = 4;
+// Pieces to a thread: more hold registers, fewer look slots up again (32767 tokens of 8 heads of 128 into 8 bits, 128 threads: 1 49 us,
+// 2 46, 3 49, 4 47, 8 68; 256 threads, 4 51).
+constexpr int WT = 128, WU = 2;
 
 struct WriteShape {
     int lanes;          // of a token
@@ -70,7 +72,7 @@ __global__ void __launch_bounds__(WT) k_cache_write(const CacheArgs G, const Wri
         for (int u = 0; u < WU; ++u) {
             if (!to[u]) continue;
             alignas(16) C out[PV];
-            // with divisions 32767 tokens of 8 heads of 128 took 70 us
+            // with divisions 32767 tokens of 8 heads of 128 took 70 us instead of 49
             const bool quick = sizeof(C) == 1 && scale[u] >= 8.673617e-19f && scale[u] <= 1.1529215e18f;
             const float r = 1.f / scale[u];
 #pragma unroll
