@@ -10,7 +10,7 @@
 // itself (a scan over up to 8 requests a thread) and keeps the sums in shared memory, so that the tokens and
 // pages can be dealt out evenly, each finding its request by bisection.  Only lengths and the count of free
 // pages are both read and written: a cluster barrier lies between (8 CTAs from 4096 tokens on, one below), or, from
-// 32768 tokens on, where slots are the most of it, another launch, which the CTAs of the first have all ended before.
+// 32768 tokens on, where slots are the most of it, another launch, which writes them when the first's CTAs have all ended.
 #include "gdn_attn.h"
 #include "gdn_paged.cuh"
 
