@@ -40,10 +40,11 @@ template <int D> struct Fwd {
 constexpr int SPECIAL = 8;
 
 struct Shared {
-    uint64_t full[8], empty[8], q_full, q_empty, s_ready[2], p_half[2], p_ready[2], pv_done[2], o_free[2], issued[SPECIAL], clean[SPECIAL], drain;
+    uint64_t full[8], empty[8], q_full, q_empty, s_ready[2], p_half[2], p_ready[2], pv_done[2], o_free[2], issued[SPECIAL], clean[SPECIAL], bad_free[2][4], drain;
     uint32_t tmem;
-    // infinite and NaN values of the last four tiles of queries: which of them had any, and of each of its tiles with masked
-    // keys which one it is and which keys
+    // Infinite and NaN values of the last four tiles of queries with masked keys, counted by themselves: which of them had any,
+    // and of each of its tiles with masked keys which one it is and which keys.  A place is written again when the warps of
+    // weights of either half are done with it (bad_free).
     int bad_item[4], bad_tile[4][SPECIAL];
     uint32_t bad[4][SPECIAL][4];
 };
@@ -53,6 +54,7 @@ struct Walk {
     int begin[2], end[2], lo, hi;
     int clean_to, clean_from;  // tiles below and from which on some query of the CTA masks some key (or the tile goes past the keys)
     __device__ __forceinline__ bool special(int j) const { return j < clean_to || j >= clean_from; }
+    __device__ __forceinline__ int specials() const { return hi - lo - max(0, min(hi, clean_from) - max(lo, clean_to)); }
     __device__ __forceinline__ bool in(int w, int j) const { return w == 0 ? j >= begin[0] && j < end[0] : j >= begin[1] && j < end[1]; }
 };
 template <int NQ>
@@ -152,6 +154,8 @@ __global__ void __launch_bounds__(Fwd<D>::T, 1)
             tc::mbar_init(&sh.issued[i], 1);
             tc::mbar_init(&sh.clean[i], 2);
         }
+        for (int i = 0; i < 4; ++i)
+            for (int w = 0; w < 2; ++w) tc::mbar_init(&sh.bad_free[w][i], 4);
         tc::mbar_init(&sh.drain, 1);
         tc::mbar_fence_init();
         for (int i = 0; i < 4; ++i) sh.bad_item[i] = -1;
@@ -203,9 +207,23 @@ __global__ void __launch_bounds__(Fwd<D>::T, 1)
         }
     } else if (warp >= NQ * 4 + 2) {  // ---- cleaning: half of the rows each
         const int half = warp - (NQ * 4 + 2);
-        int n0 = 0, done = 0, item = 0;
+        int n0 = 0, done = 0, record = 0;
+        uint32_t used = 0, odd = 0;  // a bit to a half and a place: whether it was used, and whether an odd number of times
         while (ok && it.next(p)) {
             if (k.lo >= k.hi) continue;
+            // A place is free when the halves that used it are done with it.  The products do not see to that: a tile of queries
+            // of which one half has no rows, or sees no key, waits for the other half's results alone, and the warps of this one
+            // may be several tiles behind, or ahead.  A half uses the places of the records in which it sees keys; it cannot be done
+            // with one before its tiles are cleaned here, so no phase is passed over.
+            if (k.specials() > 0) {
+#pragma unroll
+                for (int w = 0; w < NQ; ++w) {
+                    const uint32_t bit = 1u << (w * 4 + (record & 3));
+                    if (ok && (used & bit)) ok = warp_wait(&sh.bad_free[w][record & 3], odd & bit ? 0 : 1);
+                    if (k.end[w] > k.begin[w]) used |= bit, odd ^= bit;
+                }
+                if (!ok) break;
+            }
             int nth = 0;
             for (int j = k.lo; j < k.hi && ok; ++j) {
                 if (!k.special(j)) continue;
@@ -217,13 +235,11 @@ __global__ void __launch_bounds__(Fwd<D>::T, 1)
                     if (ok) clean_tile<DC>(ring + slot * L::PIECE, s.lk - j * 128, half, bad);
                 }
                 if (lane == 0 && nth < SPECIAL) {
-                    // (a tile of queries has 6 at most, 3 at either end of the keys that it sees.)  The place's last use is over:
-                    // the products of two tiles back were begun after the results of three back were read.
-                    const int at = item & 3;
+                    const int at = record & 3;  // (a tile of queries has 6 at most, 3 at either end of the keys that it sees)
                     sh.bad_tile[at][nth] = j;
                     sh.bad[at][nth][2 * half] = bad[0];
                     sh.bad[at][nth][2 * half + 1] = bad[1];
-                    if (bad[0] | bad[1]) sh.bad_item[at] = item;
+                    if (bad[0] | bad[1]) sh.bad_item[at] = record;
                 }
                 tc::fence_proxy_async_smem();
                 __syncwarp();
@@ -232,7 +248,7 @@ __global__ void __launch_bounds__(Fwd<D>::T, 1)
                 ++nth;
             }
             n0 += 2 * (k.hi - k.lo) * NC;
-            ++item;
+            record += k.specials() > 0;
         }
     } else if (warp == NQ * 4) {  // ---- products
         constexpr uint32_t IS = tc::make_idesc(128, 128, 0, 0), IO = tc::make_idesc(128, DC, 0, 1);
@@ -379,7 +395,7 @@ __global__ void __launch_bounds__(Fwd<D>::T, 1)
         const uint32_t mine = tmem + (uint32_t(warp & 3) << 21);
         const float zs = p.scale * LOG2E;
         const bool wide = wide_aligned(A.o) && wide_aligned(A.o_rest);
-        int count = 0, item = 0;  // key tiles, tiles of queries so far
+        int count = 0, record = 0;  // key tiles, tiles of queries with masked keys so far
         while (ok && it.next(p)) {
             const int r = it.row + tid, i_row = min(r, s.lq - 1), begin = w == 0 ? k.begin[0] : k.begin[1], steps = (w == 0 ? k.end[0] : k.end[1]) - begin;
             const bool live = r < s.lq;
@@ -464,7 +480,7 @@ __global__ void __launch_bounds__(Fwd<D>::T, 1)
             }
             if (!ok) break;
             // written before the last product
-            const int bad_tiles = steps > 0 && sh.bad_item[item & 3] == item ? k.hi - k.lo - max(0, min(k.hi, k.clean_from) - max(k.lo, k.clean_to)) : 0;
+            const int specials = k.specials(), bad_tiles = steps > 0 && specials > 0 && sh.bad_item[record & 3] == record ? specials : 0;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 float x[32];
@@ -480,8 +496,8 @@ __global__ void __launch_bounds__(Fwd<D>::T, 1)
                 for (int i = 0; i < min(bad_tiles, SPECIAL); ++i)  // infinite and NaN values that this row sees
 #pragma unroll 1
                     for (int t = 0; t < 128; ++t) {
-                        const int key = sh.bad_tile[item & 3][i] * 128 + t;
-                        if (!(sh.bad[item & 3][i][t >> 5] >> (t & 31) & 1) || key < first || key > last) continue;
+                        const int key = sh.bad_tile[record & 3][i] * 128 + t;
+                        if (!(sh.bad[record & 3][i][t >> 5] >> (t & 31) & 1) || key < first || key > last) continue;
                         const __nv_bfloat16* bv = static_cast<const __nv_bfloat16*>(A.v) + (int64_t(s.k0) + key) * p.v_stride + int64_t(it.h / G) * D + c;
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
@@ -501,10 +517,13 @@ __global__ void __launch_bounds__(Fwd<D>::T, 1)
             if (steps > 0) {
                 tc::fence_before_sync();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&sh.o_free[w]);
+                if (lane == 0) {
+                    tc::mbar_arrive(&sh.o_free[w]);
+                    if (specials > 0) tc::mbar_arrive(&sh.bad_free[w][record & 3]);
+                }
             }
             count += steps;
-            item += k.lo < k.hi;
+            record += specials > 0;
         }
     }
     if (!ok) g_gave_up = 1;
