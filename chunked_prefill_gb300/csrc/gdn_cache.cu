@@ -254,7 +254,8 @@ __global__ void __launch_bounds__(TT_) k_table_trim(const TableArgs A, const Fas
         const int64_t len = length_of(A, n), keep = min(len, int64_t(max(A.change[n], 0)));
         const int has = pages_of(len), kept = pages_of(keep);
         before += has - kept;
-        req[n] = {int(all - before), int(keep), has, kept};
+        // 8192 rows can have more pages than 31 bits count; such places are past every stack's end
+        req[n] = {int(min(all - before, int64_t(0x7fffffff))), int(keep), has, kept};
     }
     const int ctas = int(gridDim.x), cta = int(blockIdx.x);
     cluster_barrier(ctas > 1);

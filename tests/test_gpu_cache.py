@@ -188,6 +188,18 @@ def test_trim_undoes_extend(gdn):
     assert torch.equal(l, before) and s.tolist() == stack.tolist() and int(f) == 300
 
 
+def test_trim_of_more_pages_than_31_bits_count(gdn):
+    """Every sequence gives up its whole row: the last ones' pages fill the stack, the others are dropped."""
+    N, width, size = 8192, (1 << 18) + 5, 1000
+    t = torch.full((N, width), -3, dtype=I32, device="cuda")
+    t[-1] = torch.arange(width, device="cuda")
+    l, s, f = torch.full((N,), width, dtype=I32, device="cuda"), torch.full((size + 64,), 77, dtype=I32, device="cuda"), dev([10])
+    gdn.page_table_trim(t, l, torch.zeros_like(l), s[32:32 + size], f, 1)
+    assert (l == 0).all() and int(f) == size
+    assert (s[:42] == 77).all() and (s[32 + size:] == 77).all()
+    assert s[42:32 + size].tolist() == list(range(width - 1, width - 1 - (size - 10), -1))
+
+
 def test_no_sequences_and_no_pages(gdn):
     e = torch.zeros(0, dtype=I32, device="cuda")
     f = dev([3])
