@@ -25,6 +25,11 @@ gdn_status check_cache_strides(int64_t unit, int64_t a, int64_t b, int64_t c, in
     return GDN_OK;
 }
 
+// Whether a page, token or head of the caches stands for several.
+template <typename P> bool no_stride(const P& p) {
+    return (p.num_pages > 1 && !(p.k_page_stride && p.v_page_stride)) || (p.page_size > 1 && !(p.k_token_stride && p.v_token_stride)) || (p.Hkv > 1 && !(p.k_head_stride && p.v_head_stride));
+}
+
 gdn_status check_prompt(gdn_prompt_problem& p) {
     TRY(check_heads(p.Hq, p.Hkv, p.D));
     if (p.dtype != GDN_BF16 && p.dtype != GDN_FP32) return fail(GDN_ERR_INVALID_ARG, "dtype must be GDN_BF16 or GDN_FP32");
@@ -69,7 +74,10 @@ gdn_status check_tree(gdn_tree_problem& p) {
     TRY(check_stride("k_new_stride", p.k_new_stride, int64_t(p.Hkv) * p.D, act));
     TRY(check_stride("v_new_stride", p.v_new_stride, int64_t(p.Hkv) * p.D, act));
     TRY(check_stride("table_stride", p.table_stride, p.max_pages, 1));
-    return check_cache_strides(16 / int64_t(elem(p.cache_dtype)), p.k_page_stride, p.k_token_stride, p.k_head_stride, p.v_page_stride, p.v_token_stride, p.v_head_stride);
+    TRY(check_cache_strides(16 / int64_t(elem(p.cache_dtype)), p.k_page_stride, p.k_token_stride, p.k_head_stride, p.v_page_stride, p.v_token_stride, p.v_head_stride));
+    // the tensor cores' kernels read pages through tensor maps, whose strides are not to be 0
+    if (p.dtype == GDN_BF16 && no_stride(p)) return fail(GDN_ERR_INVALID_ARG, "a bf16 or 8-bit cache must not have strides of 0 (an expanded view)");
+    return GDN_OK;
 }
 
 gdn_status check_cache(gdn_cache_problem& p) {
@@ -85,9 +93,7 @@ gdn_status check_cache(gdn_cache_problem& p) {
     TRY(check_stride("v_stride", p.v_stride, int64_t(p.Hkv) * p.D, act));
     TRY(check_cache_strides(16 / int64_t(elem(p.cache_dtype)), p.k_page_stride, p.k_token_stride, p.k_head_stride, p.v_page_stride, p.v_token_stride, p.v_head_stride));
     // a head, token or page that stands for several would be written by each
-    if ((p.num_pages > 1 && !(p.k_page_stride && p.v_page_stride)) || (p.page_size > 1 && !(p.k_token_stride && p.v_token_stride)) ||
-        (p.Hkv > 1 && !(p.k_head_stride && p.v_head_stride)))
-        return fail(GDN_ERR_INVALID_ARG, "a cache that is written to must not have strides of 0");
+    if (no_stride(p)) return fail(GDN_ERR_INVALID_ARG, "a cache that is written to must not have strides of 0");
     return GDN_OK;
 }
 

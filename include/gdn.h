@@ -446,7 +446,8 @@ gdn_status gdn_attn_device_status(void* stream);
  *
  * Types, scales, roundings, lengths past the table, page numbers out of range and slots without tokens: as
  * in gdn_paged_attn_decode, but that query values are not split under 8-bit caches (keys and values are widened to
- * bf16, exactly, and weights rounded to bf16).  1 <= T <= 64.
+ * bf16, exactly, and weights rounded to bf16), and that strides of bf16 and 8-bit caches are not 0 where there is more than
+ * one page, token or head.  1 <= T <= 64.
  * ------------------------------------------------------------------------------------ */
 typedef struct gdn_tree_problem {
     int32_t num_seqs;

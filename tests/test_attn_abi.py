@@ -86,6 +86,25 @@ def test_tree_refusals(L, kw, code):
     assert got == code and size == code
 
 
+STRIDES = [f"{c}_{n}_stride" for c in "kv" for n in ("page", "token", "head")]
+
+
+@pytest.mark.parametrize("cache_dtype", [0, 2])
+@pytest.mark.parametrize("name", STRIDES)
+def test_tree_refuses_caches_without_a_stride(L, name, cache_dtype):
+    """An expanded cache: a tensor map does not have strides of 0.  In a dimension of one the stride is not used."""
+    got, size, _ = tree(L, cache_dtype=cache_dtype, **{name: 0})
+    assert got == 1 and size == 1 and b"strides of 0" in L.lib().gdn_last_error()
+    n = ctypes.c_size_t(0)
+    one = dict(num_seqs=2, T=4, Hq=4, Hkv=1, D=128, cache_dtype=cache_dtype, scale=0.1, page_size=1, max_pages=8, num_pages=1)
+    assert L.lib().gdn_paged_attn_tree_workspace_size(ctypes.byref(L.GdnTreeProblem(**one)), ctypes.byref(n)) == 0
+
+
+@pytest.mark.parametrize("name", STRIDES)
+def test_tree_over_an_expanded_fp32_cache(L, name):
+    assert tree(L, dtype=1, cache_dtype=1, **{name: 0})[1] == 0
+
+
 @pytest.mark.parametrize("ptrs", [dict(q=None), dict(q=ODD), dict(k_new=None), dict(v_new=ODD), dict(k=ODD), dict(v=None), dict(table=None), dict(lens=None),
                                   dict(parents=None), dict(parents=FAKE + 1), dict(o=ODD), dict(ks=ODD), dict(lse=ODD)])
 def test_tree_pointer_refusals(L, ptrs):
