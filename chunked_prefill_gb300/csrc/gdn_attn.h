@@ -29,9 +29,11 @@ cudaError_t launch_prompt_bwd_simt(const PromptArgs& A, cudaStream_t st);
 // bf16, on the tensor cores
 cudaError_t launch_prompt_fwd_tc(const PromptArgs& A, cudaStream_t st);
 int prompt_fwd_status();  // not 0 where a wait of an earlier launch gave up (reads and clears it; synchronises)
+cudaError_t prompt_fwd_wait_out(int32_t limit_us, cudaStream_t st);  // of its test: a wait that gives up
 cudaError_t launch_prompt_bwd_tc(const PromptArgs& A, cudaStream_t st);
 int prompt_bwd_parts(const gdn_prompt_problem& p);
 int prompt_bwd_status();
+cudaError_t prompt_bwd_wait_out(int32_t limit_us, cudaStream_t st);
 cudaError_t launch_prompt_stat(const PromptArgs& A, cudaStream_t st);
 
 struct TreeArgs {
@@ -63,6 +65,8 @@ cudaError_t launch_tree_bf16(const TreeArgs& A, const TreePlan& plan, cudaStream
 cudaError_t launch_tree_f8(const TreeArgs& A, const TreePlan& plan, cudaStream_t st);
 int tree_status_bf16();
 int tree_status_f8();
+cudaError_t tree_wait_out_bf16(int32_t limit_us, cudaStream_t st);
+cudaError_t tree_wait_out_f8(int32_t limit_us, cudaStream_t st);
 cudaError_t launch_tree(const TreeArgs& A, cudaStream_t st);
 
 struct CacheArgs {

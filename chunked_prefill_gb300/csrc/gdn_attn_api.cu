@@ -217,6 +217,15 @@ gdn_status gdn_attn_device_status(void* stream) try {
     return no_host_memory();
 }
 
+gdn_status gdn_debug_attn_wait_timeout(int32_t kernels, int32_t limit_us, void* stream) try {
+    if (kernels < 0 || kernels > 3) return fail(GDN_ERR_INVALID_ARG, "kernels must be in [0, 3]");
+    if (limit_us < 1 || limit_us > 1000000) return fail(GDN_ERR_INVALID_ARG, "limit_us must be in [1, 1000000]");
+    const auto wait_out = kernels == 0 ? gdn::prompt_fwd_wait_out : kernels == 1 ? gdn::prompt_bwd_wait_out : kernels == 2 ? gdn::tree_wait_out_bf16 : gdn::tree_wait_out_f8;
+    return done(wait_out(limit_us, static_cast<cudaStream_t>(stream)));
+} catch (...) {
+    return no_host_memory();
+}
+
 gdn_status gdn_paged_attn_tree_workspace_size(const gdn_tree_problem* problem, size_t* bytes) try {
     if (!problem) return fail(GDN_ERR_INVALID_ARG, "problem is NULL");
     if (!bytes) return fail(GDN_ERR_INVALID_ARG, "bytes is NULL");

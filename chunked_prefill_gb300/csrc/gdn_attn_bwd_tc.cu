@@ -446,5 +446,6 @@ int prompt_bwd_parts(const gdn_prompt_problem& p) {
 cudaError_t launch_prompt_bwd_tc(const PromptArgs& A, cudaStream_t st) { return A.p.D == 64 ? both<64>(A, st) : A.p.D == 128 ? both<128>(A, st) : both<256>(A, st); }
 
 int prompt_bwd_status() { return take_gave_up(); }
+cudaError_t prompt_bwd_wait_out(int32_t limit_us, cudaStream_t st) { return launch_wait_out(limit_us, st); }
 
 }  // namespace gdn

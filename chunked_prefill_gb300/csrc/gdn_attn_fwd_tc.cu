@@ -563,5 +563,6 @@ cudaError_t launch_d(const PromptArgs& A, cudaStream_t st) {
 cudaError_t launch_prompt_fwd_tc(const PromptArgs& A, cudaStream_t st) { return A.p.D == 64 ? launch_d<64>(A, st) : A.p.D == 128 ? launch_d<128>(A, st) : launch_d<256>(A, st); }
 
 int prompt_fwd_status() { return take_gave_up(); }
+cudaError_t prompt_fwd_wait_out(int32_t limit_us, cudaStream_t st) { return launch_wait_out(limit_us, st); }
 
 }  // namespace gdn

@@ -18,15 +18,15 @@ inline int take_gave_up() {
     return x;
 }
 
-// A wait that gives up after 4e9 cycles (2 s).
-__device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t phase) {
+// A wait that gives up after `limit` cycles (4e9: 2 s).
+__device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t phase, long long limit = 4000000000ll) {
     if (tc::mbar_try_wait(bar, phase)) return true;
     const long long t0 = clock64();
     for (;;) {
 #pragma unroll 1
         for (int i = 0; i < 8; ++i)
             if (tc::mbar_try_wait(bar, phase)) return true;
-        if (clock64() - t0 > 4000000000ll) return false;
+        if (clock64() - t0 > limit) return false;
     }
 }
 // The same without suspending the thread, whose waking is on the critical path.
@@ -43,6 +43,19 @@ __device__ __forceinline__ bool bounded_spin(uint64_t* bar, uint32_t phase) {
 // by a whole warp
 __device__ __forceinline__ bool warp_spin(uint64_t* bar, uint32_t phase) { return __all_sync(0xffffffffu, bounded_spin(bar, phase)); }
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t phase) { return __all_sync(0xffffffffu, bounded_wait(bar, phase)); }
+
+// Of the failure report's test: a wait for a barrier at which nothing arrives.
+__global__ void __launch_bounds__(32) k_wait_out(long long limit) {
+    __shared__ uint64_t bar;
+    if (threadIdx.x > 0) return;
+    tc::mbar_init(&bar, 1);
+    tc::mbar_fence_init();
+    if (!bounded_wait(&bar, 0, limit)) g_gave_up = 1;
+}
+inline cudaError_t launch_wait_out(int32_t limit_us, cudaStream_t st) {
+    k_wait_out<<<1, 32, 0, st>>>(2000ll * limit_us);
+    return cudaGetLastError();
+}
 
 // The thread of a warp that issues its products.  The warp runs their loop as a whole and on values that the compiler
 // sees to be the same in all lanes (broadcast by same()), so that descriptors and addresses stay in uniform registers:

@@ -176,6 +176,8 @@ def lib():
             getattr(L, f).restype = ctypes.c_int
         L.gdn_attn_device_status.argtypes = [vp]
         L.gdn_attn_device_status.restype = ctypes.c_int
+        L.gdn_debug_attn_wait_timeout.argtypes = [ctypes.c_int32, ctypes.c_int32, vp]
+        L.gdn_debug_attn_wait_timeout.restype = ctypes.c_int
         L.gdn_device_status.argtypes = [vp, vp]
         L.gdn_device_status.restype = ctypes.c_int
         L.gdn_debug_wait_timeout.argtypes = [vp, ctypes.c_int32, vp]
@@ -206,6 +208,12 @@ def gdn_attn_device_status(stream=None) -> int:
     """Wait for the stream: GDN_OK, or GDN_ERR_TIMEOUT when a device-side wait of an attention call over
     prompts or drafted trees has given up since the last time (see include/gdn.h)."""
     return lib().gdn_attn_device_status(_stream(stream))
+
+
+def gdn_debug_attn_wait_timeout(kernels: int, limit_us: int, stream=None):
+    """Test hook: a wait that runs out after limit_us and leaves the mark of the kernels 0 to 3 (prompts forward and
+    backward, trees over bf16 and 8 bits) for gdn_attn_device_status."""
+    _check(lib().gdn_debug_attn_wait_timeout(int(kernels), int(limit_us), _stream(stream)))
 
 
 def gdn_debug_wait_timeout(workspace, limit_us: int, stream=None):

@@ -433,6 +433,10 @@ gdn_status gdn_prompt_attn_bwd(const gdn_prompt_problem* p, const void* q, const
  * up since it was last asked (that call's outputs are not valid).  Not to be called while a stream is captured. */
 gdn_status gdn_attn_device_status(void* stream);
 
+/* Test hook of that report: a wait that nothing ends gives up after limit_us microseconds (1 .. 1000000) and leaves the mark of
+ * the kernels 0 (prompts forward), 1 (prompts backward), 2 (trees, bf16) or 3 (trees, 8 bits).  Asynchronous on `stream`. */
+gdn_status gdn_debug_attn_wait_timeout(int32_t kernels, int32_t limit_us, void* stream);
+
 /* ------------------------------------------------------------------------------------
  * Attention of a tree of drafted tokens over a paged key-value cache (their verification: all branches
  * in one call).  Sequence n has seq_lens[n] tokens in its pages, as in gdn_paged_attn_decode, but none of

@@ -171,6 +171,11 @@ def test_table_output_refusals(L):
     assert table(L, ptrs=dict(slots=FAKE + 4)) == 1 and table(L, ptrs=dict(slots=None)) == 1 and table(L, ptrs=dict(cu=None)) == 1
 
 
+def test_wait_timeout_refusals(L):
+    for kernels, limit in ((-1, 100), (4, 100), (0, 0), (3, 1000001)):
+        assert L.lib().gdn_debug_attn_wait_timeout(kernels, limit, None) == 1 and L.lib().gdn_last_error()
+
+
 # ------------------------------------------------------------------------------ the Python side
 def prompt_args(B=2, T=3, Tk=3, Hq=4, Hkv=2, D=64):
     z = lambda *s: torch.zeros(*s, dtype=BF)  # noqa: E731
