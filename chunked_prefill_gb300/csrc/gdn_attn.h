@@ -45,7 +45,7 @@ struct TreeArgs {
     float* lse;
     // Blocks of rows (drafted token by drafted token, the query heads of a kv-head), kv-head by kv-head, dealt
     // to `groups` groups of `heads` blocks: as PagedArgs.
-    int cluster, groups, heads;
+    int groups, heads;
     int64_t* before;  // [num_seqs + 1] tiles before each sequence, per block
     float* part;      // partial results, two places per CTA
     float2* part_ml;

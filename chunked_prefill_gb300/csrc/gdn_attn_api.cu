@@ -1,5 +1,6 @@
 // C ABI of attention over prompts, of drafted trees over a paged cache, and of the cache's own operators:
-// argument checks, defaults of the strides and the launches.  Nothing here allocates, frees or synchronises.
+// argument checks, defaults of the strides and the launches.  Nothing here allocates, frees or synchronises, but
+// that gdn_attn_device_status waits for its stream and copies from the device.
 #include "gdn_attn.h"
 #include "gdn_checks.h"
 #include "gdn_internal.h"

@@ -36,9 +36,9 @@ template <int D, bool KEYS> struct Bwd {
 
 template <int BN> struct BwdShared {
     uint64_t full0[3], empty0[3], full1[3], empty1[3], res_full, s_ready, p_ready, dp_ready, ds_ready, stat_full[2], stat_empty[2], issued[4], clean[4], done, drain;
-    alignas(16) float nlse[2][BN];
+    alignas(16) float nlse[2][BN];  // of the streamed queries, negated
     float ndrop[2][BN];
-    uint32_t tmem;  // of the streamed queries, negated
+    uint32_t tmem;
 };
 
 struct BwdMaps {
@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(Bwd<D, KEYS>::T, 1) k_prompt_bwd_tc(const Prom
     const int hk = KEYS ? sub / L::HALVES / parts : sub / G, heads = KEYS ? G / parts : 1, h0 = KEYS ? hk * G + part * heads : sub;
     Seq s;
     int row;
-    if (!find_tile<128>(p, KEYS, KEYS ? number : tiles - 1 - number, s, row)) return;  // those with the most to do first
+    if (!find_tile<128>(p, KEYS, KEYS ? number : tiles - 1 - number, s, row)) return;  // of a sequence those with the most to do first
     const int rows = min(128, (KEYS ? s.lk : s.lq) - row), streamed = KEYS ? s.lq : s.lk;
     const int64_t res0 = (KEYS ? s.k0 : s.q0) + int64_t(row);
     const int str_at = KEYS ? s.q0 : s.k0;

@@ -11,9 +11,9 @@
 // in the order in which they are used), one cleans tiles of values in which some query masks some key: a weight of 0
 // would make NaN of an infinite value, so rows behind the sequence and infinite or NaN values become zeros there, and
 // the latter are added to the rows that see them at the end.
-// Tiles of queries go by descending length, all heads of one after another, so that neighbours read the same keys; a CTA
-// has one, or takes one after another (see launch_d): while one tile's result is written the next one's queries and
-// keys come and its first scores are made.
+// Tiles of queries go from the last to the first, so that of each sequence those with the most keys come first, all heads
+// of one after another, so that neighbours read the same keys; a CTA has one, or takes one after another (see launch_d):
+// while one tile's result is written the next one's queries and keys come and its first scores are made.
 // Bound: the tensor cores (4 D flops per pair of a query and a key that it attends to); a tile's weights (a max, a
 // multiply-add, an exponential, an addition and half a conversion for each of 16384 scores) take about as long as its
 // products with 128 features, and longer with 64.  Measured, TFLOP/s: 1 x 32768 tokens, 16 / 4 heads, 128 features
@@ -114,7 +114,7 @@ template <int NQ> struct Items {
     __device__ __forceinline__ bool next(const gdn_prompt_problem& p) {
         for (; at < all; at += gridDim.x) {
             const int number = int(at / p.Hq);
-            if (!find_tile<NQ * 128>(p, false, tiles - 1 - number, s, row)) continue;  // the longest first
+            if (!find_tile<NQ * 128>(p, false, tiles - 1 - number, s, row)) continue;  // of a sequence those with the most keys first
             h = int(at - int64_t(number) * p.Hq);
             k = walk_of<NQ>(p, s, row);
             at += gridDim.x;

@@ -19,7 +19,7 @@ __global__ void __launch_bounds__(ST) k_prompt_fwd_simt(const PromptArgs A) {
     const gdn_prompt_problem& p = A.p;
     Seq s;
     int row;
-    if (!find_tile<M>(p, false, gridDim.x - 1 - blockIdx.x, s, row)) return;  // the longest first
+    if (!find_tile<M>(p, false, gridDim.x - 1 - blockIdx.x, s, row)) return;  // of a sequence those with the most keys first
     const int h = blockIdx.y, j = h / (p.Hq / p.Hkv), rows = min(M, s.lq - row);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int k_end = s.rest ? 0 : min(s.lk, last_key(s, row + rows - 1) + 1), k_begin = k_end > 0 ? first_key(p, s, row) / B * B : 0;

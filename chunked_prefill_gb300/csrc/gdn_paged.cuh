@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "gdn_common.cuh"
 #include "gdn_decode.h"
 #include "gdn_internal.h"
@@ -56,11 +58,13 @@ __device__ __forceinline__ int64_t share_of(int64_t total, int parts, int warps)
 // CTA 0 also leaves the number of tiles before each sequence (per block of heads) in A.before.
 template <int T, typename Args>
 __device__ Part find_part(const Args& A, int tok, int warps) {
-    if (A.cluster) {  // a cluster of CTAs per (sequence, block of heads), equal parts of its tiles
-        const int pair = blockIdx.x / A.cluster, r = blockIdx.x % A.cluster, blocks = A.groups * A.heads, n = pair / blocks, b = pair % blocks;
-        const int tiles = range_of(A, n).tiles(tok), share = ((tiles + A.cluster - 1) / A.cluster + warps - 1) / warps * warps;
-        const int at = min(r * share, tiles);
-        return {0, min(share, tiles - at), n, b % A.groups, b / A.groups, at};
+    if constexpr (std::is_same_v<Args, PagedArgs>) {
+        if (A.cluster) {  // a cluster of CTAs per (sequence, block of heads), equal parts of its tiles
+            const int pair = blockIdx.x / A.cluster, r = blockIdx.x % A.cluster, blocks = A.groups * A.heads, n = pair / blocks, b = pair % blocks;
+            const int tiles = range_of(A, n).tiles(tok), share = ((tiles + A.cluster - 1) / A.cluster + warps - 1) / warps * warps;
+            const int at = min(r * share, tiles);
+            return {0, min(share, tiles - at), n, b % A.groups, b / A.groups, at};
+        }
     }
     __shared__ int64_t wsum[T / 32];
     __shared__ int found[3];

@@ -28,26 +28,27 @@ struct Tree {
     uint64_t sees[64];
     int depth[64];
 };
+__device__ __forceinline__ void read_token(const TreeArgs& A, int n, int t, uint64_t& sees, int& depth) {
+    const int32_t* parents = A.parents + int64_t(n) * A.p.T;
+    sees = 0, depth = -1;
+    for (int at = t; at >= 0;) {
+        ++depth;
+        if (A.p.window == 0 || depth < A.p.window) sees |= uint64_t(1) << at;
+        const int up = parents[at];
+        if (up < -1 || up >= at) {
+            sees = 0, depth = -1;
+            break;
+        }
+        at = up;
+    }
+}
 // By the first 64 threads of the CTA; the caller synchronises.
 __device__ __forceinline__ void read_tree(const TreeArgs& A, int n, Tree& tree) {
     const int t = threadIdx.x;
     if (t >= 64) return;
     uint64_t sees = 0;
     int depth = -1;
-    if (t < A.p.T) {
-        const int32_t* parents = A.parents + int64_t(n) * A.p.T;
-        int at = t;
-        while (at >= 0) {
-            ++depth;
-            if (A.p.window == 0 || depth < A.p.window) sees |= uint64_t(1) << at;
-            const int up = parents[at];
-            if (up < -1 || up >= at) {
-                sees = 0, depth = -1;
-                break;
-            }
-            at = up;
-        }
-    }
+    if (t < A.p.T) read_token(A, n, t, sees, depth);
     tree.sees[t] = sees;
     tree.depth[t] = depth;
 }

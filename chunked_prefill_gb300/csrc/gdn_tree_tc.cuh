@@ -511,20 +511,7 @@ __global__ void __launch_bounds__(TreeTc<C, D, NQ>::T, 1) k_tree_tc(const TreeAr
             // what this row's drafted token attends to
             uint64_t sees = 0;
             int depth = -1;
-            if (r < all_rows) {
-                const int32_t* parents = A.parents + int64_t(it.n) * p.T;
-                int at = t;
-                while (at >= 0) {
-                    ++depth;
-                    if (p.window == 0 || depth < p.window) sees |= uint64_t(1) << at;
-                    const int up = parents[at];
-                    if (up < -1 || up >= at) {
-                        sees = 0, depth = -1;
-                        break;
-                    }
-                    at = up;
-                }
-            }
+            if (r < all_rows) read_token(A, it.n, t, sees, depth);
             // A row without a token goes along unmasked, for a warp with a masked row takes twice as long, and is dropped at the end.
             const bool live = depth >= 0;
             const int first = live ? first_cached(A, it.R, depth) : 0;
