@@ -55,6 +55,9 @@ struct Walk {
     int clean_to, clean_from;  // tiles below and from which on some query of the CTA masks some key (or the tile goes past the keys)
     __device__ __forceinline__ bool special(int j) const { return j < clean_to || j >= clean_from; }
     __device__ __forceinline__ int specials() const { return hi - lo - max(0, min(hi, clean_from) - max(lo, clean_to)); }
+    // Whether a record of bad values is kept of it.  With one tile of queries of every one: each has results, for which the next
+    // one's products wait, and its queries' place keeps the cleaning within two tiles of them.
+    template <int NQ> __device__ __forceinline__ bool recorded() const { return NQ == 2 ? specials() > 0 : lo < hi; }
     __device__ __forceinline__ bool in(int w, int j) const { return w == 0 ? j >= begin[0] && j < end[0] : j >= begin[1] && j < end[1]; }
 };
 template <int NQ>
@@ -215,9 +218,9 @@ __global__ void __launch_bounds__(Fwd<D>::T, 1)
             // of which one half has no rows, or sees no key, waits for the other half's results alone, and the warps of this one
             // may be several tiles behind, or ahead.  A half uses the places of the records in which it sees keys; it cannot be done
             // with one before its tiles are cleaned here, so no phase is passed over.
-            if (k.specials() > 0) {
+            if (NQ == 2 && k.recorded<NQ>()) {
 #pragma unroll
-                for (int w = 0; w < NQ; ++w) {
+                for (int w = 0; w < 2; ++w) {
                     const uint32_t bit = 1u << (w * 4 + (record & 3));
                     if (ok && (used & bit)) ok = warp_wait(&sh.bad_free[w][record & 3], odd & bit ? 0 : 1);
                     if (k.end[w] > k.begin[w]) used |= bit, odd ^= bit;
@@ -248,7 +251,7 @@ __global__ void __launch_bounds__(Fwd<D>::T, 1)
                 ++nth;
             }
             n0 += 2 * (k.hi - k.lo) * NC;
-            record += k.specials() > 0;
+            record += k.recorded<NQ>();
         }
     } else if (warp == NQ * 4) {  // ---- products
         constexpr uint32_t IS = tc::make_idesc(128, 128, 0, 0), IO = tc::make_idesc(128, DC, 0, 1);
@@ -480,7 +483,8 @@ __global__ void __launch_bounds__(Fwd<D>::T, 1)
             }
             if (!ok) break;
             // written before the last product
-            const int specials = k.specials(), bad_tiles = steps > 0 && specials > 0 && sh.bad_item[record & 3] == record ? specials : 0;
+            const bool recorded = k.recorded<NQ>();
+            const int bad_tiles = steps > 0 && recorded && sh.bad_item[record & 3] == record ? k.specials() : 0;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 float x[32];
@@ -519,11 +523,11 @@ __global__ void __launch_bounds__(Fwd<D>::T, 1)
                 __syncwarp();
                 if (lane == 0) {
                     tc::mbar_arrive(&sh.o_free[w]);
-                    if (specials > 0) tc::mbar_arrive(&sh.bad_free[w][record & 3]);
+                    if (NQ == 2 && recorded) tc::mbar_arrive(&sh.bad_free[w][record & 3]);
                 }
             }
             count += steps;
-            record += specials > 0;
+            record += recorded;
         }
     }
     if (!ok) g_gave_up = 1;
