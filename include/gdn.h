@@ -385,7 +385,8 @@ gdn_status gdn_rmsnorm_bwd(const gdn_norm_problem* p, const void* s, const void*
  * Sequences are packed: queries [cu_seqlens[n], cu_seqlens[n+1]), keys by cu_seqlens_k (NULL: by
  * cu_seqlens, with total_k = total_q); without cu_seqlens there are num_seqs of equal lengths.  Both are
  * read on the device alone, and cut to [0, total], so a captured call serves other lengths; sequences must
- * not overlap.  Rows that no sequence covers are left as they were (clear_rest = 0), or get o = 0, lse = -inf
+ * not overlap.  Nothing that this or a following entry point writes may overlap what it reads, unless it is the same
+ * argument.  Rows that no sequence covers are left as they were (clear_rest = 0), or get o = 0, lse = -inf
  * and gradients of 0 (clear_rest = 1).  What lies there, NaN or not, is not used.
  *
  * gdn_prompt_attn_bwd: the gradients of <o, dO> + <lse, dlse> (dlse NULL: 0) with respect to q, k and v,

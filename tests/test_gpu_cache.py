@@ -229,6 +229,40 @@ def test_captured_table_steps(gdn):
         model = want[:3]
 
 
+def test_captured_table_steps_of_many_tokens(gdn):
+    """The form with two launches, twice in a graph, on another stream and again and again; then all that was taken is
+    given back, in the order that giving back has."""
+    rng = np.random.default_rng(3)
+    N, page, width = 300, 16, 40
+    table, lens, stack = state(rng, N, width, page, 9000, 0)
+    lens = np.minimum(lens, 60)
+    t, l, s, f = dev(table), dev(lens), dev(stack), dev([9000])
+    new, before = [rng.multinomial(40000, rng.dirichlet(np.full(N, 20.0))) for _ in range(2)], l.clone()
+    given, total = [dev(n) for n in new], 40000
+    want, model = [], (table.tolist(), lens.tolist(), 9000)
+    for n in new:
+        want.append(attention.extend(model[0], model[1], n.tolist(), stack.tolist(), model[2], page, total))
+        model = want[-1][:3]
+    end = attention.trim(model[0], model[1], before.tolist(), stack.tolist(), model[2], page)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            out = []
+            for n in given:
+                out.append((*gdn.page_table_extend(t, l, n, s, f, page, total), l.clone(), f.clone(), t.clone()))
+            gdn.page_table_trim(t, l, before, s, f, page)
+        for _ in range(3):
+            graph.replay()
+            side.synchronize()
+            for (slots, cu, length, free, pages), w in zip(out, want):
+                assert slots.tolist() == w[3] and cu.tolist() == w[4] and length.tolist() == w[1] and int(free) == w[2] and pages.tolist() == w[0]
+            assert l.tolist() == end[0] == before.tolist() and s.tolist() == end[1] and int(f) == end[2] == 9000
+            t.copy_(dev(table))
+            s.copy_(dev(stack))
+
+
 # --------------------------------------------------------------------------- all of them together
 @pytest.mark.parametrize("dtype,D", [(BF, 64), (BF, 128), (F32, 64)])
 def test_from_a_prompt_to_accepted_drafts(gdn, dtype, D):

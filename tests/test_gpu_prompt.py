@@ -398,6 +398,28 @@ def test_two_calls_at_once(gdn):
         same(outs)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_graphs_that_share_a_workspace(gdn, dtype):
+    """Two captured gradients over one workspace, whatever it held before, replayed one after the other."""
+    xs = [make([(300, 300), (40, 90)], 8, 2, 64, dtype, seed=s, behind=9) for s in (1, 2)]
+    fwd = [gdn.prompt_attention(x["q"], x["k"], x["v"], return_lse=True, **args(x)) for x in xs]
+    grad = lambda x, f, **kw: gdn.gdn_prompt_attn_bwd(x["q"], x["k"], x["v"], *f, x["do"], **args(x), **kw)  # noqa: E731
+    want = [grad(x, f) for x, f in zip(xs, fwd)]
+    ws = torch.full((1 << 26,), 255, dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graphs, outs = [], []
+    with torch.cuda.stream(side):
+        for x, f in zip(xs, fwd):
+            graphs.append(torch.cuda.CUDAGraph())
+            with torch.cuda.graph(graphs[-1], stream=side):
+                outs.append(grad(x, f, workspace=ws))
+        for graph in graphs * 2:
+            graph.replay()
+    side.synchronize()
+    assert all(torch.equal(a, b) for g, w in zip(outs, want) for a, b in zip(g, w))
+
+
 def test_on_another_stream(gdn):
     x = make([(300, 300)], 4, 2, 128, seed=4)
     want = run(gdn, x)
