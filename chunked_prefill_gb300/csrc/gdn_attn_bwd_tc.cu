@@ -15,9 +15,9 @@
 // dealt to several CTAs, whose fp32 sums a last kernel adds up in order.
 // Streamed rows behind the sequence are made zeros, for a product of a weight of 0 with what lies there could be NaN.
 // Bound: the tensor cores.  Measured, of the 10 D flops per pair that one pass would take (these do 14 D), with the
-// statistics and sums, TFLOP/s: 1 x 32768 tokens, 16 / 4 heads, 128 features 9.75 ms, 1127; 2 x 8192, 32 / 8,
-// 128 2.52 ms, 1091; 1 x 16384, 32 / 8, 64 4.07 ms, 675 (the weights); 1 x 16384, 16 / 2, 256 7.4 ms, 741 (S and dP of a
-// tile of keys made by two CTAs, one stage of dO).  The keys' pass keeps the tensor cores 68 % busy, the queries' 59 %.
+// statistics and sums, TFLOP/s: 1 x 32768 tokens, 16 / 4 heads, 128 features 9.73 ms, 1130; 2 x 8192, 32 / 8,
+// 128 2.51 ms, 1097; 1 x 16384, 32 / 8, 64 4.06 ms, 676 (the weights); 1 x 16384, 16 / 2, 256 7.4 to 7.5 ms, 732 to 741 (S and
+// dP of a tile of keys made by two CTAs, one stage of dO).  The keys' pass keeps the tensor cores 69 % busy, the queries' 63 %.
 #include "gdn_attn_tc.cuh"
 
 namespace gdn {

@@ -17,8 +17,8 @@
 // Bound: the tensor cores (4 D flops per pair of a query and a key that it attends to); a tile's weights (a max, a
 // multiply-add, an exponential, an addition and half a conversion for each of 16384 scores) take about as long as its
 // products with 128 features, and longer with 64.  Measured, TFLOP/s: 1 x 32768 tokens, 16 / 4 heads, 128 features
-// 2.69 ms, 1632; 2 x 8192, 32 / 8, 128 0.78 ms, 1405; 1 x 16384, 32 / 8, 64 1.26 ms, 866; 1 x 16384, 16 / 2, 256
-// 1.33 ms, 1653.  Short sequences: a tile's setup, masked softmax and end, which do not shrink with its products.
+// 2.72 to 2.85 ms, 1545 to 1615; 2 x 8192, 32 / 8, 128 0.80 ms, 1383; 1 x 16384, 32 / 8, 64 1.28 ms, 859; 1 x 16384,
+// 16 / 2, 256 1.34 ms, 1646; 2 x 8192, 32 / 8, 128 with a window of 512 0.25 ms, 523.  Short sequences: a tile's setup, masked softmax and end, which do not shrink with its products.
 #include "gdn_attn_tc.cuh"
 
 namespace gdn {
@@ -552,8 +552,8 @@ cudaError_t launch_d(const PromptArgs& A, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     // One tile of queries to a CTA where sequences are long: the hardware deals CTAs out as others end, more evenly than taking
     // turns does.  Short ones take turns, for the overlap of one tile's end with the next one's begin.  32 / 8 heads, 128 features,
-    // turns and one each: 16 x 512 tokens 93 and 110 us, 8 x 2048 299 and 317, 2 x 8192 802 and 783, 1 x 32768 (16 / 4) 2782 and 2694
-    // (before masks were made of words).
+    // turns and one each: 16 x 512 tokens 90 and 105 us, 8 x 2048 296 and 315, 4 x 4096 464 and 474, 2 x 8192 815 and 796,
+    // 1 x 32768 (16 / 4) 2862 and 2724; 64 features, 4 x 4096: 384 and 404; 256 features (16 / 2): 413 and 421.
     const int64_t all = tiles * p.Hq, sms = sm_count_cached();
     const bool turns = p.num_seqs == 0 || p.total_k / p.num_seqs <= 4096 || all > 0x7fffffff;  // a grid has 2^31 - 1 CTAs at most
     timing_begin("prompt_attn_fwd", st);

@@ -1,7 +1,9 @@
 // Attention over prompts and its gradient on the CUDA cores, in fp32 throughout (see include/gdn.h): the tensor cores
 // would round products to 10 bits.  Tiles of queries against tiles of keys in shared memory, a running softmax, 4 x 4
 // values of a product in a thread's registers; the gradient in two passes, keys and queries, as with bf16.  Bound: the
-// fp32 units on long prompts, latency on short ones (2 x 100 tokens, 8 / 2 heads, 64 features: 10 us a call).
+// fp32 units' instructions and the reads of shared memory between them on long prompts (4 x 2048 tokens, 16 / 4 heads: forward
+// 1.09, 2.21 and 4.51 ms with 64, 128 and 256 features, 31 TFLOP/s; gradient 4.2, 7.8 and 22.3 ms, 20, 22 and 15 TFLOP/s of the
+// 10 D flops of one pass), latency on short ones (2 x 100 tokens, 8 / 2 heads, 64 features: 10 us a call).
 #include "gdn_attn_simt.cuh"
 
 namespace gdn {

@@ -3,7 +3,7 @@
 //
 // gdn_paged_cache_write moves every value once: bound by HBM for a prompt, by the launch for a few tokens.
 // Up to 32 lanes have a token, whose slot and row they look up once, and two 16-byte pieces of the output each.
-// 32767 tokens of 8 heads of 128 from bf16 into 8 bits: 45 us, 4.5 TB/s; the conversion's instructions beside the
+// 32767 tokens of 8 heads of 128 from bf16 into 8 bits: 44 us, 4.6 TB/s; the conversion's instructions beside the
 // bytes.  96 accepted tokens: 5 us a call.
 //
 // gdn_page_table_extend and _trim are latency: one launch, in which every CTA sums the requests' needs for

@@ -8,7 +8,9 @@
 // leaves (accumulator, maximum, sum), and a second kernel joins them in the list's order.
 // v_scale goes into the weights of the cached tokens, so that drafted ones join them as they are.
 //
-// bf16 and 8-bit caches: k_tree_tc (gdn_tree_tc.cuh), on the tensor cores.  fp32: k_tree_simt, here.
+// bf16 and 8-bit caches: k_tree_tc (gdn_tree_tc.cuh), on the tensor cores.  fp32: k_tree_simt, here; bound by its products' 4 x 4
+// values a thread, whose loads nothing overlaps: 32 sequences, 400 MB of keys and values, 32 / 8 heads, 8 drafted tokens 0.84, 1.35
+// and 1.38 ms with 64, 128 and 256 features, 4 to 7 % of HBM's rate, whatever the page size; 64 drafted tokens 3.9, 6.5, 6.5 ms.
 #include "gdn_attn_simt.cuh"
 #include "gdn_tree.cuh"
 

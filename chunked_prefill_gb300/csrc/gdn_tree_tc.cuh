@@ -10,7 +10,10 @@
 // Pages lie anywhere, but their rows are at regular distances: TMA brings pieces of up to 16 tokens (the largest power of
 // two that divides the page size), issued by the lanes of one warp, straight into the swizzled tiles that the tensor cores
 // read; of 8-bit caches into a ring of their own, from where six warps widen them to bf16 (exactly).  A page number out of
-// range is replaced by one past the last, which TMA reads as zeros.  (Copied by cp.async, in 16-byte pieces by 128 to 224
+// range is replaced by one past the last, which TMA reads as zeros.  Every piece is a request of its own, some 120 cycles of
+// the warp that makes it, so pages whose size has no factor of 16 take longer, odd ones by far: 32 sequences, 400 MB of keys and
+// values, 32 / 8 heads of 128, 16 drafted tokens, pages of 16 or 48, 24, 100, 5 or 1 tokens (pieces of 16, 8, 4, 1): bf16 109, 115,
+// 143, 387 us; 8 bits, where one warp requests both sides, 206, 264, 382, 1108.  (Copied by cp.async, in 16-byte pieces by 128 to 224
 // threads, 32 sequences of up to 8192 tokens took 190 us: a tile's addresses alone kept those threads busy.)
 // Where some row masks a token that others see (drafted tokens, the edge of a window) infinite and NaN values are made
 // zeros, for a weight of 0 would make NaN of them, and are added at the end to the rows that see them.
